@@ -182,7 +182,8 @@ def _heads(n, counts, d, dtype, fused, g):
 def _quantise(x):
     """Codes and power-of-two scale bytes of pages x [..., page, d]."""
     m, e = torch.frexp(x.abs().amax((-1, -2)))
-    e = torch.where(m <= 0.875, e - 9, e - 8).clamp(-126, 127)
+    e = torch.where(m <= 0.875, e - 9, e - 8)
+    e = torch.where(m > 0, e, -126).clamp(-126, 127)
     codes = torch.ldexp(x, -e[..., None, None]).clamp(-448, 448).to(torch.float8_e4m3fn)
     return codes, (e + 127).to(torch.uint8).view(torch.float8_e8m0fnu)
 
@@ -350,7 +351,8 @@ def _plain_append(s):
         amax = torch.zeros((c["B"] * M, Hkv), device=DEV)
         amax = amax.scatter_reduce(0, (at[0] * M + at[1])[:, None].expand(-1, Hkv), a, "amax")
         m, e = torch.frexp(amax.view(c["B"], M, Hkv)[again])
-        e = torch.where(m <= 0.875, e - 9, e - 8).clamp(-126, 127)
+        e = torch.where(m <= 0.875, e - 9, e - 8)
+        e = torch.where(m > 0, e, -126).clamp(-126, 127)
         scale, codes = s["cache"][name + "_scale"].view(torch.uint8), s["cache"][name].view(torch.uint8)
         old = scale[page].int() - 127
         e = torch.where((start == 0)[..., None], e, torch.maximum(e, old))
@@ -447,7 +449,7 @@ def _exact_rows(x, w, pos, table, layout):
 
 def _exact_exponent(top):
     m, e = torch.frexp(top.double() / 448.0)
-    return (e - (m == 0.5).int()).clamp(-126, 127)
+    return torch.where(top > 0, e - (m == 0.5).int(), -126).clamp(-126, 127)
 
 
 def _exact_append(s):

@@ -1,0 +1,284 @@
+// Internals shared by the softmax-attention operators: resolved arguments,
+// e4m3 / e8m0 conversions and the per-head norm and rotation of a row piece.
+#pragma once
+
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+#include "common.cuh"
+
+namespace falcon {
+
+// Rows of one of q, k, v, o: pointer, elements from token to token, and
+// whether every row starts on a 16-byte boundary.
+struct RowsIn {
+  const void* p;
+  int64_t stride;
+  bool vec;
+};
+struct RowsOut {
+  void* p;
+  int64_t stride;
+  bool vec;
+};
+
+// How the rows of a head are normed and rotated.
+struct HeadArgs {
+  int d, norm;
+  float eps;
+  int rot, layout, rows;
+  const float2* table;
+};
+
+int launch_rope_table(const double* inv_freq, int rot, int rows, float mscale, float* table, cudaStream_t s);
+int launch_qk_norm_rope(const HeadArgs& h, int dtype, int64_t tokens, int Hq, int Hkv, RowsIn q, RowsIn k,
+                        const float* w_q, const float* w_k, const int64_t* pos, RowsOut qo, RowsOut ko,
+                        cudaStream_t s);
+
+struct AppendArgs {
+  int B, Hkv, page, num_pages, max_pages, max_q;
+  int64_t tokens;
+  RowsIn k, v;
+  const float* w_k;
+  const int32_t* cu;
+  const int32_t* ctx;
+  const int32_t* blocks;
+  falcon_kv_cache_t cache;
+};
+int launch_kv_append(const HeadArgs& h, int dtype, const AppendArgs& a, cudaStream_t s);
+
+struct DecodeArgs {
+  int B, Hq, Hkv, d, page, num_pages, max_pages, max_k;
+  float scale;
+  RowsIn q;
+  RowsOut o;
+  float* lse;
+  const int32_t* blocks;
+  const int32_t* lens;
+  falcon_kv_cache_t cache;
+  void* ws;
+};
+size_t attn_decode_ws_bytes(int B, int Hq, int Hkv, int d, int page, int max_k);
+int launch_attn_decode(const DecodeArgs& a, int dtype, cudaStream_t s);
+
+struct PromptArgs {
+  int B, Hq, Hkv, d, max_q, max_k;
+  float scale;
+  int64_t tokens, k_tokens;
+  RowsIn q, k, v;
+  RowsOut o;
+  float* lse;
+  const int32_t* cu_q;
+  const int32_t* cu_k;
+  void* ws;
+};
+int launch_attn_prompt(const PromptArgs& a, int dtype, cudaStream_t s);
+
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kLn2 = 0.6931471805599453f;
+
+// ---------------------------------------------------------------- rows
+template <typename T> struct Raw8;                       // 8 elements as loaded
+template <> struct Raw8<__nv_bfloat16> { uint4 v; };
+template <> struct Raw8<float> { float4 a, b; };
+
+template <bool VEC>
+__device__ __forceinline__ Raw8<__nv_bfloat16> load8(const __nv_bfloat16* p) {
+  Raw8<__nv_bfloat16> r;
+  if (VEC) {
+    r.v = *reinterpret_cast<const uint4*>(p);
+  } else {
+    const unsigned short* u = reinterpret_cast<const unsigned short*>(p);
+    uint32_t w[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) w[i] = u[2 * i] | (static_cast<uint32_t>(u[2 * i + 1]) << 16);
+    r.v = make_uint4(w[0], w[1], w[2], w[3]);
+  }
+  return r;
+}
+template <bool VEC>
+__device__ __forceinline__ Raw8<float> load8(const float* p) {
+  Raw8<float> r;
+  if (VEC) {
+    r.a = *reinterpret_cast<const float4*>(p);
+    r.b = *reinterpret_cast<const float4*>(p + 4);
+  } else {
+    r.a = make_float4(p[0], p[1], p[2], p[3]);
+    r.b = make_float4(p[4], p[5], p[6], p[7]);
+  }
+  return r;
+}
+__device__ __forceinline__ void unpack8(const Raw8<__nv_bfloat16>& r, float (&x)[8]) {
+  const uint32_t w[4] = {r.v.x, r.v.y, r.v.z, r.v.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    x[2 * i] = __uint_as_float(w[i] << 16);
+    x[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
+  }
+}
+__device__ __forceinline__ void unpack8(const Raw8<float>& r, float (&x)[8]) {
+  x[0] = r.a.x; x[1] = r.a.y; x[2] = r.a.z; x[3] = r.a.w;
+  x[4] = r.b.x; x[5] = r.b.y; x[6] = r.b.z; x[7] = r.b.w;
+}
+template <bool VEC>
+__device__ __forceinline__ void store8(__nv_bfloat16* p, const float (&x)[8]) {
+  uint32_t w[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    __nv_bfloat162 v = __floats2bfloat162_rn(x[2 * i], x[2 * i + 1]);
+    w[i] = *reinterpret_cast<uint32_t*>(&v);
+  }
+  if (VEC) {
+    *reinterpret_cast<uint4*>(p) = make_uint4(w[0], w[1], w[2], w[3]);
+  } else {
+    unsigned short* u = reinterpret_cast<unsigned short*>(p);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      u[2 * i] = static_cast<unsigned short>(w[i]);
+      u[2 * i + 1] = static_cast<unsigned short>(w[i] >> 16);
+    }
+  }
+}
+template <bool VEC>
+__device__ __forceinline__ void store8(float* p, const float (&x)[8]) {
+  if (VEC) {
+    *reinterpret_cast<float4*>(p) = make_float4(x[0], x[1], x[2], x[3]);
+    *reinterpret_cast<float4*>(p + 4) = make_float4(x[4], x[5], x[6], x[7]);
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) p[i] = x[i];
+  }
+}
+
+// Norm and rotation of 8 consecutive elements c0 .. c0 + 7 of a head row; the
+// d / 8 lanes of the row are neighbours in the warp and every lane of the
+// warp takes part (lanes without a row pass x = 0).  w8 holds this lane's
+// norm weights, (co, si) the table's entries of its pairs.  Rows are normed
+// and rotated in fp32; `row` gives the raw row again for partners that no
+// whole lane holds (rot / 2 not a multiple of 8).
+struct HeadPiece {
+  float w[8];
+  float co[8], si[8];  // HALF: per element; INTERLEAVED: per pair (the first 4)
+};
+__device__ __forceinline__ void load_weights(HeadPiece& hp, const HeadArgs& h, const float* w, int c0) {
+#pragma unroll
+  for (int i = 0; i < 8; ++i) hp.w[i] = (h.norm && w) ? __ldg(w + c0 + i) : 1.f;
+}
+// Angles of this lane's elements at `pos`; outside the table they are NaN.
+__device__ __forceinline__ void load_angles(HeadPiece& hp, const HeadArgs& h, int64_t pos, int c0) {
+  if (h.rot == 0) return;
+  const bool in = pos >= 0 && pos < h.rows;
+  const int half = h.rot >> 1;
+  const float2* t = h.table + (in ? pos : 0) * half;
+  const float nan = __int_as_float(0x7fffffff);
+  if (h.layout == FALCON_ROPE_HALF) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const int c = c0 + i;
+      if (c < h.rot) {
+        const float2 a = __ldg(t + (c < half ? c : c - half));
+        hp.co[i] = in ? a.x : nan;
+        hp.si[i] = in ? (c < half ? -a.y : a.y) : nan;
+      } else {
+        hp.co[i] = 1.f;
+        hp.si[i] = 0.f;
+      }
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int j = (c0 >> 1) + i;
+      if (j < half) {
+        const float2 a = __ldg(t + j);
+        hp.co[i] = in ? a.x : nan;
+        hp.si[i] = in ? a.y : nan;
+      } else {
+        hp.co[i] = 1.f;
+        hp.si[i] = 0.f;
+      }
+    }
+  }
+}
+template <typename T>
+__device__ __forceinline__ void norm_rotate8(float (&x)[8], const HeadPiece& hp, const HeadArgs& h,
+                                             const float* w, const T* row, bool live, int c0, int lane) {
+  const int L = h.d >> 3;
+  float r = 1.f;
+  if (h.norm) {
+    float s = 0.f;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) s = fmaf(x[i], x[i], s);
+    for (int o = L >> 1; o; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+    r = rsqrtf(s / static_cast<float>(h.d) + h.eps);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) x[i] = x[i] * r * hp.w[i];
+  }
+  if (h.rot == 0) return;
+  if (h.layout == FALCON_ROPE_INTERLEAVED) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      if (c0 + 2 * i < h.rot) {
+        const float a = x[2 * i], b = x[2 * i + 1];
+        x[2 * i] = a * hp.co[i] - b * hp.si[i];
+        x[2 * i + 1] = b * hp.co[i] + a * hp.si[i];
+      }
+    }
+    return;
+  }
+  const int half = h.rot >> 1;
+  float y[8];
+  if ((half & 7) == 0) {  // the partners are one other lane's 8 elements
+    const int off = half >> 3;
+    const int src = c0 < half ? lane + off : lane - off;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) y[i] = __shfl_sync(0xffffffffu, x[i], src & 31);
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const int c = c0 + i, pc = c < half ? c + half : c - half;
+      y[i] = 0.f;
+      if (live && c < h.rot) {
+        y[i] = to_f32(row[pc]);
+        if (h.norm) y[i] = y[i] * r * (w ? __ldg(w + pc) : 1.f);
+      }
+    }
+    __syncwarp();
+  }
+#pragma unroll
+  for (int i = 0; i < 8; ++i)
+    if (c0 + i < h.rot) x[i] = x[i] * hp.co[i] + y[i] * hp.si[i];
+}
+
+// ---------------------------------------------------------------- 8-bit cache
+// 2^e as a float, e in [-149, 127]
+__device__ __forceinline__ float exp2i(int e) {
+  return e >= -126 ? __int_as_float((e + 127) << 23) : __int_as_float(1 << (e + 149));
+}
+// value of a scale byte (e8m0)
+__device__ __forceinline__ float e8m0(uint32_t byte) {
+  return byte ? __uint_as_float(byte << 23) : __uint_as_float(0x00400000u);
+}
+// smallest e in [-126, 127] with amax <= 448 * 2^e (448 = 0.875 * 2^9)
+__device__ __forceinline__ int scale_exponent(float amax) {
+  if (!(amax > 0.f)) return -126;
+  int x;
+  const float m = frexpf(amax, &x);
+  const int e = m <= 0.875f ? x - 9 : x - 8;
+  return e < -126 ? -126 : e > 127 ? 127 : e;
+}
+// two floats -> two e4m3 codes (lo in the low byte), nearest even, saturating
+__device__ __forceinline__ uint32_t to_e4m3x2(float lo, float hi) {
+  uint16_t r;
+  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+// two e4m3 codes -> packed halves (exact)
+__device__ __forceinline__ uint32_t e4m3x2_to_half2(uint32_t two) {
+  uint32_t r;
+  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(r) : "h"(static_cast<uint16_t>(two)));
+  return r;
+}
+
+}  // namespace falcon

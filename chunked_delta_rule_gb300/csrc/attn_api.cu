@@ -1,0 +1,204 @@
+// C ABI of the softmax-attention operators: argument checks on the host and
+// dispatch to the kernels.  Nothing here allocates device memory.
+
+#include <cmath>
+#include <cstdint>
+
+#include "attn.cuh"
+
+using namespace falcon;
+
+namespace {
+
+size_t esize(const falcon_attn_params_t* p) { return p->dtype == FALCON_BF16 ? 2 : 4; }
+
+bool misaligned(const void* x, size_t n) { return (reinterpret_cast<uintptr_t>(x) & (n - 1)) != 0; }
+
+// a row stride: 0 (dense) or at least the row's H * d elements
+bool stride_ok(int64_t s, int H, int d) { return s == 0 || s >= static_cast<int64_t>(H) * d; }
+int64_t stride_of(int64_t s, int H, int d) { return s ? s : static_cast<int64_t>(H) * d; }
+
+bool vec_rows(const falcon_attn_params_t* p, const void* x, int64_t stride) {
+  return !misaligned(x, 16) && (stride * esize(p)) % 16 == 0;
+}
+RowsIn rows_in(const falcon_attn_params_t* p, const void* x, int64_t s, int H) {
+  const int64_t st = stride_of(s, H, p->d);
+  return RowsIn{x, st, vec_rows(p, x, st)};
+}
+RowsOut rows_out(const falcon_attn_params_t* p, void* x, int64_t s, int H) {
+  const int64_t st = stride_of(s, H, p->d);
+  return RowsOut{x, st, vec_rows(p, x, st)};
+}
+// bytes from the first to past the last element of n rows
+size_t span(const falcon_attn_params_t* p, int64_t n, int64_t s, int H) {
+  const int64_t row = static_cast<int64_t>(H) * p->d;
+  return n <= 0 ? 0 : static_cast<size_t>((n - 1) * stride_of(s, H, p->d) + row) * esize(p);
+}
+bool overlap(const void* a, size_t na, const void* b, size_t nb) {
+  if (!a || !b || na == 0 || nb == 0) return false;
+  const auto pa = reinterpret_cast<uintptr_t>(a), pb = reinterpret_cast<uintptr_t>(b);
+  return pa < pb + nb && pb < pa + na;
+}
+
+int check_attn(const falcon_attn_params_t* p) {
+  if (!p) return FALCON_ERR_INVALID_ARG;
+  if (p->Hq < 1 || p->Hkv < 1 || p->Hq % p->Hkv) return FALCON_ERR_INVALID_ARG;
+  if (p->dtype != FALCON_BF16 && p->dtype != FALCON_F32) return FALCON_ERR_INVALID_ARG;
+  if (p->d != 16 && p->d != 32 && p->d != 64 && p->d != 128) return FALCON_ERR_UNSUPPORTED;
+  if (p->tokens < 0 || p->k_tokens < 0 || p->max_q < 0 || p->max_k < 0) return FALCON_ERR_INVALID_ARG;
+  if (!stride_ok(p->q_stride, p->Hq, p->d) || !stride_ok(p->k_stride, p->Hkv, p->d) ||
+      !stride_ok(p->v_stride, p->Hkv, p->d) || !stride_ok(p->o_stride, p->Hq, p->d))
+    return FALCON_ERR_INVALID_ARG;
+  return FALCON_OK;
+}
+int check_scale(const falcon_attn_params_t* p) {
+  return std::isfinite(p->scale) && p->scale >= 0.f ? FALCON_OK : FALCON_ERR_INVALID_ARG;
+}
+float scale_of(const falcon_attn_params_t* p) {
+  return p->scale > 0.f ? p->scale : 1.f / std::sqrt(static_cast<float>(p->d));
+}
+// norm and rotation settings, with the table that they need
+int check_head(const falcon_attn_params_t* p, const float* table, const float* w_q, const float* w_k) {
+  if (p->qk_norm && !(p->norm_eps > 0.f && std::isfinite(p->norm_eps))) return FALCON_ERR_INVALID_ARG;
+  if (p->rot < 0 || p->rot > p->d || (p->rot & 1)) return FALCON_ERR_INVALID_ARG;
+  if (p->rope_layout != FALCON_ROPE_HALF && p->rope_layout != FALCON_ROPE_INTERLEAVED) return FALCON_ERR_INVALID_ARG;
+  if (p->rot > 0 && (!table || p->rope_rows < 1 || misaligned(table, 8))) return FALCON_ERR_INVALID_ARG;
+  if (p->qk_norm && (misaligned(w_q, 4) || misaligned(w_k, 4))) return FALCON_ERR_INVALID_ARG;
+  return FALCON_OK;
+}
+HeadArgs head_args(const falcon_attn_params_t* p, const float* table) {
+  return HeadArgs{p->d, p->qk_norm ? 1 : 0, p->norm_eps, p->rot, p->rope_layout, p->rope_rows,
+                  reinterpret_cast<const float2*>(table)};
+}
+int check_cache(const falcon_attn_params_t* p, const falcon_kv_cache_t* c, const int32_t* blocks) {
+  if (p->page != 16 && p->page != 32 && p->page != 64 && p->page != 128) return FALCON_ERR_UNSUPPORTED;
+  if (p->B < 1 || p->num_pages < 1 || p->max_pages < 0) return FALCON_ERR_INVALID_ARG;
+  if (!c || !c->k || !c->v || !c->k_scale || !c->v_scale) return FALCON_ERR_INVALID_ARG;
+  if (misaligned(c->k, 16) || misaligned(c->v, 16)) return FALCON_ERR_INVALID_ARG;
+  if (p->max_pages > 0 && (!blocks || misaligned(blocks, 4))) return FALCON_ERR_INVALID_ARG;
+  return FALCON_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+int falcon_rope_table(const double* inv_freq, int32_t rot, int32_t rows, float mscale, float* table, void* stream) {
+  if (rot < 0 || (rot & 1) || rows < 0 || !std::isfinite(mscale)) return FALCON_ERR_INVALID_ARG;
+  if (rot > 0 && rows > 0 && (!inv_freq || !table || misaligned(inv_freq, 8) || misaligned(table, 8)))
+    return FALCON_ERR_INVALID_ARG;
+  return launch_rope_table(inv_freq, rot, rows, mscale, table, reinterpret_cast<cudaStream_t>(stream));
+}
+
+int falcon_qk_norm_rope(const falcon_attn_params_t* p, const void* q, const void* k, const float* w_q,
+                        const float* w_k, const int64_t* positions, const float* table, void* q_out, void* k_out,
+                        void* stream) {
+  int st = check_attn(p);
+  if (st == FALCON_OK) st = check_head(p, table, w_q, w_k);
+  if (st != FALCON_OK) return st;
+  if (p->tokens == 0) return FALCON_OK;
+  if ((!q && !k) || (q && !q_out) || (k && !k_out)) return FALCON_ERR_INVALID_ARG;
+  if (p->rot > 0 && (!positions || misaligned(positions, 8))) return FALCON_ERR_INVALID_ARG;
+  for (const void* x : {q, k, static_cast<const void*>(q_out), static_cast<const void*>(k_out)})
+    if (misaligned(x, esize(p))) return FALCON_ERR_INVALID_ARG;
+  const RowsIn qi = rows_in(p, q, p->q_stride, p->Hq), ki = rows_in(p, k, p->k_stride, p->Hkv);
+  const RowsOut qo = rows_out(p, q_out, p->o_stride, p->Hq), ko = rows_out(p, k_out, 0, p->Hkv);
+  const size_t nq = q ? span(p, p->tokens, p->q_stride, p->Hq) : 0, nk = k ? span(p, p->tokens, p->k_stride, p->Hkv) : 0;
+  const size_t nqo = q ? span(p, p->tokens, p->o_stride, p->Hq) : 0, nko = k ? span(p, p->tokens, 0, p->Hkv) : 0;
+  const bool q_inplace = q == q_out && qi.stride == qo.stride, k_inplace = k == k_out && ki.stride == ko.stride;
+  if ((!q_inplace && overlap(q, nq, q_out, nqo)) || (!k_inplace && overlap(k, nk, k_out, nko)) ||
+      overlap(k, nk, q_out, nqo) || overlap(q, nq, k_out, nko) || overlap(q_out, nqo, k_out, nko))
+    return FALCON_ERR_INVALID_ARG;
+  return launch_qk_norm_rope(head_args(p, table), p->dtype, p->tokens, p->Hq, p->Hkv, qi, ki, w_q, w_k, positions, qo,
+                             ko, reinterpret_cast<cudaStream_t>(stream));
+}
+
+int falcon_kv_append(const falcon_attn_params_t* p, const void* k, const void* v, const float* w_k,
+                     const float* table, const int32_t* cu_new, const int32_t* ctx_lens, const int32_t* block_table,
+                     const falcon_kv_cache_t* cache, void* stream) {
+  int st = check_attn(p);
+  if (st == FALCON_OK) st = check_head(p, table, nullptr, w_k);
+  if (st == FALCON_OK) st = check_cache(p, cache, block_table);
+  if (st != FALCON_OK) return st;
+  if (p->tokens == 0 || p->max_q == 0 || p->max_pages == 0) return FALCON_OK;
+  if (!k || !v || !cu_new || !ctx_lens) return FALCON_ERR_INVALID_ARG;
+  if (misaligned(k, esize(p)) || misaligned(v, esize(p)) || misaligned(cu_new, 4) || misaligned(ctx_lens, 4))
+    return FALCON_ERR_INVALID_ARG;
+  const size_t codes = static_cast<size_t>(p->num_pages) * p->Hkv * p->page * p->d;
+  const size_t scales = static_cast<size_t>(p->num_pages) * p->Hkv;
+  const void* outs[4] = {cache->k, cache->v, cache->k_scale, cache->v_scale};
+  const size_t nout[4] = {codes, codes, scales, scales};
+  const void* ins[2] = {k, v};
+  const size_t nin[2] = {span(p, p->tokens, p->k_stride, p->Hkv), span(p, p->tokens, p->v_stride, p->Hkv)};
+  for (int i = 0; i < 4; ++i) {
+    for (int j = 0; j < 2; ++j)
+      if (overlap(outs[i], nout[i], ins[j], nin[j])) return FALCON_ERR_INVALID_ARG;
+    for (int j = i + 1; j < 4; ++j)
+      if (overlap(outs[i], nout[i], outs[j], nout[j])) return FALCON_ERR_INVALID_ARG;
+  }
+  const AppendArgs a{p->B, p->Hkv, p->page, p->num_pages, p->max_pages, p->max_q, p->tokens,
+                     rows_in(p, k, p->k_stride, p->Hkv), rows_in(p, v, p->v_stride, p->Hkv), w_k, cu_new, ctx_lens,
+                     block_table, *cache};
+  return launch_kv_append(head_args(p, table), p->dtype, a, reinterpret_cast<cudaStream_t>(stream));
+}
+
+size_t falcon_attn_decode_workspace_size(const falcon_attn_params_t* p) {
+  if (check_attn(p) != FALCON_OK || p->B < 1) return 0;
+  if (p->page != 16 && p->page != 32 && p->page != 64 && p->page != 128) return 0;
+  return align_up(attn_decode_ws_bytes(p->B, p->Hq, p->Hkv, p->d, p->page, p->max_k), 256);
+}
+
+int falcon_attn_decode(const falcon_attn_params_t* p, const void* q, const falcon_kv_cache_t* cache,
+                       const int32_t* block_table, const int32_t* lens, void* o, float* lse, void* workspace,
+                       size_t workspace_bytes, void* stream) {
+  int st = check_attn(p);
+  if (st == FALCON_OK) st = check_scale(p);
+  if (st == FALCON_OK) st = check_cache(p, cache, block_table);
+  if (st != FALCON_OK) return st;
+  if (!q || !o || !lens || misaligned(q, esize(p)) || misaligned(o, esize(p)) || misaligned(lens, 4) ||
+      misaligned(lse, 4))
+    return FALCON_ERR_INVALID_ARG;
+  const size_t no = span(p, p->B, p->o_stride, p->Hq), nl = lse ? static_cast<size_t>(p->B) * p->Hq * 4 : 0;
+  if (overlap(q, span(p, p->B, p->q_stride, p->Hq), o, no) || overlap(o, no, lse, nl)) return FALCON_ERR_INVALID_ARG;
+  const size_t need = falcon_attn_decode_workspace_size(p);
+  if (!workspace || workspace_bytes < need || misaligned(workspace, 256)) return FALCON_ERR_WORKSPACE;
+  const DecodeArgs a{p->B, p->Hq, p->Hkv, p->d, p->page, p->num_pages, p->max_pages, p->max_k, scale_of(p),
+                     rows_in(p, q, p->q_stride, p->Hq), rows_out(p, o, p->o_stride, p->Hq), lse, block_table, lens,
+                     *cache, workspace};
+  return launch_attn_decode(a, p->dtype, reinterpret_cast<cudaStream_t>(stream));
+}
+
+size_t falcon_attn_prompt_workspace_size(const falcon_attn_params_t* p) {
+  if (check_attn(p) != FALCON_OK || p->B < 1) return 0;
+  return 256;
+}
+
+int falcon_attn_prompt(const falcon_attn_params_t* p, const void* q, const void* k, const void* v,
+                       const int32_t* cu_q, const int32_t* cu_k, void* o, float* lse, void* workspace,
+                       size_t workspace_bytes, void* stream) {
+  int st = check_attn(p);
+  if (st == FALCON_OK) st = check_scale(p);
+  if (st != FALCON_OK) return st;
+  if (p->B < 1) return FALCON_ERR_INVALID_ARG;
+  if (p->tokens == 0 || p->max_q == 0) return FALCON_OK;
+  if (!q || !o || !cu_q || !cu_k || (p->k_tokens > 0 && (!k || !v))) return FALCON_ERR_INVALID_ARG;
+  for (const void* x : {q, k, v, static_cast<const void*>(o)})
+    if (misaligned(x, esize(p))) return FALCON_ERR_INVALID_ARG;
+  if (misaligned(cu_q, 4) || misaligned(cu_k, 4) || misaligned(lse, 4)) return FALCON_ERR_INVALID_ARG;
+  const size_t no = span(p, p->tokens, p->o_stride, p->Hq), nl = lse ? static_cast<size_t>(p->tokens) * p->Hq * 4 : 0;
+  const void* ins[3] = {q, k, v};
+  const size_t nin[3] = {span(p, p->tokens, p->q_stride, p->Hq), span(p, p->k_tokens, p->k_stride, p->Hkv),
+                         span(p, p->k_tokens, p->v_stride, p->Hkv)};
+  for (int i = 0; i < 3; ++i)
+    if (overlap(ins[i], nin[i], o, no) || overlap(ins[i], nin[i], lse, nl)) return FALCON_ERR_INVALID_ARG;
+  if (overlap(o, no, lse, nl)) return FALCON_ERR_INVALID_ARG;
+  if (!workspace || workspace_bytes < falcon_attn_prompt_workspace_size(p) || misaligned(workspace, 256))
+    return FALCON_ERR_WORKSPACE;
+  const PromptArgs a{p->B, p->Hq, p->Hkv, p->d, p->max_q, p->max_k, scale_of(p), p->tokens, p->k_tokens,
+                     rows_in(p, q, p->q_stride, p->Hq), rows_in(p, k, p->k_stride, p->Hkv),
+                     rows_in(p, v, p->v_stride, p->Hkv), rows_out(p, o, p->o_stride, p->Hq), lse, cu_q, cu_k,
+                     workspace};
+  return launch_attn_prompt(a, p->dtype, reinterpret_cast<cudaStream_t>(stream));
+}
+
+}  // extern "C"

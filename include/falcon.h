@@ -339,6 +339,126 @@ int falcon_backward(const falcon_params_t* p, const void* q, const void* k, cons
                     float* dbeta, float* dlambda, float* dS_in, void* dk_prev, void* workspace,
                     size_t workspace_bytes, void* stream);
 
+/* ------------------------------------------------------------------------
+ * Softmax-attention layers (the full-attention layers a stack of Falcon
+ * layers is interleaved with; the pages have no counterpart).  Four
+ * operators for serving, forward only: falcon_qk_norm_rope over a token's
+ * queries and keys, falcon_attn_prompt over whole packed prompts,
+ * falcon_kv_append into a paged cache held in 8 bits, falcon_attn_decode of
+ * one token per sequence over that cache.
+ *
+ * Layouts: q [tokens, Hq, d], k and v [tokens, Hkv, d] in the params' dtype,
+ * tokens of all sequences packed one after the other, heads and dims dense,
+ * q_stride / k_stride / v_stride / o_stride elements from one token to the
+ * next (0 = dense; larger for slices of a fused projection).  Query head h
+ * reads key / value head h / (Hq / Hkv). */
+
+/* Which dims of a head form the rotated pairs: HALF (i, i + rot/2),
+ * INTERLEAVED (2i, 2i + 1), i < rot/2. */
+typedef enum { FALCON_ROPE_HALF = 0, FALCON_ROPE_INTERLEAVED = 1 } falcon_rope_layout_t;
+
+typedef struct {
+  int32_t B;            /* sequences (kv_append, attn_decode, attn_prompt) */
+  int32_t Hq, Hkv;      /* query heads, key / value heads (Hkv divides Hq) */
+  int32_t d;            /* head dim: 16, 32, 64 or 128 */
+  int32_t dtype;        /* falcon_dtype_t of q, k, v, o */
+  int32_t qk_norm;      /* nonzero: RMS norm of each head row (qk_norm_rope, kv_append) */
+  int32_t rot;          /* leading dims of a head that are rotated: even, 0 .. d */
+  int32_t rope_layout;  /* falcon_rope_layout_t */
+  int32_t rope_rows;    /* positions the rotary table holds */
+  int32_t page;         /* tokens per cache page: 16, 32, 64 or 128 */
+  int32_t num_pages;    /* pages in the cache */
+  int32_t max_pages;    /* columns of block_table */
+  int32_t max_q;        /* no sequence brings more tokens than this to the call */
+  int32_t max_k;        /* no sequence has more keys than this (attn_decode) */
+  float norm_eps;       /* > 0 where qk_norm is set */
+  float scale;          /* of the scores; 0 = 1 / sqrt(d) */
+  int64_t tokens;       /* rows of q (qk_norm_rope, attn_prompt) or of the new k, v (kv_append) */
+  int64_t k_tokens;     /* rows of k, v (attn_prompt) */
+  int64_t q_stride, k_stride, v_stride, o_stride;
+} falcon_attn_params_t;
+
+/* The paged cache.  Page p, head h, slot s of K is the row
+ * k[((p Hkv + h) page + s) d ..] of e4m3 codes; its value is code times the
+ * power of two of the scale byte k_scale[p Hkv + h] (e8m0: 2^(byte - 127)).
+ * V the same.  k and v 16-byte aligned.  Sequence b's token t sits in page
+ * block_table[b max_pages + t / page], slot t % page. */
+typedef struct {
+  uint8_t* k;        /* [num_pages, Hkv, page, d] */
+  uint8_t* v;        /* [num_pages, Hkv, page, d] */
+  uint8_t* k_scale;  /* [num_pages, Hkv] */
+  uint8_t* v_scale;  /* [num_pages, Hkv] */
+} falcon_kv_cache_t;
+
+/* Rotary table [rows, rot/2, 2] fp32: (cos, sin) of position times
+ * inv_freq[i] (device fp64 [rot/2]), times mscale; angles in 64 bits.  Long
+ * contexts are scaled through inv_freq and mscale. */
+int falcon_rope_table(const double* inv_freq, int32_t rot, int32_t rows, float mscale, float* table,
+                      void* stream);
+
+/* Norm of queries and keys for each head and rotation, one pass:
+ *   y = x / sqrt(mean(x^2) + norm_eps) * w     (qk_norm; w_q, w_k fp32 [d], NULL = ones)
+ *   (a, b) -> (a c - b s, b c + a s)           on the rot/2 pairs, (c, s) = table[position, i]
+ * fp32 arithmetic, rounded once to the dtype.  q -> q_out (row stride
+ * o_stride, 0 = dense), k -> k_out (dense); q or k may be NULL (skipped).  An
+ * output may be its own input when their strides agree (in place), and must
+ * not overlap an input otherwise.  positions: int64 [tokens], needed with
+ * rot > 0, as is table; the rotated dims of a token whose position is not
+ * in [0, rope_rows) are NaN. */
+int falcon_qk_norm_rope(const falcon_attn_params_t* p, const void* q, const void* k, const float* w_q,
+                        const float* w_k, const int64_t* positions, const float* table, void* q_out,
+                        void* k_out, void* stream);
+
+/* Append new keys and values to the cache, with the norm (qk_norm, w_k) and
+ * the rotation (rot, table) of falcon_qk_norm_rope applied to the keys on
+ * the way.  cu_new (int32 [B + 1], as cu_seqlens) delimits each sequence's
+ * rows of k and v, ctx_lens (int32 [B]) holds its tokens cached before; new
+ * token i has position ctx_lens[b] + i.  Each page that receives tokens:
+ *   e_new = smallest e in [-126, 127] with amax <= 448 * 2^e over its new
+ *           tokens' finite values, for K and for V, for each head
+ *   e     = e_new if its slot 0 is written now, else max(e_old, e_new)
+ *   codes already there -> rounded again to 2^e where e > e_old
+ *   new code = e4m3(x * 2^-e), rounded to nearest even; infinities
+ *   saturate to 448, NaN stays NaN
+ * The slots past the new tokens keep their bytes.  One page must not belong
+ * to two sequences that append in the same call.  Tokens whose block_table
+ * entry is outside [0, num_pages), whose column is past max_pages, or that
+ * are past max_q tokens of their sequence are not stored.  Slot 0 of a page
+ * that starts within the call never depends on what the page held. */
+int falcon_kv_append(const falcon_attn_params_t* p, const void* k, const void* v, const float* w_k,
+                     const float* table, const int32_t* cu_new, const int32_t* ctx_lens,
+                     const int32_t* block_table, const falcon_kv_cache_t* cache, void* stream);
+
+/* Bytes of workspace falcon_attn_decode needs (0 when the params are invalid). */
+size_t falcon_attn_decode_workspace_size(const falcon_attn_params_t* p);
+
+/* Attention of one token per sequence over the cache: q [B, Hq, d],
+ *   s_j = scale <q, K_j>, j < lens[b];  o = sum_j exp(s_j) V_j / sum_j exp(s_j)
+ *   lse = log sum_j exp(s_j)   (fp32 [B, Hq], NULL = not wanted)
+ * lens: int32 [B], at most max_k (and max_pages * page) of them are read;
+ * lens[b] <= 0 gives o = 0 and lse = -inf.  Whatever lies in the slots past
+ * lens[b] is not used.  Keys of a page whose block_table entry is outside
+ * [0, num_pages) are masked.  o [B, Hq, d] with row stride o_stride. */
+int falcon_attn_decode(const falcon_attn_params_t* p, const void* q, const falcon_kv_cache_t* cache,
+                       const int32_t* block_table, const int32_t* lens, void* o, float* lse,
+                       void* workspace, size_t workspace_bytes, void* stream);
+
+/* Bytes of workspace falcon_attn_prompt needs (0 when the params are invalid). */
+size_t falcon_attn_prompt_workspace_size(const falcon_attn_params_t* p);
+
+/* Causal attention over packed prompts.  cu_q / cu_k (int32 [B + 1]) delimit
+ * each sequence's lq rows of q and lk rows of k, v (lq <= max_q;
+ * lq != lk for a prompt that continues earlier tokens).  The causal mask is
+ * aligned at the end: query i sees the keys j <= i + lk - lq.  A row that
+ * sees no key gives o = 0 and lse = -inf.  o [tokens, Hq, d] with row stride
+ * o_stride, lse fp32 [tokens, Hq] (NULL = not wanted).  Rows of q past max_q
+ * of their sequence are not computed.  The bf16 d = 64 and 128 kernel runs
+ * its products on the tensor cores with bounded waits, reported through
+ * falcon_workspace_status(workspace, stream) as for the chunk forward. */
+int falcon_attn_prompt(const falcon_attn_params_t* p, const void* q, const void* k, const void* v,
+                       const int32_t* cu_q, const int32_t* cu_k, void* o, float* lse, void* workspace,
+                       size_t workspace_bytes, void* stream);
+
 /* Status of the last tensor-core chunk forward that used `workspace`
  * (falcon_chunk_fwd_plan reports FALCON_IMPL_TC for it; falcon_chunk_fwd,
  * _timed, _varlen), or, with workspace == NULL, of the last

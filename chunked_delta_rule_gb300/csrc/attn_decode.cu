@@ -247,19 +247,24 @@ __global__ void __launch_bounds__(kWarps * 32) attn_decode_kernel(DecodeArgs a, 
   for (int tile = warp; tile < tiles; tile += kWarps) {
     asm volatile("cp.async.wait_group %0;" ::"n"(L::kStages - 2) : "memory");
     const uint32_t src0 = ring + stage * L::kStage;
+    // scores of the stage's 16-key tiles, two sums each for short chains
+    float sc[L::kSub][NG][4];
+    uint32_t bytes[L::kSub];
+    bool past = false;
+    int evmax = E;
 #pragma unroll
     for (int sub = 0; sub < L::kSub; ++sub) {
       const int t = first + tile * L::kKeys + sub * 16, col = t >> page_shift;
-      if (t >= end) break;
-      if (col - sbase >= 32) load_scales(col);
-      const uint32_t bytes = __shfl_sync(0xffffffffu, sbytes, (col - sbase) & 31);
-      if (bytes & 0x10000u) continue;
+      if (t < end && col - sbase >= 32) load_scales(col);
+      bytes[sub] = __shfl_sync(0xffffffffu, sbytes, (col - sbase) & 31);
+      const bool some = t < end && !(bytes[sub] & 0x10000u);
+      if (!some) bytes[sub] = 0;  // zeros in the ring, weights 0, the smallest V scale
       const uint32_t src = src0 + sub * (L::kStage / L::kSub);
-      float s[NG][4];
+      float s[NG][2][4];
 #pragma unroll
       for (int n = 0; n < NG; ++n)
 #pragma unroll
-        for (int i = 0; i < 4; ++i) s[n][i] = 0.f;
+        for (int i = 0; i < 4; ++i) s[n][0][i] = s[n][1][i] = 0.f;
 #pragma unroll
       for (int ld = 0; ld < L::kKLoads; ++ld) {
         uint32_t k0[KW], k1[KW];
@@ -273,49 +278,53 @@ __global__ void __launch_bounds__(kWarps * 32) attn_decode_kernel(DecodeArgs a, 
           for (int n = 0; n < NG; ++n)
 #pragma unroll
             for (int p = 0; p < NP; ++p)
-              mma_f16(s[n], a0, a1, a2, a3, qf[n][p][ld * KW + j][0], qf[n][p][ld * KW + j][1]);
+              mma_f16(s[n][j & 1], a0, a1, a2, a3, qf[n][p][ld * KW + j][0], qf[n][p][ld * KW + j][1]);
         }
       }
-      const float ks = e8m0(bytes & 0xFFu);
-      const bool in0 = t + gid < end, in1 = t + gid + 8 < end;
-      bool past = false;
+      const float ks = e8m0(bytes[sub] & 0xFFu);
+      const bool in0 = some && t + gid < end, in1 = some && t + gid + 8 < end;
 #pragma unroll
       for (int n = 0; n < NG; ++n)
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
-          s[n][i] = in0 ? s[n][i] * hs[n][i] * ks : -INFINITY;
-          s[n][2 + i] = in1 ? s[n][2 + i] * hs[n][i] * ks : -INFINITY;
-          past |= fmaxf(s[n][i], s[n][2 + i]) > m[n][i] + kSlack;
+          const float f = hs[n][i] * ks;
+          sc[sub][n][i] = in0 ? (s[n][0][i] + s[n][1][i]) * f : -INFINITY;
+          sc[sub][n][2 + i] = in1 ? (s[n][0][2 + i] + s[n][1][2 + i]) * f : -INFINITY;
+          past |= fmaxf(sc[sub][n][i], sc[sub][n][2 + i]) > m[n][i] + kSlack;
         }
-      if (__any_sync(0xffffffffu, past)) {  // move the reference to the maximum
+      evmax = max(evmax, static_cast<int>(bytes[sub] >> 8) - 127);
+    }
+    if (__any_sync(0xffffffffu, past)) {  // move the reference to the maximum
 #pragma unroll
-        for (int n = 0; n < NG; ++n)
+      for (int n = 0; n < NG; ++n)
 #pragma unroll
-          for (int i = 0; i < 2; ++i) {
-            float x = fmaxf(s[n][i], s[n][2 + i]);
-            x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 4));
-            x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 8));
-            x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 16));
-            x = fmaxf(x, m[n][i]);
-            const float f = x == -INFINITY ? 1.f : ex2(m[n][i] - x);
-            m[n][i] = x;
-            l[n][i] *= f;
+        for (int i = 0; i < 2; ++i) {
+          float x = m[n][i];
 #pragma unroll
-            for (int j = 0; j < KS; ++j) o[n][j][i] *= f, o[n][j][2 + i] *= f;
-          }
-      }
-      const int ev = static_cast<int>(bytes >> 8) - 127;
-      if (ev > E) {  // sums so far in units of the new, larger V scale
-        const float f = exp2i(max(E - ev, -149));
-        E = ev;
+          for (int sub = 0; sub < L::kSub; ++sub) x = fmaxf(x, fmaxf(sc[sub][n][i], sc[sub][n][2 + i]));
+          x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 4));
+          x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 8));
+          x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 16));
+          const float f = x == -INFINITY ? 1.f : ex2(m[n][i] - x);
+          m[n][i] = x;
+          l[n][i] *= f;
 #pragma unroll
-        for (int n = 0; n < NG; ++n)
+          for (int j = 0; j < KS; ++j) o[n][j][i] *= f, o[n][j][2 + i] *= f;
+        }
+    }
+    if (evmax > E) {  // sums so far in units of the new, larger V scale
+      const float f = exp2i(max(E - evmax, -149));
+      E = evmax;
 #pragma unroll
-          for (int j = 0; j < KS; ++j)
+      for (int n = 0; n < NG; ++n)
 #pragma unroll
-            for (int i = 0; i < 4; ++i) o[n][j][i] *= f;
-      }
-      const float vs = exp2i(max(ev - E + kHeadroom, -126));
+        for (int j = 0; j < KS; ++j)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) o[n][j][i] *= f;
+    }
+#pragma unroll
+    for (int sub = 0; sub < L::kSub; ++sub) {
+      const float vs = exp2i(max(static_cast<int>(bytes[sub] >> 8) - 127 - E + kHeadroom, -126));
       uint32_t pb[NG][NP][2];
 #pragma unroll
       for (int n = 0; n < NG; ++n) {
@@ -323,7 +332,7 @@ __global__ void __launch_bounds__(kWarps * 32) attn_decode_kernel(DecodeArgs a, 
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           const float ref = m[n][i & 1];
-          p[i] = ex2(s[n][i] - (ref == -INFINITY ? 0.f : ref));
+          p[i] = ex2(sc[sub][n][i] - (ref == -INFINITY ? 0.f : ref));
         }
         l[n][0] += p[0] + p[2];
         l[n][1] += p[1] + p[3];
@@ -336,7 +345,7 @@ __global__ void __launch_bounds__(kWarps * 32) attn_decode_kernel(DecodeArgs a, 
           pb[n][x][1] = transpose8x8(f1[x]);
         }
       }
-      const uint32_t vsrc = src + 2 * L::kKLoads * 32 * L::kKSize;
+      const uint32_t vsrc = src0 + sub * (L::kStage / L::kSub) + 2 * L::kKLoads * 32 * L::kKSize;
       uint32_t v[4][VW];
 #pragma unroll
       for (int r = 0; r < 4; ++r) {
@@ -409,55 +418,67 @@ __global__ void __launch_bounds__(kWarps * 32) attn_decode_kernel(DecodeArgs a, 
   }
 }
 
-// Joins the chunks of a sequence: one warp per query head, lanes over dims.
+// Joins the chunks of a sequence: one CTA per query head; D / 4 lanes take the
+// head's dims, the groups of lanes the chunks in turn.
 template <typename T, int D>
-__global__ void __launch_bounds__(128) attn_decode_join_kernel(DecodeArgs a, DecodePlan pl, const float* part_o,
+__global__ void __launch_bounds__(256) attn_decode_join_kernel(DecodeArgs a, DecodePlan pl, const float* part_o,
                                                                const float2* part_ml) {
-  constexpr int N = (D + 31) / 32;
-  const int lane = threadIdx.x & 31;
-  const int64_t bh = blockIdx.x * static_cast<int64_t>(4) + (threadIdx.x >> 5);
+  constexpr int W = D / 4, NGR = 256 / W;
+  __shared__ float4 so[NGR][W];
+  __shared__ float2 sml[NGR];
+  const int w = threadIdx.x % W, g = threadIdx.x / W;
+  const int64_t bh = blockIdx.x, b = bh / a.Hq;
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  if (bh >= static_cast<int64_t>(a.B) * a.Hq) return;
-  const int64_t b = bh / a.Hq;
   const int h = static_cast<int>(bh % a.Hq);
   const int64_t cap = min(static_cast<int64_t>(a.max_k), static_cast<int64_t>(a.max_pages) * a.page);
   const int len = static_cast<int>(min(static_cast<int64_t>(a.lens[b]), cap));
   if (len <= pl.chunk) return;  // written by its only CTA
   const int n = (len + pl.chunk - 1) / pl.chunk;
   const float2* ml = part_ml + bh * pl.chunks;
-  const float* po = part_o + bh * pl.chunks * D;
-  float top = -INFINITY;
-  for (int i = lane; i < n; i += 32) top = fmaxf(top, ml[i].x);
-#pragma unroll
-  for (int k = 16; k; k >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, k));
-  float sum = 0.f, acc[N];
-#pragma unroll
-  for (int j = 0; j < N; ++j) acc[j] = 0.f;
+  const float4* po = reinterpret_cast<const float4*>(part_o + bh * pl.chunks * D);
+  float top = -INFINITY, sum = 0.f;
+  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 4
-  for (int i = 0; i < n; ++i) {
+  for (int i = g; i < n; i += NGR) top = fmaxf(top, ml[i].x);
+#pragma unroll 4
+  for (int i = g; i < n; i += NGR) {
     const float2 x = ml[i];
+    const float4 v = po[static_cast<int64_t>(i) * W + w];
     const float f = x.x == -INFINITY ? (x.y == 0.f ? 0.f : 1.f) : ex2(x.x - top);
     sum += x.y * f;
+    acc.x += v.x * f, acc.y += v.y * f, acc.z += v.z * f, acc.w += v.w * f;
+  }
+  so[g][w] = acc;
+  if (w == 0) sml[g] = make_float2(top, sum);
+  __syncthreads();
+  if (threadIdx.x >= D) return;
+  const int d = threadIdx.x;
+  top = -INFINITY, sum = 0.f;
+  float y = 0.f;
 #pragma unroll
-    for (int j = 0; j < N; ++j)
-      if (lane + 32 * j < D) acc[j] += po[static_cast<int64_t>(i) * D + lane + 32 * j] * f;
+  for (int i = 0; i < NGR; ++i) top = fmaxf(top, sml[i].x);
+#pragma unroll
+  for (int i = 0; i < NGR; ++i) {
+    const float2 x = sml[i];
+    const float f = x.x == -INFINITY ? (x.y == 0.f ? 0.f : 1.f) : ex2(x.x - top);
+    sum += x.y * f;
+    y += reinterpret_cast<const float*>(so[i])[d] * f;
   }
   T* out = static_cast<T*>(a.o.p) + b * a.o.stride + static_cast<int64_t>(h) * D;
-#pragma unroll
-  for (int j = 0; j < N; ++j)
-    if (lane + 32 * j < D) out[lane + 32 * j] = from_f32<T>(sum == 0.f ? 0.f : acc[j] / sum);
-  if (a.lse && lane == 0) a.lse[bh] = sum == 0.f ? -INFINITY : ((top == -INFINITY ? 0.f : top) + log2f(sum)) * kLn2;
+  out[d] = from_f32<T>(sum == 0.f ? 0.f : y / sum);
+  if (a.lse && d == 0) a.lse[bh] = sum == 0.f ? -INFINITY : ((top == -INFINITY ? 0.f : top) + log2f(sum)) * kLn2;
 }
 
-// Keys of a CTA: enough CTAs to fill the card three times over at four warps
-// each, at least 256 keys (the partial results of a chunk are then at most a
-// sixteenth of what it reads), whole 128-key pages.
+// Keys of a CTA: as many CTAs as the card holds at a time (two 131072-key
+// sequences: 48 us, with twice as many 61), at least 256 keys (the partial
+// results of a chunk are then at most a sixteenth of what it reads), whole
+// 128-key pages.
 DecodePlan decode_plan(int B, int Hq, int Hkv, int max_k) {
   DecodePlan p;
   const int G = Hq / Hkv;
   p.per = G <= 8 ? 8 : 16;
   p.groups = (G + p.per - 1) / p.per;
-  const int64_t rows = static_cast<int64_t>(B) * Hkv * p.groups, want = 152 * 9;
+  const int64_t rows = static_cast<int64_t>(B) * Hkv * p.groups, want = 152 * 4;
   int64_t chunks = (want + rows - 1) / rows;
   int64_t chunk = (max_k + chunks - 1) / chunks;
   chunk = (chunk + 127) / 128 * 128;
@@ -484,8 +505,8 @@ int launch_decode(const DecodeArgs& a, const DecodePlan& p, cudaStream_t s) {
   FwdArgs fa = {};
   fa.stream = s;
   const int64_t rows = static_cast<int64_t>(a.B) * a.Hq;
-  return tcu::launch_overlapped(fa, attn_decode_join_kernel<T, D>, dim3(static_cast<unsigned>((rows + 3) / 4)),
-                                dim3(128), 0, a, p, static_cast<const float*>(po), static_cast<const float2*>(ml));
+  if (rows > INT32_MAX) return FALCON_ERR_UNSUPPORTED;
+  return tcu::launch_overlapped(fa, attn_decode_join_kernel<T, D>, dim3(static_cast<unsigned>(rows)), dim3(256), 0, a, p, static_cast<const float*>(po), static_cast<const float2*>(ml));
 }
 template <typename T, int D>
 int launch_decode_g(const DecodeArgs& a, const DecodePlan& p, cudaStream_t s) {

@@ -75,6 +75,8 @@ struct PromptArgs {
   void* ws;
 };
 int launch_attn_prompt(const PromptArgs& a, int dtype, cudaStream_t s);
+bool attn_prompt_tc_supported(const PromptArgs& a, int dtype);
+int launch_attn_prompt_tc(const PromptArgs& a, cudaStream_t s);
 
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;

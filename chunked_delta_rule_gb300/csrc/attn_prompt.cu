@@ -5,7 +5,7 @@
 // One warp per (query, head); lane t holds dims t, t + 32, ...; the running
 // maximum and sum of the softmax in fp32.
 
-#include "attn.cuh"
+#include "attn_row.cuh"
 
 namespace falcon {
 namespace {
@@ -26,36 +26,20 @@ __global__ void __launch_bounds__(128) attn_prompt_kernel(PromptArgs a, int64_t 
   const T* q = static_cast<const T*>(a.q.p) + (q0 + i) * a.q.stride + h * a.d;
   const T* k = static_cast<const T*>(a.k.p) + k0 * a.k.stride + hk * a.d;
   const T* v = static_cast<const T*>(a.v.p) + k0 * a.v.stride + hk * a.d;
-  float qv[4], o[4] = {0.f, 0.f, 0.f, 0.f}, m = -INFINITY, l = 0.f;
-#pragma unroll
-  for (int j = 0; j < 4; ++j) qv[j] = lane + 32 * j < a.d ? to_f32(q[lane + 32 * j]) * a.scale : 0.f;
-  for (int t = 0; t < n; ++t) {
-    float s = 0.f;
-#pragma unroll
-    for (int j = 0; j < 4; ++j)
-      if (lane + 32 * j < a.d) s = fmaf(qv[j], to_f32(k[t * a.k.stride + lane + 32 * j]), s);
-#pragma unroll
-    for (int x = 16; x; x >>= 1) s += __shfl_xor_sync(0xffffffffu, s, x);
-    const float mn = fmaxf(m, s), ref = mn == -INFINITY ? 0.f : mn;
-    const float old = expf(m - ref), p = expf(s - ref);
-    l = l * old + p;
-#pragma unroll
-    for (int j = 0; j < 4; ++j)
-      if (lane + 32 * j < a.d) o[j] = o[j] * old + p * to_f32(v[t * a.v.stride + lane + 32 * j]);
-    m = mn;
-  }
+  float o[4], lse;
+  attention_row(q, k, a.k.stride, v, a.v.stride, n, a.d, a.scale, o, &lse);
   T* out = static_cast<T*>(a.o.p) + (q0 + i) * a.o.stride + h * a.d;
-  const bool none = l == 0.f;
 #pragma unroll
   for (int j = 0; j < 4; ++j)
-    if (lane + 32 * j < a.d) out[lane + 32 * j] = from_f32<T>(none ? 0.f : o[j] / l);
-  if (a.lse && lane == 0) a.lse[(q0 + i) * a.Hq + h] = none ? -INFINITY : m + logf(l);
+    if (lane + 32 * j < a.d) out[lane + 32 * j] = from_f32<T>(o[j]);
+  if (a.lse && lane == 0) a.lse[(q0 + i) * a.Hq + h] = lse;
 }
 
 }  // namespace
 
 int launch_attn_prompt(const PromptArgs& a, int dtype, cudaStream_t s) {
   if (a.max_q == 0 || a.tokens == 0) return FALCON_OK;
+  if (attn_prompt_tc_supported(a, dtype)) return launch_attn_prompt_tc(a, s);
   const int64_t items = static_cast<int64_t>(a.B) * a.max_q * a.Hq, blocks = (items + 3) / 4;
   if (blocks > INT32_MAX) return FALCON_ERR_UNSUPPORTED;
   if (dtype == FALCON_BF16)

@@ -445,6 +445,26 @@ def test_prompt_more_rows_than_a_head_count_divides(F):
     _check_attention(o, lse, _np(want), _np(torch.logsumexp(s, -1).T), 5.0, "bf16", 1.25 * U)
 
 
+@pytest.mark.parametrize("d", [64, 128])
+def test_prompt_reports_a_wait_that_ran_out(F, d):
+    """A load that is held back: the bounded waits give up, the call says so once, the next one is clean."""
+    q, k, v, cq, ck = _prompt_case([300, 20], [300, 20], 2, 1, d, "bf16", 63)
+    cu = torch.from_numpy(cq).cuda()
+    good, lse = _prompt(F, q, k, v, cq, ck)
+    p = F.AttnParams(B=2, Hq=2, Hkv=1, d=d, dtype=F.FALCON_BF16, max_q=300, tokens=320, k_tokens=320)
+    ws = F.alloc_workspace(F.falcon_attn_prompt_workspace_size(p))
+    o = torch.zeros_like(q)
+    F.falcon_test_hooks(2_000_000, True)
+    try:
+        F.falcon_attn_prompt(p, q, k, v, cu, cu, o, None, ws)
+        assert F.falcon_workspace_status(ws) == F.FALCON_ERR_TIMEOUT
+        assert F.falcon_workspace_status(ws) == F.FALCON_OK and not o.any()
+        F.falcon_attn_prompt(p, q, k, v, cu, cu, o, None, ws)
+        assert F.falcon_workspace_status(ws) == F.FALCON_OK and torch.equal(o, good)
+    finally:
+        F.falcon_test_hooks(0, False)
+
+
 # ---------------------------------------------------------------- streams, repeats, the pieces together
 def test_same_bits_again_and_on_another_stream(F):
     lens = [700, 90]

@@ -3,18 +3,21 @@
 //   S = Q K^T (128 queries x 128 keys),  P = exp(scale S - m),  O += P V
 //
 // Bound by the tensor cores: 4 d flops a visible (query, key) pair and head.
-// A CTA takes 256 queries of one head as two 128-row tiles.  One thread issues
-// every tcgen05.mma; while it runs one tile's P V and next Q K^T, the other
-// tile's softmax runs, so that neither waits for the other:
-//   warps 0-3, 4-7   softmax of tile 0 and 1, a row a thread: the scores are
-//                    read from TMEM once, P (bf16) goes back over them and
-//                    is the next product's A operand from there
-//   warp 8           TMA loads: Q once, K and V tiles through a ring
-//   warp 9           the products (warps 10 and 11 fill the warpgroup)
+// A CTA takes 256 queries of one head as two 128-row tiles (d = 128), or two
+// CTAs of an SM one tile each (d = 64): while one tile's P V and next Q K^T run,
+// the other's softmax does, so that neither waits for the other:
+//   8 warps a tile   softmax: two threads a row, 64 of a tile's keys each; the
+//                    scores are read from TMEM once, P (bf16) goes back over
+//                    them and is the next product's A operand from there
+//   load warp        TMA: Q once, K and V tiles through a ring
+//   a warp a tile    the products (idle warps fill the last warpgroup)
 // TMEM: S0 | S1 (128 columns each, P in their first 64) | O0 | O1 (d each).
-// The reference m of a row moves only when a score passes it by more than
-// 2^8, so O is rescaled rarely; sums are of the unrounded weights, fp32.
-// P is rounded to bf16 as V is held in it: at most 2^-8 of a weight.
+// The reference m of a row is the maximum of its first tile.  Weights, sums and
+// O keep their relative precision at any scale (bf16 has fp32's range), so m
+// moves, and O is rescaled, only after a tile whose sum passed 2^40: the other
+// tiles need no maximum.  (A score that passes m by 2^127 at once overflows, and
+// its row is computed again as below.)  Sums are of the unrounded weights, fp32.  P is rounded to bf16
+// as V is held in it: at most 2^-8 of a weight.
 //
 // Masked scores are set to -inf after the product, so what the masked keys
 // hold does not matter; a masked weight is 0, but 0 times an infinite or NaN
@@ -31,21 +34,30 @@ namespace {
 using namespace tcu;
 
 constexpr int kTile = 128;        // queries and keys of a tile
-constexpr int kThreads = 384;
-// Registers: 384 x 168 at launch; 256 softmax threads take 208, the other 128 keep 88 (the same sum).
-constexpr float kSlack = 8.f;     // log2
+constexpr float kMost = 1099511627776.f;  // 2^40: a larger sum of a tile's weights moves the reference at the next
+
+struct Bars {
+  uint64_t q[2], full[8], empty[8], s[2], p[2], read, o, drain[2], stall;
+  uint32_t tmem;
+  float row[2][kTile];  // of each tile: what the two threads of a row tell each other
+};
 
 template <int D>
 struct Cfg {
+  static constexpr int kTiles = D == 64 ? 1 : 2;          // query tiles of a CTA
+  static constexpr int kCtas = D == 64 ? 2 : 1;           // CTAs of an SM
+  static constexpr int kSplit = D == 64 ? 1 : 2;          // softmax threads of a row
+  static constexpr int kWarps = 4 * kSplit;               // softmax warps of a tile
+  static constexpr int kLoadWarp = kWarps * kTiles, kMmaWarp = kLoadWarp + 1;
+  static constexpr int kThreads = 32 * kLoadWarp + 128;
   static constexpr int kTileBytes = kTile * D * 2;
-  static constexpr int kStages = D == 64 ? 8 : 5;
-  static constexpr int kSmem = (2 + kStages) * kTileBytes + 1024 + 256;
-  static constexpr uint32_t kColS = 0, kColO = 256;
-};
-
-struct Bars {
-  uint64_t q[2], full[8], empty[8], s[2], p[2], drain, stall;
-  uint32_t tmem;
+  static constexpr int kStages = D == 64 ? 4 : 5;
+  static constexpr int kSmem = (kTiles + kStages) * kTileBytes + 1024 + static_cast<int>(sizeof(Bars));
+  // d = 64 leaves room for P beside S, so that S of the next keys is formed
+  // while the softmax of these runs; at d = 128 P lies over S
+  static constexpr bool kAhead = D == 64;
+  static constexpr uint32_t kColS = 0, kColP = kAhead ? 128 : 0, kColO = kAhead ? 192 : kTiles * kTile;
+  static constexpr uint32_t kCols = D == 64 ? 256 : 512;
 };
 
 struct TcArgs {
@@ -60,6 +72,30 @@ __device__ __forceinline__ float ex2(float x) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
+}
+// pairs of floats in one instruction
+__device__ __forceinline__ uint64_t pack2(float lo, float hi) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+  return r;
+}
+__device__ __forceinline__ void unpack2(uint64_t x, float& lo, float& hi) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(x));
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float r;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
 }
 __device__ __forceinline__ void tma_load_3d(void* dst, const CUtensorMap* map, uint64_t* bar, int c0, int c1, int c2) {
   asm volatile(
@@ -77,6 +113,12 @@ __device__ __forceinline__ void umma_ts(uint32_t d, uint32_t a, uint64_t b, uint
       : "memory");
 }
 
+__device__ __forceinline__ bool elect_one() {
+  uint32_t r;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(r));
+  return r != 0;
+}
+
 // tiles of 128 keys that rows up to (and with) `last` of a sequence see
 __device__ __forceinline__ int key_tiles(int last, int off, int lk) {
   const int n = min(last + off + 1, lk);
@@ -84,7 +126,7 @@ __device__ __forceinline__ int key_tiles(int last, int off, int lk) {
 }
 
 template <int D>
-__global__ void __launch_bounds__(kThreads, 1)
+__global__ void __launch_bounds__(Cfg<D>::kThreads, Cfg<D>::kCtas)
     attn_prompt_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtensorMap mk,
                           const __grid_constant__ CUtensorMap mv, const TcArgs t) {
   using C = Cfg<D>;
@@ -93,208 +135,337 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (blockIdx.x == 0 && tid == 0) atomicExch(t.status, 0u);  // before any wait of this call can run out
 
   // the longest rows first: blocks of queries descend, sequences and heads within
-  const int64_t bh = static_cast<int64_t>(a.B) * a.Hq;
+  const uint32_t bh = static_cast<uint32_t>(a.B) * a.Hq, at = blockIdx.x % bh;
   const int qb = t.qblocks - 1 - static_cast<int>(blockIdx.x / bh);
-  const int b = static_cast<int>(blockIdx.x % bh) / a.Hq, h = static_cast<int>(blockIdx.x % bh) % a.Hq;
+  const int b = static_cast<int>(at) / a.Hq, h = static_cast<int>(at) % a.Hq;
   const int64_t q0 = a.cu_q[b], k0 = a.cu_k[b];
   const int lq_all = static_cast<int>(a.cu_q[b + 1] - q0), lk = static_cast<int>(a.cu_k[b + 1] - k0);
-  const int lq = min(lq_all, a.max_q), off = lk - lq_all, row0 = qb * 2 * kTile;
+  const int lq = min(lq_all, a.max_q), off = lk - lq_all, row0 = qb * C::kTiles * kTile;
   if (row0 >= lq || q0 < 0 || k0 < 0 || q0 + lq_all > a.tokens || k0 + lk > a.k_tokens) return;
   const int hk = h / (a.Hq / a.Hkv);
-  int n[2];
+  int n[C::kTiles], nmax = 0;
 #pragma unroll
-  for (int x = 0; x < 2; ++x) {
+  for (int x = 0; x < C::kTiles; ++x) {
     const int r = row0 + x * kTile;
     n[x] = r < lq ? key_tiles(min(r + kTile, lq) - 1, off, lk) : 0;
+    nmax = max(nmax, n[x]);
   }
-  const int nmax = max(n[0], n[1]);
 
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = align1024(smem_raw);
   uint8_t* sQ = smem;
-  uint8_t* ring = smem + 2 * C::kTileBytes;
+  uint8_t* ring = smem + C::kTiles * C::kTileBytes;
   Bars* bar = reinterpret_cast<Bars*>(ring + C::kStages * C::kTileBytes);
-  if (warp == 9) {
-    tmem_alloc(&bar->tmem, 512);
+  // stage i of the ring's loads: K0 V0 K1 V1 ...
+  auto load = [&](int i) {
+    const int st = i % C::kStages;
+    mbar_arrive_expect_tx(&bar->full[st], C::kTileBytes);
+    uint8_t* dst = ring + st * C::kTileBytes;
+    const CUtensorMap* m = (i & 1) ? &mv : &mk;
+    for (int c = 0; c < D / 64; ++c)
+      tma_load_3d(dst + c * kTile * 128, m, &bar->full[st], c * 64, hk, static_cast<int>(k0 + (i >> 1) * kTile));
+  };
+  int issued = 0;
+  if (warp == C::kMmaWarp) {
+    tmem_alloc(&bar->tmem, C::kCols);
     tmem_relinquish();
   }
-  if (tid == 0) {
-    for (int x = 0; x < 2; ++x) {
+  if (warp == C::kLoadWarp && lane == 0) {
+    for (int x = 0; x < C::kTiles; ++x) {
       mbar_init(&bar->q[x], 1);
       mbar_init(&bar->s[x], 1);
-      mbar_init(&bar->p[x], kTile);
+      mbar_init(&bar->drain[x], 1);
+      mbar_init(&bar->p[x], C::kWarps);
     }
     for (int i = 0; i < C::kStages; ++i) {
       mbar_init(&bar->full[i], 1);
-      mbar_init(&bar->empty[i], 1);
+      mbar_init(&bar->empty[i], C::kTiles);
     }
-    mbar_init(&bar->drain, 1);
+    mbar_init(&bar->read, C::kWarps);
+    mbar_init(&bar->o, 1);
     mbar_init(&bar->stall, 1);
     fence_mbar_init();
+    if (!t.stall && nmax > 0) {  // the first loads need nothing of the other warps
+      load(0);
+      for (int x = 0; x < C::kTiles; ++x) {
+        if (n[x] == 0) continue;
+        mbar_arrive_expect_tx(&bar->q[x], C::kTileBytes);
+        for (int c = 0; c < D / 64; ++c)
+          tma_load_3d(sQ + x * C::kTileBytes + c * kTile * 128, &mq, &bar->q[x], c * 64, h,
+                      static_cast<int>(q0 + row0 + x * kTile));
+      }
+      issued = min(2 * nmax, C::kStages);
+      for (int i = 1; i < issued; ++i) load(i);
+    }
   }
   __syncthreads();
   const uint32_t tmem = bar->tmem;
   auto wait = [&](uint64_t* m, uint32_t parity) {
-    if (mbar_wait(m, parity, t.limit)) return true;
+    if (mbar_wait_sleep(m, parity, t.limit)) return true;
     atomicExch(t.status, kStatusTimeout);
     return false;
   };
 
-  if (warp >= 8) asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
-  if (warp == 8) {
+  // registers: the softmax threads take what the last warpgroup gives up
+  // (512 x 104 + 128 x 64 = 640 x 96; 128 x 200 + 128 x 56 = 256 x 128)
+  if (warp >= C::kLoadWarp) {
+    if (D == 64) asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
+    else asm volatile("setmaxnreg.dec.sync.aligned.u32 64;");
+  }
+  if (warp == C::kLoadWarp) {
     if (lane == 0 && nmax > 0) {
-      bool ok = !t.stall || wait(&bar->stall, 0);
-      int issued = 0;
-      if (ok) {
-        for (int x = 0; x < 2; ++x) {
-          if (n[x] == 0) continue;
-          mbar_arrive_expect_tx(&bar->q[x], C::kTileBytes);
-          for (int c = 0; c < D / 64; ++c)
-            tma_load_3d(sQ + x * C::kTileBytes + c * kTile * 128, &mq, &bar->q[x], c * 64, h,
-                        static_cast<int>(q0 + row0 + x * kTile));
-        }
-        for (int i = 0; i < 2 * nmax; ++i) {  // K0 V0 K1 V1 ...
-          const int st = i % C::kStages;
-          if (i >= C::kStages && !(ok = wait(&bar->empty[st], (i / C::kStages - 1) & 1))) break;
-          mbar_arrive_expect_tx(&bar->full[st], C::kTileBytes);
-          uint8_t* dst = ring + st * C::kTileBytes;
-          const CUtensorMap* m = (i & 1) ? &mv : &mk;
-          for (int c = 0; c < D / 64; ++c)
-            tma_load_3d(dst + c * kTile * 128, m, &bar->full[st], c * 64, hk,
-                        static_cast<int>(k0 + (i >> 1) * kTile));
+      if (t.stall) {
+        wait(&bar->stall, 0);  // runs out: nothing has been loaded, nothing is
+      } else {
+        for (int i = issued; i < 2 * nmax; ++i) {
+          if (!wait(&bar->empty[i % C::kStages], (i / C::kStages - 1) & 1)) break;
+          load(i);
           issued = i + 1;
         }
         // every copy has landed before the CTA may end
-        for (int x = 0; x < 2; ++x)
+        for (int x = 0; x < C::kTiles; ++x)
           if (n[x] > 0) wait(&bar->q[x], 0);
         for (int i = max(0, issued - C::kStages); i < issued; ++i)
           wait(&bar->full[i % C::kStages], (i / C::kStages) & 1);
       }
     }
-  } else if (warp == 9) {
-    if (lane == 0 && nmax > 0) {
+  } else if (warp >= C::kMmaWarp && warp < C::kMmaWarp + C::kTiles) {
+    // A warp a tile.  With two tiles they take turns (named barriers 9 and 10): a warp has waited for all
+    // that its products need before its turn, so that the tensor cores go from one tile to the other without
+    // a pause, and the tiles stay half a step apart.  Both walk every step, also after a wait that ran out.
+    // The whole warp walks the loop, so that descriptors stay uniform; one lane issues.
+    if (nmax > 0) {
       constexpr uint32_t id_s = idesc_bf16(kTile, kTile), id_o = idesc_bf16(kTile, D, false, true);
-      auto scores = [&](int x, int st) {
-        const uint32_t qa = smem_u32(sQ + x * C::kTileBytes), kb = smem_u32(ring + st * C::kTileBytes);
-#pragma unroll
-        for (int ks = 0; ks < D / 16; ++ks)
-          umma_bf16(tmem + C::kColS + x * kTile, kdesc<kTile>(qa, ks), kdesc<kTile>(kb, ks), id_s, ks > 0);
-        umma_commit(&bar->s[x]);
+      const int x = __shfl_sync(0xffffffffu, warp - C::kMmaWarp, 0), nx = x == 0 ? n[0] : n[C::kTiles - 1];
+      const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0), tm_s = tm + C::kColS + x * kTile;
+      const uint32_t tm_p = tm + C::kColP + x * kTile, tm_o = tm + C::kColO + x * D;
+      const uint64_t qd = sdesc_k128(smem_u32(sQ + x * C::kTileBytes)), kd = sdesc_k128(smem_u32(ring));
+      const uint64_t vd = D == 64 ? sdesc_mn128(smem_u32(ring)) : sdesc_mn128_wide(smem_u32(ring), kTile * 128);
+      auto arrived = [&](uint64_t* m, uint32_t parity) {  // one answer for the warp
+        return __all_sync(0xffffffffu, wait(m, parity)) != 0;
       };
-      auto values = [&](int x, int st, bool acc) {
-        const uint32_t vb = smem_u32(ring + st * C::kTileBytes);
+      auto turn = [&]() {
+        if (C::kTiles == 2) named_bar(9 + x, 64);
+      };
+      auto pass = [&](bool again) {  // the other tile's turn; the first tile has none after its last step
+        if (C::kTiles == 2 && (x == 0 || again)) asm volatile("bar.arrive %0, %1;" ::"r"(10 - x), "r"(64) : "memory");
+      };
+      // each is followed by what its completion tells: S or O is ready, a stage is free
+      auto scores = [&](int st) {
+        const uint64_t ks0 = kd + st * (C::kTileBytes >> 4);
+        if (elect_one()) {
 #pragma unroll
-        for (int ks = 0; ks < kTile / 16; ++ks) {
-          const uint64_t vd = D == 64 ? sdesc_mn128(vb + ks * 2048) : sdesc_mn128_wide(vb + ks * 2048, kTile * 128);
-          umma_ts(tmem + C::kColO + x * D, tmem + C::kColS + x * kTile + ks * 8, vd, id_o, acc || ks > 0);
+          for (int ks = 0; ks < D / 16; ++ks) {
+            const uint32_t at = ((ks >> 2) * kTile * 128 + (ks & 3) * 32) >> 4;
+            umma_bf16(tm_s, qd + at, ks0 + at, id_s, ks > 0);
+          }
+          umma_commit(&bar->s[x]);
+          umma_commit(&bar->empty[st]);
         }
+        __syncwarp();
       };
-      bool ok = wait(&bar->full[0], 0);
-      for (int x = 0; x < 2 && ok; ++x) {
-        if (n[x] == 0) continue;
-        ok = wait(&bar->q[x], 0);
-        if (ok) scores(x, 0);
+      auto values = [&](int st, bool acc, uint64_t* then) {
+        const uint64_t vs = vd + st * (C::kTileBytes >> 4);
+        if (elect_one()) {
+#pragma unroll
+          for (int ks = 0; ks < kTile / 16; ++ks) umma_ts(tm_o, tm_p + ks * 8, vs + ks * 128, id_o, acc || ks > 0);
+          if (then) umma_commit(then);
+          umma_commit(&bar->empty[st]);
+        }
+        __syncwarp();
+      };
+      auto leave = [&](int st) {  // a stage that this tile has no use for
+        if (elect_one()) mbar_arrive(&bar->empty[st]);
+        __syncwarp();
+      };
+      if (x == 1) pass(true);
+      bool ok = arrived(&bar->full[0], 0);
+      if (ok && nx > 0) ok = arrived(&bar->q[x], 0);
+      turn();
+      if (ok) {
+        if (nx > 0) scores(0);
+        else leave(0);
       }
-      if (ok) umma_commit(&bar->empty[0]);
-      for (int j = 0; j < nmax && ok; ++j) {
-        const int iv = 2 * j + 1, ik = 2 * j + 2, sv = iv % C::kStages, sk = ik % C::kStages;
-        ok = wait(&bar->full[sv], (iv / C::kStages) & 1);
-        if (ok && j + 1 < nmax) ok = wait(&bar->full[sk], (ik / C::kStages) & 1);
-        for (int x = 0; x < 2 && ok; ++x) {
-          if (j >= n[x]) continue;
-          ok = wait(&bar->p[x], j & 1);
-          if (!ok) break;
-          tc_fence_after();
-          values(x, sv, j > 0);
-          if (j + 1 < n[x]) scores(x, sk);
-          else umma_commit(&bar->s[x]);  // O is complete
+      pass(true);
+      int sv = 1, pv = 0, sk = 2 % C::kStages, pk = 2 / C::kStages;  // stages of V_j and K_{j+1}, their phases
+      for (int j = 0; j < nmax; ++j) {
+        const bool more = j + 1 < nmax, mine = j < nx, next = j + 1 < nx;
+        if (C::kAhead && next) {
+          ok = ok && arrived(&bar->full[sk], pk) && arrived(&bar->read, j & 1);
+          if (ok) {
+            tc_fence_after();
+            scores(sk);
+          }
         }
+        ok = ok && arrived(&bar->full[sv], pv);
+        if (!C::kAhead && more) ok = ok && arrived(&bar->full[sk], pk);
+        if (mine) ok = ok && arrived(&bar->p[x], j & 1);
+        turn();
         if (ok) {
-          umma_commit(&bar->empty[sv]);
-          if (j + 1 < nmax) umma_commit(&bar->empty[sk]);
+          if (mine) {
+            tc_fence_after();
+            values(sv, j > 0, C::kAhead ? &bar->o : next ? nullptr : &bar->s[x]);
+            if (!C::kAhead && next) scores(sk);
+          } else {
+            leave(sv);
+          }
+          if (more && !next) leave(sk);
         }
+        pass(more);
+        sv += 2, sk += 2;
+        if (sv >= C::kStages) sv -= C::kStages, pv ^= 1;
+        if (sk >= C::kStages) sk -= C::kStages, pk ^= 1;
       }
-      umma_commit(&bar->drain);  // products in flight end before the memory is freed
-      wait(&bar->drain, 0);
+      if (elect_one()) umma_commit(&bar->drain[x]);  // products in flight end before the memory is freed
+      __syncwarp();
+      wait(&bar->drain[x], 0);
     }
     __syncwarp();
-  } else if (warp < 8) {
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
-    const int x = warp >> 2, quad = warp & 3, r = quad * 32 + lane, row = row0 + x * kTile + r;
+  } else if (warp < C::kLoadWarp) {
+    if (D == 64) asm volatile("setmaxnreg.inc.sync.aligned.u32 200;");
+    else asm volatile("setmaxnreg.inc.sync.aligned.u32 104;");
+    constexpr int kHalf = kTile / C::kSplit, kOut = D / C::kSplit;  // scores and output dims of a thread
+    // with two threads a row, warps w and w + 4 of a tile take the same rows, the first and the second 64 keys
+    const int x = warp / C::kWarps, half = C::kSplit == 2 ? (warp >> 2) & 1 : 0, quad = warp & 3, r = quad * 32 + lane;
+    const int row = row0 + x * kTile + r, pair = 1 + x * 4 + quad;  // named barrier of the two warps
     const uint32_t lanes = static_cast<uint32_t>(quad * 32) << 16;
-    const uint32_t ts = tmem + C::kColS + x * kTile + lanes, to = tmem + C::kColO + x * D + lanes;
+    const uint32_t ts = tmem + C::kColS + x * kTile + half * kHalf + lanes;      // scores
+    const uint32_t tp = tmem + C::kColP + x * kTile + half * kHalf / 2 + lanes;  // weights
+    const uint32_t to = tmem + C::kColO + x * D + half * kOut + lanes;           // this thread's part of O
     const float sl2 = a.scale * kLog2e;
-    const int seen = row + off + 1;  // keys that this row sees (before lk)
-    float m = -INFINITY, l = 0.f;    // reference (raw scores) and sum
+    const int seen = min(row + off + 1, lk) - half * kHalf;             // keys that this row sees
+    const int all = min(row0 + x * kTile + off + 1, lk) - half * kHalf;  // that every row of the tile sees
+    float* told = &bar->row[x][r];
+    auto any = [&](bool p) {  // over the warps that share the rows
+      return C::kSplit == 2 ? named_bar_any(pair, 64, p) : __any_sync(0xffffffffu, p) != 0;
+    };
+    auto arrive = [&](uint64_t* b) {  // once for the warp: arrivals of 32 lanes on one word take their turns
+      __syncwarp();
+      if (lane == 0) mbar_arrive(b);
+    };
+    float m = -INFINITY, l = 0.f;  // reference (raw scores), sum over this thread's keys
     bool ok = true;
-    for (int j = 0; j < n[x]; ++j) {
-      if (!(ok = wait(&bar->s[x], j & 1))) break;
-      tc_fence_after();
-      float s[kTile];
+    float s[kHalf];
+    uint32_t u[32];  // packed weights
+    // scores of tile j into s, those that the row does not see as -inf
+    auto read_scores = [&](int j) {
 #pragma unroll
-      for (int c = 0; c < 4; ++c) {
-        uint32_t u[32];
-        tmem_ld32(ts + c * 32, u);
+      for (int c = 0; c < kHalf / 32; ++c) {
+        uint32_t v[32];
+        tmem_ld32(ts + c * 32, v);
 #pragma unroll
-        for (int i = 0; i < 32; ++i) s[c * 32 + i] = __uint_as_float(u[i]);
+        for (int i = 0; i < 32; ++i) s[c * 32 + i] = __uint_as_float(v[i]);
       }
       tmem_wait_ld();
-      const int lim = min(seen, lk) - j * kTile;  // the row's keys in this tile
-      if (j * kTile + kTile > min(row0 + x * kTile + off + 1, lk)) {  // some row of the tile sees less
+      if (j * kTile + kHalf > all) {
+        const int lim = seen - j * kTile;
 #pragma unroll
-        for (int i = 0; i < kTile; ++i)
+        for (int i = 0; i < kHalf; ++i)
           if (i >= lim) s[i] = -INFINITY;
       }
-      float top = fmaxf(s[0], s[1]);
+    };
+    // weights of s against the reference m, their sum; where P has a place of its own they go there at once
+    auto weigh = [&]() {
+      const float ref = m == -INFINITY ? 0.f : m * sl2;
+      const uint64_t scale2 = pack2(sl2, sl2), ref2 = pack2(-ref, -ref);
+      uint64_t l2[2] = {0, 0};  // pairs of +0
 #pragma unroll
-      for (int i = 2; i < kTile; i += 2) top = fmaxf(top, fmaxf(s[i], s[i + 1]));
-      if (__any_sync(0xffffffffu, (top - m) * sl2 > kSlack || (m == -INFINITY && top > -INFINITY))) {
-        const float mn = fmaxf(m, top);
+      for (int c = 0; c < kHalf / 64; ++c) {
+#pragma unroll
+        for (int i = 0; i < 32; ++i) {
+          float p0, p1;
+          unpack2(fma2(pack2(s[c * 64 + 2 * i], s[c * 64 + 2 * i + 1]), scale2, ref2), p0, p1);
+          p0 = ex2(p0), p1 = ex2(p1);
+          l2[i & 1] = add2(l2[i & 1], pack2(p0, p1));
+          u[i] = pack_bf16(p0, p1);
+        }
+        if (C::kAhead) tmem_st32(tp + c * 32, u);
+      }
+      float la, lb;
+      unpack2(add2(l2[0], l2[1]), la, lb);
+      return la + lb;
+    };
+    float lt = 0.f;  // sum of the last tile's weights
+    for (int j = 0; j < n[x]; ++j) {
+      ok = wait(&bar->s[x], j & 1);
+      tc_fence_after();
+      read_scores(j);
+      if (C::kAhead) {
+        tc_fence_before();
+        arrive(&bar->read);
+        if (j > 0) {  // the last product has left P and O
+          ok = wait(&bar->o, (j - 1) & 1) && ok;
+          tc_fence_after();
+        }
+      }
+      // also, with two threads a row: both have read their scores, the weights may go over them
+      const bool move = any(!ok || m == -INFINITY || !(lt <= kMost));
+      if (move) {         // the reference moves to the maximum so far
+        if (any(!ok)) {   // all leave together
+          ok = false;
+          break;
+        }
+        float t4[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) t4[i] = s[i];
+#pragma unroll
+        for (int i = 4; i < kHalf - 4; i += 8)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) t4[e] = max3(t4[e], s[i + e], s[i + 4 + e]);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) t4[e] = fmaxf(t4[e], s[kHalf - 4 + e]);
+        float mn = fmaxf(m, max3(t4[0], t4[1], fmaxf(t4[2], t4[3])));
+        if (C::kSplit == 2) {
+          if (half == 1) *told = mn;
+          named_bar(pair, 64);
+          if (half == 0) *told = fmaxf(mn, *told);
+          named_bar(pair, 64);
+          mn = *told;
+        }
         const float f = mn == -INFINITY ? 1.f : ex2((m - mn) * sl2);
         m = mn;
         l *= f;
         if (j > 0) {
 #pragma unroll
-          for (int c = 0; c < D / 32; ++c) {
-            uint32_t u[32];
-            tmem_ld32(to + c * 32, u);
+          for (int c = 0; c < kOut / 16; ++c) {
+            uint32_t v[16];
+            tmem_ld16(to + c * 16, v);
             tmem_wait_ld();
 #pragma unroll
-            for (int i = 0; i < 32; ++i) u[i] = __float_as_uint(__uint_as_float(u[i]) * f);
-            tmem_st32(to + c * 32, u);
+            for (int i = 0; i < 16; ++i) v[i] = __float_as_uint(__uint_as_float(v[i]) * f);
+            tmem_st16(to + c * 16, v);
           }
         }
       }
-      const float ref = m == -INFINITY ? 0.f : m * sl2;
-      float l4[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-      for (int c = 0; c < 2; ++c) {
-        uint32_t u[32];
-#pragma unroll
-        for (int i = 0; i < 32; ++i) {
-          const float p0 = ex2(fmaf(s[c * 64 + 2 * i], sl2, -ref)), p1 = ex2(fmaf(s[c * 64 + 2 * i + 1], sl2, -ref));
-          l4[(2 * i) & 3] += p0;
-          l4[(2 * i + 1) & 3] += p1;
-          u[i] = pack_bf16(p0, p1);
-        }
-        tmem_st32(ts + c * 32, u);
-      }
-      l += (l4[0] + l4[1]) + (l4[2] + l4[3]);
+      lt = weigh();
+      l += lt;
+      if (!C::kAhead) tmem_st32(tp, u);
       tmem_wait_st();
       tc_fence_before();
-      mbar_arrive(&bar->p[x]);
+      arrive(&bar->p[x]);
     }
-    if (ok && row0 + x * kTile < lq) {  // some row of this tile is the call's
-      if (n[x] > 0) ok = wait(&bar->s[x], n[x] & 1);
-      if (ok) {
+    if (row0 + x * kTile < lq) {  // some row of this tile is the call's
+      if (ok && n[x] > 0) ok = C::kAhead ? wait(&bar->o, (n[x] - 1) & 1) : wait(&bar->s[x], n[x] & 1);
+      if (C::kSplit == 2) {
+        named_bar(pair, 64);  // the last maximum has been read
+        if (half == 1) *told = l;
+      }
+      if (!any(!ok)) {
         tc_fence_after();
+        if (C::kSplit == 2) {
+          if (half == 0) *told += l;
+          named_bar(pair, 64);
+          l = *told;
+        }
         const bool live = row < lq;
         const int64_t g = q0 + row;
-        __nv_bfloat16* out = static_cast<__nv_bfloat16*>(a.o.p) + g * a.o.stride + h * D;
         const float inv = l == 0.f ? 0.f : 1.f / l;
-        bool bad = false;
+        bool bad = !(l <= 3.402823466e38f);
+        // a warp's 32 rows x 64 dims through shared memory (Q's place: every product is done; 16-byte pieces
+        // swizzled by row), so that a store covers whole lines
+        uint8_t* stage = sQ + x * C::kTileBytes + half * kTile * 128;
 #pragma unroll
-        for (int c = 0; c < D / 32; ++c) {
+        for (int c = 0; c < 2; ++c) {
           uint32_t u[32];
           if (n[x] > 0) {
             tmem_ld32(to + c * 32, u);
@@ -302,23 +473,49 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
-            float y[8];
+            uint32_t w[4];
 #pragma unroll
-            for (int e = 0; e < 8; ++e) {
-              y[e] = l == 0.f ? 0.f : __uint_as_float(u[8 * i + e]) * inv;
-              bad |= n[x] > 0 && !(fabsf(__uint_as_float(u[8 * i + e])) <= 3.402823466e38f);
+            for (int e = 0; e < 4; ++e) {
+              const float z0 = n[x] > 0 ? __uint_as_float(u[8 * i + 2 * e]) : 0.f;
+              const float z1 = n[x] > 0 ? __uint_as_float(u[8 * i + 2 * e + 1]) : 0.f;
+              bad |= !(fmaxf(fabsf(z0), fabsf(z1)) <= 3.402823466e38f) || z0 != z0 || z1 != z1;
+              w[e] = l == 0.f ? 0u : pack_bf16(z0 * inv, z1 * inv);
             }
-            if (live) {
-              if (a.o.vec) store8<true>(out + c * 32 + i * 8, y);
-              else store8<false>(out + c * 32 + i * 8, y);
+            *reinterpret_cast<uint4*>(stage + sw128(r, c * 32 + i * 8)) = make_uint4(w[0], w[1], w[2], w[3]);
+          }
+        }
+        __syncwarp();
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const int rr = quad * 32 + i * 4 + (lane >> 3), c = (lane & 7) * 8, grow = row0 + x * kTile + rr;
+          if (grow >= lq) continue;
+          const uint4 w = *reinterpret_cast<const uint4*>(stage + sw128(rr, c));
+          __nv_bfloat16* out = static_cast<__nv_bfloat16*>(a.o.p) + (q0 + grow) * a.o.stride + h * D + half * kOut + c;
+          if (a.o.vec) {
+            *reinterpret_cast<uint4*>(out) = w;
+          } else {
+            unsigned short* o16 = reinterpret_cast<unsigned short*>(out);
+            const uint32_t ws[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              o16[2 * e] = static_cast<unsigned short>(ws[e]);
+              o16[2 * e + 1] = static_cast<unsigned short>(ws[e] >> 16);
             }
           }
         }
-        bad |= !(l <= 3.402823466e38f);
-        if (live && a.lse) a.lse[g * a.Hq + h] = l == 0.f ? -INFINITY : m * a.scale + logf(l);
-        // rows that are not finite, once more from the definition
-        for (uint32_t again = __ballot_sync(0xffffffffu, live && bad); again; again &= again - 1) {
-          const int rr = __ffs(again) - 1, i = row0 + x * kTile + quad * 32 + rr;
+        if (live && half == 0 && a.lse) a.lse[g * a.Hq + h] = l == 0.f ? -INFINITY : m * a.scale + logf(l);
+        // rows that are not finite, once more from the definition; with two threads a row by the second's warp,
+        // after the first's has written its part
+        bad = bad && live;
+        __syncwarp();
+        if (C::kSplit == 2) {
+          named_bar(pair, 64);
+          if (half == 0) *told = bad ? 1.f : 0.f;
+          named_bar(pair, 64);
+          bad = half == 1 && (bad || *told > 0.f);
+        }
+        for (uint32_t again = __ballot_sync(0xffffffffu, bad); again; again &= again - 1) {
+          const int i = row0 + x * kTile + quad * 32 + __ffs(again) - 1;
           const int64_t gi = q0 + i;
           const __nv_bfloat16* q = static_cast<const __nv_bfloat16*>(a.q.p) + gi * a.q.stride + h * D;
           const __nv_bfloat16* k = static_cast<const __nv_bfloat16*>(a.k.p) + k0 * a.k.stride + hk * D;
@@ -335,9 +532,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     tc_fence_before();
   }
   __syncthreads();
-  if (warp == 9) {
+  if (warp == C::kMmaWarp) {
     tc_fence_after();
-    tmem_dealloc(tmem, 512);
+    tmem_dealloc(tmem, C::kCols);
   }
 }
 
@@ -358,7 +555,7 @@ template <int D>
 int launch_tc(const PromptArgs& a, cudaStream_t s) {
   TcArgs t;
   t.a = a;
-  t.qblocks = (a.max_q + 2 * kTile - 1) / (2 * kTile);
+  t.qblocks = (a.max_q + Cfg<D>::kTiles * kTile - 1) / (Cfg<D>::kTiles * kTile);
   t.status = static_cast<uint32_t*>(a.ws);
   t.limit = wait_limit_ns();
   t.stall = take_test_stall() ? 1 : 0;
@@ -370,7 +567,7 @@ int launch_tc(const PromptArgs& a, cudaStream_t s) {
     return FALCON_ERR_CUDA;
   const auto kern = attn_prompt_tc_kernel<D>;
   if (!set_smem_limit(reinterpret_cast<const void*>(kern), Cfg<D>::kSmem)) return FALCON_ERR_CUDA;
-  kern<<<static_cast<unsigned>(n), kThreads, Cfg<D>::kSmem, s>>>(mq, mk, mv, t);
+  kern<<<static_cast<unsigned>(n), Cfg<D>::kThreads, Cfg<D>::kSmem, s>>>(mq, mk, mv, t);
   return cudaGetLastError() == cudaSuccess ? FALCON_OK : FALCON_ERR_CUDA;
 }
 

@@ -56,6 +56,25 @@ __device__ __forceinline__ bool mbar_wait(uint64_t* bar, uint32_t parity,
   }
   return true;
 }
+// The same bound for warps that share their scheduler with busy ones: the
+// thread sleeps in the hardware for up to 2 us a try instead of polling.
+__device__ __forceinline__ bool mbar_wait_sleep(uint64_t* bar, uint32_t parity,
+                                                uint64_t limit_ns = kWaitLimitNs) {
+  if (mbar_try_wait(bar, parity)) return true;
+  const uint64_t t0 = globaltimer();
+  for (;;) {
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(smem_u32(bar)), "r"(parity), "r"(2000u)
+        : "memory");
+    if (ok) return true;
+    if (globaltimer() - t0 > limit_ns) return false;
+  }
+}
 
 // ------------------------------------------------------------ async proxy
 __device__ __forceinline__ void fence_proxy_async() {

@@ -27,10 +27,19 @@ struct RowsOut {
 // How the rows of a head are normed and rotated.
 struct HeadArgs {
   int d, norm;
-  float eps;
+  float eps, inv_d;
   int rot, layout, rows;
   const float2* table;
+  bool wide;  // table rows and weights on 16-byte boundaries
 };
+// How a kernel rotates: not at all, whole 8-element pieces of the half or the
+// interleaved layout (16-byte loads of the table), or any pairs.
+enum RotMode { kRotNone = 0, kRotHalf = 1, kRotInterleaved = 2, kRotAny = 3 };
+inline RotMode rot_mode(const HeadArgs& h) {
+  if (h.rot == 0) return kRotNone;
+  if (h.layout == FALCON_ROPE_HALF) return h.wide && h.rot % 16 == 0 ? kRotHalf : kRotAny;
+  return h.wide && h.rot % 8 == 0 ? kRotInterleaved : kRotAny;
+}
 
 int launch_rope_table(const double* inv_freq, int rot, int rows, float mscale, float* table, cudaStream_t s);
 int launch_qk_norm_rope(const HeadArgs& h, int dtype, int64_t tokens, int Hq, int Hkv, RowsIn q, RowsIn k,
@@ -156,72 +165,85 @@ __device__ __forceinline__ void store8(float* p, const float (&x)[8]) {
 
 // Norm and rotation of 8 consecutive elements c0 .. c0 + 7 of a head row; the
 // d / 8 lanes of the row are neighbours in the warp and every lane of the
-// warp takes part (lanes without a row pass x = 0).  w8 holds this lane's
-// norm weights, (co, si) the table's entries of its pairs.  Rows are normed
-// and rotated in fp32; `row` gives the raw row again for partners that no
-// whole lane holds (rot / 2 not a multiple of 8).
+// warp takes part (lanes without a row pass x = 0).
 struct HeadPiece {
-  float w[8];
-  float co[8], si[8];  // HALF: per element; INTERLEAVED: per pair (the first 4)
+  float w[8];          // norm weights
+  float co[8], si[8];  // HALF: per element (si signed); INTERLEAVED: per pair (the first 4)
 };
 __device__ __forceinline__ void load_weights(HeadPiece& hp, const HeadArgs& h, const float* w, int c0) {
+  if (!h.norm) return;
+  if (w && h.wide) {
+    const float4 a = __ldg(reinterpret_cast<const float4*>(w + c0)), b = __ldg(reinterpret_cast<const float4*>(w + c0) + 1);
+    hp.w[0] = a.x; hp.w[1] = a.y; hp.w[2] = a.z; hp.w[3] = a.w;
+    hp.w[4] = b.x; hp.w[5] = b.y; hp.w[6] = b.z; hp.w[7] = b.w;
+    return;
+  }
 #pragma unroll
-  for (int i = 0; i < 8; ++i) hp.w[i] = (h.norm && w) ? __ldg(w + c0 + i) : 1.f;
+  for (int i = 0; i < 8; ++i) hp.w[i] = w ? __ldg(w + c0 + i) : 1.f;
 }
 // Angles of this lane's elements at `pos`; outside the table they are NaN.
+template <int MODE>
 __device__ __forceinline__ void load_angles(HeadPiece& hp, const HeadArgs& h, int64_t pos, int c0) {
-  if (h.rot == 0) return;
+  if (MODE == kRotNone || c0 >= h.rot) return;
   const bool in = pos >= 0 && pos < h.rows;
   const int half = h.rot >> 1;
   const float2* t = h.table + (in ? pos : 0) * half;
   const float nan = __int_as_float(0x7fffffff);
-  if (h.layout == FALCON_ROPE_HALF) {
+  if (MODE == kRotHalf || MODE == kRotInterleaved) {
+    constexpr int n = MODE == kRotHalf ? 4 : 2;
+    const bool low = MODE == kRotHalf && c0 < half;
+    const float4* v = reinterpret_cast<const float4*>(t + (MODE == kRotInterleaved ? c0 >> 1 : low ? c0 : c0 - half));
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const int c = c0 + i;
-      if (c < h.rot) {
-        const float2 a = __ldg(t + (c < half ? c : c - half));
-        hp.co[i] = in ? a.x : nan;
-        hp.si[i] = in ? (c < half ? -a.y : a.y) : nan;
-      } else {
-        hp.co[i] = 1.f;
-        hp.si[i] = 0.f;
-      }
+    for (int i = 0; i < n; ++i) {
+      const float4 a = __ldg(v + i);
+      hp.co[2 * i] = a.x; hp.si[2 * i] = low ? -a.y : a.y;
+      hp.co[2 * i + 1] = a.z; hp.si[2 * i + 1] = low ? -a.w : a.w;
     }
-  } else {
+    if (!in) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int j = (c0 >> 1) + i;
-      if (j < half) {
-        const float2 a = __ldg(t + j);
-        hp.co[i] = in ? a.x : nan;
-        hp.si[i] = in ? a.y : nan;
-      } else {
-        hp.co[i] = 1.f;
-        hp.si[i] = 0.f;
-      }
+      for (int i = 0; i < 2 * n; ++i) hp.co[i] = nan;
+    }
+    return;
+  }
+  const bool hl = h.layout == FALCON_ROPE_HALF;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const int c = c0 + i;  // HALF: element c; INTERLEAVED: pair c0 / 2 + i
+    hp.co[i] = 1.f, hp.si[i] = 0.f;
+    if (hl ? c < h.rot : (i < 4 && (c0 >> 1) + i < half)) {
+      const float2 a = __ldg(t + (hl ? (c < half ? c : c - half) : (c0 >> 1) + i));
+      hp.co[i] = in ? a.x : nan;
+      hp.si[i] = hl && c < half ? -a.y : a.y;
     }
   }
 }
-template <typename T>
+// `row` and `w` give the raw row and weights again for partners that no whole
+// lane holds (kRotAny).
+template <int MODE, typename T>
 __device__ __forceinline__ void norm_rotate8(float (&x)[8], const HeadPiece& hp, const HeadArgs& h,
                                              const float* w, const T* row, bool live, int c0, int lane) {
-  const int L = h.d >> 3;
   float r = 1.f;
   if (h.norm) {
     float s = 0.f;
 #pragma unroll
     for (int i = 0; i < 8; ++i) s = fmaf(x[i], x[i], s);
-    for (int o = L >> 1; o; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
-    r = rsqrtf(s / static_cast<float>(h.d) + h.eps);
+    // over the d / 8 lanes: 2, 4, 8 or 16
+    s += __shfl_xor_sync(0xffffffffu, s, 1);
+    float v = __shfl_xor_sync(0xffffffffu, s, 2);
+    s += h.d > 16 ? v : 0.f;
+    v = __shfl_xor_sync(0xffffffffu, s, 4);
+    s += h.d > 32 ? v : 0.f;
+    v = __shfl_xor_sync(0xffffffffu, s, 8);
+    s += h.d > 64 ? v : 0.f;
+    r = rsqrtf(fmaf(s, h.inv_d, h.eps));
 #pragma unroll
     for (int i = 0; i < 8; ++i) x[i] = x[i] * r * hp.w[i];
   }
-  if (h.rot == 0) return;
-  if (h.layout == FALCON_ROPE_INTERLEAVED) {
+  if (MODE == kRotNone) return;
+  if (MODE == kRotInterleaved || (MODE == kRotAny && h.layout == FALCON_ROPE_INTERLEAVED)) {
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      if (c0 + 2 * i < h.rot) {
+      if (c0 + (MODE == kRotAny ? 2 * i : 0) < h.rot) {
         const float a = x[2 * i], b = x[2 * i + 1];
         x[2 * i] = a * hp.co[i] - b * hp.si[i];
         x[2 * i + 1] = b * hp.co[i] + a * hp.si[i];
@@ -231,12 +253,15 @@ __device__ __forceinline__ void norm_rotate8(float (&x)[8], const HeadPiece& hp,
   }
   const int half = h.rot >> 1;
   float y[8];
-  if ((half & 7) == 0) {  // the partners are one other lane's 8 elements
-    const int off = half >> 3;
-    const int src = c0 < half ? lane + off : lane - off;
+  if constexpr (MODE == kRotHalf) {  // the partners are one other lane's 8 elements
+    const int src = c0 < half ? lane + (half >> 3) : lane - (half >> 3);
 #pragma unroll
     for (int i = 0; i < 8; ++i) y[i] = __shfl_sync(0xffffffffu, x[i], src & 31);
-  } else {
+    if (c0 < h.rot) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) x[i] = x[i] * hp.co[i] + y[i] * hp.si[i];
+    }
+  } else if constexpr (MODE == kRotAny) {
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
       const int c = c0 + i, pc = c < half ? c + half : c - half;
@@ -246,11 +271,11 @@ __device__ __forceinline__ void norm_rotate8(float (&x)[8], const HeadPiece& hp,
         if (h.norm) y[i] = y[i] * r * (w ? __ldg(w + pc) : 1.f);
       }
     }
-    __syncwarp();
-  }
+    __syncwarp();  // read before any lane writes the row in place
 #pragma unroll
-  for (int i = 0; i < 8; ++i)
-    if (c0 + i < h.rot) x[i] = x[i] * hp.co[i] + y[i] * hp.si[i];
+    for (int i = 0; i < 8; ++i)
+      if (c0 + i < h.rot) x[i] = x[i] * hp.co[i] + y[i] * hp.si[i];
+  }
 }
 
 // ---------------------------------------------------------------- 8-bit cache

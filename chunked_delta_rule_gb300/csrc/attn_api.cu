@@ -66,9 +66,10 @@ int check_head(const falcon_attn_params_t* p, const float* table, const float* w
   if (p->qk_norm && (misaligned(w_q, 4) || misaligned(w_k, 4))) return FALCON_ERR_INVALID_ARG;
   return FALCON_OK;
 }
-HeadArgs head_args(const falcon_attn_params_t* p, const float* table) {
-  return HeadArgs{p->d, p->qk_norm ? 1 : 0, p->norm_eps, p->rot, p->rope_layout, p->rope_rows,
-                  reinterpret_cast<const float2*>(table)};
+HeadArgs head_args(const falcon_attn_params_t* p, const float* table, const float* w_q, const float* w_k) {
+  const bool wide = !misaligned(table, 16) && !misaligned(w_q, 16) && !misaligned(w_k, 16) && p->rot % 4 == 0;
+  return HeadArgs{p->d, p->qk_norm ? 1 : 0, p->norm_eps, 1.f / static_cast<float>(p->d), p->rot, p->rope_layout, p->rope_rows,
+                  reinterpret_cast<const float2*>(table), wide};
 }
 int check_cache(const falcon_attn_params_t* p, const falcon_kv_cache_t* c, const int32_t* blocks) {
   if (p->page != 16 && p->page != 32 && p->page != 64 && p->page != 128) return FALCON_ERR_UNSUPPORTED;
@@ -109,7 +110,7 @@ int falcon_qk_norm_rope(const falcon_attn_params_t* p, const void* q, const void
   if ((!q_inplace && overlap(q, nq, q_out, nqo)) || (!k_inplace && overlap(k, nk, k_out, nko)) ||
       overlap(k, nk, q_out, nqo) || overlap(q, nq, k_out, nko) || overlap(q_out, nqo, k_out, nko))
     return FALCON_ERR_INVALID_ARG;
-  return launch_qk_norm_rope(head_args(p, table), p->dtype, p->tokens, p->Hq, p->Hkv, qi, ki, w_q, w_k, positions, qo,
+  return launch_qk_norm_rope(head_args(p, table, w_q, w_k), p->dtype, p->tokens, p->Hq, p->Hkv, qi, ki, w_q, w_k, positions, qo,
                              ko, reinterpret_cast<cudaStream_t>(stream));
 }
 
@@ -139,7 +140,7 @@ int falcon_kv_append(const falcon_attn_params_t* p, const void* k, const void* v
   const AppendArgs a{p->B, p->Hkv, p->page, p->num_pages, p->max_pages, p->max_q, p->tokens,
                      rows_in(p, k, p->k_stride, p->Hkv), rows_in(p, v, p->v_stride, p->Hkv), w_k, cu_new, ctx_lens,
                      block_table, *cache};
-  return launch_kv_append(head_args(p, table), p->dtype, a, reinterpret_cast<cudaStream_t>(stream));
+  return launch_kv_append(head_args(p, table, nullptr, w_k), p->dtype, a, reinterpret_cast<cudaStream_t>(stream));
 }
 
 size_t falcon_attn_decode_workspace_size(const falcon_attn_params_t* p) {

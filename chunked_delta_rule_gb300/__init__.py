@@ -179,6 +179,9 @@ def _stream(stream) -> int | None:
     if stream is None:
         try:
             import torch
+            # torch.cuda.current_stream().cuda_stream without the Stream object (3 us a call)
+            return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
+        except AttributeError:  # pragma: no cover
             return torch.cuda.current_stream().cuda_stream
         except Exception:  # pragma: no cover
             return None

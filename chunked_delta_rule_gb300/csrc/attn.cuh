@@ -32,12 +32,12 @@ struct HeadArgs {
   const float2* table;
   bool wide;  // table rows and weights on 16-byte boundaries
 };
-// How a kernel rotates: not at all, whole 8-element pieces of the half or the
-// interleaved layout (16-byte loads of the table), or any pairs.
+// How a kernel rotates: not at all, lanes that hold whole pairs of the half or
+// the interleaved layout (16-byte loads of the table), or any pairs.
 enum RotMode { kRotNone = 0, kRotHalf = 1, kRotInterleaved = 2, kRotAny = 3 };
 inline RotMode rot_mode(const HeadArgs& h) {
   if (h.rot == 0) return kRotNone;
-  if (h.layout == FALCON_ROPE_HALF) return h.wide && h.rot % 16 == 0 ? kRotHalf : kRotAny;
+  if (h.layout == FALCON_ROPE_HALF) return h.wide && h.rot % 8 == 0 ? kRotHalf : kRotAny;
   return h.wide && h.rot % 8 == 0 ? kRotInterleaved : kRotAny;
 }
 
@@ -91,38 +91,49 @@ constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 
 // ---------------------------------------------------------------- rows
-template <typename T> struct Raw8;                       // 8 elements as loaded
-template <> struct Raw8<__nv_bfloat16> { uint4 v; };
+// A lane's 8 elements of a head row: two pieces of 4, at a and b.  They are
+// neighbours (b = a + 4), or with the half layout (SPLIT) the two members of
+// the lane's four pairs.
+struct Pieces {
+  int a, b;
+};
+template <typename T> struct Raw8;  // as loaded
+template <> struct Raw8<__nv_bfloat16> { uint2 a, b; };
 template <> struct Raw8<float> { float4 a, b; };
 
-template <bool VEC>
-__device__ __forceinline__ Raw8<__nv_bfloat16> load8(const __nv_bfloat16* p) {
+template <bool VEC, bool SPLIT>
+__device__ __forceinline__ Raw8<__nv_bfloat16> load8(const __nv_bfloat16* row, Pieces at) {
   Raw8<__nv_bfloat16> r;
-  if (VEC) {
-    r.v = *reinterpret_cast<const uint4*>(p);
+  if (VEC && !SPLIT) {
+    const uint4 v = *reinterpret_cast<const uint4*>(row + at.a);
+    r.a = make_uint2(v.x, v.y);
+    r.b = make_uint2(v.z, v.w);
+  } else if (VEC) {
+    r.a = *reinterpret_cast<const uint2*>(row + at.a);
+    r.b = *reinterpret_cast<const uint2*>(row + at.b);
   } else {
-    const unsigned short* u = reinterpret_cast<const unsigned short*>(p);
-    uint32_t w[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) w[i] = u[2 * i] | (static_cast<uint32_t>(u[2 * i + 1]) << 16);
-    r.v = make_uint4(w[0], w[1], w[2], w[3]);
+    const unsigned short* u = reinterpret_cast<const unsigned short*>(row + at.a);
+    const unsigned short* v = reinterpret_cast<const unsigned short*>(row + at.b);
+    r.a = make_uint2(u[0] | (static_cast<uint32_t>(u[1]) << 16), u[2] | (static_cast<uint32_t>(u[3]) << 16));
+    r.b = make_uint2(v[0] | (static_cast<uint32_t>(v[1]) << 16), v[2] | (static_cast<uint32_t>(v[3]) << 16));
   }
   return r;
 }
-template <bool VEC>
-__device__ __forceinline__ Raw8<float> load8(const float* p) {
+template <bool VEC, bool SPLIT>
+__device__ __forceinline__ Raw8<float> load8(const float* row, Pieces at) {
   Raw8<float> r;
   if (VEC) {
-    r.a = *reinterpret_cast<const float4*>(p);
-    r.b = *reinterpret_cast<const float4*>(p + 4);
+    r.a = *reinterpret_cast<const float4*>(row + at.a);
+    r.b = *reinterpret_cast<const float4*>(row + at.b);
   } else {
-    r.a = make_float4(p[0], p[1], p[2], p[3]);
-    r.b = make_float4(p[4], p[5], p[6], p[7]);
+    const float *u = row + at.a, *v = row + at.b;
+    r.a = make_float4(u[0], u[1], u[2], u[3]);
+    r.b = make_float4(v[0], v[1], v[2], v[3]);
   }
   return r;
 }
 __device__ __forceinline__ void unpack8(const Raw8<__nv_bfloat16>& r, float (&x)[8]) {
-  const uint32_t w[4] = {r.v.x, r.v.y, r.v.z, r.v.w};
+  const uint32_t w[4] = {r.a.x, r.a.y, r.b.x, r.b.y};
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     x[2 * i] = __uint_as_float(w[i] << 16);
@@ -133,95 +144,88 @@ __device__ __forceinline__ void unpack8(const Raw8<float>& r, float (&x)[8]) {
   x[0] = r.a.x; x[1] = r.a.y; x[2] = r.a.z; x[3] = r.a.w;
   x[4] = r.b.x; x[5] = r.b.y; x[6] = r.b.z; x[7] = r.b.w;
 }
-template <bool VEC>
-__device__ __forceinline__ void store8(__nv_bfloat16* p, const float (&x)[8]) {
+template <bool VEC, bool SPLIT>
+__device__ __forceinline__ void store8(__nv_bfloat16* row, Pieces at, const float (&x)[8]) {
   uint32_t w[4];
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     __nv_bfloat162 v = __floats2bfloat162_rn(x[2 * i], x[2 * i + 1]);
     w[i] = *reinterpret_cast<uint32_t*>(&v);
   }
-  if (VEC) {
-    *reinterpret_cast<uint4*>(p) = make_uint4(w[0], w[1], w[2], w[3]);
+  if (VEC && !SPLIT) {
+    *reinterpret_cast<uint4*>(row + at.a) = make_uint4(w[0], w[1], w[2], w[3]);
+  } else if (VEC) {
+    *reinterpret_cast<uint2*>(row + at.a) = make_uint2(w[0], w[1]);
+    *reinterpret_cast<uint2*>(row + at.b) = make_uint2(w[2], w[3]);
   } else {
-    unsigned short* u = reinterpret_cast<unsigned short*>(p);
+    unsigned short* u = reinterpret_cast<unsigned short*>(row + at.a);
+    unsigned short* v = reinterpret_cast<unsigned short*>(row + at.b);
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
+    for (int i = 0; i < 2; ++i) {
       u[2 * i] = static_cast<unsigned short>(w[i]);
       u[2 * i + 1] = static_cast<unsigned short>(w[i] >> 16);
+      v[2 * i] = static_cast<unsigned short>(w[2 + i]);
+      v[2 * i + 1] = static_cast<unsigned short>(w[2 + i] >> 16);
     }
   }
 }
-template <bool VEC>
-__device__ __forceinline__ void store8(float* p, const float (&x)[8]) {
+template <bool VEC, bool SPLIT>
+__device__ __forceinline__ void store8(float* row, Pieces at, const float (&x)[8]) {
   if (VEC) {
-    *reinterpret_cast<float4*>(p) = make_float4(x[0], x[1], x[2], x[3]);
-    *reinterpret_cast<float4*>(p + 4) = make_float4(x[4], x[5], x[6], x[7]);
+    *reinterpret_cast<float4*>(row + at.a) = make_float4(x[0], x[1], x[2], x[3]);
+    *reinterpret_cast<float4*>(row + at.b) = make_float4(x[4], x[5], x[6], x[7]);
   } else {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) p[i] = x[i];
+    for (int i = 0; i < 4; ++i) row[at.a + i] = x[i], row[at.b + i] = x[4 + i];
   }
 }
 
-// Norm and rotation of 8 consecutive elements c0 .. c0 + 7 of a head row; the
-// d / 8 lanes of the row are neighbours in the warp and every lane of the
-// warp takes part (lanes without a row pass x = 0).
+// Norm and rotation of a lane's 8 elements of a head row; the d / 8 lanes of
+// the row are neighbours in the warp and every lane of the warp takes part
+// (lanes without a row pass x = 0).  The pairs are (x[i], x[4 + i]) with the
+// half layout and (x[2i], x[2i + 1]) with the interleaved one.
 struct HeadPiece {
   float w[8];          // norm weights
-  float co[8], si[8];  // HALF: per element (si signed); INTERLEAVED: per pair (the first 4)
+  float co[4], si[4];  // angles of the lane's pairs
 };
-__device__ __forceinline__ void load_weights(HeadPiece& hp, const HeadArgs& h, const float* w, int c0) {
+// The pieces of lane li of a row: pairs first, then the dims that are not rotated.
+template <int MODE>
+__device__ __forceinline__ Pieces pieces_of(const HeadArgs& h, int li) {
+  const bool pairs = MODE == kRotHalf && li * 8 < h.rot;
+  return pairs ? Pieces{li * 4, (h.rot >> 1) + li * 4} : Pieces{li * 8, li * 8 + 4};
+}
+__device__ __forceinline__ void load_weights(HeadPiece& hp, const HeadArgs& h, const float* w, Pieces at) {
   if (!h.norm) return;
   if (w && h.wide) {
-    const float4 a = __ldg(reinterpret_cast<const float4*>(w + c0)), b = __ldg(reinterpret_cast<const float4*>(w + c0) + 1);
+    const float4 a = __ldg(reinterpret_cast<const float4*>(w + at.a)), b = __ldg(reinterpret_cast<const float4*>(w + at.b));
     hp.w[0] = a.x; hp.w[1] = a.y; hp.w[2] = a.z; hp.w[3] = a.w;
     hp.w[4] = b.x; hp.w[5] = b.y; hp.w[6] = b.z; hp.w[7] = b.w;
     return;
   }
 #pragma unroll
-  for (int i = 0; i < 8; ++i) hp.w[i] = w ? __ldg(w + c0 + i) : 1.f;
+  for (int i = 0; i < 4; ++i) hp.w[i] = w ? __ldg(w + at.a + i) : 1.f, hp.w[4 + i] = w ? __ldg(w + at.b + i) : 1.f;
 }
-// Angles of this lane's elements at `pos`; outside the table they are NaN.
+// The table's row of a position, NULL outside the table.
+__device__ __forceinline__ const float2* table_row(const HeadArgs& h, int64_t pos) {
+  return pos >= 0 && pos < h.rows ? h.table + pos * (h.rot >> 1) : nullptr;
+}
+// Angles of this lane's pairs; outside the table they are NaN.
 template <int MODE>
-__device__ __forceinline__ void load_angles(HeadPiece& hp, const HeadArgs& h, int64_t pos, int c0) {
-  if (MODE == kRotNone || c0 >= h.rot) return;
-  const bool in = pos >= 0 && pos < h.rows;
-  const int half = h.rot >> 1;
-  const float2* t = h.table + (in ? pos : 0) * half;
-  const float nan = __int_as_float(0x7fffffff);
-  if (MODE == kRotHalf || MODE == kRotInterleaved) {
-    constexpr int n = MODE == kRotHalf ? 4 : 2;
-    const bool low = MODE == kRotHalf && c0 < half;
-    const float4* v = reinterpret_cast<const float4*>(t + (MODE == kRotInterleaved ? c0 >> 1 : low ? c0 : c0 - half));
+__device__ __forceinline__ void load_angles(HeadPiece& hp, const HeadArgs& h, const float2* row, Pieces at) {
+  if ((MODE != kRotHalf && MODE != kRotInterleaved) || at.a >= h.rot) return;
+  const float4* v = reinterpret_cast<const float4*>((row ? row : h.table) + (MODE == kRotHalf ? at.a : at.a >> 1));
+  const float4 a = __ldg(v), b = __ldg(v + 1);
+  hp.co[0] = a.x; hp.si[0] = a.y; hp.co[1] = a.z; hp.si[1] = a.w;
+  hp.co[2] = b.x; hp.si[2] = b.y; hp.co[3] = b.z; hp.si[3] = b.w;
+  if (!row) {
 #pragma unroll
-    for (int i = 0; i < n; ++i) {
-      const float4 a = __ldg(v + i);
-      hp.co[2 * i] = a.x; hp.si[2 * i] = low ? -a.y : a.y;
-      hp.co[2 * i + 1] = a.z; hp.si[2 * i + 1] = low ? -a.w : a.w;
-    }
-    if (!in) {
-#pragma unroll
-      for (int i = 0; i < 2 * n; ++i) hp.co[i] = nan;
-    }
-    return;
-  }
-  const bool hl = h.layout == FALCON_ROPE_HALF;
-#pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const int c = c0 + i;  // HALF: element c; INTERLEAVED: pair c0 / 2 + i
-    hp.co[i] = 1.f, hp.si[i] = 0.f;
-    if (hl ? c < h.rot : (i < 4 && (c0 >> 1) + i < half)) {
-      const float2 a = __ldg(t + (hl ? (c < half ? c : c - half) : (c0 >> 1) + i));
-      hp.co[i] = in ? a.x : nan;
-      hp.si[i] = hl && c < half ? -a.y : a.y;
-    }
+    for (int i = 0; i < 4; ++i) hp.co[i] = __int_as_float(0x7fffffff);
   }
 }
-// `row` and `w` give the raw row and weights again for partners that no whole
-// lane holds (kRotAny).
+// raw, w, row: the raw row, its weights and the table's row again (kRotAny: any pairs).
 template <int MODE, typename T>
-__device__ __forceinline__ void norm_rotate8(float (&x)[8], const HeadPiece& hp, const HeadArgs& h,
-                                             const float* w, const T* row, bool live, int c0, int lane) {
+__device__ __forceinline__ void norm_rotate8(float (&x)[8], const HeadPiece& hp, const HeadArgs& h, const float* w,
+                                             const float2* row, const T* raw, bool live, Pieces at) {
   float r = 1.f;
   if (h.norm) {
     float s = 0.f;
@@ -239,42 +243,37 @@ __device__ __forceinline__ void norm_rotate8(float (&x)[8], const HeadPiece& hp,
 #pragma unroll
     for (int i = 0; i < 8; ++i) x[i] = x[i] * r * hp.w[i];
   }
-  if (MODE == kRotNone) return;
-  if (MODE == kRotInterleaved || (MODE == kRotAny && h.layout == FALCON_ROPE_INTERLEAVED)) {
+  if constexpr (MODE == kRotHalf || MODE == kRotInterleaved) {
+    if (at.a < h.rot) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      if (c0 + (MODE == kRotAny ? 2 * i : 0) < h.rot) {
-        const float a = x[2 * i], b = x[2 * i + 1];
-        x[2 * i] = a * hp.co[i] - b * hp.si[i];
-        x[2 * i + 1] = b * hp.co[i] + a * hp.si[i];
+      for (int i = 0; i < 4; ++i) {
+        constexpr bool kHalf = MODE == kRotHalf;
+        float &p = x[kHalf ? i : 2 * i], &q = x[kHalf ? 4 + i : 2 * i + 1];
+        const float a = p, b = q;
+        p = a * hp.co[i] - b * hp.si[i];
+        q = b * hp.co[i] + a * hp.si[i];
       }
     }
-    return;
-  }
-  const int half = h.rot >> 1;
-  float y[8];
-  if constexpr (MODE == kRotHalf) {  // the partners are one other lane's 8 elements
-    const int src = c0 < half ? lane + (half >> 3) : lane - (half >> 3);
-#pragma unroll
-    for (int i = 0; i < 8; ++i) y[i] = __shfl_sync(0xffffffffu, x[i], src & 31);
-    if (c0 < h.rot) {
-#pragma unroll
-      for (int i = 0; i < 8; ++i) x[i] = x[i] * hp.co[i] + y[i] * hp.si[i];
-    }
   } else if constexpr (MODE == kRotAny) {
+    const int half = h.rot >> 1;
+    const bool hl = h.layout == FALCON_ROPE_HALF;
+    float y[8];
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-      const int c = c0 + i, pc = c < half ? c + half : c - half;
-      y[i] = 0.f;
+      const int c = at.a + i, j = hl ? (c < half ? c : c - half) : c >> 1;  // element, its pair
+      const bool low = hl ? c < half : !(c & 1);
+      y[i] = x[i];
       if (live && c < h.rot) {
-        y[i] = to_f32(row[pc]);
-        if (h.norm) y[i] = y[i] * r * (w ? __ldg(w + pc) : 1.f);
+        const int pc = hl ? (low ? c + half : c - half) : c ^ 1;
+        float other = to_f32(raw[pc]);
+        if (h.norm) other = other * r * (w ? __ldg(w + pc) : 1.f);
+        const float2 t = row ? __ldg(row + j) : make_float2(__int_as_float(0x7fffffff), 0.f);
+        y[i] = x[i] * t.x + (low ? -t.y : t.y) * other;
       }
     }
     __syncwarp();  // read before any lane writes the row in place
 #pragma unroll
-    for (int i = 0; i < 8; ++i)
-      if (c0 + i < h.rot) x[i] = x[i] * hp.co[i] + y[i] * hp.si[i];
+    for (int i = 0; i < 8; ++i) x[i] = y[i];
   }
 }
 

@@ -40,13 +40,15 @@ __global__ void __launch_bounds__(256) kv_append_kernel(HeadArgs h, AppendArgs a
   if (row0 + n > a.tokens) return;
   const int pg = a.blocks[static_cast<int64_t>(b) * a.max_pages + pcol];
 
-  const int ls = 28 - __clz(h.d), rows = THREADS >> ls, c0 = (tid & ((1 << ls) - 1)) * 8, r0 = tid >> ls;
+  const int ls = 28 - __clz(h.d), rows = THREADS >> ls, r0 = tid >> ls;
+  const Pieces at = pieces_of<MODE>(h, tid & ((1 << ls) - 1));
+  constexpr bool kSplit = MODE == kRotHalf;
   const RowsIn in = is_v ? a.v : a.k;
   const T* src = static_cast<const T*>(in.p) + row0 * in.stride + static_cast<int64_t>(head) * h.d;
   Raw8<T> raw[NP];
 #pragma unroll
   for (int u = 0; u < NP; ++u)
-    if (r0 + u * rows < n) raw[u] = load8<VEC>(src + (r0 + u * rows) * in.stride + c0);
+    if (r0 + u * rows < n) raw[u] = load8<VEC, kSplit>(src + (r0 + u * rows) * in.stride, at);
   if (pg < 0 || pg >= a.num_pages) return;
   const int64_t ph = static_cast<int64_t>(pg) * a.Hkv + head;
   uint8_t* scale = (is_v ? a.cache.v_scale : a.cache.k_scale) + ph;
@@ -65,12 +67,13 @@ __global__ void __launch_bounds__(256) kv_append_kernel(HeadArgs h, AppendArgs a
   }
   if (!is_v && (MODE != kRotNone || h.norm)) {
     HeadPiece hp;
-    load_weights(hp, h, a.w_k, c0);
+    load_weights(hp, h, a.w_k, at);
 #pragma unroll
     for (int u = 0; u < NP; ++u) {
       const int r = r0 + u * rows;
-      load_angles<MODE>(hp, h, t0 + r, c0);
-      norm_rotate8<MODE, T>(x[u], hp, h, a.w_k, src + r * in.stride, r < n, c0, lane);
+      const float2* row = MODE != kRotNone && h.rot ? table_row(h, t0 + r) : nullptr;
+      load_angles<MODE>(hp, h, row, at);
+      norm_rotate8<MODE, T>(x[u], hp, h, a.w_k, row, src + r * in.stride, r < n, at);
     }
   }
 #pragma unroll
@@ -124,7 +127,7 @@ __global__ void __launch_bounds__(256) kv_append_kernel(HeadArgs h, AppendArgs a
   }
   if (tid == 0) *scale = static_cast<uint8_t>(e + 127);
   const float f = exp2i(-e);
-  codes += slot0 * h.d + c0;
+  codes += slot0 * h.d;
 #pragma unroll
   for (int u = 0; u < NP; ++u) {
     const int r = r0 + u * rows;
@@ -132,7 +135,13 @@ __global__ void __launch_bounds__(256) kv_append_kernel(HeadArgs h, AppendArgs a
       uint32_t w[4];
 #pragma unroll
       for (int i = 0; i < 4; ++i) w[i] = to_e4m3x2(x[u][2 * i] * f, x[u][2 * i + 1] * f);
-      *reinterpret_cast<uint2*>(codes + r * h.d) = make_uint2(w[0] | (w[1] << 16), w[2] | (w[3] << 16));
+      const uint2 c = make_uint2(w[0] | (w[1] << 16), w[2] | (w[3] << 16));
+      if (kSplit) {
+        *reinterpret_cast<uint32_t*>(codes + r * h.d + at.a) = c.x;
+        *reinterpret_cast<uint32_t*>(codes + r * h.d + at.b) = c.y;
+      } else {
+        *reinterpret_cast<uint2*>(codes + r * h.d + at.a) = c;
+      }
     }
   }
 }

@@ -4,12 +4,14 @@
 //   y = x / sqrt(mean(x^2) + eps) * w,  (a, b) -> (a c - b s, b c + a s)
 //
 // Memory bound: each row is read and written once (2 d elements), the table
-// row of a token once per warp.  d / 8 neighbouring lanes hold a head row (8
-// elements a lane, so a bf16 row is one 16-byte access a lane), the sum of
-// squares is a shuffle over them, and with the half layout the partner
-// elements come from another lane by shuffle.  A warp keeps one token's
-// angles and weights in registers and takes several of its heads, all loads
-// first.
+// row of a token once per warp.  d / 8 neighbouring lanes hold a head row, 8
+// elements a lane: one 16-byte access, or with the half layout two of 8, so
+// that a lane holds both members of its pairs.  The sum of squares is a
+// shuffle over the row's lanes.  A warp keeps one token's angles and weights in
+// registers and takes its heads, two passes' loads at a time (with four, 80
+// registers leave too few warps: 84 us for the case below).
+// 32768 tokens x (16 + 4) heads of 128, bf16: 344 MB in 74 us, 4.7 TB/s;
+// 9984 x (12 + 4) of 64, fp32: 82 MB in 18.5 us with the launch.
 
 #include "attn.cuh"
 
@@ -24,12 +26,12 @@ __global__ void rope_table_kernel(const double* __restrict__ f, int half, int64_
   out[i] = make_float2(static_cast<float>(c * static_cast<double>(m)), static_cast<float>(s * static_cast<double>(m)));
 }
 
-// A warp takes up to kBatch passes of 256 / d rows of one token, its query
-// rows first and then its key rows.
-constexpr int kBatch = 4;
+// A warp takes passes of 256 / d rows of one token, its query rows first and
+// then its key rows, kBatch passes at a time.
+constexpr int kBatch = 2;
 
 template <typename T, bool VEC, int MODE>
-__global__ void __launch_bounds__(256) qk_norm_rope_kernel(HeadArgs h, int64_t tokens, int Hq, int Hkv, int passes,
+__global__ void __launch_bounds__(256, 4) qk_norm_rope_kernel(HeadArgs h, int64_t tokens, int Hq, int Hkv, int passes,
                                                            RowsIn q, RowsIn k, const float* __restrict__ w_q,
                                                            const float* __restrict__ w_k,
                                                            const int64_t* __restrict__ pos, RowsOut qo, RowsOut ko) {
@@ -37,42 +39,49 @@ __global__ void __launch_bounds__(256) qk_norm_rope_kernel(HeadArgs h, int64_t t
   const int64_t tok = blockIdx.x * static_cast<int64_t>(8) + (threadIdx.x >> 5);
   if (tok >= tokens) return;
   const int ls = 28 - __clz(h.d), rows = 32 >> ls;  // log2 of the lanes of a row, rows of a pass
-  const int c0 = (lane & ((1 << ls) - 1)) * 8;
+  const Pieces at = pieces_of<MODE>(h, lane & ((1 << ls) - 1));
+  constexpr bool kSplit = MODE == kRotHalf;
   const int first = static_cast<int>(blockIdx.y) * passes * rows + (lane >> ls), end = min(static_cast<int>(blockIdx.y + 1) * passes * rows, Hq + Hkv);
   const T* src_q = static_cast<const T*>(q.p) + tok * q.stride;
   const T* src_k = static_cast<const T*>(k.p) + tok * k.stride;
   auto source = [&](int r) { return r < Hq ? src_q + r * h.d : src_k + (r - Hq) * h.d; };
 
-  Raw8<T> raw[kBatch];
-#pragma unroll
-  for (int u = 0; u < kBatch; ++u) {
-    const int r = first + u * rows;
-    if (r < end) raw[u] = load8<VEC>(source(r) + c0);
-  }
   HeadPiece hp;
-  load_angles<MODE>(hp, h, MODE != kRotNone && h.rot ? pos[tok] : 0, c0);
-  load_weights(hp, h, first < Hq ? w_q : w_k, c0);
   bool of_q = first < Hq;  // whose weights hp holds
+  const float2* row = nullptr;
+  for (int p = 0; p < passes; p += kBatch) {
+    Raw8<T> raw[kBatch];
 #pragma unroll
-  for (int u = 0; u < kBatch; ++u) {
-    const int r = first + u * rows;
-    const bool live = r < end;
-    if (live && of_q && r >= Hq) {
-      of_q = false;
-      load_weights(hp, h, w_k, c0);
+    for (int u = 0; u < kBatch; ++u) {
+      const int r = first + (p + u) * rows;
+      if (r < end) raw[u] = load8<VEC, kSplit>(source(r), at);
     }
-    float x[8];
-    if (live) {
-      unpack8(raw[u], x);
-    } else {
+    if (p == 0) {
+      if (MODE != kRotNone && h.rot) row = table_row(h, pos[tok]);
+      load_angles<MODE>(hp, h, row, at);
+      load_weights(hp, h, of_q ? w_q : w_k, at);
+    }
 #pragma unroll
-      for (int i = 0; i < 8; ++i) x[i] = 0.f;
-    }
-    norm_rotate8<MODE, T>(x, hp, h, of_q ? w_q : w_k, live ? source(r) : nullptr, live, c0, lane);
-    if (live) {
-      T* dst = r < Hq ? static_cast<T*>(qo.p) + tok * qo.stride + r * h.d
-                      : static_cast<T*>(ko.p) + tok * ko.stride + (r - Hq) * h.d;
-      store8<VEC>(dst + c0, x);
+    for (int u = 0; u < kBatch; ++u) {
+      const int r = first + (p + u) * rows;
+      const bool live = r < end;
+      if (live && of_q && r >= Hq) {
+        of_q = false;
+        load_weights(hp, h, w_k, at);
+      }
+      float x[8];
+      if (live) {
+        unpack8(raw[u], x);
+      } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) x[i] = 0.f;
+      }
+      norm_rotate8<MODE, T>(x, hp, h, of_q ? w_q : w_k, row, live ? source(r) : nullptr, live, at);
+      if (live) {
+        T* dst = r < Hq ? static_cast<T*>(qo.p) + tok * qo.stride + r * h.d
+                        : static_cast<T*>(ko.p) + tok * ko.stride + (r - Hq) * h.d;
+        store8<VEC, kSplit>(dst, at, x);
+      }
     }
   }
 }
@@ -95,7 +104,9 @@ static int launch_norm(const HeadArgs& h, int64_t tokens, int Hq, int Hkv, RowsI
   if (!k.p) Hkv = 0;
   if (tokens == 0 || Hq + Hkv == 0) return FALCON_OK;
   const bool vec = (!q.p || (q.vec && qo.vec)) && (!k.p || (k.vec && ko.vec));
-  const int all = (Hq + Hkv + 256 / h.d - 1) / (256 / h.d), parts = (all + kBatch - 1) / kBatch;
+  // a warp a token where that fills the card (32768 tokens x 20 heads of 128: 74 us, with three warps a token
+  // 88), else a warp for every kBatch passes
+  const int all = (Hq + Hkv + 256 / h.d - 1) / (256 / h.d), parts = tokens >= 152 * 32 ? 1 : (all + kBatch - 1) / kBatch;
   const int64_t blocks = (tokens + 7) / 8;
   if (blocks > INT32_MAX || parts > 65535) return FALCON_ERR_UNSUPPORTED;
   const dim3 g(static_cast<unsigned>(blocks), static_cast<unsigned>(parts));

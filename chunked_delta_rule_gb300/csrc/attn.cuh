@@ -69,7 +69,7 @@ struct DecodeArgs {
   falcon_kv_cache_t cache;
   void* ws;
 };
-size_t attn_decode_ws_bytes(int B, int Hq, int Hkv, int d, int page, int max_k);
+size_t attn_decode_ws_bytes(int B, int Hq, int Hkv, int d, int elem, int max_k);
 int launch_attn_decode(const DecodeArgs& a, int dtype, cudaStream_t s);
 
 struct PromptArgs {

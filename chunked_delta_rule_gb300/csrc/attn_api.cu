@@ -146,7 +146,7 @@ int falcon_kv_append(const falcon_attn_params_t* p, const void* k, const void* v
 size_t falcon_attn_decode_workspace_size(const falcon_attn_params_t* p) {
   if (check_attn(p) != FALCON_OK || p->B < 1) return 0;
   if (p->page != 16 && p->page != 32 && p->page != 64 && p->page != 128) return 0;
-  return align_up(attn_decode_ws_bytes(p->B, p->Hq, p->Hkv, p->d, p->page, p->max_k), 256);
+  return align_up(attn_decode_ws_bytes(p->B, p->Hq, p->Hkv, p->d, static_cast<int>(esize(p)), p->max_k), 256);
 }
 
 int falcon_attn_decode(const falcon_attn_params_t* p, const void* q, const falcon_kv_cache_t* cache,

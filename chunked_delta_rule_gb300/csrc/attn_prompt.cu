@@ -4,8 +4,8 @@
 //   S = Q K^T,  P = exp(scale S - m),  O += P V
 //
 // Warp-level tf32 MMAs (m16n8k8) with fp32 sums.  An fp32 operand is split into
-// two tf32 parts, x = hi + lo with hi its top 11 bits, and a product taken as
-// hi hi + hi lo + lo hi: about 2^-21 of it is lost.  bf16 inputs are exact in
+// two tf32 parts, hi rounded and lo the rest, and a product taken as hi hi +
+// hi lo + lo hi: about 2^-21 of it is lost at most.  bf16 inputs are exact in
 // tf32; their weights are rounded to 11 bits.  A CTA takes 64 queries of one
 // head, 16 rows a warp; K and V tiles of 64 keys lie in shared memory as fp32,
 // rows padded by 4 words so that no fragment load has a bank conflict.  The
@@ -57,8 +57,8 @@ __device__ __forceinline__ void split(float x, uint32_t (&out)[NP]) {
   if (NP == 1) {
     out[0] = __float_as_uint(x);
   } else {
-    out[0] = __float_as_uint(x) & 0xFFFFE000u;
-    out[NP - 1] = __float_as_uint(x - __uint_as_float(out[0]));
+    out[0] = (__float_as_uint(x) + 0x1000u) & 0xFFFFE000u;  // to nearest; cvt to tf32 has a quarter of the rate
+    out[NP - 1] = __float_as_uint(x - __uint_as_float(out[0]));  // its lowest bits are ignored
   }
 }
 template <int NP>

@@ -46,7 +46,7 @@ template <int D>
 struct Cfg {
   static constexpr int kTiles = D == 64 ? 1 : 2;          // query tiles of a CTA
   static constexpr int kCtas = D == 64 ? 2 : 1;           // CTAs of an SM
-  static constexpr int kSplit = 2;          // softmax threads of a row
+  static constexpr int kSplit = D == 64 ? 1 : 2;          // softmax threads of a row
   static constexpr int kWarps = 4 * kSplit;               // softmax warps of a tile
   static constexpr int kLoadWarp = kWarps * kTiles, kMmaWarp = kLoadWarp + 1;
   static constexpr int kThreads = 32 * kLoadWarp + 128;
@@ -209,7 +209,7 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, Cfg<D>::kCtas)
   // registers: the softmax threads take what the last warpgroup gives up
   // (512 x 104 + 128 x 64 = 640 x 96; 128 x 200 + 128 x 56 = 256 x 128)
   if (warp >= C::kLoadWarp) {
-    if (D == 64) asm volatile("setmaxnreg.dec.sync.aligned.u32 48;");
+    if (D == 64) asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
     else asm volatile("setmaxnreg.dec.sync.aligned.u32 64;");
   }
   if (warp == C::kLoadWarp) {
@@ -322,7 +322,7 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, Cfg<D>::kCtas)
     }
     __syncwarp();
   } else if (warp < C::kLoadWarp) {
-    if (D == 64) asm volatile("setmaxnreg.inc.sync.aligned.u32 96;");
+    if (D == 64) asm volatile("setmaxnreg.inc.sync.aligned.u32 200;");
     else asm volatile("setmaxnreg.inc.sync.aligned.u32 104;");
     constexpr int kHalf = kTile / C::kSplit, kOut = D / C::kSplit;  // scores and output dims of a thread
     // with two threads a row, warps w and w + 4 of a tile take the same rows, the first and the second 64 keys
@@ -463,10 +463,10 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, Cfg<D>::kCtas)
         bool bad = !(l <= 3.402823466e38f);
         // a warp's 32 rows x 64 dims through shared memory (Q's place: every product is done; 16-byte pieces
         // swizzled by row), so that a store covers whole lines
-        uint8_t* stage = sQ + x * C::kTileBytes + half * kOut / 64 * kTile * 128;
-        const int col0 = half * kOut % 64;
+        uint8_t* stage = sQ + x * C::kTileBytes + half * kTile * 128;
 #pragma unroll
-        for (int c = 0; c < kOut / 32; ++c) {
+        for (int c = 0; c < 2; ++c) {
+          uint32_t u[32];
           if (n[x] > 0) {
             tmem_ld32(to + c * 32, u);
             tmem_wait_ld();
@@ -481,16 +481,15 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, Cfg<D>::kCtas)
               bad |= !(fmaxf(fabsf(z0), fabsf(z1)) <= 3.402823466e38f) || z0 != z0 || z1 != z1;
               w[e] = l == 0.f ? 0u : pack_bf16(z0 * inv, z1 * inv);
             }
-            *reinterpret_cast<uint4*>(stage + sw128(r, col0 + c * 32 + i * 8)) = make_uint4(w[0], w[1], w[2], w[3]);
+            *reinterpret_cast<uint4*>(stage + sw128(r, c * 32 + i * 8)) = make_uint4(w[0], w[1], w[2], w[3]);
           }
         }
         __syncwarp();
 #pragma unroll
-        for (int i = 0; i < kOut / 8; ++i) {
-          constexpr int kPieces = kOut / 8;  // lanes of a row
-          const int rr = quad * 32 + i * (32 / kPieces) + lane / kPieces, c = lane % kPieces * 8, grow = row0 + x * kTile + rr;
+        for (int i = 0; i < 8; ++i) {
+          const int rr = quad * 32 + i * 4 + (lane >> 3), c = (lane & 7) * 8, grow = row0 + x * kTile + rr;
           if (grow >= lq) continue;
-          const uint4 w = *reinterpret_cast<const uint4*>(stage + sw128(rr, col0 + c));
+          const uint4 w = *reinterpret_cast<const uint4*>(stage + sw128(rr, c));
           __nv_bfloat16* out = static_cast<__nv_bfloat16*>(a.o.p) + (q0 + grow) * a.o.stride + h * D + half * kOut + c;
           if (a.o.vec) {
             *reinterpret_cast<uint4*>(out) = w;

@@ -404,7 +404,8 @@ int falcon_rope_table(const double* inv_freq, int32_t rot, int32_t rows, float m
  * output may be its own input when their strides agree (in place), and must
  * not overlap an input otherwise.  positions: int64 [tokens], needed with
  * rot > 0, as is table; the rotated dims of a token whose position is not
- * in [0, rope_rows) are NaN. */
+ * in [0, rope_rows) are NaN.  Errors: FALCON_ERR_INVALID_ARG,
+ * FALCON_ERR_UNSUPPORTED, FALCON_ERR_CUDA. */
 int falcon_qk_norm_rope(const falcon_attn_params_t* p, const void* q, const void* k, const float* w_q,
                         const float* w_k, const int64_t* positions, const float* table, void* q_out,
                         void* k_out, void* stream);
@@ -424,7 +425,8 @@ int falcon_qk_norm_rope(const falcon_attn_params_t* p, const void* q, const void
  * to two sequences that append in the same call.  Tokens whose block_table
  * entry is outside [0, num_pages), whose column is past max_pages, or that
  * are past max_q tokens of their sequence are not stored.  Slot 0 of a page
- * that starts within the call never depends on what the page held. */
+ * that starts within the call never depends on what the page held.  Errors:
+ * FALCON_ERR_INVALID_ARG, FALCON_ERR_UNSUPPORTED, FALCON_ERR_CUDA. */
 int falcon_kv_append(const falcon_attn_params_t* p, const void* k, const void* v, const float* w_k,
                      const float* table, const int32_t* cu_new, const int32_t* ctx_lens,
                      const int32_t* block_table, const falcon_kv_cache_t* cache, void* stream);
@@ -438,7 +440,11 @@ size_t falcon_attn_decode_workspace_size(const falcon_attn_params_t* p);
  * lens: int32 [B], at most max_k (and max_pages * page) of them are read;
  * lens[b] <= 0 gives o = 0 and lse = -inf.  Whatever lies in the slots past
  * lens[b] is not used.  Keys of a page whose block_table entry is outside
- * [0, num_pages) are masked.  o [B, Hq, d] with row stride o_stride. */
+ * [0, num_pages) are masked.  o [B, Hq, d] with row stride o_stride.  One
+ * kernel, or two where max_k is larger; waits on copies are bounded and
+ * reported through falcon_workspace_status(workspace, stream).
+ * Errors: FALCON_ERR_INVALID_ARG, FALCON_ERR_UNSUPPORTED (dims, page sizes, a
+ * cache of 2^38 bytes or more), FALCON_ERR_WORKSPACE, FALCON_ERR_CUDA. */
 int falcon_attn_decode(const falcon_attn_params_t* p, const void* q, const falcon_kv_cache_t* cache,
                        const int32_t* block_table, const int32_t* lens, void* o, float* lse,
                        void* workspace, size_t workspace_bytes, void* stream);
@@ -454,7 +460,10 @@ size_t falcon_attn_prompt_workspace_size(const falcon_attn_params_t* p);
  * o_stride, lse fp32 [tokens, Hq] (NULL = not wanted).  Rows of q past max_q
  * of their sequence are not computed.  The bf16 d = 64 and 128 kernel runs
  * its products on the tensor cores with bounded waits, reported through
- * falcon_workspace_status(workspace, stream) as for the chunk forward. */
+ * falcon_workspace_status(workspace, stream) as for the chunk forward; other
+ * types, dims and alignments take a warp-level kernel.  Errors:
+ * FALCON_ERR_INVALID_ARG, FALCON_ERR_UNSUPPORTED, FALCON_ERR_WORKSPACE,
+ * FALCON_ERR_CUDA. */
 int falcon_attn_prompt(const falcon_attn_params_t* p, const void* q, const void* k, const void* v,
                        const int32_t* cu_q, const int32_t* cu_k, void* o, float* lse, void* workspace,
                        size_t workspace_bytes, void* stream);
@@ -475,16 +484,18 @@ int falcon_attn_prompt(const falcon_attn_params_t* p, const void* q, const void*
  * and clears it.  Returns FALCON_OK, FALCON_ERR_TIMEOUT (the outputs and
  * carry of that call are incomplete), FALCON_ERR_WORKSPACE (workspace not
  * 256-byte aligned) or FALCON_ERR_CUDA.  The chunked backward (Falcon-1 /
- * 1A, d = 64) keeps its word in the same place.  Other kernel families have
- * no device-side waits and do not write the word. */
+ * 1A, d = 64) and the softmax-attention operators keep their words in the
+ * same place.  Other kernel families have no device-side waits and do not
+ * write the word. */
 int falcon_workspace_status(const void* workspace, void* stream);
 
 /* Test hook of the failure-detection path (no counterpart on the pages; not
  * for production use).  wait_limit_ns > 0 sets the limit of the bounded
  * device-side waits of the Falcon-1 / 1A, 3 and 3A tensor-core kernels
- * and of the chunked backward launched from now on in this process (0
- * restores 2 s; the Falcon-2 kernel keeps 2 s).  stall != 0 makes the next
- * forward call's per-chunk kernel wait once, before it loads anything, on a barrier
+ * and of the chunked backward and the softmax-attention operators launched
+ * from now on in this process (0 restores 2 s; the Falcon-2 kernel keeps 2 s).
+ * stall != 0 makes the next forward call's per-chunk kernel (or the next
+ * falcon_attn_decode, or tensor-core falcon_attn_prompt) wait once, before it loads anything, on a barrier
  * that nothing completes: that wait runs out after the limit, the timeout is
  * recorded as described at falcon_workspace_status and the call's later
  * kernels skip their work.  No fault, trap or unbounded wait is involved;

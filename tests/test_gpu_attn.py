@@ -337,6 +337,58 @@ def test_cache_past_32_bits(F):
     _check_attention(o, lse, want, want_lse, 5.0, "bf16", 2.0 ** -11)
 
 
+@pytest.mark.parametrize("n,d", [(300, 64), (2000, 128)])
+def test_decode_reports_a_wait_that_ran_out(F, n, d):
+    """A load that is held back: the bounded waits give up, the call says so once, the next one is clean (one CTA a
+    row, and rows in shares)."""
+    bt, cache, q = _decode_case(F, [n, n], 4, 2, d, 64, "bf16", 38)
+    dev, bt, ln = _cuda(cache), torch.from_numpy(bt).cuda(), torch.tensor([n, n], dtype=torch.int32).cuda()
+    good = F.attn_decode(q, dev, bt, ln, n)
+    p = F.AttnParams(B=2, Hq=4, Hkv=2, d=d, dtype=F.FALCON_BF16, max_k=n, page=64, num_pages=dev["k"].shape[0],
+                     max_pages=bt.shape[1])
+    ws = F.alloc_workspace(F.falcon_attn_decode_workspace_size(p))
+    o = torch.zeros_like(q)
+    F.falcon_test_hooks(2_000_000, True)
+    try:
+        F.falcon_attn_decode(p, q, dev, bt, ln, o, None, ws)
+        assert F.falcon_workspace_status(ws) == F.FALCON_ERR_TIMEOUT
+        assert F.falcon_workspace_status(ws) == F.FALCON_OK
+        F.falcon_attn_decode(p, q, dev, bt, ln, o, None, ws)
+        assert F.falcon_workspace_status(ws) == F.FALCON_OK and torch.equal(o, good)
+    finally:
+        F.falcon_test_hooks(0, False)
+
+
+@pytest.mark.parametrize("lens", [[0, 0, 0], [3000, 0, 1, 0, 700], [1] * 300, list(range(0, 4000, 37))])
+def test_decode_shares_of_uneven_lengths(F, lens):
+    """Lengths known on the device only: none at all, most of them empty, one key each, every length in steps."""
+    Hq, Hkv, d, page = 4, 2, 64, 16
+    bt, pages = _paged([max(n, 1) for n in lens], page, 0, 39)
+    cols = -(-4000 // page)
+    bt = np.pad(bt, ((0, 0), (0, cols - bt.shape[1])), constant_values=-1)
+    g = torch.Generator(device="cuda").manual_seed(39)
+    cache = {n: (torch.randn((pages, Hkv, page, d), generator=g, device="cuda") * 100).clamp(-448, 448)
+             .to(torch.float8_e4m3fn).view(torch.uint8) for n in ("k", "v")}
+    cache.update({n + "_scale": torch.randint(118, 122, (pages, Hkv), generator=g, device="cuda").to(torch.uint8)
+                  for n in ("k", "v")})
+    q = _rand((len(lens), Hq, d), "bf16", 39)
+    o, lse = F.attn_decode(q, cache, torch.from_numpy(bt).cuda(), torch.tensor(lens, dtype=torch.int32).cuda(), 4000,
+                           want_lse=True)
+    at = torch.from_numpy(bt).cuda().long().clamp(min=0)
+
+    def keys(n):  # [B, T, Hkv, d] in 64 bits
+        x = cache[n].view(torch.float8_e4m3fn).double() * torch.exp2(cache[n + "_scale"].double() - 127)[..., None, None]
+        return x[at].transpose(2, 3).reshape(len(lens), -1, Hkv, d)
+
+    k, v = keys("k").repeat_interleave(Hq // Hkv, 2), keys("v").repeat_interleave(Hq // Hkv, 2)
+    s = torch.einsum("bhd,bthd->bht", q.double(), k) * d ** -0.5
+    n = torch.tensor(lens).cuda()
+    s.masked_fill_(torch.arange(s.shape[2]).cuda() >= n[:, None, None], -float("inf"))
+    want_lse = torch.logsumexp(s, -1)
+    want = torch.einsum("bht,bthd->bhd", torch.exp(s - torch.where(n[:, None] > 0, want_lse, 0.0)[..., None]), v)
+    _check_attention(o, lse, _np(want), _np(want_lse), 448 * 2.0 ** (121 - 127), "bf16", 2.0 ** -11)
+
+
 # ---------------------------------------------------------------- prompt
 def _prompt_case(lq, lk, Hq, Hkv, d, dtype, seed, fused=0):
     cq, ck = np.concatenate([[0], np.cumsum(lq)]).astype(np.int32), np.concatenate([[0], np.cumsum(lk)]).astype(np.int32)

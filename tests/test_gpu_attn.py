@@ -415,6 +415,20 @@ def test_prompt(F, dtype, lq, lk, Hq, Hkv, d, fused):
     _check_attention(o, lse, want, want_lse, max(1.0, v.abs().max().item() if v.numel() else 1.0), dtype, 1.25 * U)
 
 
+@pytest.mark.parametrize("d", [64, 128])
+def test_prompt_of_more_blocks_than_fit(F, d):
+    """Far more blocks of queries than the GPU holds at a time, some without rows, some without a key."""
+    rng = np.random.default_rng(46)
+    lq = [int(n) for n in rng.integers(0, 400, 40)]
+    lk = [max(0, n + (0, 150, -n, -30, 1)[i % 5]) for i, n in enumerate(lq)]
+    q, k, v, cq, ck = _prompt_case(lq, lk, 12, 4, d, "bf16", 47, 1)
+    o, lse = _prompt(F, q, k, v, cq, ck, 512)
+    want, want_lse = O.prompt(_np(q), _np(k), _np(v), cq, ck, d ** -0.5)
+    _check_attention(o, lse, want, want_lse, max(1.0, v.abs().max().item()), "bf16", 1.25 * U)
+    again, _ = _prompt(F, q, k, v, cq, ck, 512)
+    assert torch.equal(o, again)
+
+
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
 @pytest.mark.parametrize("d", [64, 128])
 def test_prompt_infinities_and_nan_in_masked_places(F, dtype, d):

@@ -80,6 +80,7 @@ __global__ void __launch_bounds__(128) attn_prompt_kernel(PromptArgs a, int qblo
   extern __shared__ float smem[];
   float *sq = smem, *sk = sq + kRows * LD, *sv = sk + kKeys * LD;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, gid = lane >> 2, tig = lane & 3;
+  if (blockIdx.x == 0 && threadIdx.x == 0) *static_cast<uint32_t*>(a.ws) = 0;  // the status: no wait here can run out
   const uint32_t bh = static_cast<uint32_t>(a.B) * a.Hq, at = blockIdx.x % bh;
   const int qb = qblocks - 1 - static_cast<int>(blockIdx.x / bh);  // the longest rows first
   const int b = static_cast<int>(at) / a.Hq, h = static_cast<int>(at) % a.Hq, hk = h / (a.Hq / a.Hkv);

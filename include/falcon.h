@@ -484,9 +484,9 @@ int falcon_attn_prompt(const falcon_attn_params_t* p, const void* q, const void*
  * and clears it.  Returns FALCON_OK, FALCON_ERR_TIMEOUT (the outputs and
  * carry of that call are incomplete), FALCON_ERR_WORKSPACE (workspace not
  * 256-byte aligned) or FALCON_ERR_CUDA.  The chunked backward (Falcon-1 /
- * 1A, d = 64) and the softmax-attention operators keep their words in the
- * same place.  Other kernel families have no device-side waits and do not
- * write the word. */
+ * 1A, d = 64) and falcon_attn_decode / _prompt keep their words in the same
+ * place (a call without rows launches nothing and leaves the word alone).
+ * Other kernel families have no device-side waits and do not write the word. */
 int falcon_workspace_status(const void* workspace, void* stream);
 
 /* Test hook of the failure-detection path (no counterpart on the pages; not

@@ -531,6 +531,18 @@ def test_prompt_reports_a_wait_that_ran_out(F, d):
         F.falcon_test_hooks(0, False)
 
 
+@pytest.mark.parametrize("dtype,n,d", [("f32", 70, 64), ("bf16", 20, 64), ("bf16", 300, 32), ("bf16", 300, 128)])
+def test_prompt_clears_the_status_of_a_new_workspace(F, dtype, n, d):
+    """Whatever the workspace held before: after a call whose waits all came back its status is clean."""
+    q, k, v, cq, ck = _prompt_case([n], [n], 2, 1, d, dtype, 64)
+    cu = torch.from_numpy(cq).cuda()
+    p = F.AttnParams(B=1, Hq=2, Hkv=1, d=d, dtype=F.FALCON_BF16 if dtype == "bf16" else F.FALCON_F32, max_q=n,
+                     tokens=n, k_tokens=n)
+    ws = torch.full((F.falcon_attn_prompt_workspace_size(p),), 1, dtype=torch.uint8, device="cuda")
+    F.falcon_attn_prompt(p, q, k, v, cu, cu, torch.empty_like(q), None, ws)
+    assert F.falcon_workspace_status(ws) == F.FALCON_OK
+
+
 # ---------------------------------------------------------------- streams, repeats, the pieces together
 def test_same_bits_again_and_on_another_stream(F):
     lens = [700, 90]

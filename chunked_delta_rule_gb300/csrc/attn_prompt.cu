@@ -1,5 +1,5 @@
 // Causal attention over packed prompts where the tcgen05 kernel does not go:
-// fp32, head dims 16 and 32, rows off the 16-byte boundaries.
+// fp32, rows off the 16-byte boundaries, a few short prompts.
 //
 //   S = Q K^T,  P = exp(scale S - m),  O += P V
 //

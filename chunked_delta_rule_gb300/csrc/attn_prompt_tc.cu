@@ -1,4 +1,4 @@
-// Causal attention over packed prompts on the tensor cores (bf16, d = 64, 128).
+// Causal attention over packed prompts on the tensor cores (bf16).
 //
 //   S = Q K^T (128 queries x 128 keys),  P = exp(scale S - m),  O += P V
 //
@@ -14,7 +14,8 @@
 //   load warp        TMA: queries, K and V tiles through a ring
 //   a warp a tile    the products (idle warps fill the last warpgroup)
 // TMEM: S0 | S1 (128 columns each, P in their first 64) | O0 | O1 (d each), or
-// S | P | O at d = 64.
+// S | P | O at d = 64.  Rows of 16 and 32 dims run as 64, the rest zeros from the
+// TMA copies: 8 x 2048 x 12 heads of 32 take 64 us, 248 with warp-level tf32 MMAs.
 // The grid has a block for every 256 (128) queries and head, the longest rows
 // first.  At d = 64, where a block is over in 2 to 20 us, a CTA that nears its
 // end asks for one of those that have not begun and goes on with it: the next
@@ -579,6 +580,7 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, Cfg<D>::kCtas)
             named_bar(pair, 64);
             l = *told;
           }
+          const int d = D == 64 ? a.d : D;  // of the rows
           const bool live = row < lq;
           const int64_t g = q0 + row;
           const float inv = l == 0.f ? 0.f : 1.f / l;
@@ -616,9 +618,10 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, Cfg<D>::kCtas)
 #pragma unroll
           for (int i = 0; i < 8; ++i) {
             const int rr = quad * 32 + i * 4 + (lane >> 3), c = (lane & 7) * 8, grow = row0 + x * kTile + rr;
-            if (grow >= lq) continue;
+            if (grow >= lq || (D == 64 && c >= a.d)) continue;
             const uint4 w = *reinterpret_cast<const uint4*>(stage + sw128(rr, c));
-            __nv_bfloat16* out = static_cast<__nv_bfloat16*>(a.o.p) + (q0 + grow) * a.o.stride + h * D + half * kOut + c;
+            __nv_bfloat16* out =
+                static_cast<__nv_bfloat16*>(a.o.p) + (q0 + grow) * a.o.stride + h * d + half * kOut + c;
             if (a.o.vec) {
               *reinterpret_cast<uint4*>(out) = w;
             } else {
@@ -648,14 +651,15 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, Cfg<D>::kCtas)
           for (uint32_t again = __ballot_sync(0xffffffffu, bad); again; again &= again - 1) {
             const int i = row0 + x * kTile + quad * 32 + __ffs(again) - 1;
             const int64_t gi = q0 + i;
-            const __nv_bfloat16* q = static_cast<const __nv_bfloat16*>(a.q.p) + gi * a.q.stride + h * D;
-            const __nv_bfloat16* k = static_cast<const __nv_bfloat16*>(a.k.p) + k0 * a.k.stride + hk * D;
-            const __nv_bfloat16* v = static_cast<const __nv_bfloat16*>(a.v.p) + k0 * a.v.stride + hk * D;
+            const __nv_bfloat16* q = static_cast<const __nv_bfloat16*>(a.q.p) + gi * a.q.stride + h * d;
+            const __nv_bfloat16* k = static_cast<const __nv_bfloat16*>(a.k.p) + k0 * a.k.stride + hk * d;
+            const __nv_bfloat16* v = static_cast<const __nv_bfloat16*>(a.v.p) + k0 * a.v.stride + hk * d;
             float y[4], z;
-            attention_row(q, k, a.k.stride, v, a.v.stride, min(i + off + 1, lk), D, a.scale, y, &z);
-            __nv_bfloat16* oi = static_cast<__nv_bfloat16*>(a.o.p) + gi * a.o.stride + h * D;
+            attention_row(q, k, a.k.stride, v, a.v.stride, min(i + off + 1, lk), d, a.scale, y, &z);
+            __nv_bfloat16* oi = static_cast<__nv_bfloat16*>(a.o.p) + gi * a.o.stride + h * d;
 #pragma unroll
-            for (int e = 0; e < D / 32; ++e) oi[lane + 32 * e] = __float2bfloat16_rn(y[e]);
+            for (int e = 0; e < D / 32; ++e)
+              if (lane + 32 * e < d) oi[lane + 32 * e] = __float2bfloat16_rn(y[e]);
             if (a.lse && lane == 0) a.lse[gi * a.Hq + h] = z;
           }
         } else {
@@ -676,12 +680,12 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, Cfg<D>::kCtas)
   }
 }
 
-// [tokens, H, D] bf16 rows, boxes of 64 columns x 128 tokens
-bool make_rows_map(CUtensorMap* m, const RowsIn& r, int64_t tokens, int H, int D) {
+// [tokens, H, d] bf16 rows, boxes of 64 columns x 128 tokens: zeros past a row's end
+bool make_rows_map(CUtensorMap* m, const RowsIn& r, int64_t tokens, int H, int d) {
   EncodeFn enc = get_encode();
   if (!enc) return false;
-  cuuint64_t dims[3] = {(cuuint64_t)D, (cuuint64_t)H, (cuuint64_t)tokens};
-  cuuint64_t strides[2] = {(cuuint64_t)D * 2, (cuuint64_t)r.stride * 2};
+  cuuint64_t dims[3] = {(cuuint64_t)d, (cuuint64_t)H, (cuuint64_t)tokens};
+  cuuint64_t strides[2] = {(cuuint64_t)d * 2, (cuuint64_t)r.stride * 2};
   cuuint32_t box[3] = {64, 1, kTile};
   cuuint32_t es[3] = {1, 1, 1};
   return enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(r.p), dims, strides, box, es,
@@ -700,8 +704,8 @@ int launch_tc(const PromptArgs& a, cudaStream_t s) {
   const int64_t n = static_cast<int64_t>(t.qblocks) * a.B * a.Hq;
   if (n > INT32_MAX) return FALCON_ERR_UNSUPPORTED;
   CUtensorMap mq, mk, mv;
-  if (!make_rows_map(&mq, a.q, a.tokens, a.Hq, D) || !make_rows_map(&mk, a.k, a.k_tokens, a.Hkv, D) ||
-      !make_rows_map(&mv, a.v, a.k_tokens, a.Hkv, D))
+  if (!make_rows_map(&mq, a.q, a.tokens, a.Hq, a.d) || !make_rows_map(&mk, a.k, a.k_tokens, a.Hkv, a.d) ||
+      !make_rows_map(&mv, a.v, a.k_tokens, a.Hkv, a.d))
     return FALCON_ERR_CUDA;
   const auto kern = attn_prompt_tc_kernel<D>;
   if (!set_smem_limit(reinterpret_cast<const void*>(kern), Cfg<D>::kSmem)) return FALCON_ERR_CUDA;
@@ -711,17 +715,20 @@ int launch_tc(const PromptArgs& a, cudaStream_t s) {
 
 }  // namespace
 
-// The tensor-core kernel takes bf16 rows of 64 or 128 dims on 16-byte
-// boundaries (its TMA copies), with token strides below the maps' 2^40 bytes.
+// The tensor-core kernel takes bf16 rows on 16-byte boundaries (its TMA copies),
+// with token strides below the maps' 2^40 bytes.  A call of a few short prompts
+// is over before its pipeline has filled: 16 tokens x 12 heads of 64 take 8.2 us
+// here and 6.2 on warp MMAs, 64 tokens of 32 dims 8.2 and 7.2, but 64 of 64 dims
+// 8.2 and 8.9, 128 of 32 dims 8.2 and 9.2.
 bool attn_prompt_tc_supported(const PromptArgs& a, int dtype) {
-  if (dtype != FALCON_BF16 || (a.d != 64 && a.d != 128) || a.k_tokens == 0) return false;
+  if (dtype != FALCON_BF16 || a.k_tokens == 0 || (a.d <= 64 && a.k_tokens * a.d <= 2048)) return false;
   if (!a.q.vec || !a.k.vec || !a.v.vec || a.tokens > INT32_MAX || a.k_tokens > INT32_MAX) return false;
   for (int64_t st : {a.q.stride, a.k.stride, a.v.stride})
     if (st * 2 >= (int64_t(1) << 40)) return false;
   return true;
 }
 int launch_attn_prompt_tc(const PromptArgs& a, cudaStream_t s) {
-  return a.d == 64 ? launch_tc<64>(a, s) : launch_tc<128>(a, s);
+  return a.d <= 64 ? launch_tc<64>(a, s) : launch_tc<128>(a, s);
 }
 
 }  // namespace falcon

@@ -458,12 +458,12 @@ size_t falcon_attn_prompt_workspace_size(const falcon_attn_params_t* p);
  * aligned at the end: query i sees the keys j <= i + lk - lq.  A row that
  * sees no key gives o = 0 and lse = -inf.  o [tokens, Hq, d] with row stride
  * o_stride, lse fp32 [tokens, Hq] (NULL = not wanted).  Rows of q past max_q
- * of their sequence are not computed.  The bf16 d = 64 and 128 kernel runs
- * its products on the tensor cores with bounded waits, reported through
- * falcon_workspace_status(workspace, stream) as for the chunk forward; other
- * types, dims and alignments take a warp-level kernel.  Errors:
- * FALCON_ERR_INVALID_ARG, FALCON_ERR_UNSUPPORTED, FALCON_ERR_WORKSPACE,
- * FALCON_ERR_CUDA. */
+ * of their sequence are not computed.  bf16 rows on 16-byte boundaries run
+ * their products on the tensor cores with bounded waits, reported through
+ * falcon_workspace_status(workspace, stream) as for the chunk forward; fp32,
+ * other alignments and calls of a few short prompts take a warp-level kernel.
+ * Errors: FALCON_ERR_INVALID_ARG, FALCON_ERR_UNSUPPORTED,
+ * FALCON_ERR_WORKSPACE, FALCON_ERR_CUDA. */
 int falcon_attn_prompt(const falcon_attn_params_t* p, const void* q, const void* k, const void* v,
                        const int32_t* cu_q, const int32_t* cu_k, void* o, float* lse, void* workspace,
                        size_t workspace_bytes, void* stream);

@@ -415,7 +415,7 @@ def test_prompt(F, dtype, lq, lk, Hq, Hkv, d, fused):
     _check_attention(o, lse, want, want_lse, max(1.0, v.abs().max().item() if v.numel() else 1.0), dtype, 1.25 * U)
 
 
-@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("d", [16, 32, 64, 128])
 def test_prompt_of_more_blocks_than_fit(F, d):
     """Far more blocks of queries than the GPU holds at a time, some without rows, some without a key."""
     rng = np.random.default_rng(46)
@@ -541,6 +541,11 @@ def test_prompt_clears_the_status_of_a_new_workspace(F, dtype, n, d):
     ws = torch.full((F.falcon_attn_prompt_workspace_size(p),), 1, dtype=torch.uint8, device="cuda")
     F.falcon_attn_prompt(p, q, k, v, cu, cu, torch.empty_like(q), None, ws)
     assert F.falcon_workspace_status(ws) == F.FALCON_OK
+
+
+@pytest.mark.parametrize("d", [16, 32])
+def test_prompt_small_dims_infinities_and_nan_in_masked_places(F, d):
+    test_prompt_infinities_and_nan_in_masked_places(F, "bf16", d)
 
 
 # ---------------------------------------------------------------- streams, repeats, the pieces together

@@ -5,7 +5,10 @@
 //
 // Warp-level tf32 MMAs (m16n8k8) with fp32 sums.  An fp32 operand is split into
 // two tf32 parts, hi rounded and lo the rest, and a product taken as hi hi +
-// hi lo + lo hi: about 2^-21 of it is lost at most.  bf16 inputs are exact in
+// hi lo + lo hi: about 2^-21 of it is lost at most.  The tensor cores cut their
+// sums off instead of rounding them, which adds up over many steps: for fp32 the
+// small products of S have sums of their own, and so has P V of every tile (at
+// 2000 keys, d = 64 an error of 5.5e-7; 4.2e-6 without).  bf16 inputs are exact in
 // tf32; their weights are rounded to 11 bits.  A CTA takes 64 queries of one
 // head, 16 rows a warp; K and V tiles of 64 keys lie in shared memory as fp32,
 // rows padded by 4 words so that no fragment load has a bank conflict.  The
@@ -14,7 +17,8 @@
 //
 // Bound by the chain of a row block: products of three parts, the splits, the
 // softmax, tile after tile.  Measured: 7 prompts of <= 333, 12 / 4 heads of 64,
-// fp32: 37 us with the call; 8 x 1024 x 12 x 64, fp32: 233 us.
+// fp32: 37 us with the call; 8 x 1024 x 12 x 64, fp32: 274 us (233 without the sums
+// apart).
 //
 // Keys that no row of the tile sees are not touched, tile rows past the last key
 // are zeros.  A row whose result is not finite (a masked key of its own
@@ -106,11 +110,11 @@ __global__ void __launch_bounds__(128) attn_prompt_kernel(PromptArgs a, int qblo
     stage_rows<T, D>(sk, k, a.k.stride, a.k.vec, j0, lk);
     stage_rows<T, D>(sv, v, a.v.stride, a.v.vec, j0, lk);
     __syncthreads();
-    float s[NT][4];
+    float s[NT][4], low[NT][4];  // fp32: the small products apart
 #pragma unroll
     for (int t = 0; t < NT; ++t)
 #pragma unroll
-      for (int e = 0; e < 4; ++e) s[t][e] = 0.f;
+      for (int e = 0; e < 4; ++e) s[t][e] = low[t][e] = 0.f;
 #pragma unroll 2
     for (int ks = 0; ks < D / 8; ++ks) {
       uint32_t af[NP][4];
@@ -134,8 +138,18 @@ __global__ void __launch_bounds__(128) attn_prompt_kernel(PromptArgs a, int qblo
 #pragma unroll
           for (int p = 0; p < NP; ++p) bf[p][e] = w[p];
         }
-        product<NP>(s[t], af, bf);
+        tc::mma_tf32_16x8x8(s[t], af[0], bf[0]);
+        if (NP == 2) {
+          tc::mma_tf32_16x8x8(low[t], af[0], bf[NP - 1]);
+          tc::mma_tf32_16x8x8(low[t], af[NP - 1], bf[0]);
+        }
       }
+    }
+    if (NP == 2) {
+#pragma unroll
+      for (int t = 0; t < NT; ++t)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) s[t][e] += low[t][e];
     }
     // columns 2 tig and 2 tig + 1 of each group of 8 keys
     const int lim0 = min(row0 + r0 + off + 1, lk) - j0, lim1 = min(row0 + r0 + 8 + off + 1, lk) - j0;
@@ -173,6 +187,12 @@ __global__ void __launch_bounds__(128) attn_prompt_kernel(PromptArgs a, int qblo
 #pragma unroll
       for (int t = 0; t < D / 8; ++t) o[t][2 * i] *= f, o[t][2 * i + 1] *= f;
     }
+    // fp32: a tile's products in sums of their own
+    float part[D / 8][4];
+#pragma unroll
+    for (int i = 0; i < D / 8; ++i)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) part[i][e] = 0.f;
 #pragma unroll
     for (int t = 0; t < NT; ++t) {
       uint32_t pf[NP][4];
@@ -195,8 +215,14 @@ __global__ void __launch_bounds__(128) attn_prompt_kernel(PromptArgs a, int qblo
 #pragma unroll
           for (int p = 0; p < NP; ++p) bf[p][e] = w[p];
         }
-        product<NP>(o[i], pf, bf);
+        product<NP>(NP == 2 ? part[i] : o[i], pf, bf);
       }
+    }
+    if (NP == 2) {
+#pragma unroll
+      for (int i = 0; i < D / 8; ++i)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) o[i][e] += part[i][e];
     }
   }
 

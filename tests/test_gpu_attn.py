@@ -531,6 +531,19 @@ def test_prompt_reports_a_wait_that_ran_out(F, d):
         F.falcon_test_hooks(0, False)
 
 
+@pytest.mark.parametrize("d", [16, 64, 128])
+def test_prompt_fp32_error_does_not_grow_with_the_keys(F, d):
+    """The tensor cores cut sums off: 2^-24 of a sum a step in the mean.  A score has d / 8 steps, a tile's weighted
+    values 8 steps of three products: 2^-24 (16 + 24) at most, also at 2000 keys."""
+    n, H = 2000, 3
+    q, k, v, cq, ck = _prompt_case([n], [n], H, H, d, "f32", 65)
+    o, _ = _prompt(F, q, k, v, cq, ck)
+    s = torch.einsum("ihd,jhd->hij", q.double(), k.double()) * d ** -0.5
+    s.masked_fill_(torch.ones((n, n), dtype=torch.bool, device="cuda").triu(1), -float("inf"))
+    want = torch.einsum("hij,jhd->ihd", s.softmax(-1), v.double())
+    assert ((o.double() - want).norm() / want.norm()).item() < 40 * 2.0 ** -24
+
+
 @pytest.mark.parametrize("dtype,n,d", [("f32", 70, 64), ("bf16", 20, 64), ("bf16", 300, 32), ("bf16", 300, 128)])
 def test_prompt_clears_the_status_of_a_new_workspace(F, dtype, n, d):
     """Whatever the workspace held before: after a call whose waits all came back its status is clean."""

@@ -22,9 +22,11 @@
 // Queries are scaled by a power of two for each head to at most 2 in
 // magnitude before they become halves: bf16 queries are then exact, up to
 // elements 2^-22 below the largest.  fp32 queries and weights are split in two
-// halves each.  Weights p = 2^(s - m) carry the page's V scale relative to
-// the largest one seen, 2^(ev - E); the running reference m moves only when a
-// score passes it by more than 8, so most tiles need no exchange between lanes.
+// halves each, and every tile's products have sums of their own: the tensor cores
+// cut theirs off, which adds up over the keys.  Weights p = 2^(s - m) carry the
+// page's V scale relative to the largest one seen, 2^(ev - E); the running
+// reference m moves only when a score passes it by more than 8, so most tiles need
+// no exchange between lanes.
 //
 // Every CTA gets the same number of keys (the lengths are known on the device
 // only); a second kernel joins the rows that several CTAs share.
@@ -489,8 +491,15 @@ __global__ void __launch_bounds__((kWarps + 1) * 32, ctas_of_sm(sizeof(T), D))
           const uint32_t lo = __byte_perm(v[0][j / 2], v[1][j / 2], sel), hi = __byte_perm(v[2][j / 2], v[3][j / 2], sel);
           const uint32_t a0 = e4m3x2_to_half2(lo & 0xFFFFu), a1 = e4m3x2_to_half2(lo >> 16);
           const uint32_t a2 = e4m3x2_to_half2(hi & 0xFFFFu), a3 = e4m3x2_to_half2(hi >> 16);
+          if (NP == 1) {
+            mma_f16(o[j], a0, a1, a2, a3, pb[0][0], pb[0][1]);
+          } else {  // added rounded
+            float part[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-          for (int x = 0; x < NP; ++x) mma_f16(o[j], a0, a1, a2, a3, pb[x][0], pb[x][1]);
+            for (int x = 0; x < NP; ++x) mma_f16(part, a0, a1, a2, a3, pb[x][0], pb[x][1]);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) o[j][e] += part[e];
+          }
         }
       }
       __syncwarp();

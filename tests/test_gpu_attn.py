@@ -286,6 +286,27 @@ def test_decode(F, dtype, lens, Hq, Hkv, d, page):
     _check_attention(o, lse, want, want_lse, 448 * 2.0 ** (121 - 127), dtype, 2.0 ** -11)
 
 
+@pytest.mark.parametrize("d,B,n", [(16, 96, 12800), (128, 48, 6400)])
+def test_decode_fp32_error_does_not_grow_with_the_keys(F, d, B, n):
+    """The tensor cores cut sums off: 2^-24 of a sum a step in the mean.  A score has d / 16 steps of two products, a
+    tile's weighted values two; queries and weights in two halves lose 2^-22 each, and as much is left for the rest:
+    2^-24 (d / 8 + 12), however many keys a warp sums over."""
+    Hq, Hkv, page = 6, 2, 128
+    g = torch.Generator().manual_seed(33)
+    k, v = ((torch.randn((B * n // page, Hkv, page, d), generator=g) * 100).clamp(-448, 448).to(torch.float8_e4m3fn).cuda()
+            for _ in "kv")
+    scale = torch.full((B * n // page, Hkv), 120, dtype=torch.uint8, device="cuda")
+    q = _rand((B, Hq, d), "f32", 34)
+    cache = {"k": k.view(torch.uint8), "v": v.view(torch.uint8), "k_scale": scale, "v_scale": scale.clone()}
+    table = torch.arange(B * n // page, dtype=torch.int32, device="cuda").view(B, -1)
+    o, _ = F.attn_decode(q, cache, table, torch.full((B,), n, dtype=torch.int32, device="cuda"), n, want_lse=True)
+    # [B, Hkv, n, d] and, for a key head's queries, [B, Hkv, Hq / Hkv, d]
+    kd, vd = (x.double().view(B, n // page, Hkv, page, d).transpose(1, 2).reshape(B, Hkv, n, d) / 128 for x in (k, v))
+    w = (q.double().view(B, Hkv, -1, d) @ kd.transpose(2, 3) * d ** -0.5).softmax(-1)
+    want = (w @ vd).view(B, Hq, d)
+    assert ((o.double() - want).norm() / want.norm()).item() < (d / 8 + 12) * 2.0 ** -24
+
+
 def test_decode_strides_scale_and_bounds(F):
     """q a slice of a wider projection, o inside wider rows, a scale of its own, lengths past max_len, a page that
     does not exist, no lse, a workspace of garbage."""

@@ -73,7 +73,7 @@ size_t attn_decode_ws_bytes(int B, int Hq, int Hkv, int d, int elem, int max_k);
 int launch_attn_decode(const DecodeArgs& a, int dtype, cudaStream_t s);
 
 struct PromptArgs {
-  int B, Hq, Hkv, d, max_q, max_k;
+  int B, Hq, Hkv, d, max_q;
   float scale;
   int64_t tokens, k_tokens;
   RowsIn q, k, v;

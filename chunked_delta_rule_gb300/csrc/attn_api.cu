@@ -1,6 +1,7 @@
 // C ABI of the softmax-attention operators: argument checks on the host and
 // dispatch to the kernels.  Nothing here allocates device memory.
 
+#include <algorithm>
 #include <cmath>
 #include <cstdint>
 
@@ -11,6 +12,10 @@ using namespace falcon;
 namespace {
 
 size_t esize(const falcon_attn_params_t* p) { return p->dtype == FALCON_BF16 ? 2 : 4; }
+
+// Rows of a sequence: the kernels' 32-bit row and key numbers, rounded up to
+// whole tiles, have to stay below 2^31.
+constexpr int64_t kMostRows = INT32_MAX - 1024;
 
 bool misaligned(const void* x, size_t n) { return (reinterpret_cast<uintptr_t>(x) & (n - 1)) != 0; }
 
@@ -45,6 +50,8 @@ int check_attn(const falcon_attn_params_t* p) {
   if (p->Hq < 1 || p->Hkv < 1 || p->Hq % p->Hkv) return FALCON_ERR_INVALID_ARG;
   if (p->dtype != FALCON_BF16 && p->dtype != FALCON_F32) return FALCON_ERR_INVALID_ARG;
   if (p->d != 16 && p->d != 32 && p->d != 64 && p->d != 128) return FALCON_ERR_UNSUPPORTED;
+  // offsets within a token are 32-bit
+  if ((static_cast<int64_t>(p->Hq) + p->Hkv) * p->d > INT32_MAX) return FALCON_ERR_UNSUPPORTED;
   if (p->tokens < 0 || p->k_tokens < 0 || p->max_q < 0 || p->max_k < 0) return FALCON_ERR_INVALID_ARG;
   if (!stride_ok(p->q_stride, p->Hq, p->d) || !stride_ok(p->k_stride, p->Hkv, p->d) ||
       !stride_ok(p->v_stride, p->Hkv, p->d) || !stride_ok(p->o_stride, p->Hq, p->d))
@@ -53,6 +60,12 @@ int check_attn(const falcon_attn_params_t* p) {
 }
 int check_scale(const falcon_attn_params_t* p) {
   return std::isfinite(p->scale) && p->scale >= 0.f ? FALCON_OK : FALCON_ERR_INVALID_ARG;
+}
+// most rows that one sequence brings: no more than the call has
+int64_t most_rows(const falcon_attn_params_t* p) { return std::min<int64_t>(p->max_q, p->tokens); }
+// most keys that one sequence has in the cache
+int64_t most_keys(const falcon_attn_params_t* p) {
+  return std::min<int64_t>(p->max_k, static_cast<int64_t>(p->max_pages) * p->page);
 }
 float scale_of(const falcon_attn_params_t* p) {
   return p->scale > 0.f ? p->scale : 1.f / std::sqrt(static_cast<float>(p->d));
@@ -122,6 +135,7 @@ int falcon_kv_append(const falcon_attn_params_t* p, const void* k, const void* v
   if (st == FALCON_OK) st = check_cache(p, cache, block_table);
   if (st != FALCON_OK) return st;
   if (p->tokens == 0 || p->max_q == 0 || p->max_pages == 0) return FALCON_OK;
+  if (most_rows(p) > kMostRows) return FALCON_ERR_UNSUPPORTED;
   if (!k || !v || !cu_new || !ctx_lens) return FALCON_ERR_INVALID_ARG;
   if (misaligned(k, esize(p)) || misaligned(v, esize(p)) || misaligned(cu_new, 4) || misaligned(ctx_lens, 4))
     return FALCON_ERR_INVALID_ARG;
@@ -137,7 +151,7 @@ int falcon_kv_append(const falcon_attn_params_t* p, const void* k, const void* v
     for (int j = i + 1; j < 4; ++j)
       if (overlap(outs[i], nout[i], outs[j], nout[j])) return FALCON_ERR_INVALID_ARG;
   }
-  const AppendArgs a{p->B, p->Hkv, p->page, p->num_pages, p->max_pages, p->max_q, p->tokens,
+  const AppendArgs a{p->B, p->Hkv, p->page, p->num_pages, p->max_pages, static_cast<int>(most_rows(p)), p->tokens,
                      rows_in(p, k, p->k_stride, p->Hkv), rows_in(p, v, p->v_stride, p->Hkv), w_k, cu_new, ctx_lens,
                      block_table, *cache};
   return launch_kv_append(head_args(p, table, nullptr, w_k), p->dtype, a, reinterpret_cast<cudaStream_t>(stream));
@@ -156,6 +170,8 @@ int falcon_attn_decode(const falcon_attn_params_t* p, const void* q, const falco
   if (st == FALCON_OK) st = check_scale(p);
   if (st == FALCON_OK) st = check_cache(p, cache, block_table);
   if (st != FALCON_OK) return st;
+  // the kernel counts the batch's units of at least 64 keys in 32 bits too
+  if (most_keys(p) > kMostRows || p->B * ((most_keys(p) + 63) / 64) > INT32_MAX) return FALCON_ERR_UNSUPPORTED;
   if (!q || !o || !lens || misaligned(q, esize(p)) || misaligned(o, esize(p)) || misaligned(lens, 4) ||
       misaligned(lse, 4))
     return FALCON_ERR_INVALID_ARG;
@@ -182,6 +198,7 @@ int falcon_attn_prompt(const falcon_attn_params_t* p, const void* q, const void*
   if (st != FALCON_OK) return st;
   if (p->B < 1) return FALCON_ERR_INVALID_ARG;
   if (p->tokens == 0 || p->max_q == 0) return FALCON_OK;
+  if (most_rows(p) > kMostRows || p->k_tokens > kMostRows) return FALCON_ERR_UNSUPPORTED;
   if (!q || !o || !cu_q || !cu_k || (p->k_tokens > 0 && (!k || !v))) return FALCON_ERR_INVALID_ARG;
   for (const void* x : {q, k, v, static_cast<const void*>(o)})
     if (misaligned(x, esize(p))) return FALCON_ERR_INVALID_ARG;
@@ -195,7 +212,7 @@ int falcon_attn_prompt(const falcon_attn_params_t* p, const void* q, const void*
   if (overlap(o, no, lse, nl)) return FALCON_ERR_INVALID_ARG;
   if (!workspace || workspace_bytes < falcon_attn_prompt_workspace_size(p) || misaligned(workspace, 256))
     return FALCON_ERR_WORKSPACE;
-  const PromptArgs a{p->B, p->Hq, p->Hkv, p->d, p->max_q, p->max_k, scale_of(p), p->tokens, p->k_tokens,
+  const PromptArgs a{p->B, p->Hq, p->Hkv, p->d, static_cast<int>(most_rows(p)), scale_of(p), p->tokens, p->k_tokens,
                      rows_in(p, q, p->q_stride, p->Hq), rows_in(p, k, p->k_stride, p->Hkv),
                      rows_in(p, v, p->v_stride, p->Hkv), rows_out(p, o, p->o_stride, p->Hq), lse, cu_q, cu_k,
                      workspace};

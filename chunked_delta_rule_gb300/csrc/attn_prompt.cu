@@ -266,13 +266,13 @@ __global__ void __launch_bounds__(128) attn_prompt_kernel(PromptArgs a, int qblo
 
 template <typename T, int D>
 int launch(const PromptArgs& a, cudaStream_t s) {
-  const int qblocks = (a.max_q + kRows - 1) / kRows;
-  const int64_t n = static_cast<int64_t>(qblocks) * a.B * a.Hq;
-  if (n > INT32_MAX) return FALCON_ERR_UNSUPPORTED;
+  const int64_t qblocks = (static_cast<int64_t>(a.max_q) + kRows - 1) / kRows;
+  const int64_t heads = static_cast<int64_t>(a.B) * a.Hq, n = qblocks * heads;
+  if (heads > INT32_MAX || n < 1 || n > INT32_MAX) return FALCON_ERR_UNSUPPORTED;
   constexpr size_t smem = static_cast<size_t>(kRows + 2 * kKeys) * (D + 4) * 4;
   const auto kern = attn_prompt_kernel<T, D>;
   if (!set_smem_limit(reinterpret_cast<const void*>(kern), smem)) return FALCON_ERR_CUDA;
-  kern<<<static_cast<unsigned>(n), 128, smem, s>>>(a, qblocks);
+  kern<<<static_cast<unsigned>(n), 128, smem, s>>>(a, static_cast<int>(qblocks));
   return cudaGetLastError() == cudaSuccess ? FALCON_OK : FALCON_ERR_CUDA;
 }
 template <typename T>

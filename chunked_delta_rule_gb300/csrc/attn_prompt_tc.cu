@@ -697,12 +697,13 @@ template <int D>
 int launch_tc(const PromptArgs& a, cudaStream_t s) {
   TcArgs t;
   t.a = a;
-  t.qblocks = (a.max_q + Cfg<D>::kTiles * kTile - 1) / (Cfg<D>::kTiles * kTile);
+  constexpr int64_t rows = Cfg<D>::kTiles * kTile;  // of a block
+  t.qblocks = static_cast<int>((a.max_q + rows - 1) / rows);
   t.status = static_cast<uint32_t*>(a.ws);
   t.limit = wait_limit_ns();
   t.stall = take_test_stall() ? 1 : 0;
-  const int64_t n = static_cast<int64_t>(t.qblocks) * a.B * a.Hq;
-  if (n > INT32_MAX) return FALCON_ERR_UNSUPPORTED;
+  const int64_t heads = static_cast<int64_t>(a.B) * a.Hq, n = t.qblocks * heads;
+  if (heads > INT32_MAX || n < 1 || n > INT32_MAX) return FALCON_ERR_UNSUPPORTED;
   CUtensorMap mq, mk, mv;
   if (!make_rows_map(&mq, a.q, a.tokens, a.Hq, a.d) || !make_rows_map(&mk, a.k, a.k_tokens, a.Hkv, a.d) ||
       !make_rows_map(&mv, a.v, a.k_tokens, a.Hkv, a.d))

@@ -351,7 +351,9 @@ int falcon_backward(const falcon_params_t* p, const void* q, const void* k, cons
  * tokens of all sequences packed one after the other, heads and dims dense,
  * q_stride / k_stride / v_stride / o_stride elements from one token to the
  * next (0 = dense; larger for slices of a fused projection).  Query head h
- * reads key / value head h / (Hq / Hkv). */
+ * reads key / value head h / (Hq / Hkv).  FALCON_ERR_UNSUPPORTED past 2^31 - 1024
+ * rows or keys of one sequence, k_tokens above that, or (Hq + Hkv) d above
+ * 2^31 - 1; for attn_decode also past 2^31 units of 64 keys in the batch. */
 
 /* Which dims of a head form the rotated pairs: HALF (i, i + rot/2),
  * INTERLEAVED (2i, 2i + 1), i < rot/2. */
@@ -369,8 +371,8 @@ typedef struct {
   int32_t page;         /* tokens per cache page: 16, 32, 64 or 128 */
   int32_t num_pages;    /* pages in the cache */
   int32_t max_pages;    /* columns of block_table */
-  int32_t max_q;        /* no sequence brings more tokens than this to the call */
-  int32_t max_k;        /* no sequence has more keys than this (attn_decode) */
+  int32_t max_q;        /* no sequence brings more tokens than this to the call; any larger bound will do */
+  int32_t max_k;        /* no sequence has more keys than this (attn_decode); any larger bound will do */
   float norm_eps;       /* > 0 where qk_norm is set */
   float scale;          /* of the scores; 0 = 1 / sqrt(d) */
   int64_t tokens;       /* rows of q (qk_norm_rope, attn_prompt) or of the new k, v (kv_append) */

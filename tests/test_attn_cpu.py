@@ -167,6 +167,31 @@ def test_attention_workspace_scale_and_overlap(F):
     _refused(F, -1, F.falcon_attn_prompt, p, X[0], None, X[2], X[3], X[4], X[5], None, X[9], 256, 0)
 
 
+FAR = [(i + 1) << 46 for i in range(10)]
+
+
+@pytest.mark.parametrize("n", [2**31 - 1, 2**31 - 1023, 2**33])
+def test_sequences_past_32_bits(F, n):
+    """Rows and keys are numbered in 32 bits, whole tiles of them: longer sequences are refused, also where the bound is
+    2^31 - 1 and the tokens say the rest."""
+    cache = dict(zip(("k", "v", "k_scale", "v_scale"), FAR[4:8]))
+    p = _p(F, tokens=n, k_tokens=10, max_q=2**31 - 1)
+    _refused(F, -2, F.falcon_attn_prompt, p, FAR[0], FAR[1], FAR[2], FAR[3], FAR[8], FAR[5], None, FAR[9], 256, 0)
+    _refused(F, -2, F.falcon_kv_append, p, FAR[0], FAR[1], None, None, FAR[2], FAR[3], FAR[8], cache, 0)
+    p = _p(F, tokens=10, k_tokens=n)
+    _refused(F, -2, F.falcon_attn_prompt, p, FAR[0], FAR[1], FAR[2], FAR[3], FAR[8], FAR[5], None, FAR[9], 256, 0)
+    for kw in (dict(max_k=2**31 - 1, max_pages=2**25), dict(B=1 << 22, max_k=2**31 - 1, max_pages=1 << 10)):
+        p = _p(F, **kw)
+        _refused(F, -2, F.falcon_attn_decode, p, FAR[0], cache, FAR[8], FAR[1], FAR[2], None, FAR[9], 1 << 40, 0)
+
+
+def test_heads_past_32_bits(F):
+    p, cache = _p(F, Hq=1 << 25, Hkv=1 << 25), dict(zip(("k", "v", "k_scale", "v_scale"), FAR[4:8]))
+    _refused(F, -2, F.falcon_qk_norm_rope, p, FAR[0], FAR[1], None, None, None, None, FAR[2], FAR[3], 0)
+    _refused(F, -2, F.falcon_attn_prompt, p, FAR[0], FAR[1], FAR[2], FAR[3], FAR[8], FAR[5], None, FAR[9], 256, 0)
+    _refused(F, -2, F.falcon_attn_decode, p, FAR[0], cache, FAR[8], FAR[1], FAR[2], None, FAR[9], 1 << 40, 0)
+
+
 def test_empty_calls_do_nothing(F):
     """No tokens: accepted without a pointer, nothing is enqueued."""
     p, cache = _p(F, tokens=0), dict(zip(("k", "v", "k_scale", "v_scale"), X[4:8]))

@@ -582,6 +582,39 @@ def test_prompt_small_dims_infinities_and_nan_in_masked_places(F, d):
     test_prompt_infinities_and_nan_in_masked_places(F, "bf16", d)
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("Hq,d", [(64, 64), (64, 128), (16, 32)])
+def test_no_bound_on_the_rows_of_a_sequence(F, dtype, Hq, d):
+    """max_q is an upper bound, 2^31 - 1 none at all: the same bits as with the longest length (192 sequence-heads
+    times the tiles of 2^31 rows is a number that wraps to a grid)."""
+    lq = [3, 130, 70]
+    q, k, v, cq, ck = _prompt_case(lq, lq, Hq, 2, d, dtype, 66)
+    o, lse = _prompt(F, q, k, v, cq, ck, max(lq))
+    for bound in (2**31 - 1, 2**31 - 64, 1 << 20, 203):
+        o2, lse2 = _prompt(F, q, k, v, cq, ck, bound)
+        assert torch.equal(o, o2) and torch.equal(lse, lse2)
+
+
+def test_no_bound_on_the_tokens_appended(F):
+    lens, B = [3, 40, 17] * 6, 18
+    cu = torch.from_numpy(np.concatenate([[0], np.cumsum(lens)]).astype(np.int32)).cuda()
+    bt, pages = _paged(lens, 16, 0, 67)
+    bt, ctx = torch.from_numpy(bt).cuda(), torch.zeros(B, dtype=torch.int32).cuda()
+    k, v = (_rand((sum(lens), 2, 64), "bf16", 68 + i) for i in range(2))
+    caches = [F.empty_kv_cache(pages, 2, 16, 64) for _ in range(2)]
+    for cache, bound in zip(caches, (40, 2**31 - 1)):
+        F.kv_append(cache, k, v, cu, ctx, bt, bound)
+    assert all(torch.equal(caches[0][n], caches[1][n]) for n in caches[0])
+
+
+def test_no_bound_on_the_keys(F):
+    lens = [700, 90]
+    bt, cache, q = _decode_case(F, lens, 8, 2, 64, 64, "bf16", 69)
+    dev, bt, ln = _cuda(cache), torch.from_numpy(bt).cuda(), torch.tensor(lens, dtype=torch.int32).cuda()
+    got = [F.attn_decode(q, dev, bt, ln, n, want_lse=True) for n in (11 * 64, 2**31 - 1)]
+    assert all(torch.equal(a, b) for a, b in zip(*got))
+
+
 # ---------------------------------------------------------------- streams, repeats, the pieces together
 def test_same_bits_again_and_on_another_stream(F):
     lens = [700, 90]

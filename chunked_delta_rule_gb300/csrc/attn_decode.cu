@@ -20,19 +20,24 @@
 //   V: the keys of two columns of the weights (lane % 4), the lane group's eighth
 //      of the head dim; pairs of keys are interleaved with byte permutes
 // Queries are scaled by a power of two for each head to at most 2 in
-// magnitude before they become halves: bf16 queries are then exact, up to
-// elements 2^-22 below the largest.  fp32 queries and weights are split in two
-// halves each, and every tile's products have sums of their own: the tensor cores
-// cut theirs off, which adds up over the keys.  Weights p = 2^(s - m) carry the
-// page's V scale relative to the largest one seen, 2^(ev - E); the running
-// reference m moves only when a score passes it by more than 8, so most tiles need
-// no exchange between lanes.
+// magnitude before they become halves: bf16 elements are then exact down to
+// 2^-17 of the head's largest, below that off by 2^-25 of it at most.  fp32
+// queries and weights are split in two halves each: 2^-22.
+// Weights p = 2^(s - m) become halves (11 bits) relative to the largest one of
+// their tile and head, a power of two found with three shuffles, and the tile's
+// products are added to the fp32 sums times that power and the page's V scale: no
+// weight and no V scale is lost to another tile's.  (Halves relative to what the warp
+// had met before would drop weights under 2^-31 of the largest, or values beside a
+// page of a larger scale; they took 66 and 39 us where these take 69 and 41.)  Sums of their own for every tile are also what keeps fp32
+// results: the tensor cores cut their sums off, which adds up over the keys.  The
+// running reference m moves only when a score passes it by more than 8.
 //
 // Every CTA gets the same number of keys (the lengths are known on the device
 // only); a second kernel joins the rows that several CTAs share.
 // Measured: 256 sequences of 410 .. 2048 keys, 16 / 4 heads of 128: 325 MB of
-// codes in 66 us, 4.9 TB/s (about 4 us a row and CTA around the stream); 2 of
-// <= 131072 keys, 16 / 2 heads of 128: 39 us; 1 x 777 keys: 10.2 us, the call.
+// codes in 69 us, 4.7 TB/s (about 4 us a row and CTA around the stream; fp32: 84 us);
+// 2 of <= 131072 keys, 16 / 2 heads of 128: 41 us (fp32: 43); 1 x 777 keys: 10.2 us,
+// the call.
 // Waits are bounded and reported through the workspace's status word.
 
 #include "attn.cuh"
@@ -42,8 +47,8 @@ namespace falcon {
 namespace {
 
 constexpr int kWarps = 4;           // consumers
-constexpr float kSlack = 8.f;       // scores may pass the reference by 2^8 ...
-constexpr int kHeadroom = 6;        // ... and weights are kept 2^6 up: 2^14 < 65504
+constexpr float kSlack = 8.f;       // scores (log2) may pass the reference by this
+constexpr int kTop = 14;            // a tile's largest weight for a head lies in [2^14, 2^15) as a half (< 65504)
 
 template <int D>
 struct Tile {
@@ -380,7 +385,6 @@ __global__ void __launch_bounds__((kWarps + 1) * 32, ctas_of_sm(sizeof(T), D))
     for (int j = 0; j < KS; ++j)
 #pragma unroll
       for (int i = 0; i < 4; ++i) o[j][i] = 0.f;
-    int E = -1000;  // largest V exponent so far
 
     for (int u = off; u < off + count; ++u) {
       ok = ok && __all_sync(0xffffffffu, wait(&full[stage], phase)) != 0;
@@ -390,13 +394,12 @@ __global__ void __launch_bounds__((kWarps + 1) * 32, ctas_of_sm(sizeof(T), D))
       uint32_t bytes[L::kSub];
       int have[L::kSub];
       bool past = false;
-      int evmax = E;
 #pragma unroll
       for (int sub = 0; sub < L::kSub; ++sub) {
         const int t = u * L::kKeys + (warp * L::kSub + sub) * 16;
         bytes[sub] = scales[stage * L::kSub * kWarps + warp * L::kSub + sub];
         have[sub] = ok && !(bytes[sub] & 0x10000u) ? keys - t : 0;  // keys of the tile that exist
-        if (have[sub] <= 0) bytes[sub] = 0;                         // weights 0, the smallest V scale
+        if (have[sub] <= 0) bytes[sub] = 0;                         // weights 0, the smallest scales
         const uint32_t src = src0 + sub * 2 * L::kBytes;
         float s[2][4];
 #pragma unroll
@@ -424,7 +427,6 @@ __global__ void __launch_bounds__((kWarps + 1) * 32, ctas_of_sm(sizeof(T), D))
           sc[sub][2 + i] = in1 ? (s[0][2 + i] + s[1][2 + i]) * f : -INFINITY;
           past |= fmaxf(sc[sub][i], sc[sub][2 + i]) > m[i] + kSlack;
         }
-        evmax = max(evmax, static_cast<int>(bytes[sub] >> 8) - 127);
       }
       if (__any_sync(0xffffffffu, past)) {  // move the reference to the maximum
 #pragma unroll
@@ -442,17 +444,8 @@ __global__ void __launch_bounds__((kWarps + 1) * 32, ctas_of_sm(sizeof(T), D))
           for (int j = 0; j < KS; ++j) o[j][i] *= f, o[j][2 + i] *= f;
         }
       }
-      if (evmax > E) {  // sums so far in units of the new, larger V scale
-        const float f = exp2i(max(E - evmax, -149));
-        E = evmax;
-#pragma unroll
-        for (int j = 0; j < KS; ++j)
-#pragma unroll
-          for (int i = 0; i < 4; ++i) o[j][i] *= f;
-      }
 #pragma unroll
       for (int sub = 0; sub < L::kSub; ++sub) {
-        const float vs = exp2i(max(static_cast<int>(bytes[sub] >> 8) - 127 - E + kHeadroom, -126));
         uint32_t pb[NP][2];
         float p[4];
 #pragma unroll
@@ -462,9 +455,23 @@ __global__ void __launch_bounds__((kWarps + 1) * 32, ctas_of_sm(sizeof(T), D))
         }
         l[0] += p[0] + p[2];
         l[1] += p[1] + p[3];
+        // the exponent of each head's largest weight of the tile: upper halves of two floats side by side
+        uint32_t big = __byte_perm(__float_as_uint(fmaxf(p[0], p[2])), __float_as_uint(fmaxf(p[1], p[3])), 0x7632);
+#pragma unroll
+        for (int x = 4; x < 32; x <<= 1) big = __vmaxu2(big, __shfl_xor_sync(0xffffffffu, big, x));
+        // weights times up[] become halves, the tile's products times back[] are values again
+        float up[2], back[2];
+        const int ev = static_cast<int>(bytes[sub] >> 8) - 127;
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          const int e = max(static_cast<int>(big >> (7 + 16 * i)) & 0xFF, kTop);
+          up[i] = __uint_as_float(static_cast<uint32_t>(2 * 127 + kTop - e) << 23);
+          const int x = e - 127 - kTop + ev;
+          back[i] = x < -149 ? 0.f : exp2i(x);
+        }
         uint32_t f0[NP], f1[NP];
-        split2<NP>(p[0] * vs, p[1] * vs, f0);
-        split2<NP>(p[2] * vs, p[3] * vs, f1);
+        split2<NP>(p[0] * up[0], p[1] * up[1], f0);
+        split2<NP>(p[2] * up[0], p[3] * up[1], f1);
 #pragma unroll
         for (int x = 0; x < NP; ++x) {
           pb[x][0] = transpose8x8(f0[x]);
@@ -491,15 +498,11 @@ __global__ void __launch_bounds__((kWarps + 1) * 32, ctas_of_sm(sizeof(T), D))
           const uint32_t lo = __byte_perm(v[0][j / 2], v[1][j / 2], sel), hi = __byte_perm(v[2][j / 2], v[3][j / 2], sel);
           const uint32_t a0 = e4m3x2_to_half2(lo & 0xFFFFu), a1 = e4m3x2_to_half2(lo >> 16);
           const uint32_t a2 = e4m3x2_to_half2(hi & 0xFFFFu), a3 = e4m3x2_to_half2(hi >> 16);
-          if (NP == 1) {
-            mma_f16(o[j], a0, a1, a2, a3, pb[0][0], pb[0][1]);
-          } else {  // added rounded
-            float part[4] = {0.f, 0.f, 0.f, 0.f};
+          float part[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-            for (int x = 0; x < NP; ++x) mma_f16(part, a0, a1, a2, a3, pb[x][0], pb[x][1]);
+          for (int x = 0; x < NP; ++x) mma_f16(part, a0, a1, a2, a3, pb[x][0], pb[x][1]);
 #pragma unroll
-            for (int e = 0; e < 4; ++e) o[j][e] += part[e];
-          }
+          for (int e = 0; e < 4; ++e) o[j][e] = fmaf(part[e], back[e & 1], o[j][e]);
         }
       }
       __syncwarp();
@@ -519,7 +522,6 @@ __global__ void __launch_bounds__((kWarps + 1) * 32, ctas_of_sm(sizeof(T), D))
     if (left > 0) next_row();
 
     // join the warps: weights of each head, then the sums by halves
-    const float unit = exp2i(max(min(E - kHeadroom, 127), -149));
     float top[2], sum[2];
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
@@ -538,7 +540,7 @@ __global__ void __launch_bounds__((kWarps + 1) * 32, ctas_of_sm(sizeof(T), D))
       for (int w = 0; w < kWarps; ++w) top[i] = fmaxf(top[i], x[w * H8].x);
 #pragma unroll
       for (int w = 0; w < kWarps; ++w) sum[i] += x[w * H8].y * weight_of(x[w * H8], top[i]);
-      const float f = weight_of(x[warp * H8], top[i]) * unit;
+      const float f = weight_of(x[warp * H8], top[i]);
 #pragma unroll
       for (int j = 0; j < KS; ++j) o[j][i] *= f, o[j][2 + i] *= f;
     }

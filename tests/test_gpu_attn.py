@@ -307,6 +307,63 @@ def test_decode_fp32_error_does_not_grow_with_the_keys(F, d, B, n):
     assert ((o.double() - want).norm() / want.norm()).item() < (d / 8 + 12) * 2.0 ** -24
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("d,lens", [(16, [333, 500, 70]), (64, [600, 1300, 520]), (128, [333, 500, 70]),
+                                    (128, [600, 1300, 520])])
+@pytest.mark.parametrize("ratio", [8, 16, 20, 24, 32, 60])
+def test_decode_value_scales_far_apart(F, dtype, d, lens, ratio):
+    """One page whose values are 2^ratio larger: the first or the last of a sequence with next to no weight (30 nats
+    down), or with its share of the weight and one dim alone.  Weights are known to 11 bits (bf16) and everything else to
+    2e-5, relative to sum_j p_j |v_j| of the element itself: nothing is lost to another page's scale."""
+    Hq, Hkv, page = 6, 2, 16
+    bt, pages = _paged(lens, page, 0, 90)
+    g = np.random.default_rng(90 + d)
+    cache = {n: O.e4m3_encode(g.standard_normal((pages, Hkv, page, d)) * f) for n, f in (("k", 3.0), ("v", 100.0))}
+    cache["k_scale"] = np.full((pages, Hkv), 125, np.uint8)
+    cache["v_scale"] = g.integers(118, 122, (pages, Hkv)).astype(np.uint8)
+    for b, c in ((0, 0), (1, (lens[1] - 1) // page), (2, 1)):
+        at = bt[b, c]
+        cache["v_scale"][at] = 120 + ratio
+        if b < 2:
+            cache["k"][at] = 0
+            cache["k"][at, :, :, 0] = O.e4m3_encode(-240.0)
+        else:
+            cache["v"][at, :, :, 1:] = 0
+    q = _rand((3, Hq, d), dtype, 91)
+    q[:, :, 0] = 4.0
+    o, lse = F.attn_decode(q, _cuda(cache), torch.from_numpy(bt).cuda(), torch.tensor(lens, dtype=torch.int32).cuda(),
+                           max(lens), 0.125, want_lse=True)
+    want, want_lse = O.decode(_np(q), cache, bt, lens, 0.125)
+    size, _ = O.decode(_np(q), {**cache, "v": cache["v"] & 127}, bt, lens, 0.125)
+    tol = (2e-5 + (2.0 ** -11 if dtype == "bf16" else 0.0)) * size + (U * np.abs(want) if dtype == "bf16" else 0.0)
+    assert (np.abs(_np(o) - want) <= tol).all(), (np.abs(_np(o) - want) / size).max()
+    assert (np.abs(_np(lse) - want_lse) <= 2e-5 * (4 + np.abs(want_lse))).all()
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("d", [16, 64, 128])
+def test_decode_many_small_weights(F, dtype, d):
+    """131071 keys 22 nats under a strong one (2^-31.7 each) carry 3.7e-5 of the weight and, with larger values, a
+    percent of the result.  fp32: weights in two halves 2^-22, at most 24 sums in a row of 2^-24 each."""
+    n, page, at = 131072, 128, 70001
+    g = torch.Generator().manual_seed(92)
+    k = torch.zeros((n // page, 1, page, d))
+    v = 300.0 + 100.0 * torch.rand((n // page, 1, page, d), generator=g)
+    k[at // page, 0, at % page, 0], v[at // page, 0, at % page] = 44.0, 1.0
+    codes = {x: y.to(torch.float8_e4m3fn).cuda() for x, y in (("k", k), ("v", v))}
+    cache = {x: y.view(torch.uint8) for x, y in codes.items()}
+    cache.update({x + "_scale": torch.full((n // page, 1), 127, dtype=torch.uint8, device="cuda") for x in "kv"})
+    q = torch.zeros((1, 2, d), dtype=DT[dtype], device="cuda")
+    q[:, :, 0] = 4.0
+    o, lse = F.attn_decode(q, cache, torch.arange(n // page, dtype=torch.int32, device="cuda")[None],
+                           torch.tensor([n], dtype=torch.int32).cuda(), n, 0.125, want_lse=True)
+    s = codes["k"].double().view(n, d)[:, 0] * 0.5
+    want = torch.softmax(s, 0) @ codes["v"].double().view(n, d)
+    tol = want * (U + 2.0 ** -11 if dtype == "bf16" else 2.0 ** -19)
+    assert ((o[0].double() - want).abs() <= tol).all(), ((o[0].double() - want) / want).abs().max().item()
+    assert (lse.double() - torch.logsumexp(s, 0)).abs().max().item() < 2e-5 * 26
+
+
 def test_decode_strides_scale_and_bounds(F):
     """q a slice of a wider projection, o inside wider rows, a scale of its own, lengths past max_len, a page that
     does not exist, no lse, a workspace of garbage."""

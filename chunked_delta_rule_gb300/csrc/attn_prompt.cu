@@ -255,10 +255,10 @@ __global__ void __launch_bounds__(128) attn_prompt_kernel(PromptArgs a, int qblo
       const int g = (__ffs(again) - 1) >> 2, row = row0 + warp * 16 + g + 8 * i;
       again &= ~(0xFu << (4 * g));
       float y[4], z;
-      attention_row(q + row * a.q.stride, k, a.k.stride, v, a.v.stride, min(row + off + 1, lk), D, a.scale, y, &z);
+      attention_row<T, D>(q + row * a.q.stride, k, a.k.stride, v, a.v.stride, min(row + off + 1, lk), D, a.scale, y, &z);
       T* out = static_cast<T*>(a.o.p) + (q0 + row) * a.o.stride + static_cast<int64_t>(h) * D;
 #pragma unroll
-      for (int e = 0; e < 4; ++e)
+      for (int e = 0; e < (D + 31) / 32; ++e)
         if (lane + 32 * e < D) out[lane + 32 * e] = from_f32<T>(y[e]);
       if (a.lse && lane == 0) a.lse[(q0 + row) * a.Hq + h] = z;
     }

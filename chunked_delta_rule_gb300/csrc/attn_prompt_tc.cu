@@ -38,7 +38,8 @@
 // hold does not matter; a masked weight is 0, but 0 times an infinite or NaN
 // value of a key that only other rows see would still spoil the row.  A row
 // whose result is not finite is therefore computed again from the definition,
-// by its warp, touching only the keys that it sees.
+// by its warp, touching only the keys that it sees, after the CTA's last block: a
+// CTA that has found such rows asks for no further one.
 
 #include "attn_row.cuh"
 #include "tc_util.cuh"
@@ -55,6 +56,7 @@ constexpr float kMost = 1099511627776.f;  // 2^40: a larger sum of a tile's weig
 // keys that each of its query tiles sees.
 template <int TILES>
 struct Item {
+  uint32_t id;  // of the grid
   int h, hk, lq, lk, off, row0, nmax, n[TILES];
   int64_t q0, k0;
   bool valid;
@@ -65,6 +67,8 @@ struct Bars {
   uint4 next;       // answer to the request for one more block
   Item<1> item[2];  // whose queries the buffers hold (d = 64)
   uint32_t tmem;
+  uint32_t stop;    // some row has to be computed again: no more blocks are asked for
+  uint2 again[4][4];  // (block, rows) of them: 4 entries a warp
   float row[2][kTile];  // of each tile: what the two threads of a row tell each other
 };
 
@@ -181,6 +185,7 @@ template <int TILES>
 __device__ __forceinline__ Item<TILES> item_at(const TcArgs& t, uint32_t id) {
   const PromptArgs& a = t.a;
   Item<TILES> w;
+  w.id = id;
   // the longest rows first: blocks of queries descend, sequences and heads within
   const uint32_t bh = static_cast<uint32_t>(a.B) * a.Hq, at = id % bh;
   const int qb = t.qblocks - 1 - static_cast<int>(id / bh), b = static_cast<int>(at) / a.Hq;
@@ -242,6 +247,9 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, Cfg<D>::kCtas)
     mbar_init(&bar->o, 1);
     mbar_init(&bar->stall, 1);
     mbar_init(&bar->answer, 1);
+    bar->stop = 0;
+    if (C::kLoop)
+      for (int i = 0; i < 16; ++i) bar->again[i >> 2][i & 3].y = 0;
     fence_mbar_init();
   }
   __syncthreads();
@@ -299,9 +307,11 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, Cfg<D>::kCtas)
           ++used;
         }
         if (end) break;
+        bool asked = false;
         for (int i = 0; i <= 2 * w.nmax; ++i) {
           // one more block, asked for shortly before it is needed
-          if (C::kLoop && i == max(2 * w.nmax - 4, 0)) {
+          if (C::kLoop && i == max(2 * w.nmax - 4, 0) && !*static_cast<volatile uint32_t*>(&bar->stop)) {
+            asked = true;
             mbar_arrive_expect_tx(&bar->answer, 16);
             request_block(&bar->next, &bar->answer);
           }
@@ -315,6 +325,10 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, Cfg<D>::kCtas)
           ++loads;
         }
         if (!C::kLoop) break;
+        if (!asked) {
+          end = true;
+          continue;
+        }
         ok = wait(&bar->answer, round & 1) && ok;
         if (ok) end = !block_given(&bar->next, id);
         fence_proxy_async();  // the answer has been read before the next is written
@@ -450,6 +464,24 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, Cfg<D>::kCtas)
       __syncwarp();
       if (lane == 0) mbar_arrive(b);
     };
+    // rows of the warp (a bit each) of a block from the definition
+    auto compute_again = [&](const W& w, uint32_t rows) {
+      const int d = D == 64 ? a.d : D;
+      for (; rows; rows &= rows - 1) {
+        const int i = w.row0 + x * kTile + quad * 32 + __ffs(rows) - 1;
+        const int64_t gi = w.q0 + i;
+        const __nv_bfloat16* q = static_cast<const __nv_bfloat16*>(a.q.p) + gi * a.q.stride + w.h * d;
+        const __nv_bfloat16* k = static_cast<const __nv_bfloat16*>(a.k.p) + w.k0 * a.k.stride + w.hk * d;
+        const __nv_bfloat16* v = static_cast<const __nv_bfloat16*>(a.v.p) + w.k0 * a.v.stride + w.hk * d;
+        float y[4], z;
+        attention_row<__nv_bfloat16, D>(q, k, a.k.stride, v, a.v.stride, min(i + w.off + 1, w.lk), d, a.scale, y, &z);
+        __nv_bfloat16* oi = static_cast<__nv_bfloat16*>(a.o.p) + gi * a.o.stride + w.h * d;
+#pragma unroll
+        for (int e = 0; e < D / 32; ++e)
+          if (lane + 32 * e < d) oi[lane + 32 * e] = __float2bfloat16_rn(y[e]);
+        if (a.lse && lane == 0) a.lse[gi * a.Hq + w.h] = z;
+      }
+    };
     bool ok = true;
     int tiles = 0, ss = 0;  // key tiles and phases of bar->s so far
     W w;
@@ -562,8 +594,8 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, Cfg<D>::kCtas)
         arrive(&bar->p[x]);
       }
       if constexpr (C::kLoop) w = bar->item[buf];  // (not held through the loop)
-      const int row0 = w.row0, lq = w.lq, lk = w.lk, off = w.off, h = w.h, hk = w.hk;
-      const int64_t q0 = w.q0, k0 = w.k0;
+      const int row0 = w.row0, lq = w.lq, h = w.h;
+      const int64_t q0 = w.q0;
       if (row0 + x * kTile < lq) {  // some row of this tile is the call's
         if (ok && nx > 0) ok = C::kAhead ? wait(&bar->o, (tiles - 1) & 1) : wait(&bar->s[x], ss & 1);
         if (!C::kAhead && nx > 0) ++ss;
@@ -648,19 +680,13 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, Cfg<D>::kCtas)
             named_bar(pair, 64);
             bad = half == 1 && (bad || *told > 0.f);
           }
-          for (uint32_t again = __ballot_sync(0xffffffffu, bad); again; again &= again - 1) {
-            const int i = row0 + x * kTile + quad * 32 + __ffs(again) - 1;
-            const int64_t gi = q0 + i;
-            const __nv_bfloat16* q = static_cast<const __nv_bfloat16*>(a.q.p) + gi * a.q.stride + h * d;
-            const __nv_bfloat16* k = static_cast<const __nv_bfloat16*>(a.k.p) + k0 * a.k.stride + hk * d;
-            const __nv_bfloat16* v = static_cast<const __nv_bfloat16*>(a.v.p) + k0 * a.v.stride + hk * d;
-            float y[4], z;
-            attention_row(q, k, a.k.stride, v, a.v.stride, min(i + off + 1, lk), d, a.scale, y, &z);
-            __nv_bfloat16* oi = static_cast<__nv_bfloat16*>(a.o.p) + gi * a.o.stride + h * d;
-#pragma unroll
-            for (int e = 0; e < D / 32; ++e)
-              if (lane + 32 * e < d) oi[lane + 32 * e] = __float2bfloat16_rn(y[e]);
-            if (a.lse && lane == 0) a.lse[gi * a.Hq + h] = z;
+          const uint32_t again = __ballot_sync(0xffffffffu, bad);
+          if constexpr (!C::kLoop) {
+            compute_again(w, again);
+          } else if (again != 0 && lane == 0) {
+            // when the pipeline has ended: rows of many keys take longer than a wait in it may
+            bar->again[warp][used & 3] = make_uint2(w.id, again);
+            *static_cast<volatile uint32_t*>(&bar->stop) = 1;
           }
         } else {
           ok = false;  // all leave together
@@ -669,6 +695,15 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, Cfg<D>::kCtas)
       if (C::kLoop) {
         fence_proxy_async();  // the next queries' copy comes after what was written here
         arrive(&bar->q_free[buf]);
+      }
+    }
+    // At most two further blocks come to a warp after its first one with such rows: one is on its way, and one may
+    // have been asked for; before the next question their queries' place must be free, which comes after `stop`.
+    if constexpr (C::kLoop) {
+      __syncwarp();
+      for (int e = 0; e < 4; ++e) {
+        const uint2 g = bar->again[warp][e];
+        if (g.y != 0) compute_again(item_at<C::kTiles>(t, g.x), g.y);
       }
     }
     tc_fence_before();

@@ -6,35 +6,63 @@
 
 namespace falcon {
 
-// o (lane t's dims t, t + 32, ...) and the log of the sum of exponentials of
-// the first n keys; o = 0 and -inf where nothing weighs.
-template <typename T>
-__device__ __noinline__ void attention_row(const T* q, const T* k, int64_t k_stride, const T* v,
-                                              int64_t v_stride, int n, int d, float scale, float (&o)[4], float* lse) {
+// out (lane t's dims t, t + 32, ...) and the log of the sum of exponentials of
+// the first n keys; out = 0 and -inf where nothing weighs.  A few keys at a time:
+// all their loads are in flight before the first is used, and their sums over
+// the lanes run side by side (0.15 us a key, 0.5 one by one).  Ends where the sum is
+// NaN: it and every dim stay so.
+template <typename T, int D>
+__device__ __noinline__ void attention_row(const T* q, const T* k, int64_t k_stride, const T* v, int64_t v_stride,
+                                           int n, int d, float scale, float (&out)[4], float* lse) {
+  constexpr int J = (D + 31) / 32, kBatch = J == 4 ? 4 : 8;
   const int lane = threadIdx.x & 31;
-  float qv[4], m = -INFINITY, l = 0.f;
+  float qv[J], o[J], m = -INFINITY, l = 0.f;
+  int at[J];
 #pragma unroll
-  for (int j = 0; j < 4; ++j) {
-    qv[j] = lane + 32 * j < d ? to_f32(q[lane + 32 * j]) * scale : 0.f;
+  for (int j = 0; j < J; ++j) {
+    at[j] = min(lane + 32 * j, d - 1);
+    qv[j] = lane + 32 * j < d ? to_f32(q[at[j]]) * scale : 0.f;
     o[j] = 0.f;
   }
-  for (int t = 0; t < n; ++t) {
-    float s = 0.f;
+  for (int t = 0; t < n && l == l; t += kBatch) {
+    T kt[kBatch][J], vt[kBatch][J];
 #pragma unroll
-    for (int j = 0; j < 4; ++j)
-      if (lane + 32 * j < d) s = fmaf(qv[j], to_f32(k[t * k_stride + lane + 32 * j]), s);
+    for (int u = 0; u < kBatch; ++u)
 #pragma unroll
-    for (int x = 16; x; x >>= 1) s += __shfl_xor_sync(0xffffffffu, s, x);
-    const float mn = fmaxf(m, s), ref = mn == -INFINITY ? 0.f : mn;
-    const float old = expf(m - ref), p = expf(s - ref);
-    l = l * old + p;
+      for (int j = 0; j < J; ++j) kt[u][j] = k[min(t + u, n - 1) * k_stride + at[j]];
 #pragma unroll
-    for (int j = 0; j < 4; ++j)
-      if (lane + 32 * j < d) o[j] = o[j] * old + p * to_f32(v[t * v_stride + lane + 32 * j]);
-    m = mn;
+    for (int u = 0; u < kBatch; ++u)
+#pragma unroll
+      for (int j = 0; j < J; ++j) vt[u][j] = v[min(t + u, n - 1) * v_stride + at[j]];
+    float s[kBatch], top = m;
+#pragma unroll
+    for (int u = 0; u < kBatch; ++u) {
+      s[u] = 0.f;
+#pragma unroll
+      for (int j = 0; j < J; ++j) s[u] = fmaf(qv[j], lane + 32 * j < d ? to_f32(kt[u][j]) : 0.f, s[u]);
+    }
+#pragma unroll
+    for (int x = 16; x; x >>= 1)
+#pragma unroll
+      for (int u = 0; u < kBatch; ++u) s[u] += __shfl_xor_sync(0xffffffffu, s[u], x);
+#pragma unroll
+    for (int u = 0; u < kBatch; ++u) top = fmaxf(top, s[u]);  // (the last key's score again past the end)
+    const float ref = top == -INFINITY ? 0.f : top, old = expf(m - ref);
+    l *= old;
+#pragma unroll
+    for (int j = 0; j < J; ++j) o[j] *= old;
+#pragma unroll
+    for (int u = 0; u < kBatch; ++u) {
+      const bool in = t + u < n;
+      const float p = in ? expf(s[u] - ref) : 0.f;
+      l += p;
+#pragma unroll
+      for (int j = 0; j < J; ++j) o[j] = fmaf(p, in ? to_f32(vt[u][j]) : 0.f, o[j]);
+    }
+    m = top;
   }
 #pragma unroll
-  for (int j = 0; j < 4; ++j) o[j] = l == 0.f ? 0.f : o[j] / l;
+  for (int j = 0; j < J; ++j) out[j] = l == 0.f ? 0.f : o[j] / l;
   *lse = l == 0.f ? -INFINITY : m + logf(l);
 }
 

@@ -672,6 +672,58 @@ def test_no_bound_on_the_keys(F):
     assert all(torch.equal(a, b) for a, b in zip(*got))
 
 
+@pytest.mark.parametrize("d", [32, 64, 128])
+def test_prompt_rows_computed_again_are_no_timeout(F, d):
+    """An infinity in one dim of an early value sends every later row through the definition.  That takes longer than a
+    wait may (3 ms here), which is no reason for the waits of the same block to run out."""
+    n, H = 4096, 24 if d < 128 else 4
+    q, k, v, cq, _ = _prompt_case([n], [n], H, 2, d, "bf16", 93)
+    v[5, :, 3] = float("inf")
+    cu, o = torch.from_numpy(cq).cuda(), torch.empty_like(q)
+    p = F.AttnParams(B=1, Hq=H, Hkv=2, d=d, dtype=F.FALCON_BF16, max_q=n, tokens=n, k_tokens=n)
+    ws = F.alloc_workspace(F.falcon_attn_prompt_workspace_size(p))
+    F.falcon_test_hooks(3_000_000, False)
+    try:
+        F.falcon_attn_prompt(p, q, k, v, cu, cu, o, None, ws)
+        assert F.falcon_workspace_status(ws) == F.FALCON_OK
+    finally:
+        F.falcon_test_hooks(0, False)
+    assert torch.isinf(o[5:, :, 3]).all() and torch.isfinite(o[:5]).all()
+    rest = [i for i in range(d) if i != 3]
+    for h in (0, H - 1):
+        s = q[:, h].double() @ k[:, h * 2 // H].double().T * d ** -0.5
+        s.masked_fill_(torch.ones((n, n), dtype=torch.bool, device="cuda").triu(1), -float("inf"))
+        want = s.softmax(-1) @ v[:, h * 2 // H, rest].double()
+        assert ((o[:, h, rest].double() - want).abs() <= U * want.abs() + 1.25 * U * 5).all()
+
+
+def _prompt_ms(F, q, k, v, cu):
+    """The quicker of two calls after a first one."""
+    ms = []
+    for _ in range(3):
+        a, b = (torch.cuda.Event(enable_timing=True) for _ in "ab")
+        a.record()
+        F.attn_prompt(q, k, v, cu, max_q=q.shape[0])
+        b.record()
+        b.synchronize()
+        ms.append(a.elapsed_time(b))
+    return min(ms[1:])
+
+
+@pytest.mark.parametrize("d", [64, 128])
+def test_prompt_walk_of_a_row_ends_at_nan(F, d):
+    """An early key that is NaN makes every later row NaN: computing those again ends there, so the call takes a few
+    times as long as a clean one, not the some 1000 times that walking over every key of every row does."""
+    n, H = 4096, 12
+    q, k, v, cq, _ = _prompt_case([n], [n], H, 2, d, "bf16", 95)
+    cu = torch.from_numpy(cq).cuda()
+    clean = _prompt_ms(F, q, k, v, cu)
+    k[5] = float("nan")
+    assert _prompt_ms(F, q, k, v, cu) < 50 * clean
+    o = F.attn_prompt(q, k, v, cu, max_q=n)
+    assert torch.isfinite(o[:5]).all() and torch.isnan(o[5:]).all()
+
+
 # ---------------------------------------------------------------- streams, repeats, the pieces together
 def test_same_bits_again_and_on_another_stream(F):
     lens = [700, 90]

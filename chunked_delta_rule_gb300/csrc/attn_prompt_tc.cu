@@ -30,8 +30,12 @@
 // The reference m of a row is the maximum of its first tile.  Weights, sums and
 // O keep their relative precision at any scale (bf16 has fp32's range), so m
 // moves, and O is rescaled, only after a tile whose sum passed 2^40: the other
-// tiles need no maximum.  (A score that passes m by 2^127 at once overflows, and
-// its row is computed again as below.)  Sums are of the unrounded weights, fp32.
+// tiles need no maximum.  A tile that passes m by 2^64 at once is weighed again
+// against its own maximum before anything uses it (d <= 64: 0.3 us of 66).  At d = 128
+// the two threads of a row would have to agree on that at every tile: with a barrier
+// 920 us where 709 are, with the maximum taken first 738.  There a tile that overflows
+// (2^127) sends its row through the definition as below.  Sums are of the unrounded
+// weights, fp32.
 // P is rounded to bf16 as V is held in it: at most 2^-8 of a weight.
 //
 // Masked scores are set to -inf after the product, so what the masked keys
@@ -50,7 +54,8 @@ namespace {
 using namespace tcu;
 
 constexpr int kTile = 128;        // queries and keys of a tile
-constexpr float kMost = 1099511627776.f;  // 2^40: a larger sum of a tile's weights moves the reference at the next
+constexpr float kMost = 1099511627776.f;  // 2^40: a larger sum of a tile's weights moves the reference at the next,
+constexpr float kFar = 1.8446744e19f;     // 2^64: at once (d = 64)
 
 // One block of queries of one head: where its rows and keys are, and the tiles of
 // keys that each of its query tiles sees.
@@ -548,45 +553,50 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, Cfg<D>::kCtas)
           ++tiles;
         }
         // also, with two threads a row: both have read their scores, the weights may go over them
-        const bool move = any(!ok || m == -INFINITY || !(lt <= kMost));
-        if (move) {         // the reference moves to the maximum so far
-          if (any(!ok)) {   // all leave together
-            ok = false;
-            break;
-          }
-          float t4[4];
+        bool move = any(!ok || m == -INFINITY || !(lt <= kMost));
+        if (move && any(!ok)) {  // all leave together
+          ok = false;
+          break;
+        }
+        for (;;) {
+          if (move) {         // the reference moves to the maximum so far
+            float t4[4];
 #pragma unroll
-          for (int i = 0; i < 4; ++i) t4[i] = s[i];
+            for (int i = 0; i < 4; ++i) t4[i] = s[i];
 #pragma unroll
-          for (int i = 4; i < kHalf - 4; i += 8)
+            for (int i = 4; i < kHalf - 4; i += 8)
 #pragma unroll
-            for (int e = 0; e < 4; ++e) t4[e] = max3(t4[e], s[i + e], s[i + 4 + e]);
+              for (int e = 0; e < 4; ++e) t4[e] = max3(t4[e], s[i + e], s[i + 4 + e]);
 #pragma unroll
-          for (int e = 0; e < 4; ++e) t4[e] = fmaxf(t4[e], s[kHalf - 4 + e]);
-          float mn = fmaxf(m, max3(t4[0], t4[1], fmaxf(t4[2], t4[3])));
-          if (C::kSplit == 2) {
-            if (half == 1) *told = mn;
-            named_bar(pair, 64);
-            if (half == 0) *told = fmaxf(mn, *told);
-            named_bar(pair, 64);
-            mn = *told;
-          }
-          const float f = mn == -INFINITY ? 1.f : ex2((m - mn) * sl2);
-          m = mn;
-          l *= f;
-          if (j > 0) {
+            for (int e = 0; e < 4; ++e) t4[e] = fmaxf(t4[e], s[kHalf - 4 + e]);
+            float mn = fmaxf(m, max3(t4[0], t4[1], fmaxf(t4[2], t4[3])));
+            if (C::kSplit == 2) {
+              if (half == 1) *told = mn;
+              named_bar(pair, 64);
+              if (half == 0) *told = fmaxf(mn, *told);
+              named_bar(pair, 64);
+              mn = *told;
+            }
+            const float f = mn == -INFINITY ? 1.f : ex2((m - mn) * sl2);
+            m = mn;
+            l *= f;
+            if (j > 0) {
 #pragma unroll
-            for (int c = 0; c < kOut / 16; ++c) {
-              uint32_t v[16];
-              tmem_ld16(to + c * 16, v);
-              tmem_wait_ld();
+              for (int c = 0; c < kOut / 16; ++c) {
+                uint32_t v[16];
+                tmem_ld16(to + c * 16, v);
+                tmem_wait_ld();
 #pragma unroll
-              for (int i = 0; i < 16; ++i) v[i] = __float_as_uint(__uint_as_float(v[i]) * f);
-              tmem_st16(to + c * 16, v);
+                for (int i = 0; i < 16; ++i) v[i] = __float_as_uint(__uint_as_float(v[i]) * f);
+                tmem_st16(to + c * 16, v);
+              }
             }
           }
+          lt = weigh();
+          if (move || C::kSplit == 2 || !any(lt > kFar)) break;
+          move = true;  // finite scores stay finite
+          if (C::kAhead) tmem_wait_st();  // the weights are stored once more
         }
-        lt = weigh();
         l += lt;
         if (!C::kAhead) tmem_st32(tp, u);
         tmem_wait_st();

@@ -724,6 +724,42 @@ def test_prompt_walk_of_a_row_ends_at_nan(F, d):
     assert torch.isfinite(o[:5]).all() and torch.isnan(o[5:]).all()
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("d", [32, 64, 128])
+def test_prompt_scores_that_jump(F, dtype, d):
+    """Scores that pass what a row has seen before by 60 to 2000 nats, at the start of a tile and inside one, for some of
+    the rows; values of 2^30 beside them."""
+    n = 700
+    q, k, v, cq, ck = _prompt_case([n], [n], 2, 1, d, dtype, 94)
+    q[:, :, 0], k[:, :, 0] = 1.0, 0.0
+    q[::3, :, 0] = 0.25
+    for at, jump in ((128, 100.0), (200, 60.0), (384, 300.0), (500, 2000.0)):
+        k[at, :, 0] = jump * d ** 0.5
+    v[100:140] *= 2.0 ** 30
+    o, lse = _prompt(F, q, k, v, cq, ck)
+    want, want_lse = O.prompt(_np(q), _np(k), _np(v), cq, ck, d ** -0.5)
+    size, _ = O.prompt(_np(q), _np(k), np.abs(_np(v)), cq, ck, d ** -0.5)
+    # weights to 8 bits (bf16), scores of size s to 2^-20 s
+    tol = U * np.abs(want) + (1.25 * U + 2.0 ** -20 * np.abs(want_lse)[..., None]) * size
+    if dtype == "f32":
+        tol = (2e-5 + 2.0 ** -20 * np.abs(want_lse)[..., None]) * size
+    assert (np.abs(_np(o) - want) <= tol).all(), (np.abs(_np(o) - want) / size).max()
+    assert (np.abs(_np(lse) - want_lse) <= 2e-5 * (4 + np.abs(want_lse))).all()
+
+
+@pytest.mark.parametrize("d", [32, 64])
+def test_prompt_finite_jump_costs_no_second_pass(F, d):
+    """Scores that jump by 160 nats from one key on, seen by most rows: finite scores need no row computed again (which
+    took some hundred times as long)."""
+    n, H = 4096, 12
+    q, k, v, cq, _ = _prompt_case([n], [n], H, 2, d, "bf16", 96)
+    q[:, :, 0], k[:, :, 0] = 8.0, 0.0
+    cu = torch.from_numpy(cq).cuda()
+    clean = _prompt_ms(F, q, k, v, cu)
+    k[200:, :, 0] = 20.0 * d ** 0.5
+    assert _prompt_ms(F, q, k, v, cu) < 20 * clean
+
+
 # ---------------------------------------------------------------- streams, repeats, the pieces together
 def test_same_bits_again_and_on_another_stream(F):
     lens = [700, 90]

@@ -45,6 +45,22 @@ bool overlap(const void* a, size_t na, const void* b, size_t nb) {
   return pa < pb + nb && pb < pa + na;
 }
 
+// Whether rows of a and rows of b share a byte: n rows each, of ra and rb bytes, sa and sb apart.  With one stride (slices
+// of a fused projection) the rows of one lie between those of the other; with two the spans are compared.
+bool rows_overlap(const void* a, int64_t sa, size_t ra, const void* b, int64_t sb, size_t rb, int64_t n) {
+  if (!a || !b || n <= 0) return false;
+  if (!overlap(a, (n - 1) * sa + ra, b, (n - 1) * sb + rb)) return false;
+  if (sa != sb || n == 1) return true;
+  const auto pa = reinterpret_cast<uintptr_t>(a), pb = reinterpret_cast<uintptr_t>(b);
+  const size_t s = static_cast<size_t>(sa), off = pb >= pa ? (pb - pa) % s : (s - (pa - pb) % s) % s;
+  return off < ra || s - off < rb;  // from a row of a to the next row of b, and from there to the next of a
+}
+bool rows_overlap(const falcon_attn_params_t* p, const void* a, int64_t sa, int Ha, const void* b, int64_t sb, int Hb,
+                  int64_t n) {
+  const int64_t e = static_cast<int64_t>(esize(p));
+  return rows_overlap(a, stride_of(sa, Ha, p->d) * e, Ha * p->d * e, b, stride_of(sb, Hb, p->d) * e, Hb * p->d * e, n);
+}
+
 int check_attn(const falcon_attn_params_t* p) {
   if (!p) return FALCON_ERR_INVALID_ARG;
   if (p->Hq < 1 || p->Hkv < 1 || p->Hq % p->Hkv) return FALCON_ERR_INVALID_ARG;
@@ -117,11 +133,15 @@ int falcon_qk_norm_rope(const falcon_attn_params_t* p, const void* q, const void
     if (misaligned(x, esize(p))) return FALCON_ERR_INVALID_ARG;
   const RowsIn qi = rows_in(p, q, p->q_stride, p->Hq), ki = rows_in(p, k, p->k_stride, p->Hkv);
   const RowsOut qo = rows_out(p, q_out, p->o_stride, p->Hq), ko = rows_out(p, k_out, 0, p->Hkv);
-  const size_t nq = q ? span(p, p->tokens, p->q_stride, p->Hq) : 0, nk = k ? span(p, p->tokens, p->k_stride, p->Hkv) : 0;
-  const size_t nqo = q ? span(p, p->tokens, p->o_stride, p->Hq) : 0, nko = k ? span(p, p->tokens, 0, p->Hkv) : 0;
   const bool q_inplace = q == q_out && qi.stride == qo.stride, k_inplace = k == k_out && ki.stride == ko.stride;
-  if ((!q_inplace && overlap(q, nq, q_out, nqo)) || (!k_inplace && overlap(k, nk, k_out, nko)) ||
-      overlap(k, nk, q_out, nqo) || overlap(q, nq, k_out, nko) || overlap(q_out, nqo, k_out, nko))
+  auto meet = [&](const void* x, int64_t sx, int Hx, const void* y, int64_t sy, int Hy) {
+    return rows_overlap(p, x, sx, Hx, y, sy, Hy, p->tokens);
+  };
+  const void *xq = q ? q_out : nullptr, *xk = k ? k_out : nullptr;
+  if ((!q_inplace && meet(q, p->q_stride, p->Hq, xq, p->o_stride, p->Hq)) ||
+      (!k_inplace && meet(k, p->k_stride, p->Hkv, xk, 0, p->Hkv)) ||
+      meet(k, p->k_stride, p->Hkv, xq, p->o_stride, p->Hq) || meet(q, p->q_stride, p->Hq, xk, 0, p->Hkv) ||
+      meet(xq, p->o_stride, p->Hq, xk, 0, p->Hkv))
     return FALCON_ERR_INVALID_ARG;
   return launch_qk_norm_rope(head_args(p, table, w_q, w_k), p->dtype, p->tokens, p->Hq, p->Hkv, qi, ki, w_q, w_k, positions, qo,
                              ko, reinterpret_cast<cudaStream_t>(stream));
@@ -176,7 +196,7 @@ int falcon_attn_decode(const falcon_attn_params_t* p, const void* q, const falco
       misaligned(lse, 4))
     return FALCON_ERR_INVALID_ARG;
   const size_t no = span(p, p->B, p->o_stride, p->Hq), nl = lse ? static_cast<size_t>(p->B) * p->Hq * 4 : 0;
-  if (overlap(q, span(p, p->B, p->q_stride, p->Hq), o, no) || overlap(o, no, lse, nl)) return FALCON_ERR_INVALID_ARG;
+  if (rows_overlap(p, q, p->q_stride, p->Hq, o, p->o_stride, p->Hq, p->B) || overlap(o, no, lse, nl)) return FALCON_ERR_INVALID_ARG;
   const size_t need = falcon_attn_decode_workspace_size(p);
   if (!workspace || workspace_bytes < need || misaligned(workspace, 256)) return FALCON_ERR_WORKSPACE;
   const DecodeArgs a{p->B, p->Hq, p->Hkv, p->d, p->page, p->num_pages, p->max_pages, p->max_k, scale_of(p),
@@ -208,7 +228,14 @@ int falcon_attn_prompt(const falcon_attn_params_t* p, const void* q, const void*
   const size_t nin[3] = {span(p, p->tokens, p->q_stride, p->Hq), span(p, p->k_tokens, p->k_stride, p->Hkv),
                          span(p, p->k_tokens, p->v_stride, p->Hkv)};
   for (int i = 0; i < 3; ++i)
-    if (overlap(ins[i], nin[i], o, no) || overlap(ins[i], nin[i], lse, nl)) return FALCON_ERR_INVALID_ARG;
+    if (overlap(ins[i], nin[i], lse, nl)) return FALCON_ERR_INVALID_ARG;
+  // o between the rows of a fused projection; k and v may have rows of their own number
+  const bool one = p->k_tokens == p->tokens;
+  if (rows_overlap(p, q, p->q_stride, p->Hq, o, p->o_stride, p->Hq, p->tokens) ||
+      (one ? rows_overlap(p, k, p->k_stride, p->Hkv, o, p->o_stride, p->Hq, p->tokens) ||
+                 rows_overlap(p, v, p->v_stride, p->Hkv, o, p->o_stride, p->Hq, p->tokens)
+           : overlap(ins[1], nin[1], o, no) || overlap(ins[2], nin[2], o, no)))
+    return FALCON_ERR_INVALID_ARG;
   if (overlap(o, no, lse, nl)) return FALCON_ERR_INVALID_ARG;
   if (!workspace || workspace_bytes < falcon_attn_prompt_workspace_size(p) || misaligned(workspace, 256))
     return FALCON_ERR_WORKSPACE;

@@ -403,8 +403,10 @@ int falcon_rope_table(const double* inv_freq, int32_t rot, int32_t rows, float m
  *   (a, b) -> (a c - b s, b c + a s)           on the rot/2 pairs, (c, s) = table[position, i]
  * fp32 arithmetic, rounded once to the dtype.  q -> q_out (row stride
  * o_stride, 0 = dense), k -> k_out (dense); q or k may be NULL (skipped).  An
- * output may be its own input when their strides agree (in place), and must
- * not overlap an input otherwise.  positions: int64 [tokens], needed with
+ * output may be its own input when their strides agree (in place, also inside
+ * a fused projection), and its rows must not share a byte with another
+ * operand's otherwise.  (Operands of one stride may lie between one another's
+ * rows, here and in falcon_attn_prompt and falcon_attn_decode.)  positions: int64 [tokens], needed with
  * rot > 0, as is table; the rotated dims of a token whose position is not
  * in [0, rope_rows) are NaN.  Errors: FALCON_ERR_INVALID_ARG,
  * FALCON_ERR_UNSUPPORTED, FALCON_ERR_CUDA. */

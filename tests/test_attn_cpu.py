@@ -129,6 +129,24 @@ def test_qk_norm_rope_pointers(F):
     _refused(F, -1, call, fused, X[0], X[1], None, None, None, None, X[0], X[3], 0)  # in place, other stride
 
 
+def test_rows_that_share_bytes_in_a_fused_projection(F):
+    """Rows of 8 + 2 + 2 heads of 64 bf16, 2048 elements apart.  What starts inside another operand's row, or runs into
+    the next one, is refused."""
+    call, p = F.falcon_qk_norm_rope, _p(F, q_stride=2048, k_stride=2048, o_stride=2048)
+    q, k = X[0], X[0] + 8 * 64 * 2
+    for out in (q + 2, q + 511 * 2, k, k + 127 * 2, k - 511 * 2, q + 2048 * 2 - 2, q + 2048 * 2 * 9 - 1022):
+        _refused(F, -1, call, p, q, k, None, None, None, None, out, X[3], 0)
+    _refused(F, -1, call, p, q, k, None, None, None, None, q, q + 2048 * 2 * 9, 0)   # dense k_out over the last row of q
+    _refused(F, -1, call, _p(F, q_stride=2048, k_stride=2048, o_stride=1024), q, k, None, None, None, None, q, X[3], 0)
+    p = _p(F, q_stride=2048, k_stride=2048, v_stride=2048, o_stride=2048)
+    v = k + 128 * 2
+    for out in (q, k - 2, v + 64 * 2, q - 511 * 2, v + 127 * 2):
+        _refused(F, -1, F.falcon_attn_prompt, p, q, k, v, X[3], X[4], out, None, X[9], 256, 0)
+    # keys of another number of rows: their whole span
+    p = _p(F, q_stride=2048, k_stride=2048, v_stride=2048, o_stride=2048, k_tokens=11)
+    _refused(F, -1, F.falcon_attn_prompt, p, q, k, v, X[3], X[4], v + 128 * 2, None, X[9], 256, 0)
+
+
 @pytest.mark.parametrize("kw,code", [(dict(page=48), -2), (dict(page=256), -2), (dict(B=0), -1), (dict(num_pages=0), -1),
                                      (dict(max_pages=-1), -1)])
 def test_cache_settings(F, kw, code):

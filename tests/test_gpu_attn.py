@@ -760,6 +760,48 @@ def test_prompt_finite_jump_costs_no_second_pass(F, d):
     assert _prompt_ms(F, q, k, v, cu) < 20 * clean
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_norm_in_place_in_a_fused_projection(F, dtype):
+    """q is normed where it lies between k and v of its token; k goes elsewhere, k and v stay as they were."""
+    n, Hq, Hkv, d = 37, 6, 2, 64
+    x = _rand((n, Hq + 2 * Hkv, d), dtype, 97)
+    before, (table, pos) = x.clone(), (_table(F, d, 64)[0], torch.arange(n).cuda())
+    q, k, _ = torch.split(x, [Hq, Hkv, Hkv], dim=1)
+    want = F.qk_norm_rope(q, k, pos, table)
+    p = F.AttnParams(Hq=Hq, Hkv=Hkv, d=d, dtype=F.FALCON_BF16 if dtype == "bf16" else F.FALCON_F32, tokens=n, qk_norm=1,
+                     rot=d, rope_rows=64, q_stride=x.stride(0), k_stride=x.stride(0), o_stride=x.stride(0))
+    ko = torch.empty((n, Hkv, d), dtype=x.dtype, device="cuda")
+    F.falcon_qk_norm_rope(p, q, k, None, None, pos, table, q, ko)
+    assert torch.equal(q, want[0]) and torch.equal(ko, want[1]) and torch.equal(x[:, Hq:], before[:, Hq:])
+
+
+@pytest.mark.parametrize("n,d", [(300, 64), (300, 32), (70, 128), (10, 64)])
+def test_prompt_output_in_a_fused_buffer(F, n, d):
+    """o lies between the rows of q, k and v."""
+    Hq, Hkv = 6, 2
+    x = _rand((n, 2 * Hq + 2 * Hkv, d), "bf16", 98)
+    before = x.clone()
+    q, k, v, o = torch.split(x, [Hq, Hkv, Hkv, Hq], dim=1)
+    cu, st = torch.tensor([0, n], dtype=torch.int32).cuda(), x.stride(0)
+    want = F.attn_prompt(q, k, v, cu)
+    p = F.AttnParams(B=1, Hq=Hq, Hkv=Hkv, d=d, dtype=F.FALCON_BF16, max_q=n, tokens=n, k_tokens=n, q_stride=st,
+                     k_stride=st, v_stride=st, o_stride=st)
+    F.falcon_attn_prompt(p, q, k, v, cu, cu, o, None, F.alloc_workspace(F.falcon_attn_prompt_workspace_size(p)))
+    assert torch.equal(o, want) and torch.equal(x[:, :Hq + 2 * Hkv], before[:, :Hq + 2 * Hkv])
+
+
+def test_decode_output_beside_the_queries(F):
+    lens = [90, 33, 0]
+    bt, cache, q = _decode_case(F, lens, 4, 2, 64, 16, "bf16", 99)
+    dev, bt, ln = _cuda(cache), torch.from_numpy(bt).cuda(), torch.tensor(lens, dtype=torch.int32).cuda()
+    want = F.attn_decode(q, dev, bt, ln, 96)
+    x = torch.cat([q, torch.zeros_like(q)], 1)
+    p = F.AttnParams(B=3, Hq=4, Hkv=2, d=64, dtype=F.FALCON_BF16, max_k=96, page=16, num_pages=dev["k"].shape[0],
+                     max_pages=bt.shape[1], q_stride=512, o_stride=512)
+    F.falcon_attn_decode(p, x, dev, bt, ln, x[:, 4:], None, F.alloc_workspace(F.falcon_attn_decode_workspace_size(p)))
+    assert torch.equal(x[:, 4:], want) and torch.equal(x[:, :4], q)
+
+
 # ---------------------------------------------------------------- streams, repeats, the pieces together
 def test_same_bits_again_and_on_another_stream(F):
     lens = [700, 90]

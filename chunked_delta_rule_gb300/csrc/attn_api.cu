@@ -4,6 +4,7 @@
 #include <algorithm>
 #include <cmath>
 #include <cstdint>
+#include <utility>
 
 #include "attn.cuh"
 
@@ -100,6 +101,15 @@ HeadArgs head_args(const falcon_attn_params_t* p, const float* table, const floa
   return HeadArgs{p->d, p->qk_norm ? 1 : 0, p->norm_eps, 1.f / static_cast<float>(p->d), p->rot, p->rope_layout, p->rope_rows,
                   reinterpret_cast<const float2*>(table), wide};
 }
+// the cache's four buffers and their bytes
+struct CacheParts {
+  const void* p[4];
+  size_t n[4];
+};
+CacheParts cache_parts(const falcon_attn_params_t* p, const falcon_kv_cache_t* c) {
+  const size_t scales = static_cast<size_t>(p->num_pages) * p->Hkv, codes = scales * p->page * p->d;
+  return CacheParts{{c->k, c->v, c->k_scale, c->v_scale}, {codes, codes, scales, scales}};
+}
 int check_cache(const falcon_attn_params_t* p, const falcon_kv_cache_t* c, const int32_t* blocks) {
   if (p->page != 16 && p->page != 32 && p->page != 64 && p->page != 128) return FALCON_ERR_UNSUPPORTED;
   if (p->B < 1 || p->num_pages < 1 || p->max_pages < 0) return FALCON_ERR_INVALID_ARG;
@@ -159,10 +169,9 @@ int falcon_kv_append(const falcon_attn_params_t* p, const void* k, const void* v
   if (!k || !v || !cu_new || !ctx_lens) return FALCON_ERR_INVALID_ARG;
   if (misaligned(k, esize(p)) || misaligned(v, esize(p)) || misaligned(cu_new, 4) || misaligned(ctx_lens, 4))
     return FALCON_ERR_INVALID_ARG;
-  const size_t codes = static_cast<size_t>(p->num_pages) * p->Hkv * p->page * p->d;
-  const size_t scales = static_cast<size_t>(p->num_pages) * p->Hkv;
-  const void* outs[4] = {cache->k, cache->v, cache->k_scale, cache->v_scale};
-  const size_t nout[4] = {codes, codes, scales, scales};
+  const CacheParts c = cache_parts(p, cache);
+  const void* const* outs = c.p;
+  const size_t* nout = c.n;
   const void* ins[2] = {k, v};
   const size_t nin[2] = {span(p, p->tokens, p->k_stride, p->Hkv), span(p, p->tokens, p->v_stride, p->Hkv)};
   for (int i = 0; i < 4; ++i) {
@@ -197,7 +206,15 @@ int falcon_attn_decode(const falcon_attn_params_t* p, const void* q, const falco
     return FALCON_ERR_INVALID_ARG;
   const size_t no = span(p, p->B, p->o_stride, p->Hq), nl = lse ? static_cast<size_t>(p->B) * p->Hq * 4 : 0;
   if (rows_overlap(p, q, p->q_stride, p->Hq, o, p->o_stride, p->Hq, p->B) || overlap(o, no, lse, nl)) return FALCON_ERR_INVALID_ARG;
-  const size_t need = falcon_attn_decode_workspace_size(p);
+  const size_t need = falcon_attn_decode_workspace_size(p), nq = span(p, p->B, p->q_stride, p->Hq);
+  const CacheParts c = cache_parts(p, cache);
+  for (int i = 0; i < 4; ++i)
+    if (overlap(o, no, c.p[i], c.n[i]) || overlap(lse, nl, c.p[i], c.n[i]) || overlap(workspace, need, c.p[i], c.n[i]))
+      return FALCON_ERR_INVALID_ARG;
+  if (overlap(q, nq, lse, nl)) return FALCON_ERR_INVALID_ARG;
+  for (const auto& x : {std::make_pair(q, nq), std::make_pair(static_cast<const void*>(o), no),
+                        std::make_pair(static_cast<const void*>(lse), nl)})
+    if (overlap(workspace, need, x.first, x.second)) return FALCON_ERR_INVALID_ARG;
   if (!workspace || workspace_bytes < need || misaligned(workspace, 256)) return FALCON_ERR_WORKSPACE;
   const DecodeArgs a{p->B, p->Hq, p->Hkv, p->d, p->page, p->num_pages, p->max_pages, p->max_k, scale_of(p),
                      rows_in(p, q, p->q_stride, p->Hq), rows_out(p, o, p->o_stride, p->Hq), lse, block_table, lens,
@@ -237,7 +254,11 @@ int falcon_attn_prompt(const falcon_attn_params_t* p, const void* q, const void*
            : overlap(ins[1], nin[1], o, no) || overlap(ins[2], nin[2], o, no)))
     return FALCON_ERR_INVALID_ARG;
   if (overlap(o, no, lse, nl)) return FALCON_ERR_INVALID_ARG;
-  if (!workspace || workspace_bytes < falcon_attn_prompt_workspace_size(p) || misaligned(workspace, 256))
+  const size_t need = falcon_attn_prompt_workspace_size(p);
+  for (int i = 0; i < 3; ++i)
+    if (overlap(workspace, need, ins[i], nin[i])) return FALCON_ERR_INVALID_ARG;
+  if (overlap(workspace, need, o, no) || overlap(workspace, need, lse, nl)) return FALCON_ERR_INVALID_ARG;
+  if (!workspace || workspace_bytes < need || misaligned(workspace, 256))
     return FALCON_ERR_WORKSPACE;
   const PromptArgs a{p->B, p->Hq, p->Hkv, p->d, static_cast<int>(most_rows(p)), scale_of(p), p->tokens, p->k_tokens,
                      rows_in(p, q, p->q_stride, p->Hq), rows_in(p, k, p->k_stride, p->Hkv),

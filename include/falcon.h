@@ -350,7 +350,9 @@ int falcon_backward(const falcon_params_t* p, const void* q, const void* k, cons
  * Layouts: q [tokens, Hq, d], k and v [tokens, Hkv, d] in the params' dtype,
  * tokens of all sequences packed one after the other, heads and dims dense,
  * q_stride / k_stride / v_stride / o_stride elements from one token to the
- * next (0 = dense; larger for slices of a fused projection).  Query head h
+ * next (0 = dense; larger for slices of a fused projection).  Results and
+ * workspaces must not lie over one another or over what a call reads (the cache
+ * among it).  Query head h
  * reads key / value head h / (Hq / Hkv).  FALCON_ERR_UNSUPPORTED past 2^31 - 1024
  * rows or keys of one sequence, k_tokens above that, or (Hq + Hkv) d above
  * 2^31 - 1; for attn_decode also past 2^31 units of 64 keys in the batch. */

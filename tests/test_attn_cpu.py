@@ -147,6 +147,23 @@ def test_rows_that_share_bytes_in_a_fused_projection(F):
     _refused(F, -1, F.falcon_attn_prompt, p, q, k, v, X[3], X[4], v + 128 * 2, None, X[9], 256, 0)
 
 
+def test_results_over_the_cache_or_the_workspace(F):
+    """Neither a result nor the workspace may lie over what the call reads or over one another."""
+    p, cache = _p(F), dict(zip(("k", "v", "k_scale", "v_scale"), X[4:8]))
+    n, last = F.falcon_attn_decode_workspace_size(p), 9 * 2 * 64 * 64 - 2  # of the codes
+    dec = lambda q, o, lse, ws: _refused(F, -1, F.falcon_attn_decode, p, q, cache, X[8], X[1], o, lse, ws, n, 0)  # noqa: E731
+    for at in X[4:8] + [X[4] + last, X[5] + last - 2]:
+        dec(X[0], at, None, X[9])
+        dec(X[0], X[2], at & ~3, X[9])
+    for at in X[4:8] + [X[4] + 256, X[0], X[2], X[3]]:
+        dec(X[0], X[2], X[3], at)
+    dec(X[0], X[2], X[0], X[9])      # lse over the queries
+    prompt = lambda o, lse, ws: _refused(F, -1, F.falcon_attn_prompt, p, X[0], X[1], X[2], X[3], X[4], o, lse, ws,  # noqa: E731
+                                         256, 0)
+    for at in X[0:3] + [X[5], X[6], X[0] + 10 * 8 * 64 * 2 - 256]:
+        prompt(X[5], X[6], at)
+
+
 @pytest.mark.parametrize("kw,code", [(dict(page=48), -2), (dict(page=256), -2), (dict(B=0), -1), (dict(num_pages=0), -1),
                                      (dict(max_pages=-1), -1)])
 def test_cache_settings(F, kw, code):

@@ -79,19 +79,26 @@ __device__ __forceinline__ void product(float (&d)[4], const uint32_t (&a)[NP][4
 }
 
 template <typename T, int D>
-__global__ void __launch_bounds__(128) attn_prompt_kernel(PromptArgs a, int qblocks) {
+__global__ void __launch_bounds__(128) attn_prompt_kernel(PromptArgs a, int qblocks, bool packed) {
   constexpr int NP = sizeof(T) == 4 ? 2 : 1, LD = D + 4, NT = kKeys / 8;
   extern __shared__ float smem[];
   float *sq = smem, *sk = sq + kRows * LD, *sv = sk + kKeys * LD;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, gid = lane >> 2, tig = lane & 3;
   if (blockIdx.x == 0 && threadIdx.x == 0) *static_cast<uint32_t*>(a.ws) = 0;  // the status: no wait here can run out
-  const uint32_t bh = static_cast<uint32_t>(a.B) * a.Hq, at = blockIdx.x % bh;
-  const int qb = qblocks - 1 - static_cast<int>(blockIdx.x / bh);  // the longest rows first
-  const int b = static_cast<int>(at) / a.Hq, h = static_cast<int>(at) % a.Hq, hk = h / (a.Hq / a.Hkv);
+  int b, h, row0;
+  if (packed) {
+    const int2 x = packed_block(a.cu_q, a.B, kRows, static_cast<int>(blockIdx.x / a.Hq));
+    b = x.x, row0 = x.y, h = static_cast<int>(blockIdx.x % a.Hq);
+  } else {
+    const uint32_t bh = static_cast<uint32_t>(a.B) * a.Hq, at = blockIdx.x % bh;
+    b = static_cast<int>(at) / a.Hq, h = static_cast<int>(at) % a.Hq;
+    row0 = (qblocks - 1 - static_cast<int>(blockIdx.x / bh)) * kRows;  // the longest rows first
+  }
+  const int hk = h / (a.Hq / a.Hkv);
   const int64_t q0 = a.cu_q[b], k0 = a.cu_k[b];
   const int lq_all = static_cast<int>(a.cu_q[b + 1] - q0), lk = static_cast<int>(a.cu_k[b + 1] - k0);
-  const int lq = min(lq_all, a.max_q), off = lk - lq_all, row0 = qb * kRows;
-  if (row0 >= lq || q0 < 0 || k0 < 0 || q0 + lq_all > a.tokens || k0 + lk > a.k_tokens) return;
+  const int lq = min(lq_all, a.max_q), off = lk - lq_all;
+  if (row0 < 0 || row0 >= lq || q0 < 0 || k0 < 0 || q0 + lq_all > a.tokens || k0 + lk > a.k_tokens) return;
   const T* q = static_cast<const T*>(a.q.p) + q0 * a.q.stride + static_cast<int64_t>(h) * D;
   const T* k = static_cast<const T*>(a.k.p) + k0 * a.k.stride + static_cast<int64_t>(hk) * D;
   const T* v = static_cast<const T*>(a.v.p) + k0 * a.v.stride + static_cast<int64_t>(hk) * D;
@@ -266,13 +273,13 @@ __global__ void __launch_bounds__(128) attn_prompt_kernel(PromptArgs a, int qblo
 
 template <typename T, int D>
 int launch(const PromptArgs& a, cudaStream_t s) {
-  const int64_t qblocks = (static_cast<int64_t>(a.max_q) + kRows - 1) / kRows;
-  const int64_t heads = static_cast<int64_t>(a.B) * a.Hq, n = qblocks * heads;
-  if (heads > INT32_MAX || n < 1 || n > INT32_MAX) return FALCON_ERR_UNSUPPORTED;
+  const PromptGrid g = prompt_grid(a, kRows);
+  if (g.blocks < 1 || g.blocks > INT32_MAX / a.Hq) return FALCON_ERR_UNSUPPORTED;
+  const int64_t n = g.blocks * a.Hq;
   constexpr size_t smem = static_cast<size_t>(kRows + 2 * kKeys) * (D + 4) * 4;
   const auto kern = attn_prompt_kernel<T, D>;
   if (!set_smem_limit(reinterpret_cast<const void*>(kern), smem)) return FALCON_ERR_CUDA;
-  kern<<<static_cast<unsigned>(n), 128, smem, s>>>(a, static_cast<int>(qblocks));
+  kern<<<static_cast<unsigned>(n), 128, smem, s>>>(a, static_cast<int>(g.blocks / a.B), g.packed);
   return cudaGetLastError() == cudaSuccess ? FALCON_OK : FALCON_ERR_CUDA;
 }
 template <typename T>

@@ -73,7 +73,7 @@ struct Bars {
   Item<1> item[2];  // whose queries the buffers hold (d = 64)
   uint32_t tmem;
   uint32_t stop;    // some row has to be computed again: no more blocks are asked for
-  uint2 again[4][4];  // (block, rows) of them: 4 entries a warp
+  uint2 again[4][4];  // (block, rows) of them: 4 entries a warp (d = 64)
   float row[2][kTile];  // of each tile: what the two threads of a row tell each other
 };
 
@@ -90,6 +90,7 @@ struct Cfg {
   static constexpr bool kLoop = D == 64;                  // a CTA takes one block of queries after another, or one
   static constexpr int kQBufs = kLoop ? 2 : 1;            // query buffers
   static constexpr int kSmem = (kQBufs * kTiles + kStages) * kTileBytes + 1024 + static_cast<int>(sizeof(Bars));
+  static_assert(kSmem <= 227 * 1024, "more shared memory than a CTA can have");
   // d = 64 leaves room for P beside S, so that S of the next keys is formed
   // while the softmax of these runs; at d = 128 P lies over S
   static constexpr bool kAhead = D == 64;
@@ -99,7 +100,8 @@ struct Cfg {
 
 struct TcArgs {
   PromptArgs a;
-  int qblocks;
+  int qblocks;  // of a sequence
+  bool packed;
   uint32_t* status;
   uint64_t limit;
   int stall;
@@ -191,18 +193,23 @@ __device__ __forceinline__ Item<TILES> item_at(const TcArgs& t, uint32_t id) {
   const PromptArgs& a = t.a;
   Item<TILES> w;
   w.id = id;
-  // the longest rows first: blocks of queries descend, sequences and heads within
-  const uint32_t bh = static_cast<uint32_t>(a.B) * a.Hq, at = id % bh;
-  const int qb = t.qblocks - 1 - static_cast<int>(id / bh), b = static_cast<int>(at) / a.Hq;
-  w.h = static_cast<int>(at) % a.Hq;
+  int b;
+  if (t.packed) {
+    const int2 x = packed_block(a.cu_q, a.B, TILES * kTile, static_cast<int>(id / a.Hq));
+    b = x.x, w.row0 = x.y, w.h = static_cast<int>(id % a.Hq);
+  } else {
+    // the longest rows first: blocks of queries descend, sequences and heads within
+    const uint32_t bh = static_cast<uint32_t>(a.B) * a.Hq, at = id % bh;
+    b = static_cast<int>(at) / a.Hq, w.h = static_cast<int>(at) % a.Hq;
+    w.row0 = (t.qblocks - 1 - static_cast<int>(id / bh)) * TILES * kTile;
+  }
   w.hk = w.h / (a.Hq / a.Hkv);
   w.q0 = a.cu_q[b], w.k0 = a.cu_k[b];
   const int lq_all = static_cast<int>(a.cu_q[b + 1] - w.q0);
   w.lk = static_cast<int>(a.cu_k[b + 1] - w.k0);
   w.lq = min(lq_all, a.max_q);
   w.off = w.lk - lq_all;
-  w.row0 = qb * TILES * kTile;
-  w.valid = w.row0 < w.lq && w.q0 >= 0 && w.k0 >= 0 && w.q0 + lq_all <= a.tokens && w.k0 + w.lk <= a.k_tokens;
+  w.valid = w.row0 >= 0 && w.row0 < w.lq && w.q0 >= 0 && w.k0 >= 0 && w.q0 + lq_all <= a.tokens && w.k0 + w.lk <= a.k_tokens;
   w.nmax = 0;
 #pragma unroll
   for (int x = 0; x < TILES; ++x) {
@@ -253,7 +260,7 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, Cfg<D>::kCtas)
     mbar_init(&bar->stall, 1);
     mbar_init(&bar->answer, 1);
     bar->stop = 0;
-    if (C::kLoop)
+    if constexpr (C::kLoop)
       for (int i = 0; i < 16; ++i) bar->again[i >> 2][i & 3].y = 0;
     fence_mbar_init();
   }
@@ -742,20 +749,20 @@ template <int D>
 int launch_tc(const PromptArgs& a, cudaStream_t s) {
   TcArgs t;
   t.a = a;
-  constexpr int64_t rows = Cfg<D>::kTiles * kTile;  // of a block
-  t.qblocks = static_cast<int>((a.max_q + rows - 1) / rows);
+  const PromptGrid g = prompt_grid(a, Cfg<D>::kTiles * kTile);
+  if (g.blocks < 1 || g.blocks > INT32_MAX / a.Hq) return FALCON_ERR_UNSUPPORTED;
+  t.qblocks = static_cast<int>(g.blocks / a.B);
+  t.packed = g.packed;
   t.status = static_cast<uint32_t*>(a.ws);
   t.limit = wait_limit_ns();
   t.stall = take_test_stall() ? 1 : 0;
-  const int64_t heads = static_cast<int64_t>(a.B) * a.Hq, n = t.qblocks * heads;
-  if (heads > INT32_MAX || n < 1 || n > INT32_MAX) return FALCON_ERR_UNSUPPORTED;
   CUtensorMap mq, mk, mv;
   if (!make_rows_map(&mq, a.q, a.tokens, a.Hq, a.d) || !make_rows_map(&mk, a.k, a.k_tokens, a.Hkv, a.d) ||
       !make_rows_map(&mv, a.v, a.k_tokens, a.Hkv, a.d))
     return FALCON_ERR_CUDA;
   const auto kern = attn_prompt_tc_kernel<D>;
   if (!set_smem_limit(reinterpret_cast<const void*>(kern), Cfg<D>::kSmem)) return FALCON_ERR_CUDA;
-  kern<<<static_cast<unsigned>(n), Cfg<D>::kThreads, Cfg<D>::kSmem, s>>>(mq, mk, mv, t);
+  kern<<<static_cast<unsigned>(g.blocks * a.Hq), Cfg<D>::kThreads, Cfg<D>::kSmem, s>>>(mq, mk, mv, t);
   return cudaGetLastError() == cudaSuccess ? FALCON_OK : FALCON_ERR_CUDA;
 }
 

@@ -652,6 +652,33 @@ def test_no_bound_on_the_rows_of_a_sequence(F, dtype, Hq, d):
         assert torch.equal(o, o2) and torch.equal(lse, lse2)
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("Hq,Hkv,d", [(3, 1, 64), (2, 2, 128), (4, 2, 16)])
+def test_many_prompts_under_a_loose_bound(F, dtype, Hq, Hkv, d):
+    """Blocks dealt out by the tokens instead of the bound: lengths around multiples of a block and of zero, fewer and
+    more keys than queries, the same bits as with the longest length."""
+    lq = [0, 1, 127, 128, 129, 0, 0, 255, 256, 257, 63, 64, 65, 300, 2, 0, 511, 512, 5] + [3] * 40 + [0]
+    lk = [max(0, n + (0, 150, -n, -30, 1)[i % 5]) for i, n in enumerate(lq)]
+    q, k, v, cq, ck = _prompt_case(lq, lk, Hq, Hkv, d, dtype, 65, 1)
+    o, lse = _prompt(F, q, k, v, cq, ck, 512)
+    want, want_lse = O.prompt(_np(q), _np(k), _np(v), cq, ck, d ** -0.5)
+    _check_attention(o, lse, want, want_lse, max(1.0, v.abs().max().item()), dtype, 1.25 * U)
+    for bound in (0, 2**31 - 1, 2048):
+        o2, lse2 = _prompt(F, q, k, v, cq, ck, bound)
+        assert torch.equal(o, o2) and torch.equal(lse, lse2)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("d", [64, 128])
+def test_a_loose_bound_costs_little(F, dtype, d):
+    """256 prompts of 128 tokens, the longest length left out: within three times the call with it (some 35 times where
+    every sequence had the blocks of all tokens)."""
+    n, B = 128, 256
+    q, k, v, cq, _ = _prompt_case([n] * B, [n] * B, 12, 12, d, dtype, 66)
+    cu = torch.from_numpy(cq).cuda()
+    assert _prompt_ms(F, q, k, v, cu, 0) < 3 * _prompt_ms(F, q, k, v, cu, n)
+
+
 def test_no_bound_on_the_tokens_appended(F):
     lens, B = [3, 40, 17] * 6, 18
     cu = torch.from_numpy(np.concatenate([[0], np.cumsum(lens)]).astype(np.int32)).cuda()
@@ -697,13 +724,13 @@ def test_prompt_rows_computed_again_are_no_timeout(F, d):
         assert ((o[:, h, rest].double() - want).abs() <= U * want.abs() + 1.25 * U * 5).all()
 
 
-def _prompt_ms(F, q, k, v, cu):
+def _prompt_ms(F, q, k, v, cu, max_q=None):
     """The quicker of two calls after a first one."""
     ms = []
     for _ in range(3):
         a, b = (torch.cuda.Event(enable_timing=True) for _ in "ab")
         a.record()
-        F.attn_prompt(q, k, v, cu, max_q=q.shape[0])
+        F.attn_prompt(q, k, v, cu, max_q=q.shape[0] if max_q is None else max_q)
         b.record()
         b.synchronize()
         ms.append(a.elapsed_time(b))

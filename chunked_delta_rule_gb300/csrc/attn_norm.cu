@@ -14,6 +14,7 @@
 // 9984 x (12 + 4) of 64, fp32: 82 MB in 18.5 us with the launch.
 
 #include "attn.cuh"
+#include "tc_util.cuh"
 
 namespace falcon {
 namespace {
@@ -104,9 +105,10 @@ static int launch_norm(const HeadArgs& h, int64_t tokens, int Hq, int Hkv, RowsI
   if (!k.p) Hkv = 0;
   if (tokens == 0 || Hq + Hkv == 0) return FALCON_OK;
   const bool vec = (!q.p || (q.vec && qo.vec)) && (!k.p || (k.vec && ko.vec));
-  // a warp a token where that fills the card (32768 tokens x 20 heads of 128: 74 us, with three warps a token
+  // a warp a token where that gives every SM 32 of them (32768 tokens x 20 heads of 128: 74 us, with three warps a token
   // 88), else a warp for every kBatch passes
-  const int all = (Hq + Hkv + 256 / h.d - 1) / (256 / h.d), parts = tokens >= 152 * 32 ? 1 : (all + kBatch - 1) / kBatch;
+  const int all = (Hq + Hkv + 256 / h.d - 1) / (256 / h.d);
+  const int parts = tokens >= int64_t(32) * tcu::sm_count() ? 1 : (all + kBatch - 1) / kBatch;
   const int64_t blocks = (tokens + 7) / 8;
   if (blocks > INT32_MAX || parts > 65535) return FALCON_ERR_UNSUPPORTED;
   const dim3 g(static_cast<unsigned>(blocks), static_cast<unsigned>(parts));

@@ -592,7 +592,8 @@ def _rope_fields(d: int, table, layout: int, norm: bool, norm_eps: float) -> dic
 def qk_norm_rope(q, k, positions=None, table=None, w_q=None, w_k=None, norm: bool = True, norm_eps: float = 1e-6,
                  layout: int = FALCON_ROPE_HALF, stream=None):
     """Norm and rotation of q [tokens, Hq, d] and k [tokens, Hkv, d] (k may be
-    None): returns (q_out, k_out), dense.  table None: no rotation."""
+    None): returns (q_out, k_out), dense.  table None: no rotation.  Forward
+    only: the results carry no gradient, also where an input requires one."""
     import torch
     _, Hq, d = q.shape
     p = AttnParams(Hq=Hq, Hkv=Hq if k is None else k.shape[1], d=d, dtype=_attn_dtype(q), tokens=q.shape[0],
@@ -642,7 +643,7 @@ def kv_append(cache: dict, k, v, cu_new, ctx_lens, block_table, max_new: int, ta
               norm: bool = False, norm_eps: float = 1e-6, layout: int = FALCON_ROPE_HALF, stream=None) -> None:
     """Append k, v [tokens, Hkv, d] to the cache in place; cu_new int32 [B + 1],
     ctx_lens int32 [B], block_table int32 [B, max_pages]; max_new is at least
-    the most tokens of one sequence."""
+    the most tokens of one sequence.  No gradient passes through the cache."""
     import torch
     f = _cache_fields(cache, block_table, k)
     B = block_table.shape[0]
@@ -663,7 +664,8 @@ def kv_append(cache: dict, k, v, cu_new, ctx_lens, block_table, max_new: int, ta
 
 
 def attn_decode(q, cache: dict, block_table, lens, max_len: int, scale: float = 0.0, want_lse=False, stream=None):
-    """One token per sequence: q [B, Hq, d], lens int32 [B] (at most max_len) -> o, or (o, lse)."""
+    """One token per sequence: q [B, Hq, d], lens int32 [B] (at most max_len) -> o, or (o, lse).  Forward only: the
+    results carry no gradient."""
     import torch
     f = _cache_fields(cache, block_table, q)
     if q.shape[0] != block_table.shape[0] or lens.shape != (q.shape[0],) or q.shape[2] != f["d"]:
@@ -683,7 +685,9 @@ def attn_decode(q, cache: dict, block_table, lens, max_len: int, scale: float = 
 def attn_prompt(q, k, v, cu_q, cu_k=None, max_q: int = 0, scale: float = 0.0, want_lse=False, stream=None):
     """Causal attention over packed prompts: q [tokens, Hq, d], k and v
     [k_tokens, Hkv, d], cu_q / cu_k int32 [B + 1] (cu_k None: cu_q), max_q at
-    least the longest sequence's rows of q (0: all of them) -> o, or (o, lse)."""
+    least the longest sequence's rows of q (0: all of them; the exact bound is
+    the quickest) -> o, or (o, lse).  Forward only: the results carry no
+    gradient, also where an input requires one."""
     import torch
     cu_k = cu_q if cu_k is None else cu_k
     if k.shape != v.shape or k.shape[2] != q.shape[2] or k.dtype != q.dtype or v.dtype != q.dtype:

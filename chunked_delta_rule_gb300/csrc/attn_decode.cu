@@ -27,16 +27,17 @@
 // their tile and head, a power of two found with three shuffles, and the tile's
 // products are added to the fp32 sums times that power and the page's V scale: no
 // weight and no V scale is lost to another tile's.  (Halves relative to what the warp
-// had met before would drop weights under 2^-31 of the largest, or values beside a
-// page of a larger scale; they took 66 and 39 us where these take 69 and 41.)  Sums of their own for every tile are also what keeps fp32
-// results: the tensor cores cut their sums off, which adds up over the keys.  The
-// running reference m moves only when a score passes it by more than 8.
+// had met before lose the bits of weights under 2^-20 of the largest, or values
+// beside a page of a larger scale; they took 66 and 39 us where these take 70 and 40.)  Sums
+// of their own for every tile are also what keeps fp32 results: the tensor cores
+// cut their sums off, which adds up over the keys.  The running reference m moves
+// only when a score passes it by more than 8.
 //
 // Every CTA gets the same number of keys (the lengths are known on the device
 // only); a second kernel joins the rows that several CTAs share.
 // Measured: 256 sequences of 410 .. 2048 keys, 16 / 4 heads of 128: 325 MB of
-// codes in 69 us, 4.7 TB/s (about 4 us a row and CTA around the stream; fp32: 84 us);
-// 2 of <= 131072 keys, 16 / 2 heads of 128: 41 us (fp32: 43); 1 x 777 keys: 10.2 us,
+// codes in 70 us, 4.7 TB/s (about 4 us a row and CTA around the stream; fp32: 84 us);
+// 2 of <= 131072 keys, 16 / 2 heads of 128: 40 us (fp32: 43); 1 x 777 keys: 10.2 us,
 // the call.
 // Waits are bounded and reported through the workspace's status word.
 
@@ -649,10 +650,11 @@ __global__ void __launch_bounds__(256) attn_decode_join_kernel(const DecodeArgs 
 
 
 
-// Few keys a row: a CTA for each row, one launch (256 rows of 500 keys, 4 key
-// heads of 128: 31 us, in equal shares 37).  Otherwise as many CTAs as the card
-// holds at a time, each with the same number of units, so that none waits for
-// a longer one (256 rows of 400 .. 2048 keys: 68 us, with chunks of 1024 keys 75).
+// Few keys a row: a CTA for each row, one launch (measured when the batch below
+// took 68 us: 256 rows of 500 keys, 4 key heads of 128 31 us, in equal shares
+// 37).  Otherwise as many CTAs as the card holds at a time, each with the same
+// number of units, so that none waits for a longer one (256 rows of 410 .. 2048
+// keys: 68 us, with chunks of 1024 keys 75).
 DecodePlan decode_plan(int B, int Hq, int Hkv, int d, int elem, int max_k) {
   DecodePlan p;
   const int G = Hq / Hkv;

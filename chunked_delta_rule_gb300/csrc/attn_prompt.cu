@@ -17,8 +17,8 @@
 //
 // Bound by the chain of a row block: products of three parts, the splits, the
 // softmax, tile after tile.  Measured: 7 prompts of <= 333, 12 / 4 heads of 64,
-// fp32: 37 us with the call; 8 x 1024 x 12 x 64, fp32: 274 us (233 without the sums
-// apart).
+// fp32: 37 us with the call; 8 x 1024 x 12 x 64, fp32: 261 us (the sums apart cost some
+// 40 of them).
 //
 // Keys that no row of the tile sees are not touched, tile rows past the last key
 // are zeros.  A row whose result is not finite (a masked key of its own

@@ -17,14 +17,14 @@
 // S | P | O at d = 64.  Rows of 16 and 32 dims run as 64, the rest zeros from the
 // TMA copies: 8 x 2048 x 12 heads of 32 take 64 us, 248 with warp-level tf32 MMAs.
 // The grid has a block for every 256 (128) queries and head, the longest rows
-// first.  At d = 64, where a block is over in 2 to 20 us, a CTA that nears its
+// first where max_q is near the lengths.  At d = 64, where a block is over in 2 to 20 us, a CTA that nears its
 // end asks for one of those that have not begun and goes on with it: the next
 // queries come while the last rows are written.  8 x 2048 x 12 heads: 77 us with
 // a CTA a block, 66 so, 70 with the blocks dealt out beforehand; 8 ragged prompts
 // of <= 2048: 47, 39 and 63 us.
-// Measured: 8 x 2048 x 12 heads, d = 64: 66 us, 781 TFLOP/s, bound by the softmax
+// Measured: 8 x 2048 x 12 heads, d = 64: 67 us, 775 TFLOP/s, bound by the softmax
 // warps' latencies (half the issue slots, a third of the tensor cores' time);
-// 16384 x 16/4 heads, d = 128: 720 us, 1527 TFLOP/s, bound by the products in the
+// 16384 x 16/4 heads, d = 128: 714 us, 1540 TFLOP/s, bound by the products in the
 // main loop.  (Both with the flops of the visible pairs alone.)
 //
 // The reference m of a row is the maximum of its first tile.  Weights, sums and

@@ -403,7 +403,8 @@ int falcon_rope_table(const double* inv_freq, int32_t rot, int32_t rows, float m
 /* Norm of queries and keys for each head and rotation, one pass:
  *   y = x / sqrt(mean(x^2) + norm_eps) * w     (qk_norm; w_q, w_k fp32 [d], NULL = ones)
  *   (a, b) -> (a c - b s, b c + a s)           on the rot/2 pairs, (c, s) = table[position, i]
- * fp32 arithmetic, rounded once to the dtype.  q -> q_out (row stride
+ * fp32 arithmetic, rounded once to the dtype (a row whose sum of squares passes
+ * fp32's range gives 0).  q -> q_out (row stride
  * o_stride, 0 = dense), k -> k_out (dense); q or k may be NULL (skipped).  An
  * output may be its own input when their strides agree (in place, also inside
  * a fused projection), and its rows must not share a byte with another
@@ -447,8 +448,11 @@ size_t falcon_attn_decode_workspace_size(const falcon_attn_params_t* p);
  * lens[b] <= 0 gives o = 0 and lse = -inf.  Whatever lies in the slots past
  * lens[b] is not used.  Keys of a page whose block_table entry is outside
  * [0, num_pages) are masked.  o [B, Hq, d] with row stride o_stride.  One
- * kernel, or two where max_k is larger; waits on copies are bounded and
- * reported through falcon_workspace_status(workspace, stream).
+ * kernel where max_k <= 512, or <= 1024 at d < 128 with at least three rows of
+ * work (sequence, key head, group of 8 query heads) an SM; else two.  Waits on
+ * copies are bounded and reported through falcon_workspace_status(workspace,
+ * stream).  Any scale byte of a page will do: each weight is rounded relative
+ * to its own tile's largest (11 bits for bf16, 22 for fp32).
  * Errors: FALCON_ERR_INVALID_ARG, FALCON_ERR_UNSUPPORTED (dims, page sizes, a
  * cache of 2^38 bytes or more), FALCON_ERR_WORKSPACE, FALCON_ERR_CUDA. */
 int falcon_attn_decode(const falcon_attn_params_t* p, const void* q, const falcon_kv_cache_t* cache,
@@ -464,12 +468,14 @@ size_t falcon_attn_prompt_workspace_size(const falcon_attn_params_t* p);
  * aligned at the end: query i sees the keys j <= i + lk - lq.  A row that
  * sees no key gives o = 0 and lse = -inf.  o [tokens, Hq, d] with row stride
  * o_stride, lse fp32 [tokens, Hq] (NULL = not wanted).  Rows of q past max_q
- * of their sequence are not computed; the exact bound is the quickest (the
+ * of their sequence are not computed.  Any max_q will do; the exact bound is the quickest (the
  * tokens of all sequences as the bound: 1.1 to 1.5 times the time for 16 prompts
  * of 1024 tokens and 256 of 128).  bf16 rows on 16-byte boundaries run
  * their products on the tensor cores with bounded waits, reported through
  * falcon_workspace_status(workspace, stream) as for the chunk forward; fp32,
- * other alignments and calls of a few short prompts take a warp-level kernel.
+ * other alignments and calls of a few short prompts take a warp-level kernel
+ * (bf16 rows off the 16-byte boundaries 4 to 11 times as long as on them).  The
+ * bf16 weights are rounded to 8 bits on the tensor cores, to 11 there.
  * Errors: FALCON_ERR_INVALID_ARG, FALCON_ERR_UNSUPPORTED,
  * FALCON_ERR_WORKSPACE, FALCON_ERR_CUDA. */
 int falcon_attn_prompt(const falcon_attn_params_t* p, const void* q, const void* k, const void* v,

@@ -669,6 +669,31 @@ def test_many_prompts_under_a_loose_bound(F, dtype, Hq, Hkv, d):
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("d", [32, 64, 128])
+def test_rows_computed_again_in_every_grid(F, dtype, d):
+    """An infinity in one dim of each third prompt's second value: the rows that see it are infinite there and right
+    elsewhere, those that do not see it are right (some of both are computed again), the same bits whichever way the
+    blocks are dealt out."""
+    lq = [2 + 37 * i % 300 for i in range(90)]
+    q, k, v, cq, ck = _prompt_case(lq, lq, 6, 2, d, dtype, 67)
+    clean, clean_lse = _prompt(F, q, k, v, cq, ck, max(lq))
+    hit = torch.zeros(q.shape[0], dtype=torch.bool, device="cuda")
+    for b in range(0, 90, 3):
+        v[cq[b] + 1, :, 3] = float("inf")
+        hit[cq[b] + 1:cq[b + 1]] = True
+    got = [_prompt(F, q, k, v, cq, ck, bound) for bound in (max(lq), 2**31 - 1)]
+    assert torch.equal(got[0][0], got[1][0]) and torch.equal(got[0][1], got[1][1])
+    o, lse = got[0]
+    rest = [i for i in range(d) if i != 3]
+    assert torch.isinf(o[hit][:, :, 3]).all()
+    # two roundings of the same rows: weights to 8 bits (bf16) in one of them, results to 8 bits in both
+    tol = (2 * U + 1.25 * U) * 5 if dtype == "bf16" else 2e-5 * 5
+    assert (o[hit][:, :, rest].float() - clean[hit][:, :, rest].float()).abs().max() <= tol
+    assert (o[~hit].float() - clean[~hit].float()).abs().max() <= tol
+    assert (lse - clean_lse).abs().max() <= 2e-5 * 10
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
 @pytest.mark.parametrize("d", [64, 128])
 def test_a_loose_bound_costs_little(F, dtype, d):
     """256 prompts of 128 tokens, the longest length left out: within three times the call with it (some 35 times where

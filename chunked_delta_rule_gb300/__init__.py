@@ -35,7 +35,8 @@ EXPORTED = [
     "falcon_varlen_workspace_size", "falcon_chunk_fwd_varlen", "falcon_workspace_status",
     "falcon_test_hooks", "falcon_rope_table", "falcon_qk_norm_rope", "falcon_kv_append",
     "falcon_attn_decode_workspace_size", "falcon_attn_decode", "falcon_attn_prompt_workspace_size",
-    "falcon_attn_prompt",
+    "falcon_attn_prompt", "falcon_attn_prompt_backward_workspace_size", "falcon_attn_prompt_backward",
+    "falcon_qk_norm_rope_backward_workspace_size", "falcon_qk_norm_rope_backward",
 ]
 
 
@@ -74,6 +75,11 @@ class AttnParams(ctypes.Structure):
 class falcon_kv_cache_t(ctypes.Structure):
     _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("k_scale", ctypes.c_void_p),
                 ("v_scale", ctypes.c_void_p)]
+
+
+class falcon_attn_grads_t(ctypes.Structure):
+    _fields_ = [("dq", ctypes.c_void_p), ("dk", ctypes.c_void_p), ("dv", ctypes.c_void_p)] + [
+        (n, ctypes.c_int64) for n in ("dq_stride", "dk_stride", "dv_stride", "do_stride")]
 
 
 _lib = None
@@ -135,6 +141,15 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
     lib.falcon_attn_prompt_workspace_size.restype = S
     lib.falcon_attn_prompt.argtypes = [A, V, V, V, V, V, V, V, V, S, V]
     lib.falcon_attn_prompt.restype = ctypes.c_int
+    G = ctypes.POINTER(falcon_attn_grads_t)
+    lib.falcon_attn_prompt_backward_workspace_size.argtypes = [A]
+    lib.falcon_attn_prompt_backward_workspace_size.restype = S
+    lib.falcon_attn_prompt_backward.argtypes = [A, V, V, V, V, V, V, V, V, V, G, V, S, V]
+    lib.falcon_attn_prompt_backward.restype = ctypes.c_int
+    lib.falcon_qk_norm_rope_backward_workspace_size.argtypes = [A]
+    lib.falcon_qk_norm_rope_backward_workspace_size.restype = S
+    lib.falcon_qk_norm_rope_backward.argtypes = [A, V, V, V, V, V, V, V, V, G, V, V, V, S, V]
+    lib.falcon_qk_norm_rope_backward.restype = ctypes.c_int
     lib.falcon_strerror.argtypes = [ctypes.c_int]
     lib.falcon_strerror.restype = ctypes.c_char_p
     lib.falcon_version.argtypes = []
@@ -417,6 +432,49 @@ def falcon_attn_prompt(p: AttnParams, q, k, v, cu_q, cu_k, o, lse, workspace, wo
     _check(code, "falcon_attn_prompt")
 
 
+def make_attn_grads(grads: dict | None, do_stride: int = 0) -> falcon_attn_grads_t | None:
+    """Gradient buffers {dq, dk, dv} [tokens, heads, d] (any may be None or left out; heads and dims dense) ->
+    falcon_attn_grads_t.  It holds addresses: keep the tensors while it is in use."""
+    if grads is None:
+        return None
+    x = [grads.get(n) for n in ("dq", "dk", "dv")]
+    strides = [0 if t is None or isinstance(t, int) or t.shape[0] < 2 else t.stride(0) for t in x]
+    return falcon_attn_grads_t(*(_ptr(t) for t in x), *strides, do_stride)
+
+
+def falcon_attn_prompt_backward_workspace_size(p: AttnParams) -> int:
+    return int(load_library().falcon_attn_prompt_backward_workspace_size(ctypes.byref(p)))
+
+
+def falcon_attn_prompt_backward(p: AttnParams, q, k, v, cu_q, cu_k, o, lse, dO, dlse, grads, workspace,
+                                workspace_bytes: int = 0, stream=None):
+    """grads: a falcon_attn_grads_t, or its dict as make_attn_grads takes it."""
+    if workspace is not None and not workspace_bytes and not isinstance(workspace, int):
+        workspace_bytes = workspace.numel() * workspace.element_size()
+    g = make_attn_grads(grads) if isinstance(grads, dict) else grads
+    code = load_library().falcon_attn_prompt_backward(
+        ctypes.byref(p), _ptr(q), _ptr(k), _ptr(v), _ptr(cu_q), _ptr(cu_k), _ptr(o), _ptr(lse), _ptr(dO), _ptr(dlse),
+        ctypes.byref(g) if g is not None else None, _ptr(workspace), workspace_bytes, _stream(stream))
+    _check(code, "falcon_attn_prompt_backward")
+
+
+def falcon_qk_norm_rope_backward_workspace_size(p: AttnParams) -> int:
+    return int(load_library().falcon_qk_norm_rope_backward_workspace_size(ctypes.byref(p)))
+
+
+def falcon_qk_norm_rope_backward(p: AttnParams, q, k, w_q, w_k, positions, table, dq_out, dk_out, grads, dw_q, dw_k,
+                                 workspace, workspace_bytes: int = 0, stream=None):
+    """grads: a falcon_attn_grads_t, or its dict as make_attn_grads takes it."""
+    if workspace is not None and not workspace_bytes and not isinstance(workspace, int):
+        workspace_bytes = workspace.numel() * workspace.element_size()
+    g = make_attn_grads(grads) if isinstance(grads, dict) else grads
+    code = load_library().falcon_qk_norm_rope_backward(
+        ctypes.byref(p), _ptr(q), _ptr(k), _ptr(w_q), _ptr(w_k), _ptr(positions), _ptr(table), _ptr(dq_out),
+        _ptr(dk_out), ctypes.byref(g) if g is not None else None, _ptr(dw_q), _ptr(dw_k), _ptr(workspace),
+        workspace_bytes, _stream(stream))
+    _check(code, "falcon_qk_norm_rope_backward")
+
+
 # ---------------------------------------------------------------- tensor helpers
 def alloc_workspace(nbytes: int, device="cuda"):
     """A 256-byte aligned byte buffer (torch's caching allocator aligns to 512)."""
@@ -592,8 +650,9 @@ def _rope_fields(d: int, table, layout: int, norm: bool, norm_eps: float) -> dic
 def qk_norm_rope(q, k, positions=None, table=None, w_q=None, w_k=None, norm: bool = True, norm_eps: float = 1e-6,
                  layout: int = FALCON_ROPE_HALF, stream=None):
     """Norm and rotation of q [tokens, Hq, d] and k [tokens, Hkv, d] (k may be
-    None): returns (q_out, k_out), dense.  table None: no rotation.  Forward
-    only: the results carry no gradient, also where an input requires one."""
+    None): returns (q_out, k_out), dense.  table None: no rotation.  The results
+    carry no gradient, also where an input requires one: qk_norm_rope_backward
+    forms it."""
     import torch
     _, Hq, d = q.shape
     p = AttnParams(Hq=Hq, Hkv=Hq if k is None else k.shape[1], d=d, dtype=_attn_dtype(q), tokens=q.shape[0],
@@ -686,8 +745,8 @@ def attn_prompt(q, k, v, cu_q, cu_k=None, max_q: int = 0, scale: float = 0.0, wa
     """Causal attention over packed prompts: q [tokens, Hq, d], k and v
     [k_tokens, Hkv, d], cu_q / cu_k int32 [B + 1] (cu_k None: cu_q), max_q at
     least the longest sequence's rows of q (0: all of them; the exact bound is
-    the quickest) -> o, or (o, lse).  Forward only: the results carry no
-    gradient, also where an input requires one."""
+    the quickest) -> o, or (o, lse).  The results carry no gradient, also where
+    an input requires one: attn_prompt_backward forms it from o and lse."""
     import torch
     cu_k = cu_q if cu_k is None else cu_k
     if k.shape != v.shape or k.shape[2] != q.shape[2] or k.dtype != q.dtype or v.dtype != q.dtype:
@@ -708,6 +767,101 @@ def attn_prompt(q, k, v, cu_q, cu_k=None, max_q: int = 0, scale: float = 0.0, wa
         ws = alloc_workspace(falcon_attn_prompt_workspace_size(p), q.device)
         falcon_attn_prompt(p, q, k, v, cu_q, cu_k, o, lse, ws, 0, stream)
     return (o, lse) if want_lse else o
+
+
+def _grad_buffers(want: dict, ref, out: dict | None) -> dict:
+    """Gradients by name, of the shapes in ``want``: those in ``out``, else zeros (which rows behind the last sequence
+    keep)."""
+    import torch
+    out = out or {}
+    if set(out) - set(want):
+        raise ValueError(f"out: {', '.join(want)} are wanted, not {', '.join(sorted(out))}")
+    g = {}
+    for n, shape in want.items():
+        x = out.get(n)
+        if x is None:
+            x = torch.zeros(shape, dtype=ref.dtype, device=ref.device)
+        elif tuple(x.shape) != tuple(shape) or x.dtype != ref.dtype:
+            raise ValueError(f"{n}: {tuple(shape)} of {ref.dtype} is wanted, not {tuple(x.shape)} of {x.dtype}")
+        _like(x, ref, n)
+        _token_stride(x, n)
+        g[n] = x
+    return g
+
+
+def attn_prompt_backward(q, k, v, o, lse, dO, cu_q, cu_k=None, max_q: int = 0, scale: float = 0.0, dlse=None,
+                         out: dict | None = None, stream=None) -> dict:
+    """Gradients {dq, dk, dv} of attn_prompt(q, k, v, cu_q, cu_k, max_q, scale, want_lse=True) with results o and lse:
+    dO [tokens, Hq, d] is the gradient of o, dlse fp32 [tokens, Hq] that of lse (None: zero).  ``out`` may hold buffers
+    for some of the three, slices of one fused gradient among them; the others are allocated.  Rows behind the last
+    sequence are 0 in what is allocated and left as they are in ``out``."""
+    import torch
+    cu_k = cu_q if cu_k is None else cu_k
+    if k.shape != v.shape or k.shape[2] != q.shape[2] or k.dtype != q.dtype or v.dtype != q.dtype:
+        raise ValueError("k and v: [k_tokens, Hkv, d] with q's d and dtype are wanted")
+    if cu_q.dim() != 1 or cu_q.shape != cu_k.shape or cu_q.numel() < 2:
+        raise ValueError("cu_q and cu_k: [B + 1] are wanted")
+    for x, name in ((o, "o"), (dO, "dO")):
+        if x.shape != q.shape or x.dtype != q.dtype:
+            raise ValueError(f"{name}: {tuple(q.shape)} of {q.dtype}, as q, is wanted")
+        _like(x, q, name)
+    if lse.shape != q.shape[:2] or (dlse is not None and dlse.shape != q.shape[:2]):
+        raise ValueError("lse and dlse: [tokens, Hq] are wanted")
+    _like(k, q, "k")
+    _like(v, q, "v")
+    for x, name, t in ((lse, "lse", torch.float32), (dlse, "dlse", torch.float32), (cu_q, "cu_q", torch.int32),
+                       (cu_k, "cu_k", torch.int32)):
+        _like(x, q, name, t)
+    n, Hq, d = q.shape
+    p = AttnParams(B=cu_q.numel() - 1, Hq=Hq, Hkv=k.shape[1], d=d, dtype=_attn_dtype(q), max_q=max_q or n, tokens=n,
+                   k_tokens=k.shape[0], scale=scale, q_stride=_token_stride(q, "q"), k_stride=_token_stride(k, "k"),
+                   v_stride=_token_stride(v, "v"), o_stride=_token_stride(o, "o"))
+    with _on(stream):
+        g = _grad_buffers({"dq": q.shape, "dk": k.shape, "dv": v.shape}, q, out)
+        ws = alloc_workspace(falcon_attn_prompt_backward_workspace_size(p), q.device)
+        falcon_attn_prompt_backward(p, q, k, v, cu_q, cu_k, o, lse, dO, dlse,
+                                    make_attn_grads(g, _token_stride(dO, "dO")), ws, 0, stream)
+    return g
+
+
+def qk_norm_rope_backward(q, k, dq_out, dk_out=None, positions=None, table=None, w_q=None, w_k=None, norm: bool = True,
+                          norm_eps: float = 1e-6, layout: int = FALCON_ROPE_HALF, out: dict | None = None,
+                          stream=None) -> dict:
+    """Gradients of qk_norm_rope(q, k, positions, table, ...): {dq, dk} from dq_out [tokens, Hq, d] and dk_out [tokens,
+    Hkv, d] (k and dk_out may be None), and with the norm dw_q, dw_k (fp32 [d], also where the weights are None: ones).
+    ``out`` may hold buffers for dq and dk, slices of one fused gradient or dq_out, dk_out themselves."""
+    import torch
+    _, Hq, d = q.shape
+    if (k is None) != (dk_out is None):
+        raise ValueError("k and dk_out: both or neither are wanted")
+    if k is not None and (k.shape[0] != q.shape[0] or k.shape[2] != d or k.dtype != q.dtype):
+        raise ValueError("q and k differ in tokens, head dim or dtype")
+    for x, y, name in ((q, dq_out, "dq_out"), (k, dk_out, "dk_out")):
+        if x is not None and (y.shape != x.shape or y.dtype != x.dtype):
+            raise ValueError(f"{name}: {tuple(x.shape)} of {x.dtype} is wanted")
+    if table is not None and (positions is None or positions.shape != (q.shape[0],)):
+        raise ValueError("positions: int64 [tokens] is wanted with a table")
+    for x, n in ((k, "k"), (dq_out, "dq_out"), (dk_out, "dk_out")):
+        _like(x, q, n)
+    if dk_out is not None and _token_stride(dk_out, "dk_out") not in (0, k.shape[1] * d):
+        raise ValueError("dk_out: a contiguous tensor is wanted")
+    for x, n, t in ((w_q, "w_q", torch.float32), (w_k, "w_k", torch.float32), (table, "table", torch.float32),
+                    (positions, "positions", torch.int64)):
+        _like(x, q, n, t)
+    for x, n in ((w_q, "w_q"), (w_k, "w_k")):
+        if x is not None and x.shape != (d,):
+            raise ValueError(f"{n}: [d] is wanted")
+    p = AttnParams(Hq=Hq, Hkv=Hq if k is None else k.shape[1], d=d, dtype=_attn_dtype(q), tokens=q.shape[0],
+                   q_stride=_token_stride(q, "q"), k_stride=0 if k is None else _token_stride(k, "k"),
+                   o_stride=_token_stride(dq_out, "dq_out"), **_rope_fields(d, table, layout, norm, norm_eps))
+    with _on(stream):
+        g = _grad_buffers({"dq": q.shape} if k is None else {"dq": q.shape, "dk": k.shape}, q, out)
+        dw = [torch.empty(d, dtype=torch.float32, device=q.device) if norm and x is not None else None for x in (q, k)]
+        ws = alloc_workspace(falcon_qk_norm_rope_backward_workspace_size(p), q.device)
+        falcon_qk_norm_rope_backward(p, q, k, w_q, w_k, positions, table, dq_out, dk_out, make_attn_grads(g), *dw, ws,
+                                     0, stream)
+    g.update({n: x for n, x in zip(("dw_q", "dw_k"), dw) if x is not None})
+    return g
 
 
 load_library()

@@ -46,6 +46,21 @@ int launch_qk_norm_rope(const HeadArgs& h, int dtype, int64_t tokens, int Hq, in
                         const float* w_q, const float* w_k, const int64_t* pos, RowsOut qo, RowsOut ko,
                         cudaStream_t s);
 
+// The gradient of the norm and rotation; [0] the queries, [1] the keys (H = 0: none).
+struct NormGradArgs {
+  HeadArgs h;
+  int64_t tokens;
+  int H[2];
+  RowsIn x[2], dy[2];  // x is read with the norm only
+  RowsOut dx[2];
+  const float* w[2];
+  float* dw[2];        // NULL: not wanted
+  const int64_t* pos;
+  float* partial;      // workspace: [CTAs][2][d]
+};
+size_t norm_grad_ws_bytes(int d);
+int launch_qk_norm_rope_backward(const NormGradArgs& a, int dtype, cudaStream_t s);
+
 struct AppendArgs {
   int B, Hkv, page, num_pages, max_pages, max_q;
   int64_t tokens;
@@ -89,6 +104,13 @@ int launch_attn_prompt_tc(const PromptArgs& a, cudaStream_t s);
 
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
+
+// 2^x
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
 
 // ---------------------------------------------------------------- rows
 // A lane's 8 elements of a head row: two pieces of 4, at a and b.  They are

@@ -6,7 +6,7 @@
 #include <cstdint>
 #include <utility>
 
-#include "attn.cuh"
+#include "attn_grad.cuh"
 
 using namespace falcon;
 
@@ -74,6 +74,25 @@ int check_attn(const falcon_attn_params_t* p) {
       !stride_ok(p->v_stride, p->Hkv, p->d) || !stride_ok(p->o_stride, p->Hq, p->d))
     return FALCON_ERR_INVALID_ARG;
   return FALCON_OK;
+}
+// one of the gradients' strides: as the rows' own
+bool grads_ok(const falcon_attn_params_t* p, const falcon_attn_grads_t* g) {
+  return g && stride_ok(g->dq_stride, p->Hq, p->d) && stride_ok(g->dk_stride, p->Hkv, p->d) &&
+         stride_ok(g->dv_stride, p->Hkv, p->d) && stride_ok(g->do_stride, p->Hq, p->d);
+}
+// Rows that a call reads or writes: address, row stride, heads, number.
+struct Rows {
+  const void* p;
+  int64_t stride;
+  int H;
+  int64_t n;
+};
+bool meet(const falcon_attn_params_t* p, const Rows& x, const Rows& y) {
+  return x.n == y.n ? rows_overlap(p, x.p, x.stride, x.H, y.p, y.stride, y.H, x.n)
+                    : overlap(x.p, span(p, x.n, x.stride, x.H), y.p, span(p, y.n, y.stride, y.H));
+}
+bool meet(const falcon_attn_params_t* p, const Rows& x, const void* y, size_t ny) {
+  return overlap(x.p, span(p, x.n, x.stride, x.H), y, ny);
 }
 int check_scale(const falcon_attn_params_t* p) {
   return std::isfinite(p->scale) && p->scale >= 0.f ? FALCON_OK : FALCON_ERR_INVALID_ARG;
@@ -265,6 +284,131 @@ int falcon_attn_prompt(const falcon_attn_params_t* p, const void* q, const void*
                      rows_in(p, v, p->v_stride, p->Hkv), rows_out(p, o, p->o_stride, p->Hq), lse, cu_q, cu_k,
                      workspace};
   return launch_attn_prompt(a, p->dtype, reinterpret_cast<cudaStream_t>(stream));
+}
+
+size_t falcon_attn_prompt_backward_workspace_size(const falcon_attn_params_t* p) {
+  if (check_attn(p) != FALCON_OK || p->B < 1 || p->tokens > kMostRows) return 0;
+  return align_up(attn_grad_ws_bytes(p->tokens, p->B, p->Hq), 256);
+}
+
+int falcon_attn_prompt_backward(const falcon_attn_params_t* p, const void* q, const void* k, const void* v,
+                                const int32_t* cu_q, const int32_t* cu_k, const void* o, const float* lse,
+                                const void* d_o, const float* dlse, const falcon_attn_grads_t* g, void* workspace,
+                                size_t workspace_bytes, void* stream) {
+  int st = check_attn(p);
+  if (st == FALCON_OK) st = check_scale(p);
+  if (st != FALCON_OK) return st;
+  if (p->B < 1 || !grads_ok(p, g) || (!g->dk) != (!g->dv)) return FALCON_ERR_INVALID_ARG;
+  if (p->tokens == 0 && p->k_tokens == 0) return FALCON_OK;
+  if (!g->dq && !g->dk) return FALCON_ERR_INVALID_ARG;
+  if (p->tokens > kMostRows || p->k_tokens > kMostRows) return FALCON_ERR_UNSUPPORTED;
+  const bool of_q = g->dq && p->tokens > 0 && p->max_q > 0, of_k = g->dk && p->k_tokens > 0;
+  if (!of_q && !of_k) return FALCON_OK;
+  if (!cu_q || !cu_k || (p->tokens > 0 && (!q || !o || !lse || !d_o)) || (p->k_tokens > 0 && (!k || !v)))
+    return FALCON_ERR_INVALID_ARG;
+  for (const void* x : {q, k, v, o, d_o, static_cast<const void*>(g->dq), static_cast<const void*>(g->dk),
+                        static_cast<const void*>(g->dv)})
+    if (misaligned(x, esize(p))) return FALCON_ERR_INVALID_ARG;
+  if (misaligned(cu_q, 4) || misaligned(cu_k, 4) || misaligned(lse, 4) || misaligned(dlse, 4))
+    return FALCON_ERR_INVALID_ARG;
+  const size_t need = falcon_attn_prompt_backward_workspace_size(p), nl = static_cast<size_t>(p->tokens) * p->Hq * 4;
+  const Rows outs[3] = {{g->dq, g->dq_stride, p->Hq, p->tokens}, {g->dk, g->dk_stride, p->Hkv, p->k_tokens},
+                        {g->dv, g->dv_stride, p->Hkv, p->k_tokens}};
+  const Rows ins[5] = {{q, p->q_stride, p->Hq, p->tokens}, {k, p->k_stride, p->Hkv, p->k_tokens},
+                       {v, p->v_stride, p->Hkv, p->k_tokens}, {o, p->o_stride, p->Hq, p->tokens},
+                       {d_o, g->do_stride, p->Hq, p->tokens}};
+  for (int i = 0; i < 3; ++i) {
+    for (const Rows& x : ins)
+      if (meet(p, outs[i], x)) return FALCON_ERR_INVALID_ARG;
+    for (int j = 0; j < i; ++j)
+      if (meet(p, outs[i], outs[j])) return FALCON_ERR_INVALID_ARG;
+    if (meet(p, outs[i], lse, nl) || meet(p, outs[i], dlse, nl) || meet(p, outs[i], workspace, need))
+      return FALCON_ERR_INVALID_ARG;
+  }
+  for (const Rows& x : ins)
+    if (meet(p, x, workspace, need)) return FALCON_ERR_INVALID_ARG;
+  if (overlap(workspace, need, lse, nl) || overlap(workspace, need, dlse, nl)) return FALCON_ERR_INVALID_ARG;
+  if (!workspace || workspace_bytes < need || misaligned(workspace, 256)) return FALCON_ERR_WORKSPACE;
+  GradArgs a;
+  a.a = PromptArgs{p->B, p->Hq, p->Hkv, p->d, static_cast<int>(most_rows(p)), scale_of(p), p->tokens, p->k_tokens,
+                   rows_in(p, q, p->q_stride, p->Hq), rows_in(p, k, p->k_stride, p->Hkv),
+                   rows_in(p, v, p->v_stride, p->Hkv), RowsOut{}, nullptr, cu_q, cu_k, workspace};
+  a.o = rows_in(p, o, p->o_stride, p->Hq);
+  a.d_o = rows_in(p, d_o, g->do_stride, p->Hq);
+  a.lse = lse;
+  a.dlse = dlse;
+  a.dq = rows_out(p, g->dq, g->dq_stride, p->Hq);
+  a.dk = rows_out(p, g->dk, g->dk_stride, p->Hkv);
+  a.dv = rows_out(p, g->dv, g->dv_stride, p->Hkv);
+  a.sums = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + 256);
+  a.blocks = p->tokens / kSumRows + p->B;
+  return launch_attn_grad(a, p->dtype, reinterpret_cast<cudaStream_t>(stream));
+}
+
+size_t falcon_qk_norm_rope_backward_workspace_size(const falcon_attn_params_t* p) {
+  if (check_attn(p) != FALCON_OK) return 0;
+  return align_up(norm_grad_ws_bytes(p->d), 256);
+}
+
+int falcon_qk_norm_rope_backward(const falcon_attn_params_t* p, const void* q, const void* k, const float* w_q,
+                                 const float* w_k, const int64_t* positions, const float* table, const void* dq_out,
+                                 const void* dk_out, const falcon_attn_grads_t* g, float* dw_q, float* dw_k,
+                                 void* workspace, size_t workspace_bytes, void* stream) {
+  int st = check_attn(p);
+  if (st == FALCON_OK) st = check_head(p, table, w_q, w_k);
+  if (st != FALCON_OK) return st;
+  if (!grads_ok(p, g)) return FALCON_ERR_INVALID_ARG;
+  const bool of_q = dq_out != nullptr, of_k = dk_out != nullptr;
+  if (p->tokens > 0) {
+    if ((!of_q && !of_k) || (of_q && !g->dq) || (of_k && !g->dk)) return FALCON_ERR_INVALID_ARG;
+    if (p->qk_norm && ((of_q && !q) || (of_k && !k))) return FALCON_ERR_INVALID_ARG;
+    if (p->rot > 0 && (!positions || misaligned(positions, 8))) return FALCON_ERR_INVALID_ARG;
+  }
+  for (const void* x : {q, k, dq_out, dk_out, static_cast<const void*>(g->dq), static_cast<const void*>(g->dk)})
+    if (misaligned(x, esize(p))) return FALCON_ERR_INVALID_ARG;
+  if (misaligned(dw_q, 4) || misaligned(dw_k, 4)) return FALCON_ERR_INVALID_ARG;
+  const size_t need = falcon_qk_norm_rope_backward_workspace_size(p), nw = static_cast<size_t>(p->d) * 4;
+  const Rows xs[2] = {{p->qk_norm && of_q ? q : nullptr, p->q_stride, p->Hq, p->tokens},
+                      {p->qk_norm && of_k ? k : nullptr, p->k_stride, p->Hkv, p->tokens}};
+  const Rows ys[2] = {{dq_out, p->o_stride, p->Hq, p->tokens}, {dk_out, 0, p->Hkv, p->tokens}};
+  const Rows ds[2] = {{of_q ? g->dq : nullptr, g->dq_stride, p->Hq, p->tokens},
+                      {of_k ? g->dk : nullptr, g->dk_stride, p->Hkv, p->tokens}};
+  auto same = [&](const Rows& x, const Rows& y) {  // in place
+    return x.p == y.p && stride_of(x.stride, x.H, p->d) == stride_of(y.stride, y.H, p->d);
+  };
+  const bool none = p->tokens == 0;  // the sums are 0 then, whichever rows there would be
+  float* const dws[2] = {p->qk_norm && (of_q || none) ? dw_q : nullptr, p->qk_norm && (of_k || none) ? dw_k : nullptr};
+  for (int i = 0; i < 2; ++i) {
+    for (int j = 0; j < 2; ++j) {
+      if (meet(p, ds[i], xs[j])) return FALCON_ERR_INVALID_ARG;
+      if (meet(p, ds[i], ys[j]) && !(i == j && same(ds[i], ys[j]))) return FALCON_ERR_INVALID_ARG;
+      for (const Rows& x : {xs[i], ys[i], ds[i]})
+        if (meet(p, x, dws[j], nw)) return FALCON_ERR_INVALID_ARG;
+      if (overlap(dws[i], nw, j ? w_k : w_q, nw)) return FALCON_ERR_INVALID_ARG;
+    }
+    for (const Rows& x : {xs[i], ys[i], ds[i]})
+      if ((dws[0] || dws[1]) && meet(p, x, workspace, need)) return FALCON_ERR_INVALID_ARG;
+    if (overlap(dws[i], nw, workspace, need)) return FALCON_ERR_INVALID_ARG;
+  }
+  if (meet(p, ds[0], ds[1]) || overlap(dws[0], nw, dws[1], nw)) return FALCON_ERR_INVALID_ARG;
+  if ((dws[0] || dws[1]) && (!workspace || workspace_bytes < need || misaligned(workspace, 256)))
+    return FALCON_ERR_WORKSPACE;
+  NormGradArgs a;
+  a.h = head_args(p, table, w_q, w_k);
+  a.tokens = p->tokens;
+  a.H[0] = of_q ? p->Hq : 0;
+  a.H[1] = of_k ? p->Hkv : 0;
+  const float* const ws[2] = {w_q, w_k};
+  for (int i = 0; i < 2; ++i) {
+    a.x[i] = rows_in(p, xs[i].p, xs[i].stride, xs[i].H);
+    a.dy[i] = rows_in(p, ys[i].p, ys[i].stride, ys[i].H);
+    a.dx[i] = rows_out(p, i ? g->dk : g->dq, ds[i].stride, ds[i].H);
+    a.w[i] = ws[i];
+    a.dw[i] = dws[i];
+  }
+  a.pos = positions;
+  a.partial = static_cast<float*>(workspace);
+  return launch_qk_norm_rope_backward(a, p->dtype, reinterpret_cast<cudaStream_t>(stream));
 }
 
 }  // extern "C"

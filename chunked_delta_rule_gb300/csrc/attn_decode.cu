@@ -66,11 +66,6 @@ struct Tile {
 // CTAs that the registers of an SM hold
 constexpr int ctas_of_sm(int elem, int d) { return d == 128 && elem == 4 ? 2 : 3; }
 
-__device__ __forceinline__ float ex2(float x) {
-  float y;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
 __device__ __forceinline__ void mma_f16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
                                         uint32_t b0, uint32_t b1) {
   asm volatile(

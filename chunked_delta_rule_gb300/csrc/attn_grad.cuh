@@ -1,0 +1,157 @@
+// Internals of the softmax-attention backward: resolved arguments, the rows' sums
+// that the first kernel leaves in the workspace, and one row of a gradient by one
+// warp, straight from the definition.
+#pragma once
+
+#include "attn_row.cuh"
+
+namespace falcon {
+
+// What a call needs.  `a` holds the forward's operands; a.o and a.lse are not set.
+struct GradArgs {
+  PromptArgs a;
+  RowsIn o, d_o;
+  const float* lse;
+  const float* dlse;    // may be NULL
+  RowsOut dq, dk, dv;   // dq.p, or dk.p and dv.p, may be NULL
+  float* sums;          // in the workspace, see row_sums
+  int64_t blocks;       // of 128 rows of queries, of a head, counted over the packed sequences
+};
+size_t attn_grad_ws_bytes(int64_t tokens, int B, int Hq);
+int launch_attn_grad(const GradArgs& g, int dtype, cudaStream_t s);
+
+// The rows of query block j (of 128, counted from cu_q[b] / 128 + b on for sequence b) and head h: 128 times the
+// log sum of the scores (in the unit that the kernel which reads it takes: logarithms to base e or 2), then 128 times
+// D = sum_c dO_c o_c - dlse.  Rows past the sequence and rows that see no key
+// have log sum +inf: exp(score - log sum) = 0, no weight anywhere.
+constexpr int kSumRows = 128;
+__host__ __device__ __forceinline__ int64_t row_sums(int64_t blocks, int h, int64_t j) {
+  return (static_cast<int64_t>(h) * blocks + j) * (2 * kSumRows);
+}
+// first block of a sequence whose rows begin at q0
+__device__ __forceinline__ int64_t first_block(int64_t q0, int b) { return q0 / kSumRows + b; }
+
+// Sums over the lanes, a few at a time.
+template <int N>
+__device__ __forceinline__ void lane_sums(float (&x)[N]) {
+#pragma unroll
+  for (int s = 16; s; s >>= 1)
+#pragma unroll
+    for (int i = 0; i < N; ++i) x[i] += __shfl_xor_sync(0xffffffffu, x[i], s);
+}
+
+// dq (lane t's dims t, t + 32, ...) of one query over the first n keys.  Ends where every dim is NaN: they stay so.
+template <typename T, int D>
+__device__ __noinline__ void grad_query_row(const T* q, const T* d_o, float lse, float delta, const T* k,
+                                            int64_t k_stride, const T* v, int64_t v_stride, int n, int d, float scale,
+                                            float (&out)[4]) {
+  constexpr int J = (D + 31) / 32, kBatch = 4;
+  const int lane = threadIdx.x & 31;
+  float qv[J], gv[J];
+  int at[J];
+#pragma unroll
+  for (int j = 0; j < 4; ++j) out[j] = 0.f;
+#pragma unroll
+  for (int j = 0; j < J; ++j) {
+    const bool in = lane + 32 * j < d;
+    at[j] = min(lane + 32 * j, d - 1);
+    qv[j] = in ? to_f32(q[at[j]]) : 0.f;
+    gv[j] = in ? to_f32(d_o[at[j]]) : 0.f;
+  }
+  if (lse == INFINITY) return;
+  for (int t = 0; t < n; t += kBatch) {
+    float kt[kBatch][J], s[2 * kBatch];
+#pragma unroll
+    for (int u = 0; u < kBatch; ++u) {
+      s[u] = s[kBatch + u] = 0.f;
+#pragma unroll
+      for (int j = 0; j < J; ++j) {
+        const bool in = lane + 32 * j < d;
+        kt[u][j] = in ? to_f32(k[min(t + u, n - 1) * k_stride + at[j]]) : 0.f;
+        s[u] = fmaf(qv[j], kt[u][j], s[u]);
+        s[kBatch + u] = fmaf(gv[j], in ? to_f32(v[min(t + u, n - 1) * v_stride + at[j]]) : 0.f, s[kBatch + u]);
+      }
+    }
+    lane_sums(s);
+    bool nan = true;
+#pragma unroll
+    for (int u = 0; u < kBatch; ++u) {
+      if (t + u >= n) break;
+      const float ds = expf(fmaf(s[u], scale, -lse)) * (s[kBatch + u] - delta) * scale;
+#pragma unroll
+      for (int j = 0; j < J; ++j) out[j] = fmaf(ds, kt[u][j], out[j]);
+    }
+#pragma unroll
+    for (int j = 0; j < J; ++j) nan = nan && (lane + 32 * j >= d || out[j] != out[j]);
+    if (__all_sync(0xffffffffu, nan)) break;
+  }
+}
+
+// dk and dv of one key, over the `heads` query heads of its group and the queries [i0, i1) of its sequence, whose rows
+// begin at q and d_o (of the group's first head); sums: of that head's first block, `blocks` blocks a head, log sums in
+// units of `unit`.
+template <typename T, int D>
+__device__ __noinline__ void grad_key_row(const T* k, const T* v, const T* q, int64_t q_stride, const T* d_o,
+                                          int64_t o_stride, const float* sums, int64_t blocks, int heads, int i0, int i1,
+                                          int d, float scale, float unit, float (&dk)[4], float (&dv)[4]) {
+  constexpr int J = (D + 31) / 32, kBatch = 4;
+  const int lane = threadIdx.x & 31;
+  float kv[J], vv[J];
+  int at[J];
+#pragma unroll
+  for (int j = 0; j < 4; ++j) dk[j] = dv[j] = 0.f;
+#pragma unroll
+  for (int j = 0; j < J; ++j) {
+    const bool in = lane + 32 * j < d;
+    at[j] = min(lane + 32 * j, d - 1);
+    kv[j] = in ? to_f32(k[at[j]]) : 0.f;
+    vv[j] = in ? to_f32(v[at[j]]) : 0.f;
+  }
+  for (int h = 0; h < heads; ++h, q += d, d_o += d, sums += blocks * (2 * kSumRows)) {
+    for (int t = i0; t < i1; t += kBatch) {
+      float qt[kBatch][J], gt[kBatch][J], s[2 * kBatch];
+#pragma unroll
+      for (int u = 0; u < kBatch; ++u) {
+        s[u] = s[kBatch + u] = 0.f;
+#pragma unroll
+        for (int j = 0; j < J; ++j) {
+          const bool in = lane + 32 * j < d;
+          qt[u][j] = in ? to_f32(q[min(t + u, i1 - 1) * q_stride + at[j]]) : 0.f;
+          gt[u][j] = in ? to_f32(d_o[min(t + u, i1 - 1) * o_stride + at[j]]) : 0.f;
+          s[u] = fmaf(kv[j], qt[u][j], s[u]);
+          s[kBatch + u] = fmaf(vv[j], gt[u][j], s[kBatch + u]);
+        }
+      }
+      lane_sums(s);
+#pragma unroll
+      for (int u = 0; u < kBatch; ++u) {
+        const int i = t + u;
+        if (i >= i1) break;
+        const float* row = sums + static_cast<int64_t>(i / kSumRows) * (2 * kSumRows) + i % kSumRows;
+        const float lse = row[0];
+        if (lse == INFINITY) continue;
+        const float p = expf(fmaf(s[u], scale, -lse * unit)), ds = p * (s[kBatch + u] - row[kSumRows]) * scale;
+#pragma unroll
+        for (int j = 0; j < J; ++j) {
+          dv[j] = fmaf(p, gt[u][j], dv[j]);
+          dk[j] = fmaf(ds, qt[u][j], dk[j]);
+        }
+      }
+      bool nan = true;
+#pragma unroll
+      for (int j = 0; j < J; ++j) nan = nan && (lane + 32 * j >= d || (dk[j] != dk[j] && dv[j] != dv[j]));
+      if (__all_sync(0xffffffffu, nan)) return;
+    }
+  }
+}
+
+// 32-lane rows of d dims to global memory
+template <typename T, int D>
+__device__ __forceinline__ void store_row(T* out, const float (&x)[4], int d) {
+  const int lane = threadIdx.x & 31;
+#pragma unroll
+  for (int j = 0; j < (D + 31) / 32; ++j)
+    if (lane + 32 * j < d) out[lane + 32 * j] = from_f32<T>(x[j]);
+}
+
+}  // namespace falcon

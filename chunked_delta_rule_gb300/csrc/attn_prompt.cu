@@ -24,59 +24,13 @@
 // are zeros.  A row whose result is not finite (a masked key of its own
 // sequence may hold an infinity) is computed again from the definition.
 
+#include "attn_mma.cuh"
 #include "attn_row.cuh"
-#include "tc_util.cuh"
 
 namespace falcon {
 namespace {
 
-constexpr int kRows = 64, kKeys = 64;
-
-__device__ __forceinline__ float ex2(float x) {
-  float y;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
-
-// rows [first, first + 64) of x (zeros from `end` on) as fp32 into dst, pitch D + 4
-template <typename T, int D>
-__device__ __forceinline__ void stage_rows(float* dst, const T* x, int64_t stride, bool vec, int first, int end) {
-  constexpr int kPieces = D / 8;
-  for (int i = threadIdx.x; i < kKeys * kPieces; i += 128) {
-    const int r = i / kPieces, c = i % kPieces * 8;
-    float v[8];
-    if (first + r < end) {
-      const T* row = x + (first + r) * stride;
-      if (vec) unpack8(load8<true, false>(row, Pieces{c, c + 4}), v);
-      else unpack8(load8<false, false>(row, Pieces{c, c + 4}), v);
-    } else {
-#pragma unroll
-      for (int e = 0; e < 8; ++e) v[e] = 0.f;
-    }
-    float4* o = reinterpret_cast<float4*>(dst + r * (D + 4) + c);
-    o[0] = make_float4(v[0], v[1], v[2], v[3]);
-    o[1] = make_float4(v[4], v[5], v[6], v[7]);
-  }
-}
-
-// NP = 2: x = hi + lo; NP = 1: x alone (exact in tf32, or rounded to it)
-template <int NP>
-__device__ __forceinline__ void split(float x, uint32_t (&out)[NP]) {
-  if (NP == 1) {
-    out[0] = __float_as_uint(x);
-  } else {
-    out[0] = (__float_as_uint(x) + 0x1000u) & 0xFFFFE000u;  // to nearest; cvt to tf32 has a quarter of the rate
-    out[NP - 1] = __float_as_uint(x - __uint_as_float(out[0]));  // its lowest bits are ignored
-  }
-}
-template <int NP>
-__device__ __forceinline__ void product(float (&d)[4], const uint32_t (&a)[NP][4], const uint32_t (&b)[NP][2]) {
-  tc::mma_tf32_16x8x8(d, a[0], b[0]);
-  if (NP == 2) {
-    tc::mma_tf32_16x8x8(d, a[0], b[NP - 1]);
-    tc::mma_tf32_16x8x8(d, a[NP - 1], b[0]);
-  }
-}
+constexpr int kRows = kMmaRows, kKeys = kMmaRows;
 
 template <typename T, int D>
 __global__ void __launch_bounds__(128) attn_prompt_kernel(PromptArgs a, int qblocks, bool packed) {
@@ -102,7 +56,7 @@ __global__ void __launch_bounds__(128) attn_prompt_kernel(PromptArgs a, int qblo
   const T* q = static_cast<const T*>(a.q.p) + q0 * a.q.stride + static_cast<int64_t>(h) * D;
   const T* k = static_cast<const T*>(a.k.p) + k0 * a.k.stride + static_cast<int64_t>(hk) * D;
   const T* v = static_cast<const T*>(a.v.p) + k0 * a.v.stride + static_cast<int64_t>(hk) * D;
-  stage_rows<T, D>(sq, q, a.q.stride, a.q.vec, row0, lq);
+  stage_rows<T, D, 128>(sq, q, a.q.stride, a.q.vec, row0, lq);
 
   float o[D / 8][4], m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
 #pragma unroll
@@ -114,8 +68,8 @@ __global__ void __launch_bounds__(128) attn_prompt_kernel(PromptArgs a, int qblo
   const int keys = min(min(row0 + kRows, lq) + off, lk);  // that some row of the block sees
   for (int j0 = 0; j0 < keys; j0 += kKeys) {
     __syncthreads();
-    stage_rows<T, D>(sk, k, a.k.stride, a.k.vec, j0, lk);
-    stage_rows<T, D>(sv, v, a.v.stride, a.v.vec, j0, lk);
+    stage_rows<T, D, 128>(sk, k, a.k.stride, a.k.vec, j0, lk);
+    stage_rows<T, D, 128>(sv, v, a.v.stride, a.v.vec, j0, lk);
     __syncthreads();
     float s[NT][4], low[NT][4];  // fp32: the small products apart
 #pragma unroll

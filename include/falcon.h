@@ -342,10 +342,11 @@ int falcon_backward(const falcon_params_t* p, const void* q, const void* k, cons
 /* ------------------------------------------------------------------------
  * Softmax-attention layers (the full-attention layers a stack of Falcon
  * layers is interleaved with; the pages have no counterpart).  Four
- * operators for serving, forward only: falcon_qk_norm_rope over a token's
+ * operators forward: falcon_qk_norm_rope over a token's
  * queries and keys, falcon_attn_prompt over whole packed prompts,
  * falcon_kv_append into a paged cache held in 8 bits, falcon_attn_decode of
- * one token per sequence over that cache.
+ * one token per sequence over that cache.  Two for training, the gradients of
+ * the first two: falcon_attn_prompt_backward and falcon_qk_norm_rope_backward.
  *
  * Layouts: q [tokens, Hq, d], k and v [tokens, Hkv, d] in the params' dtype,
  * tokens of all sequences packed one after the other, heads and dims dense,
@@ -481,6 +482,68 @@ size_t falcon_attn_prompt_workspace_size(const falcon_attn_params_t* p);
 int falcon_attn_prompt(const falcon_attn_params_t* p, const void* q, const void* k, const void* v,
                        const int32_t* cu_q, const int32_t* cu_k, void* o, float* lse, void* workspace,
                        size_t workspace_bytes, void* stream);
+
+/* Where a layer's gradients go, and how they and dO lie: elements from one token
+ * to the next, 0 = dense.  dq, dk and dv may be slices of one fused gradient,
+ * as q, k and v of a fused projection. */
+typedef struct {
+  void* dq;  /* [tokens, Hq, d] */
+  void* dk;  /* [k_tokens, Hkv, d] (qk_norm_rope_backward: [tokens, Hkv, d]) */
+  void* dv;  /* [k_tokens, Hkv, d]; attn_prompt_backward only */
+  int64_t dq_stride, dk_stride, dv_stride;
+  int64_t do_stride; /* of dO; attn_prompt_backward only */
+} falcon_attn_grads_t;
+
+/* Bytes of workspace falcon_attn_prompt_backward needs (0 when the params are invalid). */
+size_t falcon_attn_prompt_backward_workspace_size(const falcon_attn_params_t* p);
+
+/* Gradient of falcon_attn_prompt(p, q, k, v, cu_q, cu_k) with results o and lse,
+ * for the loss L = <o, dO> + <lse, dlse>:
+ *   P_ij = exp(scale <q_i, k_j> - lse_i) for the keys j that query i sees
+ *   D_i  = <dO_i, o_i> - dlse_i,   dS_ij = P_ij (<dO_i, v_j> - D_i)
+ *   dq_i = scale sum_j dS_ij k_j,  dk_j = scale sum_i dS_ij q_i,  dv_j = sum_i P_ij dO_i
+ * the sums of dk and dv also over the query heads that share the key head.  The
+ * weights are formed again, nothing of their size is kept.  o (row stride
+ * o_stride) and lse are what the forward returned for the same params; dO
+ * [tokens, Hq, d] in the params' dtype, dlse fp32 [tokens, Hq] or NULL (zero).
+ * g->dq may be NULL (skipped), or g->dk and g->dv.  Rows that see no key give
+ * dq = 0 and add nothing; keys that no query sees get dk = dv = 0.  Rows of q past
+ * max_q of their sequence have no gradient: their dq is left as it is and they
+ * add nothing.  So are rows of dq, dk and dv behind the last sequence.  What
+ * lies in rows that a row does not see (infinities, NaN) does not reach it.
+ * Every sum has one order: the same call gives the same bits.  Products as in
+ * falcon_attn_prompt; sums are fp32, P and dS rounded to 11 bits (bf16 rows on 16-byte
+ * boundaries: 8, on the tensor cores, whose bounded waits are reported through
+ * falcon_workspace_status(workspace, stream)); fp32 keeps 22 bits.
+ * Errors: FALCON_ERR_INVALID_ARG, FALCON_ERR_UNSUPPORTED,
+ * FALCON_ERR_WORKSPACE, FALCON_ERR_CUDA. */
+int falcon_attn_prompt_backward(const falcon_attn_params_t* p, const void* q, const void* k, const void* v,
+                                const int32_t* cu_q, const int32_t* cu_k, const void* o, const float* lse,
+                                const void* d_o, const float* dlse, const falcon_attn_grads_t* g, void* workspace,
+                                size_t workspace_bytes, void* stream);
+
+/* Bytes of workspace falcon_qk_norm_rope_backward needs (0 when the params are invalid). */
+size_t falcon_qk_norm_rope_backward_workspace_size(const falcon_attn_params_t* p);
+
+/* Gradient of falcon_qk_norm_rope(p, q, k, w_q, w_k, positions, table): from
+ * dq_out (row stride o_stride) and dk_out (dense), the gradients of its
+ * results, to g->dq and g->dk (row strides g->dq_stride, g->dk_stride) and, with
+ * qk_norm, dw_q and dw_k (fp32 [d], NULL = not wanted):
+ *   n = dy rotated back,  r = 1 / sqrt(mean(x^2) + norm_eps),  u = n w
+ *   dx = r (u - x r mean(u x r)),   dw = sum over tokens and heads of n x r
+ * (without the norm dx = n, and q and k are not read).  fp32 arithmetic and sums,
+ * dx rounded once to the dtype; every sum has one order.  dq_out or dk_out may
+ * be NULL (skipped, their dw untouched).  g->dq may be dq_out itself when
+ * their strides agree, g->dk the same; other overlaps are refused.  A row whose sum
+ * of squares passes fp32's range gives 0.  Rotated dims of a token whose
+ * position is not in [0, rope_rows) are NaN, and with the norm so are its whole
+ * rows and dw of the rotated dims.  tokens = 0 gives dw = 0.  The workspace is needed where a dw is
+ * wanted.  Errors: FALCON_ERR_INVALID_ARG, FALCON_ERR_UNSUPPORTED,
+ * FALCON_ERR_WORKSPACE, FALCON_ERR_CUDA. */
+int falcon_qk_norm_rope_backward(const falcon_attn_params_t* p, const void* q, const void* k, const float* w_q,
+                                 const float* w_k, const int64_t* positions, const float* table, const void* dq_out,
+                                 const void* dk_out, const falcon_attn_grads_t* g, float* dw_q, float* dw_k,
+                                 void* workspace, size_t workspace_bytes, void* stream);
 
 /* Status of the last tensor-core chunk forward that used `workspace`
  * (falcon_chunk_fwd_plan reports FALCON_IMPL_TC for it; falcon_chunk_fwd,

@@ -139,3 +139,45 @@ def prompt(q, k, v, cu_q, cu_k, scale):
         seen = np.arange(lk)[None] <= np.arange(lq)[:, None] + (lk - lq)
         o[i0:i1], lse[i0:i1] = attend(q[i0:i1], k[j0:j1], v[j0:j1], seen, scale)
     return o, lse
+
+
+def prompt_grad(q, k, v, cu_q, cu_k, scale, d_o, dlse=None):
+    """Gradients of ``prompt`` for <o, d_o> + <lse, dlse>, a row at a time; unseen keys are not touched."""
+    q, k, v, d_o = (np.asarray(x, dtype=np.float64) for x in (q, k, v, d_o))
+    dq, dk, dv = np.zeros(q.shape), np.zeros(k.shape), np.zeros(v.shape)
+    G = q.shape[1] // k.shape[1]
+    for b in range(len(cu_q) - 1):
+        lq, lk = cu_q[b + 1] - cu_q[b], cu_k[b + 1] - cu_k[b]
+        for i in range(lq):
+            row, j = cu_q[b] + i, cu_k[b] + np.arange(max(0, min(lk, i + lk - lq + 1)))
+            if not len(j):
+                continue
+            for h in range(q.shape[1]):
+                s = scale * (k[j, h // G] @ q[row, h])
+                p = np.exp(s - s.max())
+                p /= p.sum()
+                dp = v[j, h // G] @ d_o[row, h]
+                ds = p * (dp - p @ dp + (0.0 if dlse is None else dlse[row, h]))
+                dv[j, h // G] += p[:, None] * d_o[row, h]
+                dk[j, h // G] += scale * ds[:, None] * q[row, h]
+                dq[row, h] += scale * ds @ k[j, h // G]
+    return dq, dk, dv
+
+
+def norm_rope_grad(x, w, eps, positions, table, layout, dy):
+    """Gradients (dx, dw) of ``norm_rope`` for the results' gradient dy; dw None without the norm."""
+    n = np.array(dy, dtype=np.float64)
+    if table is not None:
+        rows, half, _ = table.shape
+        for t, pos in enumerate(positions):
+            for i in range(half):
+                a, b = (i, i + half) if layout == "half" else (2 * i, 2 * i + 1)
+                c, s = table[pos, i].astype(np.float64) if 0 <= pos < rows else (np.nan, np.nan)
+                ga, gb = n[t, :, a].copy(), n[t, :, b].copy()
+                n[t, :, a], n[t, :, b] = ga * c + gb * s, gb * c - ga * s
+    if eps is None:
+        return n, None
+    x = np.asarray(x, dtype=np.float64)
+    r = 1 / np.sqrt((x * x).mean(-1, keepdims=True) + eps)
+    u = n if w is None else n * w
+    return r * (u - x * r * r * (u * x).mean(-1, keepdims=True)), (n * x * r).sum((0, 1))

@@ -1,0 +1,525 @@
+"""Gradients of the softmax-attention operators on the GPU against fp64.
+
+Tolerances follow from the number formats, u = half a step: 2^-8 for bf16.  A is
+the sum of the absolute values of what an element of a gradient is the sum of
+(tests/attn_grad_ref.py).  bf16: the weights P are rounded once (u), dS once (u),
+o, which D is formed from, was rounded by the forward (u), the result is
+rounded once (u of itself): at most 3 u A + u |x|.  fp32: scores and dP are sums of up to
+128 products, each off by up to 2^-22 of the sum of absolute values; the
+scores' enter P through the exponential, times the largest sum of absolute values
+of a score, S: at most 2^-22 (2 S + 8) A for all of it, and 2^-21 A for the
+gradients' own sums over a tile and 2^-24 a tile after that.  Over a whole tensor roundings do
+not line up: the norm of the error is below u (bf16; u / sqrt(3) each, less where
+many terms add up) or 1e-5 (fp32) times 2 of the norm.
+"""
+
+from __future__ import annotations
+
+import math
+
+import numpy as np
+import pytest
+import torch
+
+from attn_grad_ref import attention_grad
+from oracle import softmax_attention as O
+
+pytestmark = pytest.mark.gpu
+U = 2.0 ** -8
+DT = {"bf16": torch.bfloat16, "f32": torch.float32}
+
+
+@pytest.fixture(scope="module")
+def F():
+    import chunked_delta_rule_gb300 as F
+    return F
+
+
+def _np(x):
+    return x.detach().cpu().double().numpy()
+
+
+def _cu(lens):
+    return [0] + list(np.cumsum(lens))
+
+
+def _dev(cu):
+    return torch.tensor([int(x) for x in cu], dtype=torch.int32, device="cuda")
+
+
+def _rand(shape, dtype, seed, unit=False):
+    g = torch.Generator().manual_seed(seed)
+    x = torch.randn(shape, generator=g)
+    if unit:  # as the norm leaves the rows
+        x = x / x.square().mean(-1, keepdim=True).sqrt()
+    return x.to(DT[dtype]).cuda()
+
+
+def _inputs(lq, lk, Hq, Hkv, d, dtype, seed=0, behind=0):
+    n, m = sum(lq) + behind, sum(lk) + behind
+    return (_rand((n, Hq, d), dtype, seed, True), _rand((m, Hkv, d), dtype, seed + 1, True),
+            _rand((m, Hkv, d), dtype, seed + 2), _rand((n, Hq, d), dtype, seed + 3))
+
+
+def _check(got, want, A, dtype, S):
+    for name in want:
+        x, y = got[name].double(), want[name]
+        if dtype == "bf16":
+            tol = 3 * U * A[name] + U * y.abs() + 1e-30
+        else:
+            tol = (2.0 ** -22 * (2 * S + 8) + 2.0 ** -20) * A[name] + 1e-30
+        assert torch.isfinite(x).all(), name
+        worst = ((x - y).abs() / tol).max().item() if x.numel() else 0.0
+        assert worst <= 1.0, (name, worst)
+        if x.numel() >= 4096 and y.norm() > 0.05 * A[name].norm():
+            assert (x - y).norm() <= 2 * (U if dtype == "bf16" else 1e-5) * y.norm(), name
+
+
+def _forward(F, q, k, v, cu_q, cu_k, max_q, scale=0.0):
+    return F.attn_prompt(q, k, v, cu_q, cu_k, max_q, scale, want_lse=True)
+
+
+def _S(q, k, scale):
+    """Bound of the sum of absolute values of a score."""
+    return scale * q.double().norm(dim=-1).max().item() * k.double().norm(dim=-1).max().item() if k.numel() and q.numel() else 0.0
+
+
+SHAPES = [
+    # lq, lk, Hq, Hkv, d
+    ([1], [1], 1, 1, 16), ([2], [2], 2, 1, 32), ([1, 1, 1], [5, 130, 1], 4, 2, 64), ([17], [17], 3, 3, 128),
+    ([63, 64, 65], [63, 64, 65], 4, 2, 64), ([127, 128, 129, 1], [127, 128, 129, 1], 2, 2, 128),
+    ([300], [300], 8, 1, 32), ([130, 7], [400, 260], 6, 2, 64), ([200, 3], [40, 1], 4, 4, 64),
+    ([0, 33, 0], [5, 33, 0], 2, 1, 64), ([20, 40], [0, 40], 2, 2, 128), ([257, 385], [257, 513], 4, 1, 128),
+    ([5, 300, 90], [5, 300, 90], 12, 4, 16), ([511], [640], 2, 2, 64), ([900, 1, 340], [900, 70, 340], 3, 1, 64),
+    ([140] * 5, [140] * 5, 2, 1, 128),
+]
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("lq,lk,Hq,Hkv,d", SHAPES)
+def test_gradients(F, dtype, lq, lk, Hq, Hkv, d):
+    q, k, v, dO = _inputs(lq, lk, Hq, Hkv, d, dtype, sum(lq) + d)
+    dlse = _rand(q.shape[:2], "f32", 9) if sum(lq) % 2 else None
+    cu_q, cu_k = _cu(lq), _cu(lk)
+    o, lse = _forward(F, q, k, v, _dev(cu_q), _dev(cu_k), max(lq))
+    got = F.attn_prompt_backward(q, k, v, o, lse, dO, _dev(cu_q), _dev(cu_k), max(lq), dlse=dlse)
+    _, _, want, A = attention_grad(q, k, v, cu_q, cu_k, d ** -0.5, dO, dlse)
+    _check(got, want, A, dtype, _S(q, k, d ** -0.5))
+
+
+@pytest.mark.parametrize("dtype,lq,lk,Hq,Hkv,d", [
+    ("bf16", [2048, 1000], [2048, 1000], 2, 1, 64), ("bf16", [1500], [1500], 4, 2, 128),
+    ("bf16", [1100], [1700], 2, 2, 32), ("bf16", [3000], [3000], 2, 1, 16), ("f32", [1500, 3], [1500, 3], 2, 1, 64),
+    ("f32", [1025], [1030], 2, 2, 128), ("bf16", [128] * 40, [128] * 40, 2, 2, 64), ("bf16", [4, 2100], [800, 2100], 2, 2, 128),
+])
+def test_gradients_of_long_sequences(F, dtype, lq, lk, Hq, Hkv, d):
+    q, k, v, dO = _inputs(lq, lk, Hq, Hkv, d, dtype, 77)
+    cu_q, cu_k = _cu(lq), _cu(lk)
+    o, lse = _forward(F, q, k, v, _dev(cu_q), _dev(cu_k), max(lq))
+    got = F.attn_prompt_backward(q, k, v, o, lse, dO, _dev(cu_q), _dev(cu_k), max(lq))
+    _, _, want, A = attention_grad(q, k, v, cu_q, cu_k, d ** -0.5, dO)
+    _check(got, want, A, dtype, _S(q, k, d ** -0.5))
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("scale,size", [(0.5, 4.0), (1e-3, 1.0)])
+def test_large_and_small_scores(F, dtype, scale, size):
+    """Scores of some hundreds (weights all but one-hot) and scores near zero (weights all but equal)."""
+    q, k, v, dO = _inputs([200], [200], 2, 2, 64, dtype, 5)
+    q, k = q * size, k * size
+    cu = _cu([200])
+    o, lse = _forward(F, q, k, v, _dev(cu), _dev(cu), 200, scale)
+    got = F.attn_prompt_backward(q, k, v, o, lse, dO, _dev(cu), None, 200, scale)
+    # fp32: the forward's log sum is itself off by 2^-24 of its size
+    _, _, want, A = attention_grad(q, k, v, cu, cu, scale, dO)
+    _check(got, want, A, dtype, _S(q, k, scale))
+
+
+def test_bits_do_not_change(F):
+    """The same call twice, on another stream, and its halves alone."""
+    for dtype, d in (("bf16", 64), ("bf16", 128), ("f32", 64)):
+        lens = [700, 333, 128]
+        q, k, v, dO = _inputs(lens, lens, 8, 2, d, dtype, 3)
+        cu = _dev(_cu(lens))
+        o, lse = _forward(F, q, k, v, cu, cu, 700)
+        a = F.attn_prompt_backward(q, k, v, o, lse, dO, cu, max_q=700)
+        side = torch.cuda.Stream()
+        side.wait_stream(torch.cuda.current_stream())
+        b = F.attn_prompt_backward(q, k, v, o, lse, dO, cu, max_q=700, stream=side)
+        torch.cuda.current_stream().wait_stream(side)
+        c = F.attn_prompt_backward(q, k, v, o, lse, dO, cu)  # the loose bound of all tokens
+        p = F.AttnParams(B=3, Hq=8, Hkv=2, d=d, dtype=F.FALCON_BF16 if dtype == "bf16" else F.FALCON_F32, max_q=700,
+                         tokens=sum(lens), k_tokens=sum(lens))
+        ws = F.alloc_workspace(F.falcon_attn_prompt_backward_workspace_size(p))
+        half = {n: torch.empty_like(x) for n, x in a.items()}
+        F.falcon_attn_prompt_backward(p, q, k, v, cu, cu, o, lse, dO, None, {"dq": half["dq"]}, ws)
+        F.falcon_attn_prompt_backward(p, q, k, v, cu, cu, o, lse, dO, None, {n: half[n] for n in ("dk", "dv")}, ws)
+        for n in a:
+            for other in (b, c, half):
+                assert torch.equal(a[n], other[n]), (dtype, d, n)
+
+
+def test_slices_of_fused_projections_and_gaps(F):
+    """q, k, v slices of one projection, dq, dk, dv slices of one gradient; o and dO with gaps; nothing else written."""
+    lens, Hq, Hkv, d = [150, 40, 260], 6, 2, 64
+    n = sum(lens)
+    for dtype in ("bf16", "f32"):
+        x = _rand((n, Hq + 2 * Hkv, d), dtype, 1)
+        q, k, v = torch.split(x, [Hq, Hkv, Hkv], 1)
+        cu = _cu(lens)
+        o, lse = _forward(F, q, k, v, _dev(cu), _dev(cu), 260)
+        wide = torch.full((n, Hq + 3, d), 7.0, dtype=DT[dtype], device="cuda")
+        wide[:, 1:1 + Hq] = o
+        dwide = _rand((n, Hq + 1, d), dtype, 2)
+        dO = dwide[:, 1:]
+        grad = torch.full((n + 4, Hq + 2 * Hkv + 1, d), 5.0, dtype=DT[dtype], device="cuda")
+        out = dict(zip(("dq", "dk", "dv"), torch.split(grad[2:-2, :-1], [Hq, Hkv, Hkv], 1)))
+        got = F.attn_prompt_backward(q, k, v, wide[:, 1:1 + Hq], lse, dO, _dev(cu), max_q=260, out=out)
+        assert got["dq"].data_ptr() == out["dq"].data_ptr()
+        _, _, want, A = attention_grad(q, k, v, cu, cu, d ** -0.5, dO)
+        _check(got, want, A, dtype, _S(q, k, d ** -0.5))
+        assert (grad[:2] == 5).all() and (grad[-2:] == 5).all() and (grad[:, -1] == 5).all()
+
+
+@pytest.mark.parametrize("d", [64, 128])
+def test_odd_addresses(F, d):
+    """bf16 rows off the 16-byte boundaries, each operand in turn, agree with the aligned call's tolerances."""
+    lens, Hq, Hkv = [200, 77], 4, 2
+    q, k, v, dO = _inputs(lens, lens, Hq, Hkv, d, "bf16", 8)
+    cu = _cu(lens)
+    o, lse = _forward(F, q, k, v, _dev(cu), _dev(cu), 200)
+    _, _, want, A = attention_grad(q, k, v, cu, cu, d ** -0.5, dO)
+
+    def odd(x):
+        buf = torch.empty(x.numel() + 1, dtype=x.dtype, device="cuda")
+        y = buf[1:].view(x.shape)
+        return y.copy_(x)
+
+    for which in range(6):
+        args = [odd(x) if which == i else x for i, x in enumerate((q, k, v, o))]
+        g = odd(dO) if which == 4 else dO
+        out = {n: odd(torch.zeros_like(x)) for n, x in (("dq", q), ("dk", k), ("dv", v))} if which == 5 else None
+        got = F.attn_prompt_backward(*args, lse, g, _dev(cu), max_q=200, out=out)
+        _check(got, want, A, "bf16", _S(q, k, d ** -0.5))
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_rows_behind_the_last_sequence_and_past_max_q(F, dtype):
+    lens, d = [130, 260], 64
+    q, k, v, dO = _inputs(lens, lens, 4, 2, d, dtype, 4, behind=9)
+    for x in (q, k, v, dO):
+        x[-9:] = math.nan
+    cu = _cu(lens)
+    o, lse = _forward(F, q, k, v, _dev(cu), _dev(cu), 260)
+    o[-9:], lse[-9:] = math.nan, math.nan
+    out = {n: torch.full_like(x, 3.0) for n, x in (("dq", q), ("dk", k), ("dv", v))}
+    got = F.attn_prompt_backward(q, k, v, o, lse, dO, _dev(cu), max_q=260, out=out)
+    _, _, want, A = attention_grad(q[:-9], k[:-9], v[:-9], cu, cu, d ** -0.5, dO[:-9])
+    assert all((x[-9:] == 3).all() for x in got.values())
+    _check({n: x[:-9] for n, x in got.items()}, want, A, dtype, _S(q[:-9], k[:-9], d ** -0.5))
+    fresh = F.attn_prompt_backward(q, k, v, o, lse, dO, _dev(cu), max_q=260)
+    assert all(not x[-9:].any() for x in fresh.values())
+
+    # rows past max_q of their sequence: untouched, and without influence
+    out = {n: torch.full_like(x, 3.0) for n, x in (("dq", q), ("dk", k), ("dv", v))}
+    dO2 = dO.clone()
+    dO2[100:130] = math.nan
+    o2 = o.clone()
+    o2[100:130] = math.nan
+    got = F.attn_prompt_backward(q, k, v, o2, lse, dO2, _dev(cu), max_q=100, out=out)
+    cut = torch.cat([torch.arange(100), 130 + torch.arange(100)])
+    rest = torch.tensor(sorted(set(range(390)) - set(cut.tolist())))
+    assert (got["dq"][rest.cuda()] == 3).all()
+    dO3 = torch.nan_to_num(dO2)
+    _, _, want, A = attention_grad(q[:-9], k[:-9], v[:-9], cu, cu, d ** -0.5, dO3[:-9], max_q=100)
+    got = {n: x[:-9] for n, x in got.items()}
+    got["dq"], want["dq"], A["dq"] = (x[cut.cuda()] for x in (got["dq"], want["dq"], A["dq"]))
+    _check(got, want, A, dtype, _S(q[:-9], k[:-9], d ** -0.5))
+
+
+@pytest.mark.parametrize("dtype,d", [("bf16", 64), ("bf16", 128), ("bf16", 32), ("f32", 64)])
+@pytest.mark.parametrize("value", [math.nan, math.inf])
+def test_infinities_and_nan_reach_only_what_sees_them(F, dtype, d, value):
+    """A key's row at 60 of 150 is not finite: queries before it see none of it.  A query's gradient at 100 is not finite:
+    keys after it are not touched by it.  And the next sequence's first rows are not finite."""
+    lens, Hq, Hkv = [150, 40], 2, 1
+    cu = _cu(lens)
+    for what in ("k", "v", "dO", "q", "next"):
+        q, k, v, dO = _inputs(lens, lens, Hq, Hkv, d, dtype, 6)
+        x = dict(q=q, k=k, v=v, dO=dO)
+        if what == "next":
+            for t in x.values():
+                t[150:153] = value
+        else:
+            x[what][100 if what in ("dO", "q") else 60, 0, 3] = value
+        o, lse = _forward(F, q, k, v, _dev(cu), _dev(cu), 150)
+        got = F.attn_prompt_backward(q, k, v, o, lse, dO, _dev(cu), max_q=150)
+        with np.errstate(all="ignore"):
+            want = O.prompt_grad(_np(q), _np(k), _np(v), cu, cu, d ** -0.5, _np(dO))
+        clean = [t.clone() for t in (q, k, v, dO)]
+        for t in clean:
+            torch.nan_to_num_(t, 0.0, 0.0, 0.0)
+        _, _, _, A = attention_grad(*clean[:3], cu, cu, d ** -0.5, clean[3])
+        first = 150 if what == "next" else 390
+        for name, w in zip(("dq", "dk", "dv"), want):
+            w = torch.from_numpy(w).cuda()
+            fine = torch.isfinite(w)
+            y = got[name].double()
+            # where the definition is finite, so is the result, and right; a row that reads the value is not checked further
+            tol = 3 * U * A[name] + U * w.abs() if dtype == "bf16" else 2e-5 * A[name]
+            ok = ~fine | ((y - w).abs() <= tol + 1e-30)
+            assert ok[:first].all(), (what, name, (~ok).nonzero()[:4].tolist())
+            if what == "k":
+                assert fine[:60].all() == (name == "dq"), name
+
+
+def test_no_queries_and_no_keys(F):
+    """Keys that no query sees get zeros; queries without keys too; empty calls write nothing."""
+    d = 64
+    for dtype in ("bf16", "f32"):
+        q, k, v, dO = _inputs([5, 0], [0, 70], 2, 2, d, dtype)
+        cu_q, cu_k = _dev([0, 5, 5]), _dev([0, 0, 70])
+        o, lse = _forward(F, q, k, v, cu_q, cu_k, 5)
+        out = {n: torch.full_like(x, 3.0) for n, x in (("dq", q), ("dk", k), ("dv", v))}
+        got = F.attn_prompt_backward(q, k, v, o, lse, dO, cu_q, cu_k, 5, out=out)
+        assert all(not x.any() for x in got.values())
+        e = lambda x: x[:0]  # noqa: E731
+        out = {n: torch.full_like(x, 3.0) for n, x in (("dk", k), ("dv", v))}
+        got = F.attn_prompt_backward(e(q), k, v, e(o), e(lse), e(dO), _dev([0, 0, 0]), cu_k, 1, out=out)
+        assert got["dq"].shape[0] == 0 and not got["dk"].any() and not got["dv"].any()
+        got = F.attn_prompt_backward(q, e(k), e(v), o, lse, dO, cu_q, _dev([0, 0, 0]), 5)
+        assert not got["dq"].any()
+        F.attn_prompt_backward(e(q), e(k), e(v), e(o), e(lse), e(dO), _dev([0, 0]))
+
+
+def test_captured_calls_share_a_workspace(F):
+    """Two graphs of different sizes over one workspace, replayed in turn with new inputs."""
+    d, Hq, Hkv, calls = 64, 4, 2, []
+    most = 0
+    for lens in ([300, 100], [129]):
+        n = sum(lens)
+        cu = _dev(_cu(lens))
+        q, k, v, dO = _inputs(lens, lens, Hq, Hkv, d, "bf16", n)
+        p = F.AttnParams(B=len(lens), Hq=Hq, Hkv=Hkv, d=d, dtype=F.FALCON_BF16, max_q=max(lens), tokens=n, k_tokens=n)
+        most = max(most, F.falcon_attn_prompt_backward_workspace_size(p))
+        g = {name: torch.zeros_like(x) for name, x in (("dq", q), ("dk", k), ("dv", v))}
+        calls.append((p, lens, cu, q, k, v, dO, g))
+    ws = F.alloc_workspace(most)
+    graphs = []
+    for p, lens, cu, q, k, v, dO, g in calls:
+        o, lse = _forward(F, q, k, v, cu, cu, max(lens))
+        run = lambda: F.falcon_attn_prompt_backward(p, q, k, v, cu, cu, o, lse, dO, None, g, ws)  # noqa: E731
+        run()
+        torch.cuda.synchronize()
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            run()
+        graphs.append((graph, o, lse))
+    for seed in (100, 200):
+        for (p, lens, cu, q, k, v, dO, g), (graph, o, lse) in zip(calls, graphs):
+            for t, x in zip((q, k, v, dO), _inputs(lens, lens, Hq, Hkv, d, "bf16", seed)):
+                t.copy_(x)
+            for t, x in zip((o, lse), _forward(F, q, k, v, cu, cu, max(lens))):
+                t.copy_(x)
+            for x in g.values():
+                x.fill_(9.0)
+            graph.replay()
+        for (p, lens, cu, q, k, v, dO, g), (graph, o, lse) in zip(calls, graphs):
+            want = F.attn_prompt_backward(q, k, v, o, lse, dO, cu, max_q=max(lens))
+            assert all(torch.equal(g[name], want[name]) for name in g)
+    assert F.falcon_workspace_status(ws) == F.FALCON_OK
+
+
+def test_differences_of_the_forward(F):
+    """<dx, u> against (L(x + h u) - L(x - h u)) / 2 h of the fp32 forward, L = <o, dO> + <lse, dlse>: the step's
+    h^2 / 6 of the third derivative, below 2^-10 of |dx| |u|, and two roundings of L, 2^-22 of sum |o dO| over h."""
+    lens, Hq, Hkv, d, h = [90, 33], 4, 2, 64, 2.0 ** -7
+    q, k, v, dO = _inputs(lens, lens, Hq, Hkv, d, "f32", 12)
+    dlse = _rand(q.shape[:2], "f32", 13)
+    cu = _dev(_cu(lens))
+
+    def loss(q, k, v):
+        o, lse = _forward(F, q, k, v, cu, cu, 90)
+        return ((o.double() * dO).sum() + (lse.double() * dlse).sum()).item(), (o.double() * dO).abs().sum().item()
+
+    o, lse = _forward(F, q, k, v, cu, cu, 90)
+    g = F.attn_prompt_backward(q, k, v, o, lse, dO, cu, max_q=90, dlse=dlse)
+    for name, at in (("dq", 0), ("dk", 1), ("dv", 2)):
+        x = [q, k, v]
+        u = _rand(x[at].shape, "f32", 20 + at)
+        u = u / u.norm() * g[name].norm().sqrt()
+        x[at] = x[at] + h * u
+        hi, size = loss(*x)
+        x[at] = x[at] - 2 * h * u
+        lo, _ = loss(*x)
+        want = (g[name].double() * u).sum().item()
+        tol = 2.0 ** -10 * (g[name].norm() * u.norm()).item() + 2.0 ** -22 * size / h
+        assert abs((hi - lo) / (2 * h) - want) <= tol
+
+
+# ---------------------------------------------------------------- norm and rotation
+def _norm_args(F, n, Hq, Hkv, d, rot, dtype, fused=0, seed=1):
+    g = torch.Generator().manual_seed(seed)
+    mk = lambda H, s: (_rand((n, H + fused, d), dtype, s) * (0.2 + 4.8 * torch.rand((n, 1, 1), generator=g).cuda()).to(  # noqa: E731
+        DT[dtype]))[:, fused:]
+    q, k, gq, gk = mk(Hq, 1), mk(Hkv, 2), _rand((n, Hq, d), dtype, 3), _rand((n, Hkv, d), dtype, 4)
+    wq, wk = (1 + 0.1 * torch.randn(d, generator=g)).cuda(), (1 + 0.1 * torch.randn(d, generator=g)).cuda()
+    table = F.rope_table(*F.rope_frequencies(rot)[:1], 500) if rot else None
+    pos = torch.randint(0, 500, (n,), generator=g).cuda() if rot else None
+    return q, k, gq, gk, wq, wk, table, pos
+
+
+def _check_rows(got, want, x, w, dy, dtype, norm):
+    """Some thirty fp32 roundings of terms up to r |u|_max: 2^-19 of it for a row; bf16 rounds once more."""
+    size = np.abs(dy).max(-1, keepdims=True) * 2
+    if norm:
+        r = 1 / np.sqrt((x * x).mean(-1, keepdims=True) + 1e-6)
+        # mean(u x r) x r is at most the largest |u| times |x r| |x r|_rms: below sqrt(d) of it
+        size = size * r * np.abs(w).max() * (1 + np.abs(x * r).max(-1, keepdims=True))
+    tol = 2.0 ** -19 * size + (U * np.abs(want) if dtype == "bf16" else 0)
+    assert (np.abs(got - want) <= tol + 1e-30).all()
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("n,Hq,Hkv,d,rot,layout,norm,fused", [
+    (1, 1, 1, 16, 16, "half", True, 0), (7, 12, 4, 64, 64, "half", True, 0), (33, 5, 5, 64, 32, "interleaved", True, 3),
+    (19, 16, 2, 128, 128, "half", True, 2), (9, 3, 1, 128, 6, "half", True, 0), (9, 3, 1, 32, 10, "interleaved", True, 1),
+    (5, 8, 8, 128, 50, "half", False, 0), (300, 17, 1, 32, 32, "half", True, 0), (4, 2, 2, 64, 0, "half", True, 0),
+    (1300, 2, 1, 16, 8, "half", True, 0), (77, 12, 12, 64, 64, "interleaved", False, 0), (6000, 1, 1, 64, 64, "half", True, 1),
+])
+def test_norm_rope_gradients(F, dtype, n, Hq, Hkv, d, rot, layout, norm, fused):
+    q, k, gq, gk, wq, wk, table, pos = _norm_args(F, n, Hq, Hkv, d, rot, dtype, fused)
+    lay = F.FALCON_ROPE_HALF if layout == "half" else F.FALCON_ROPE_INTERLEAVED
+    got = F.qk_norm_rope_backward(q, k, gq, gk, pos, table, wq, wk, norm=norm, layout=lay)
+    assert set(got) == ({"dq", "dk", "dw_q", "dw_k"} if norm else {"dq", "dk"})
+    for x, w, dy, a, b in ((q, wq, gq, "dq", "dw_q"), (k, wk, gk, "dk", "dw_k")):
+        dx, dw = O.norm_rope_grad(_np(x), _np(w), 1e-6 if norm else None, _np(pos).astype(int) if rot else None,
+                                  table.cpu().numpy() if rot else None, layout, _np(dy))
+        _check_rows(_np(got[a]), dx, _np(x), _np(w), _np(dy), dtype, norm)
+        if norm:
+            # terms off by 2^-21 of their size; sums of a lane, of lanes and of CTAs: at most 64 roundings deep on the way
+            r = 1 / np.sqrt((_np(x) ** 2).mean(-1, keepdims=True) + 1e-6)
+            size = 2 * (np.abs(_np(dy)).max(-1, keepdims=True) * np.abs(_np(x) * r)).sum((0, 1))
+            assert (np.abs(_np(got[b]) - dw) <= (2.0 ** -21 + 64 * 2.0 ** -24) * size).all()
+
+
+def test_norm_rope_gradients_in_place_alone_and_at_odd_addresses(F):
+    n, H, d = 37, 3, 64
+    q, k, gq, gk, wq, wk, table, pos = _norm_args(F, n, H, H, d, 64, "bf16")
+    want = F.qk_norm_rope_backward(q, k, gq, gk, pos, table, wq, wk)
+    alone = F.qk_norm_rope_backward(q, None, gq, None, pos, table, wq)
+    assert set(alone) == {"dq", "dw_q"} and torch.equal(alone["dq"], want["dq"])
+    # other CTAs share the rows out: dw's order may be another
+    assert torch.allclose(alone["dw_q"], want["dw_q"], rtol=0, atol=1e-5 * want["dw_q"].abs().max().item())
+    gq2, gk2 = gq.clone(), gk.clone()
+    got = F.qk_norm_rope_backward(q, k, gq2, gk2, pos, table, wq, wk, out={"dq": gq2, "dk": gk2})
+    assert got["dq"].data_ptr() == gq2.data_ptr()
+    assert all(torch.equal(got[m], want[m]) for m in want)
+    # rows two bytes past a boundary, in place (pairs read from memory before a row is written)
+    for layout in (F.FALCON_ROPE_HALF, F.FALCON_ROPE_INTERLEAVED):
+        want = F.qk_norm_rope_backward(q, k, gq, gk, pos, table, wq, wk, layout=layout)
+        buf = torch.full((n, H * d + 5), 2.0, dtype=torch.bfloat16, device="cuda")
+        odd = buf[:, 1:1 + H * d].unflatten(1, (H, d))
+        odd.copy_(gq)
+        got = F.qk_norm_rope_backward(q, k, odd, gk, pos, table, wq, wk, out={"dq": odd}, layout=layout)
+        for m in want:  # another order of the same roundings
+            scale = want[m].float().abs().max()
+            assert ((got[m].float() - want[m].float()).abs() <= 2 * U * want[m].float().abs() + 2.0 ** -17 * scale).all()
+        assert (buf[:, 0] == 2).all() and (buf[:, 1 + H * d:] == 2).all()
+
+
+@pytest.mark.parametrize("layout", ["half", "interleaved"])
+def test_norm_rope_gradients_of_positions_outside_the_table(F, layout):
+    q = _rand((5, 2, 64), "f32", 5)
+    g = _rand((5, 2, 64), "f32", 6)
+    table = F.rope_table(F.rope_frequencies(32)[0], 10)
+    pos = torch.tensor([-1, 0, 9, 10, 1 << 40]).cuda()
+    lay = F.FALCON_ROPE_HALF if layout == "half" else F.FALCON_ROPE_INTERLEAVED
+    got = F.qk_norm_rope_backward(q, None, g, None, pos, table, norm=False, layout=lay)
+    bad = torch.isnan(got["dq"][..., :32]).all(-1)
+    assert bad.tolist() == [[True, True], [False] * 2, [False] * 2, [True] * 2, [True] * 2]
+    assert torch.isfinite(got["dq"][..., 32:]).all() and torch.isfinite(got["dq"][1:3]).all()
+    got = F.qk_norm_rope_backward(q, None, g, None, pos, table, layout=lay)
+    assert torch.isnan(got["dq"]).flatten(1).all(1).tolist() == [True, False, False, True, True]
+    assert torch.isnan(got["dw_q"]).tolist() == [True] * 32 + [False] * 32  # dw_c is a sum of n_c alone
+
+
+def test_norm_rope_gradients_of_extreme_rows(F):
+    """Zero rows, rows of tiny values, rows whose square sum passes fp32's range, and no rows at all."""
+    x = torch.zeros((4, 1, 64), device="cuda")
+    x[1] = 1e-25
+    x[2] = 1e30
+    x[3] = _rand((1, 64), "f32", 1)
+    g = _rand((4, 1, 64), "f32", 2)
+    got = F.qk_norm_rope_backward(x, None, g, None)
+    dx, dw = O.norm_rope_grad(_np(x), None, 1e-6, None, None, "half", _np(g))
+    assert torch.allclose(got["dq"].double().cpu()[[0, 1, 3]], torch.from_numpy(dx)[[0, 1, 3]], rtol=2e-6, atol=1e-5)
+    assert not got["dq"][2].any() and torch.isfinite(got["dw_q"]).all()
+    rest = O.norm_rope_grad(_np(x)[[0, 1, 3]], None, 1e-6, None, None, "half", _np(g)[[0, 1, 3]])[1]
+    assert np.abs(_np(got["dw_q"]) - rest).max() < 1e-5
+    none = F.qk_norm_rope_backward(x[:0], x[:0], g[:0], g[:0])
+    assert not none["dw_q"].any() and not none["dw_k"].any() and none["dq"].shape[0] == 0
+
+
+def test_norm_rope_gradients_captured(F):
+    """A captured call over a workspace that an eager call uses in between; the same bits each time."""
+    q, k, gq, gk, wq, wk, table, pos = _norm_args(F, 700, 8, 2, 64, 64, "bf16")
+    p = F.AttnParams(Hq=8, Hkv=2, d=64, dtype=F.FALCON_BF16, tokens=700, qk_norm=1, rot=64, rope_rows=500)
+    ws = F.alloc_workspace(F.falcon_qk_norm_rope_backward_workspace_size(p))
+    g = {"dq": torch.empty_like(q), "dk": torch.empty_like(k)}
+    dw = [torch.empty(64, device="cuda") for _ in range(2)]
+    run = lambda: F.falcon_qk_norm_rope_backward(p, q, k, wq, wk, pos, table, gq, gk, g, *dw, ws)  # noqa: E731
+    run()
+    first = [x.clone() for x in (g["dq"], g["dk"], *dw)]
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        run()
+    for _ in range(3):
+        for x in (g["dq"], g["dk"], *dw):
+            x.fill_(4.0)
+        ws.fill_(255)
+        graph.replay()
+        assert all(torch.equal(a, b) for a, b in zip(first, (g["dq"], g["dk"], *dw)))
+
+
+# ---------------------------------------------------------------- together
+def test_a_layer_end_to_end(F):
+    """Norm, rotation and attention forward, then back to the fused projection, against fp64 differentiation of the
+    same rounded intermediate rows: each operator's own tolerance carries to the next, 2^-5 of the norm overall."""
+    lens, Hq, Hkv, d = [120, 77], 4, 2, 64
+    n = sum(lens)
+    x = _rand((n, Hq + 2 * Hkv, d), "bf16", 1)
+    wq, wk = 1 + 0.1 * _rand((d,), "f32", 2), 1 + 0.1 * _rand((d,), "f32", 3)
+    dO = _rand((n, Hq, d), "bf16", 4)
+    table = F.rope_table(F.rope_frequencies(d)[0], 200)
+    cu = _dev(_cu(lens))
+    pos = torch.cat([torch.arange(m) for m in lens]).cuda()
+    q, k, v = torch.split(x, [Hq, Hkv, Hkv], 1)
+    qr, kr = F.qk_norm_rope(q, k, pos, table, wq, wk)
+    o, lse = F.attn_prompt(qr, kr, v, cu, max_q=120, want_lse=True)
+    dx = torch.empty_like(x)
+    parts = dict(zip(("dq", "dk", "dv"), torch.split(dx, [Hq, Hkv, Hkv], 1)))
+    a = F.attn_prompt_backward(qr, kr, v, o, lse, dO, cu, max_q=120, out={"dv": parts["dv"]})
+    b = F.qk_norm_rope_backward(q, k, a["dq"], a["dk"], pos, table, wq, wk, out={m: parts[m] for m in ("dq", "dk")})
+
+    X, W = x.double().requires_grad_(), [w.double().requires_grad_() for w in (wq, wk)]
+    t = torch.view_as_complex(table.double().contiguous())[pos].unsqueeze(1)
+
+    def rotated(y, w):
+        y = y / (y.square().mean(-1, keepdim=True) + 1e-6).sqrt() * w
+        z = torch.complex(y[..., :d // 2], y[..., d // 2:]) * t
+        return torch.cat([z.real, z.imag], -1)
+
+    Q, K, V = rotated(X[:, :Hq], W[0]), rotated(X[:, Hq:Hq + Hkv], W[1]), X[:, Hq + Hkv:]
+    loss, at = 0.0, 0
+    for m in lens:
+        s = slice(at, at + m)
+        Kh, Vh = (y[s].repeat_interleave(Hq // Hkv, 1) for y in (K, V))
+        sc = torch.einsum("ihd,jhd->hij", Q[s], Kh) * d ** -0.5
+        sc = sc.masked_fill(~torch.ones((m, m), dtype=torch.bool, device="cuda").tril(), -math.inf)
+        loss = loss + (torch.einsum("hij,jhd->ihd", sc.softmax(-1), Vh) * dO[s].double()).sum()
+        at += m
+    gx, gq, gk = torch.autograd.grad(loss, [X, *W])
+    for got, want in ((dx, gx), (b["dw_q"], gq), (b["dw_k"], gk)):
+        assert (got.double() - want).norm() <= 2.0 ** -5 * want.norm()

@@ -288,7 +288,7 @@ int falcon_attn_prompt(const falcon_attn_params_t* p, const void* q, const void*
 
 size_t falcon_attn_prompt_backward_workspace_size(const falcon_attn_params_t* p) {
   if (check_attn(p) != FALCON_OK || p->B < 1 || p->tokens > kMostRows) return 0;
-  return align_up(attn_grad_ws_bytes(p->tokens, p->B, p->Hq), 256);
+  return align_up(attn_grad_ws_bytes(p->tokens, p->B, p->Hq, p->dtype), 256);
 }
 
 int falcon_attn_prompt_backward(const falcon_attn_params_t* p, const void* q, const void* k, const void* v,

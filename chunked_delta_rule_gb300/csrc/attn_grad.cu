@@ -24,9 +24,14 @@ namespace falcon {
 namespace {
 
 // ---------------------------------------------------------------- sums of the rows
+// x as three bf16 numbers (24 bits), packed in pairs
+__device__ __forceinline__ uint2 three_parts(float x) {
+  const float hi = __bfloat162float(__float2bfloat16_rn(x)), mid = __bfloat162float(__float2bfloat16_rn(x - hi));
+  return make_uint2(tcu::pack_bf16(x, x - hi), tcu::pack_bf16(x - hi - mid, 0.f));
+}
 // A CTA takes 128 rows of one head: d / 8 lanes a row.
 template <typename T>
-__global__ void __launch_bounds__(256) attn_grad_sums_kernel(GradArgs g, float scale_lse) {
+__global__ void __launch_bounds__(256) attn_grad_sums_kernel(GradArgs g) {
   const PromptArgs& a = g.a;
   if (blockIdx.x == 0 && threadIdx.x == 0) *static_cast<uint32_t*>(a.ws) = 0;  // the call's status
   const int h = static_cast<int>(blockIdx.x % a.Hq);
@@ -61,11 +66,19 @@ __global__ void __launch_bounds__(256) attn_grad_sums_kernel(GradArgs g, float s
       if (live) {
         const float l = g.lse[(q0 + i) * a.Hq + h];
         if (g.dlse) s -= g.dlse[(q0 + i) * a.Hq + h];
-        lse = l == -INFINITY ? INFINITY : l == INFINITY ? __int_as_float(0x7fffffff) : l * scale_lse;
+        lse = l == -INFINITY ? INFINITY : l == INFINITY ? __int_as_float(0x7fffffff) : l;
         if (l == -INFINITY) s = 0.f;
       }
       out[r] = lse;
       out[kSumRows + r] = s;
+      if (g.images) {
+        // no weight: as far down as bf16 goes short of an infinity, which would spoil the columns' zeros
+        const uint2 x = lse == INFINITY ? make_uint2(0xFF7Fu, 0u) : three_parts(-lse / a.scale), y = three_parts(-s);
+        uint4* to = reinterpret_cast<uint4*>(g.images + (static_cast<int64_t>(h) * g.blocks + at) * kImageBytes +
+                                             (r >> 3) * 256 + (r & 7) * 16);
+        to[0] = make_uint4(x.x, x.y, y.x, y.y);
+        to[8] = make_uint4(0u, 0u, 0u, 0u);
+      }
     }
   }
 }
@@ -336,7 +349,7 @@ __global__ void __launch_bounds__(256) attn_grad_keys_kernel(GradArgs g) {
       again &= ~(0xFu << (4 * ((__ffs(again) - 1) >> 2)));
       float xk[4], xv[4];
       grad_key_row<T, D>(k + row * a.k.stride, v + row * a.v.stride, q, a.q.stride, d_o, g.d_o.stride, sums, g.blocks, G,
-                         max(row - off, 0), lq, D, a.scale, 1.f, xk, xv);
+                         max(row - off, 0), lq, D, a.scale, xk, xv);
       store_row<T, D>(out + r * to.stride, of_k ? xk : xv, D);
     }
 }
@@ -371,9 +384,10 @@ int launch_t(const GradArgs& g, cudaStream_t s) {
   const PromptArgs& a = g.a;
   if (a.tokens > 0 && a.max_q > 0) {
     if (g.blocks > INT32_MAX / a.Hq) return FALCON_ERR_UNSUPPORTED;
-    attn_grad_sums_kernel<T><<<static_cast<unsigned>(g.blocks * a.Hq), 256, 0, s>>>(g, 1.f);
+    attn_grad_sums_kernel<T><<<static_cast<unsigned>(g.blocks * a.Hq), 256, 0, s>>>(g);
     if (cudaGetLastError() != cudaSuccess) return FALCON_ERR_CUDA;
   }
+  if (g.images) return launch_attn_grad_tc(g, s);
   switch (a.d) {
     case 16: return launch<T, 16>(g, s);
     case 32: return launch<T, 32>(g, s);
@@ -384,11 +398,14 @@ int launch_t(const GradArgs& g, cudaStream_t s) {
 
 }  // namespace
 
-size_t attn_grad_ws_bytes(int64_t tokens, int B, int Hq) {
-  return 256 + static_cast<size_t>(tokens / kSumRows + B) * Hq * (2 * kSumRows * sizeof(float));
+size_t attn_grad_ws_bytes(int64_t tokens, int B, int Hq, int dtype) {
+  const size_t block = 2 * kSumRows * sizeof(float) + (dtype == FALCON_BF16 ? kImageBytes : 0);
+  return 256 + static_cast<size_t>(tokens / kSumRows + B) * Hq * block;
 }
 
-int launch_attn_grad(const GradArgs& g, int dtype, cudaStream_t s) {
+int launch_attn_grad(const GradArgs& args, int dtype, cudaStream_t s) {
+  GradArgs g = args;
+  g.images = attn_grad_tc_supported(g, dtype) ? reinterpret_cast<uint8_t*>(g.sums + row_sums(g.blocks, g.a.Hq, 0)) : nullptr;
   return dtype == FALCON_BF16 ? launch_t<__nv_bfloat16>(g, s) : launch_t<float>(g, s);
 }
 

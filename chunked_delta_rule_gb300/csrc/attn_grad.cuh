@@ -15,19 +15,26 @@ struct GradArgs {
   const float* dlse;    // may be NULL
   RowsOut dq, dk, dv;   // dq.p, or dk.p and dv.p, may be NULL
   float* sums;          // in the workspace, see row_sums
+  uint8_t* images;      // the same as bf16 operand tiles, see kImageBytes; NULL: not wanted
   int64_t blocks;       // of 128 rows of queries, of a head, counted over the packed sequences
 };
-size_t attn_grad_ws_bytes(int64_t tokens, int B, int Hq);
+size_t attn_grad_ws_bytes(int64_t tokens, int B, int Hq, int dtype);
 int launch_attn_grad(const GradArgs& g, int dtype, cudaStream_t s);
+bool attn_grad_tc_supported(const GradArgs& g, int dtype);
+int launch_attn_grad_tc(const GradArgs& g, cudaStream_t s);
 
 // The rows of query block j (of 128, counted from cu_q[b] / 128 + b on for sequence b) and head h: 128 times the
-// log sum of the scores (in the unit that the kernel which reads it takes: logarithms to base e or 2), then 128 times
+// log sum of the scores (natural), then 128 times
 // D = sum_c dO_c o_c - dlse.  Rows past the sequence and rows that see no key
 // have log sum +inf: exp(score - log sum) = 0, no weight anywhere.
 constexpr int kSumRows = 128;
 __host__ __device__ __forceinline__ int64_t row_sums(int64_t blocks, int h, int64_t j) {
   return (static_cast<int64_t>(h) * blocks + j) * (2 * kSumRows);
 }
+// The same 128 rows as the B operand (16 columns, no swizzle: 8 rows x 16 bytes at (2 (row / 8) + half) 128) of one
+// more step of the products Q K^T and dO V^T: columns 0 to 2 hold -log sum / scale in three bf16 parts, 4 to 6 hold -D.
+// Against ones in those columns the products come out less them.
+constexpr int kImageBytes = kSumRows * 32;
 // first block of a sequence whose rows begin at q0
 __device__ __forceinline__ int64_t first_block(int64_t q0, int b) { return q0 / kSumRows + b; }
 
@@ -88,12 +95,11 @@ __device__ __noinline__ void grad_query_row(const T* q, const T* d_o, float lse,
 }
 
 // dk and dv of one key, over the `heads` query heads of its group and the queries [i0, i1) of its sequence, whose rows
-// begin at q and d_o (of the group's first head); sums: of that head's first block, `blocks` blocks a head, log sums in
-// units of `unit`.
+// begin at q and d_o (of the group's first head); sums: of that head's first block, `blocks` blocks a head.
 template <typename T, int D>
 __device__ __noinline__ void grad_key_row(const T* k, const T* v, const T* q, int64_t q_stride, const T* d_o,
                                           int64_t o_stride, const float* sums, int64_t blocks, int heads, int i0, int i1,
-                                          int d, float scale, float unit, float (&dk)[4], float (&dv)[4]) {
+                                          int d, float scale, float (&dk)[4], float (&dv)[4]) {
   constexpr int J = (D + 31) / 32, kBatch = 4;
   const int lane = threadIdx.x & 31;
   float kv[J], vv[J];
@@ -130,7 +136,7 @@ __device__ __noinline__ void grad_key_row(const T* k, const T* v, const T* q, in
         const float* row = sums + static_cast<int64_t>(i / kSumRows) * (2 * kSumRows) + i % kSumRows;
         const float lse = row[0];
         if (lse == INFINITY) continue;
-        const float p = expf(fmaf(s[u], scale, -lse * unit)), ds = p * (s[kBatch + u] - row[kSumRows]) * scale;
+        const float p = expf(fmaf(s[u], scale, -lse)), ds = p * (s[kBatch + u] - row[kSumRows]) * scale;
 #pragma unroll
         for (int j = 0; j < J; ++j) {
           dv[j] = fmaf(p, gt[u][j], dv[j]);

@@ -24,6 +24,11 @@ __device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
   asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
   return r;
 }
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
 __device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
   uint64_t r;
   asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
@@ -56,13 +61,13 @@ __device__ __forceinline__ bool elect_one() {
   return r != 0;
 }
 
-// [tokens, H, d] bf16 rows, boxes of 64 columns x 128 tokens: zeros past a row's end
-inline bool make_rows_map(CUtensorMap* m, const RowsIn& r, int64_t tokens, int H, int d) {
+// [tokens, H, d] bf16 rows, boxes of 64 columns x `rows` tokens: zeros past a row's end
+inline bool make_rows_map(CUtensorMap* m, const RowsIn& r, int64_t tokens, int H, int d, int rows = kTile) {
   EncodeFn enc = get_encode();
   if (!enc) return false;
   cuuint64_t dims[3] = {(cuuint64_t)d, (cuuint64_t)H, (cuuint64_t)tokens};
   cuuint64_t strides[2] = {(cuuint64_t)d * 2, (cuuint64_t)r.stride * 2};
-  cuuint32_t box[3] = {64, 1, kTile};
+  cuuint32_t box[3] = {64, 1, (cuuint32_t)rows};
   cuuint32_t es[3] = {1, 1, 1};
   return enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(r.p), dims, strides, box, es,
              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_128B,

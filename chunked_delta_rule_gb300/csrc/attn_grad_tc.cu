@@ -8,18 +8,25 @@
 // adds 64 KB in fp32 for every tile of 128 x 128, and in another order each
 // time).  A CTA owns 128 rows: of K and V (dK and dV; X = K Q^T, Y = V dO^T, the
 // queries of all heads of the group come past) or of Q and dO (dQ; X = Q K^T, Y = dO
-// V^T, the keys come past).  Per tile of rows that come past:
+// V^T, the keys come past).  Per tile of rows that come past (128; 64 at d = 64, with two
+// CTAs on an SM):
 //   load warp    TMA: the two tiles, through a ring of pairs
 //   MMA warp     X, Y and the sums' products in the order that keeps the tensor
 //                cores ahead of the softmax warps, see the loops
-//   softmax      4 warps (d = 64, a thread a row) or 8 (d = 128, two threads a row),
-//   warps        64 columns each: P from X, dS from P and Y.  P and dS go back to
-//                TMEM in bf16 over the scores that they came from, as the A operand
+//   softmax      32 columns of a row a thread: P from X, dS from P and Y.  They go back
+//   warps        to TMEM in bf16 over the scores that they came from, as the A operand
 //                of the sums' products.
-// dK and dV: a thread holds one key and 64 queries, so that log sums and D would be
+// dK and dV: a thread holds one key and 32 queries, so that log sums and D would be
 // loads for every element; they come out of the products instead, one more step of 16
 // columns: [K | 1] [Q | -log sum / scale]^T and [V | 1] [dO | -D]^T, in three bf16
 // parts (24 bits).
+// dQ: Q and dO are copied to TMEM, as the A operands there of X and Y: both operands in
+// shared memory would ask it for 8 KB a step of 128 x 128 x 16, all that it gives in
+// the 64 cycles of the step, before the TMA writes.  (For dK and dV the four
+// accumulators of d = 128 fill TMEM.)
+// Where the keys' blocks alone do not fill the GPU, 2, 4 or 8 CTAs of a cluster take a
+// block together, a share of the queries' tiles each; their sums are added over
+// distributed shared memory, in the CTAs' order.
 //
 // P and dS are rounded to bf16 as V and K are held in it: at most 2^-8 of each.
 // Everything else is fp32.
@@ -28,6 +35,8 @@
 // times an infinite or NaN value of a row that the owner does not see would spoil
 // it: a row of a result that is not finite is computed again from the definition,
 // after the pipeline has ended.
+
+#include <algorithm>
 
 #include "attn_grad.cuh"
 #include "attn_tc.cuh"
@@ -41,33 +50,42 @@ template <int D, bool KEYS>
 struct Cfg {
   static constexpr int kCtas = D == 64 ? 2 : 1;           // CTAs of an SM
   static constexpr int kN = D == 64 ? 64 : 128;           // rows of a tile that comes past
-  static constexpr int kSplit = D == 64 ? 1 : 2;          // softmax threads of a row, 64 columns each
+  static constexpr int kSplit = kN / 32;                  // softmax threads of a row, 32 columns each
+  static constexpr int kOut = (KEYS ? 2 : 1) * D / kSplit;  // columns of the sums that each of them writes
   static constexpr int kWarps = 4 * kSplit;
   static constexpr int kLoadWarp = kWarps, kMmaWarp = kWarps + 1;
   static constexpr int kThreads = 32 * kWarps + 128;
   static constexpr int kOwnBytes = kTile * D * 2, kTileBytes = kN * D * 2;
-  static constexpr int kPairs = D == 64 ? 3 : 2;
+  // dQ: the owned rows' place joins the ring (its last pairs) once they are in TMEM
+  static constexpr int kOwnPairs = KEYS ? 0 : kOwnBytes / kTileBytes;
+  static constexpr int kPairs = D == 64 ? (KEYS ? 3 : 5) : (KEYS ? 2 : 3);
+  static constexpr int kRing = 2 * kPairs * kTileBytes;
+  static constexpr int kOwnAt = KEYS ? kRing : kRing - 2 * kOwnBytes;
   static constexpr int kImage = kN * 32;                  // log sums and D of a tile of queries
-  static constexpr int kExtra = KEYS ? kPairs * kImage + 2 * kImageBytes : 0;
-  // X (two of them for dQ: the next one is formed while this one's dS lies over it), Y, sums
-  static constexpr uint32_t kColX = 0, kColY = KEYS ? kN : 2 * kN, kColV = 2 * kN, kColS = KEYS ? 2 * kN + D : 3 * kN;
+  static constexpr int kExtra = KEYS ? 2 * kOwnBytes + kPairs * kImage + 2 * kImageBytes : 0;
+  // TMEM: X, Y, the sums, and for dQ the owned rows
+  static constexpr uint32_t kColX = 0, kColY = kN, kColV = 2 * kN, kColS = KEYS ? 2 * kN + D : 2 * kN;
+  static constexpr uint32_t kColA1 = 2 * kN + D, kColA2 = kColA1 + D / 2;
   static constexpr uint32_t kCols = D == 64 ? 256 : 512;
 };
+constexpr int kMostPairs = 5;
 struct Bars {
-  uint64_t own, full1[3], full2[3], empty1[3], empty2[3], x[2], y, p, ds, drain, stall;
-  uint32_t tmem;
+  uint64_t own, ready, full[2 * kMostPairs], empty[2 * kMostPairs], x, x_read, y, p, ds, drain, stall;
+  uint32_t tmem, failed;
+  uint32_t bad[2][4];  // rows that are not finite, a bit each
 };
 template <int D, bool KEYS>
 constexpr int smem_bytes() {
-  using C = Cfg<D, KEYS>;
-  return 2 * C::kOwnBytes + 2 * C::kPairs * C::kTileBytes + C::kExtra + 1024 + static_cast<int>(sizeof(Bars));
+  return Cfg<D, KEYS>::kRing + Cfg<D, KEYS>::kExtra + 1024 + static_cast<int>(sizeof(Bars));
 }
-static_assert(smem_bytes<128, true>() <= 227 * 1024 && 2 * (smem_bytes<64, true>() + 1024) <= 228 * 1024, "shared memory");
+static_assert(smem_bytes<128, true>() <= 227 * 1024 && smem_bytes<128, false>() <= 227 * 1024, "shared memory");
+static_assert(smem_bytes<64, true>() <= 113 * 1024 && smem_bytes<64, false>() <= 113 * 1024, "shared memory");
 
 struct TcGradArgs {
   GradArgs g;
   int qblocks;  // of a sequence
   bool packed;
+  int split;    // CTAs of a cluster
   uint32_t* status;
   uint64_t limit;
   int stall;
@@ -82,6 +100,44 @@ __device__ __forceinline__ uint64_t sdesc_plain16(uint32_t saddr) {
   d |= static_cast<uint64_t>(1) << 46;
   return d;
 }
+// every thread of the cluster's CTAs
+__device__ __forceinline__ void cluster_barrier() {
+  asm volatile("barrier.cluster.arrive.release;\n\tbarrier.cluster.wait.acquire;" ::: "memory");
+}
+__device__ __forceinline__ uint32_t peer_smem(uint32_t addr, uint32_t rank) {
+  uint32_t r;
+  asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(addr), "r"(rank));
+  return r;
+}
+__device__ __forceinline__ float4 load_peer4(uint32_t addr) {
+  float4 v;
+  asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+               : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+               : "r"(addr)
+               : "memory");
+  return v;
+}
+__device__ __forceinline__ uint32_t load_peer(uint32_t addr) {
+  uint32_t v;
+  asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(addr) : "memory");
+  return v;
+}
+// packed_block by a whole warp: 32 sequences a look
+__device__ __forceinline__ int2 find_block(const int32_t* cu, int B, int rows, int j) {
+  const int lane = threadIdx.x & 31;
+  int lo = 0, n = B;
+  while (n > 1) {
+    const int step = (n + 31) / 32, i = lo + lane * step;
+    const bool begun = lane * step < n && static_cast<int64_t>(__ldg(cu + min(i, B))) / rows + i <= j;
+    const int c = max(__popc(__ballot_sync(0xffffffffu, begun)) - 1, 0);
+    lo += c * step;
+    n = min(step, n - c * step);
+  }
+  const int64_t first = static_cast<int64_t>(__ldg(cu + lo)) / rows + lo;
+  const int64_t next = static_cast<int64_t>(__ldg(cu + lo + 1)) / rows + lo + 1;
+  const int64_t row = (next - 1 - j) * rows;
+  return make_int2(lo, j < first || row > INT32_MAX ? -1 : static_cast<int>(row));
+}
 
 template <int D, bool KEYS>
 __global__ void __launch_bounds__(Cfg<D, KEYS>::kThreads, Cfg<D, KEYS>::kCtas)
@@ -89,61 +145,37 @@ __global__ void __launch_bounds__(Cfg<D, KEYS>::kThreads, Cfg<D, KEYS>::kCtas)
                         const __grid_constant__ CUtensorMap past1, const __grid_constant__ CUtensorMap past2,
                         const TcGradArgs t) {
   using C = Cfg<D, KEYS>;
-  constexpr int N = C::kN;
+  constexpr int N = C::kN, P = C::kPairs;
   const GradArgs& g = t.g;
   const PromptArgs& a = g.a;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
 
-  // whose rows
-  const int G = a.Hq / a.Hkv;
-  int b, head, row0;
-  if constexpr (KEYS) {
-    const int2 x = packed_block(a.cu_k, a.B, kTile, static_cast<int>(blockIdx.x / a.Hkv));
-    b = x.x, row0 = x.y, head = static_cast<int>(blockIdx.x % a.Hkv);
-  } else if (t.packed) {
-    const int2 x = packed_block(a.cu_q, a.B, kTile, static_cast<int>(blockIdx.x / a.Hq));
-    b = x.x, row0 = x.y, head = static_cast<int>(blockIdx.x % a.Hq);
-  } else {
-    const uint32_t bh = static_cast<uint32_t>(a.B) * a.Hq, at = blockIdx.x % bh;
-    b = static_cast<int>(at) / a.Hq, head = static_cast<int>(at) % a.Hq;
-    row0 = (t.qblocks - 1 - static_cast<int>(blockIdx.x / bh)) * kTile;  // the longest rows first
-  }
-  const int64_t q0 = a.cu_q[b], k0 = a.cu_k[b];
-  const int lq_all = static_cast<int>(a.cu_q[b + 1] - q0), lk = static_cast<int>(a.cu_k[b + 1] - k0);
-  const int lq = min(lq_all, a.max_q), off = lk - lq_all, rows = KEYS ? lk : lq;
-  if (row0 < 0 || row0 >= rows || q0 < 0 || k0 < 0 || q0 + lq_all > a.tokens || k0 + lk > a.k_tokens) return;
-  // a sequence's blocks are dealt out from its last; the first keys, which the most queries see, come first
-  if (KEYS) row0 = (lk - 1) / kTile * kTile - row0;
-  // the tiles that come past: [first, first + each N) of every head
-  const int first = KEYS ? max(row0 - off, 0) / N * N : 0;
-  const int end = KEYS ? lq : min(min(row0 + kTile, lq) + off, lk);
-  const int each = end > first ? (end - first + N - 1) / N : 0, n = KEYS ? each * G : each;
-
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = align1024(smem_raw);
-  uint8_t *s1 = smem, *s2 = s1 + C::kOwnBytes, *ring = s2 + C::kOwnBytes;  // pairs: first tile, second tile
-  uint8_t* images = ring + 2 * C::kPairs * C::kTileBytes;
-  uint8_t* ones = images + C::kPairs * C::kImage;
-  Bars* bar = reinterpret_cast<Bars*>(ring + 2 * C::kPairs * C::kTileBytes + C::kExtra);
+  uint8_t *ring = smem, *s1 = smem + C::kOwnAt, *s2 = s1 + C::kOwnBytes;  // ring: pairs of a first and a second tile
+  uint8_t* images = smem + C::kRing + 2 * C::kOwnBytes;
+  uint8_t* ones = images + P * C::kImage;
+  Bars* bar = reinterpret_cast<Bars*>(smem + C::kRing + C::kExtra);
   if (warp == C::kMmaWarp) {
     tmem_alloc(&bar->tmem, C::kCols);
     tmem_relinquish();
   }
   if (warp == C::kLoadWarp && lane == 0) {
     mbar_init(&bar->own, 1);
-    for (int i = 0; i < C::kPairs; ++i) {
-      mbar_init(&bar->full1[i], 1);
-      mbar_init(&bar->full2[i], 1);
-      mbar_init(&bar->empty1[i], 1);
-      mbar_init(&bar->empty2[i], 1);
+    mbar_init(&bar->ready, C::kWarps);
+    for (int i = 0; i < 2 * P; ++i) {
+      mbar_init(&bar->full[i], 1);
+      mbar_init(&bar->empty[i], 1);
     }
-    mbar_init(&bar->x[0], 1);
-    mbar_init(&bar->x[1], 1);
+    mbar_init(&bar->x, 1);
+    mbar_init(&bar->x_read, C::kWarps);
     mbar_init(&bar->y, 1);
     mbar_init(&bar->p, C::kWarps);
     mbar_init(&bar->ds, C::kWarps);
     mbar_init(&bar->drain, 1);
     mbar_init(&bar->stall, 1);
+    bar->failed = 0;
+    for (int i = 0; i < 8; ++i) bar->bad[i >> 2][i & 3] = 0;
     fence_mbar_init();
   }
   if (KEYS) {  // ones against the log sums (columns 0 to 2), ones against D (4 to 6)
@@ -156,59 +188,100 @@ __global__ void __launch_bounds__(Cfg<D, KEYS>::kThreads, Cfg<D, KEYS>::kCtas)
     }
     fence_proxy_async();
   }
+
+  // whose rows
+  const int G = a.Hq / a.Hkv;
+  const uint32_t block = KEYS ? blockIdx.x / t.split : blockIdx.x;
+  const int rank = KEYS ? static_cast<int>(blockIdx.x % t.split) : 0;
+  int b, head, row0;
+  if (KEYS) {
+    const int2 x = find_block(a.cu_k, a.B, kTile, static_cast<int>(block / a.Hkv));
+    b = x.x, row0 = x.y, head = static_cast<int>(block % a.Hkv);
+  } else if (t.packed) {
+    const int2 x = find_block(a.cu_q, a.B, kTile, static_cast<int>(block / a.Hq));
+    b = x.x, row0 = x.y, head = static_cast<int>(block % a.Hq);
+  } else {
+    const uint32_t bh = static_cast<uint32_t>(a.B) * a.Hq, at = block % bh;
+    b = static_cast<int>(at) / a.Hq, head = static_cast<int>(at) % a.Hq;
+    row0 = (t.qblocks - 1 - static_cast<int>(block / bh)) * kTile;  // the longest rows first
+  }
+  const int64_t q0 = a.cu_q[b], k0 = a.cu_k[b];
+  const int lq_all = static_cast<int>(a.cu_q[b + 1] - q0), lk = static_cast<int>(a.cu_k[b + 1] - k0);
+  const int lq = min(lq_all, a.max_q), off = lk - lq_all, rows = KEYS ? lk : lq;
+  const bool valid = row0 >= 0 && row0 < rows && q0 >= 0 && k0 >= 0 && q0 + lq_all <= a.tokens && k0 + lk <= a.k_tokens;
+  // a sequence's blocks are dealt out from its last; the first keys, which the most queries see, come first
+  if (KEYS) row0 = (lk - 1) / kTile * kTile - row0;
+  // the tiles that come past, [first, first + each N) of every head, and this CTA's of them
+  const int first = KEYS ? max(row0 - off, 0) / N * N : 0;
+  const int end = KEYS ? lq : min(min(row0 + kTile, lq) + off, lk);
+  const int each = end > first ? (end - first + N - 1) / N : 0;
+  int i0 = 0, n = each;
+  if (KEYS) {
+    const int64_t all = static_cast<int64_t>(each) * G;
+    i0 = static_cast<int>(all * rank / t.split);
+    n = static_cast<int>(all * (rank + 1) / t.split) - i0;
+  }
   __syncthreads();
   const uint32_t tmem = bar->tmem;
+  if (!valid) {  // (the whole cluster)
+    if (warp == C::kMmaWarp) tmem_dealloc(tmem, C::kCols);
+    return;
+  }
   auto wait = [&](uint64_t* m, uint32_t parity) {
     if (mbar_wait_sleep(m, parity, t.limit)) return true;
     atomicExch(t.status, kStatusTimeout);
+    *static_cast<volatile uint32_t*>(&bar->failed) = 1;
     return false;
   };
+  // Tile i's places in the ring, and how often they were used before.  dK and dV: the first tile (Q) is read until the
+  // tile's last product, the second (dO) until its last but two; they change places from use to use, so that each
+  // copy has a whole tile's products of time.
+  auto place = [&](int i, int second) { return 2 * (i % P) + (KEYS ? (i / P + second) & 1 : second); };
 
   // registers: the softmax threads take what the last warpgroup gives up
-  // (256 x 208 + 128 x 88 = 384 x 168; 128 x 200 + 128 x 56 = 256 x 128)
+  // (256 x 96 + 128 x 48 = 384 x 80; 512 x 104 + 128 x 64 = 640 x 96)
   if (warp >= C::kLoadWarp) {
-    if (D == 64) asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
-    else asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
+    if (D == 64) asm volatile("setmaxnreg.dec.sync.aligned.u32 48;");
+    else asm volatile("setmaxnreg.dec.sync.aligned.u32 64;");
   }
   if (warp == C::kLoadWarp) {
     if (lane == 0 && n > 0) {
       bool ok = !t.stall || wait(&bar->stall, 0);
-      int loads = 0, seconds = 0;
-      bool own = false;
+      int loads = 0;  // tiles begun: the first and the second of pair 0, of pair 1 ...
+      bool own = false, ready = false;
       if (ok) {
         own = true;
-        const int64_t at = (KEYS ? k0 : q0) + row0;
+        const int at = static_cast<int>((KEYS ? k0 : q0) + row0);
         mbar_arrive_expect_tx(&bar->own, 2 * C::kOwnBytes);
         for (int c = 0; c < D / 64; ++c) {
-          tma_load_3d(s1 + c * kTile * 128, &own1, &bar->own, c * 64, head, static_cast<int>(at));
-          tma_load_3d(s2 + c * kTile * 128, &own2, &bar->own, c * 64, head, static_cast<int>(at));
+          tma_load_3d(s1 + c * kTile * 128, &own1, &bar->own, c * 64, head, at);
+          tma_load_3d(s2 + c * kTile * 128, &own2, &bar->own, c * 64, head, at);
         }
       }
-      for (int i = 0; i < n && ok; ++i) {
-        const int st = i % C::kPairs, use = i / C::kPairs;
-        const int h = KEYS ? head * G + i / each : head / G, at = first + (KEYS ? i % each : i) * N;
+      for (; loads < 2 * n && ok; ++loads) {
+        const int i = loads >> 1, second = loads & 1, st = i % P, use = i / P, slot = place(i, second);
+        if (!KEYS && !ready && st >= P - C::kOwnPairs) {
+          if (!(ok = wait(&bar->ready, 0))) break;
+          ready = true;
+        }
+        if (use > 0 && !(ok = wait(&bar->empty[slot], (use - 1) & 1))) break;
+        const int h = KEYS ? head * G + (i0 + i) / each : head / G, at = first + (KEYS ? (i0 + i) % each : i) * N;
         const int row = static_cast<int>((KEYS ? q0 : k0) + at);
-        if (use > 0 && !(ok = wait(&bar->empty1[st], (use - 1) & 1))) break;
-        mbar_arrive_expect_tx(&bar->full1[st], C::kTileBytes + (KEYS ? C::kImage : 0));
+        const bool image = KEYS && !second;  // its place was last read by the product before the one that freed this
+        mbar_arrive_expect_tx(&bar->full[slot], C::kTileBytes + (image ? C::kImage : 0));
         for (int c = 0; c < D / 64; ++c)
-          tma_load_3d(ring + 2 * st * C::kTileBytes + c * N * 128, &past1, &bar->full1[st], c * 64, h, row);
-        if (KEYS)
+          tma_load_3d(ring + slot * C::kTileBytes + c * N * 128, second ? &past2 : &past1, &bar->full[slot], c * 64, h, row);
+        if (image)
           bulk_load(images + st * C::kImage,
                     g.images + (static_cast<int64_t>(h) * g.blocks + first_block(q0, b) + at / kSumRows) * kImageBytes +
                         at % kSumRows * 32,
-                    C::kImage, &bar->full1[st]);
-        ++loads;
-        if (use > 0 && !(ok = wait(&bar->empty2[st], (use - 1) & 1))) break;
-        mbar_arrive_expect_tx(&bar->full2[st], C::kTileBytes);
-        for (int c = 0; c < D / 64; ++c)
-          tma_load_3d(ring + (2 * st + 1) * C::kTileBytes + c * N * 128, &past2, &bar->full2[st], c * 64, h, row);
-        ++seconds;
+                    C::kImage, &bar->full[slot]);
       }
       // every copy has landed before the CTA may end
       if (own) wait(&bar->own, 0);
-      for (int i = max(0, loads - C::kPairs); i < loads; ++i) wait(&bar->full1[i % C::kPairs], (i / C::kPairs) & 1);
-      for (int i = max(0, seconds - C::kPairs); i < seconds; ++i) wait(&bar->full2[i % C::kPairs], (i / C::kPairs) & 1);
+      for (int l = max(0, loads - 2 * P); l < loads; ++l) wait(&bar->full[place(l >> 1, l & 1)], ((l >> 1) / P) & 1);
     }
+    __syncwarp();
   } else if (warp == C::kMmaWarp) {
     // The whole warp walks the loop, so that descriptors stay uniform; one lane issues.
     constexpr uint32_t id_x = idesc_bf16(kTile, N), id_s = idesc_bf16(kTile, D, false, true);
@@ -219,78 +292,79 @@ __global__ void __launch_bounds__(Cfg<D, KEYS>::kThreads, Cfg<D, KEYS>::kCtas)
     auto arrived = [&](uint64_t* m, uint32_t parity) {  // one answer for the warp
       return __all_sync(0xffffffffu, wait(m, parity)) != 0;
     };
-    // X (second = 0) or Y of tile i, each with what its completion tells
-    auto scores = [&](int i, int second, uint32_t to, uint64_t* then, uint64_t* then2) {
-      const int st = i % C::kPairs;
-      const uint64_t as = second ? a2 : a1, bs = bk + (2 * st + second) * (C::kTileBytes >> 4);
+    auto full = [&](int i, int second) { return arrived(&bar->full[place(i, second)], (i / P) & 1); };
+    // X (second = 0) or Y of tile i, with what its completion tells
+    auto scores = [&](int i, int second, uint64_t* then, bool frees) {
+      const int slot = place(i, second);
+      const uint64_t bs = bk + slot * (C::kTileBytes >> 4);
+      const uint32_t to = tm + (second ? C::kColY : C::kColX);
       if (elect_one()) {
 #pragma unroll
-        for (int ks = 0; ks < D / 16; ++ks)
-          umma_bf16(to, as + (((ks >> 2) * kTile * 128 + (ks & 3) * 32) >> 4), bs + (((ks >> 2) * N * 128 + (ks & 3) * 32) >> 4),
-                    id_x, ks > 0);
-        if (KEYS) umma_bf16(to, one + second * (kImageBytes >> 4), img + st * (C::kImage >> 4), id_x, 1);
+        for (int ks = 0; ks < D / 16; ++ks) {
+          const uint64_t bd = bs + (((ks >> 2) * N * 128 + (ks & 3) * 32) >> 4);
+          if (KEYS) umma_bf16(to, (second ? a2 : a1) + (((ks >> 2) * kTile * 128 + (ks & 3) * 32) >> 4), bd, id_x, ks > 0);
+          else umma_ts(to, tm + (second ? C::kColA2 : C::kColA1) + ks * 8, bd, id_x, ks > 0);
+        }
+        if (KEYS) umma_bf16(to, one + second * (kImageBytes >> 4), img + i % P * (C::kImage >> 4), id_x, 1);
         umma_commit(then);
-        if (then2) umma_commit(then2);
+        if (frees) umma_commit(&bar->empty[slot]);
       }
       __syncwarp();
     };
     // sum += W (bf16, in TMEM) times the first or second tile of pair i
-    auto add = [&](uint32_t sum, uint32_t w, int i, int second, bool acc, uint64_t* then) {
-      const uint64_t bs = bm + (2 * (i % C::kPairs) + second) * (C::kTileBytes >> 4);
+    auto add = [&](uint32_t sum, uint32_t w, int i, int second) {
+      const int slot = place(i, second);
+      const uint64_t bs = bm + slot * (C::kTileBytes >> 4);
       if (elect_one()) {
 #pragma unroll
-        for (int ks = 0; ks < N / 16; ++ks) umma_ts(sum, w + (ks >> 2) * 64 + (ks & 3) * 8, bs + ks * 128, id_s, acc || ks > 0);
-        umma_commit(then);
+        for (int ks = 0; ks < N / 16; ++ks)
+          umma_ts(tm + sum, tm + w + (ks >> 1) * 32 + (ks & 1) * 8, bs + ks * 128, id_s, i > 0 || ks > 0);
+        umma_commit(&bar->empty[slot]);
       }
       __syncwarp();
     };
-    bool ok = n > 0 && arrived(&bar->own, 0);
-    auto full1 = [&](int i) { return arrived(&bar->full1[i % C::kPairs], (i / C::kPairs) & 1); };
-    auto full2 = [&](int i) { return arrived(&bar->full2[i % C::kPairs], (i / C::kPairs) & 1); };
+    bool ok = n > 0 && arrived(KEYS ? &bar->own : &bar->ready, 0);
+    if (ok && (ok = full(0, 0))) {
+      tc_fence_after();
+      scores(0, 0, &bar->x, false);
+    }
     if constexpr (KEYS) {
       // ... X(i) dK(i - 1) Y(i) dV(i) X(i + 1) ...: P(i) is formed under dK(i - 1) and Y(i), dS(i) under dV(i) and X(i + 1)
-      if (ok && (ok = full1(0))) {
-        tc_fence_after();
-        scores(0, 0, tm + C::kColX, &bar->x[0], nullptr);
-      }
       for (int i = 0; i < n && ok; ++i) {
-        const int st = i % C::kPairs;
-        if (!(ok = full2(i))) break;
+        if (!(ok = full(i, 1))) break;
         tc_fence_after();
-        scores(i, 1, tm + C::kColY, &bar->y, nullptr);
+        scores(i, 1, &bar->y, false);
         if (!(ok = arrived(&bar->p, i & 1))) break;
         tc_fence_after();
-        add(tm + C::kColV, tm + C::kColX, i, 1, i > 0, &bar->empty2[st]);
+        add(C::kColV, C::kColX, i, 1);
         if (i + 1 < n) {
-          if (!(ok = full1(i + 1))) break;
+          if (!(ok = full(i + 1, 0))) break;
           tc_fence_after();
-          scores(i + 1, 0, tm + C::kColX, &bar->x[0], nullptr);
+          scores(i + 1, 0, &bar->x, false);
         }
         if (!(ok = arrived(&bar->ds, i & 1))) break;
         tc_fence_after();
-        add(tm + C::kColS, tm + C::kColY, i, 0, i > 0, &bar->empty1[st]);
+        add(C::kColS, C::kColY, i, 0);
       }
     } else {
-      // ... Y(i + 1) dQ(i) X(i + 2) ...: Y(i + 1) as soon as Y(i) has been read, X a tile ahead
-      for (int i = -1; i < n && ok; ++i) {
-        if (i >= 0) {
-          if (!(ok = arrived(&bar->ds, i & 1))) break;
-          tc_fence_after();
-        } else {
-          if (!(ok = full1(0))) break;
-          tc_fence_after();
-          scores(0, 0, tm + C::kColX, &bar->x[0], nullptr);
-        }
+      // ... Y(i) X(i + 1) dQ(i) Y(i + 1) ...: P(i + 1) is formed under dQ(i) and Y(i + 1), dS(i) under X(i + 1)
+      if (ok && (ok = full(0, 1))) {
+        tc_fence_after();
+        scores(0, 1, &bar->y, true);
+      }
+      for (int i = 0; i < n && ok; ++i) {
         if (i + 1 < n) {
-          if (!(ok = full2(i + 1))) break;
+          if (!(ok = full(i + 1, 0) && arrived(&bar->x_read, i & 1))) break;
           tc_fence_after();
-          scores(i + 1, 1, tm + C::kColY, &bar->y, &bar->empty2[(i + 1) % C::kPairs]);
+          scores(i + 1, 0, &bar->x, false);
         }
-        if (i >= 0) add(tm + C::kColS, tm + C::kColX + (i & 1) * N, i, 0, i > 0, &bar->empty1[i % C::kPairs]);
-        if (i + 2 < n) {
-          if (!(ok = full1(i + 2))) break;
+        if (!(ok = arrived(&bar->ds, i & 1))) break;
+        tc_fence_after();
+        add(C::kColS, C::kColY, i, 0);
+        if (i + 1 < n) {
+          if (!(ok = full(i + 1, 1))) break;
           tc_fence_after();
-          scores(i + 2, 0, tm + C::kColX + (i & 1) * N, &bar->x[i & 1], nullptr);
+          scores(i + 1, 1, &bar->y, true);
         }
       }
     }
@@ -299,111 +373,144 @@ __global__ void __launch_bounds__(Cfg<D, KEYS>::kThreads, Cfg<D, KEYS>::kCtas)
     wait(&bar->drain, 0);
     __syncwarp();
   } else if (warp < C::kLoadWarp) {
-    if (D == 64) asm volatile("setmaxnreg.inc.sync.aligned.u32 200;");
-    else asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
-    const int half = C::kSplit == 2 ? warp >> 2 : 0, quad = warp & 3, r = quad * 32 + lane;
+    if (D == 64) asm volatile("setmaxnreg.inc.sync.aligned.u32 96;");
+    else asm volatile("setmaxnreg.inc.sync.aligned.u32 104;");
+    const int part = warp >> 2, quad = warp & 3, r = quad * 32 + lane;
     const uint32_t mine = tmem + (static_cast<uint32_t>(quad * 32) << 16);
     const int row = row0 + r;
     const float sl2 = a.scale * kLog2e;
     const uint64_t scale2 = pack2(sl2, sl2);
     const float* sums = g.sums + row_sums(g.blocks, KEYS ? head * G : head, first_block(q0, b));
-    uint64_t lse2 = 0, delta2 = 0;  // of this thread's query, negative
-    if (!KEYS) {
-      const float* at = sums + static_cast<int64_t>(row0 / kSumRows) * (2 * kSumRows) + r;
-      lse2 = pack2(-at[0] * kLog2e, -at[0] * kLog2e);
-      delta2 = pack2(-at[kSumRows], -at[kSumRows]);
-    }
     auto arrive = [&](uint64_t* m) {  // once for the warp: arrivals of 32 lanes on one word take their turns
       __syncwarp();
       if (lane == 0) mbar_arrive(m);
     };
     auto waited = [&](uint64_t* m, uint32_t parity) { return __all_sync(0xffffffffu, wait(m, parity)) != 0; };
     bool ok = true;
-    for (int i = 0; i < n; ++i) {
-      const int at = first + (KEYS ? i % each : i) * N + half * 64;  // of the first column
-      const uint32_t tx = mine + C::kColX + (KEYS ? 0 : (i & 1) * N) + half * 64, ty = mine + C::kColY + half * 64;
-      if (!(ok = waited(KEYS ? &bar->x[0] : &bar->x[i & 1], (KEYS ? i : i >> 1) & 1))) break;
-      tc_fence_after();
-      float p[64];
+    uint64_t lse2 = 0, delta2 = 0;  // of this thread's query, negative
+    if (!KEYS && n > 0) {
+      const float* at = sums + static_cast<int64_t>(row0 / kSumRows) * (2 * kSumRows) + r;
+      lse2 = pack2(-at[0] * kLog2e, -at[0] * kLog2e);
+      delta2 = pack2(-at[kSumRows], -at[kSumRows]);
+      // the owned rows to TMEM, a share of the columns each; rows past the sequence are some others', or zeros
+      if ((ok = waited(&bar->own, 0))) {
+        constexpr int kShare = 2 * D / C::kSplit;  // of the 2 D elements of a row of Q and dO: 64
+        static_assert(kShare == 64, "a slab of 64 columns a thread");
+        const uint8_t* from = s1 + part * kTile * 128;
+        uint32_t w[32];
 #pragma unroll
-      for (int c = 0; c < 2; ++c) {
-        uint32_t v[32];
-        tmem_ld32(tx + c * 32, v);
-#pragma unroll
-        for (int e = 0; e < 32; ++e) p[c * 32 + e] = __uint_as_float(v[e]);
+        for (int c = 0; c < 8; ++c) {
+          const uint4 x = *reinterpret_cast<const uint4*>(from + sw128(r, c * 8));
+          w[4 * c] = x.x, w[4 * c + 1] = x.y, w[4 * c + 2] = x.z, w[4 * c + 3] = x.w;
+        }
+        tmem_st32(mine + C::kColA1 + part * 32, w);
+        tmem_wait_st();
+        tc_fence_before();
+        arrive(&bar->ready);
       }
+    }
+    for (int i = 0; i < n && ok; ++i) {
+      const int at = first + (KEYS ? (i0 + i) % each : i) * N + part * 32;  // of the first column
+      const uint32_t tx = mine + C::kColX + part * 32, ty = mine + C::kColY + part * 32;
+      if (!(ok = waited(&bar->x, i & 1))) break;
+      tc_fence_after();
+      float p[32];
+      uint32_t v[32], u[16];
+      tmem_ld32(tx, v);
       tmem_wait_ld();
+      if (!KEYS) {
+        tc_fence_before();
+        arrive(&bar->x_read);
+      }
+#pragma unroll
+      for (int e = 0; e < 32; ++e) p[e] = __uint_as_float(v[e]);
       if constexpr (KEYS) {
-        if (at + off < row0 + kTile - 1) {  // queries of this half that some key is behind
+        if (at + off < row0 + kTile - 1) {  // some key is behind a query of these
           const int lim = row - off - at;
 #pragma unroll
-          for (int e = 0; e < 64; ++e)
+          for (int e = 0; e < 32; ++e)
             if (e < lim) p[e] = -INFINITY;
         }
       } else {
-        if (at + 64 > min(row0 + off + 1, lk)) {
+        if (at + 32 > min(row0 + off + 1, lk)) {
           const int lim = min(row + off + 1, lk) - at;
 #pragma unroll
-          for (int e = 0; e < 64; ++e)
+          for (int e = 0; e < 32; ++e)
             if (e >= lim) p[e] = -INFINITY;
         }
       }
-      uint32_t u[32];
 #pragma unroll
-      for (int e = 0; e < 32; ++e) {
-        const uint64_t s = pack2(p[2 * e], p[2 * e + 1]);
-        unpack2(KEYS ? mul2(s, scale2) : fma2(s, scale2, lse2), p[2 * e], p[2 * e + 1]);
+      for (int e = 0; e < 16; ++e) {
+        const uint64_t x = pack2(p[2 * e], p[2 * e + 1]);
+        unpack2(KEYS ? mul2(x, scale2) : fma2(x, scale2, lse2), p[2 * e], p[2 * e + 1]);
         p[2 * e] = ex2(p[2 * e]), p[2 * e + 1] = ex2(p[2 * e + 1]);
         if (KEYS) u[e] = pack_bf16(p[2 * e], p[2 * e + 1]);
       }
       if (KEYS) {
-        tmem_st32(tx, u);
+        tmem_st16(tx, u);
         tmem_wait_st();
         tc_fence_before();
         arrive(&bar->p);
       }
       if (!(ok = waited(&bar->y, i & 1))) break;
       tc_fence_after();
-      uint32_t y[2][32];
-      tmem_ld32(ty, y[0]);
-      tmem_ld32(ty + 32, y[1]);
+      tmem_ld32(ty, v);
       tmem_wait_ld();
 #pragma unroll
-      for (int e = 0; e < 32; ++e) {
-        uint64_t z = pack2(__uint_as_float(y[e >> 4][(2 * e) & 31]), __uint_as_float(y[e >> 4][(2 * e + 1) & 31]));
+      for (int e = 0; e < 16; ++e) {
+        uint64_t z = pack2(__uint_as_float(v[2 * e]), __uint_as_float(v[2 * e + 1]));
         if (!KEYS) z = add2(z, delta2);
         float z0, z1;
         unpack2(mul2(pack2(p[2 * e], p[2 * e + 1]), z), z0, z1);
         u[e] = pack_bf16(z0, z1);
       }
-      tmem_st32(KEYS ? ty : tx, u);
+      tmem_st16(ty, u);
       tmem_wait_st();
       tc_fence_before();
       arrive(&bar->ds);
     }
     // the last product is the one that frees the last pair's first tile
-    if (ok && n > 0) ok = waited(&bar->empty1[(n - 1) % C::kPairs], ((n - 1) / C::kPairs) & 1);
-    ok = __all_sync(0xffffffffu, ok);
-    if (ok) {
-      tc_fence_after();
-      const int d = D == 64 ? a.d : D;  // of the rows
-#pragma unroll
-      for (int out = KEYS ? 0 : 1; out < 2; ++out) {  // dV, then dK; or dQ
-        const RowsOut& to = KEYS ? (out ? g.dk : g.dv) : g.dq;
+    if (ok && n > 0) ok = waited(&bar->empty[place(n - 1, 0)], ((n - 1) / P) & 1);
+    tc_fence_after();
+    const int d = D == 64 ? a.d : D;  // of the rows
+    // a row of a result (x1: dK or dQ, x2: dV) from the definition
+    auto compute_again = [&](int i, float (&x1)[4], float (&x2)[4]) {
+      const __nv_bfloat16 *q = static_cast<const __nv_bfloat16*>(a.q.p), *d_o = static_cast<const __nv_bfloat16*>(g.d_o.p);
+      const __nv_bfloat16 *k = static_cast<const __nv_bfloat16*>(a.k.p), *v = static_cast<const __nv_bfloat16*>(a.v.p);
+      if constexpr (KEYS) {
+        const int64_t h0 = static_cast<int64_t>(head) * G * d, hk = static_cast<int64_t>(head) * d;
+        grad_key_row<__nv_bfloat16, D>(k + (k0 + i) * a.k.stride + hk, v + (k0 + i) * a.v.stride + hk,
+                                       q + q0 * a.q.stride + h0, a.q.stride, d_o + q0 * g.d_o.stride + h0, g.d_o.stride,
+                                       sums, g.blocks, G, max(i - off, 0), lq, d, a.scale, x1, x2);
+      } else {
+        const int64_t h0 = static_cast<int64_t>(head) * d, hk = static_cast<int64_t>(head / G) * d;
+        const float* s = sums + static_cast<int64_t>(i / kSumRows) * (2 * kSumRows) + i % kSumRows;
+        grad_query_row<__nv_bfloat16, D>(q + (q0 + i) * a.q.stride + h0, d_o + (q0 + i) * g.d_o.stride + h0, s[0],
+                                         s[kSumRows], k + k0 * a.k.stride + hk, a.k.stride, v + k0 * a.v.stride + hk,
+                                         a.v.stride, min(i + off + 1, lk), d, a.scale, x1);
+      }
+    };
+    if (!KEYS || t.split == 1) {
+      if (__all_sync(0xffffffffu, ok)) {
+        // this thread's columns of a row: of dV (the first ones) or dK; of dQ
+        const bool of_v = KEYS && part * C::kOut < D;
+        const int c0 = part * C::kOut % D;
+        const RowsOut& to = KEYS ? (of_v ? g.dv : g.dk) : g.dq;
         __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(to.p) + ((KEYS ? k0 : q0) + row0) * to.stride +
-                             static_cast<int64_t>(head) * d;
-        const float f = out ? a.scale : 1.f;
+                             static_cast<int64_t>(head) * d + c0;
+        const float f = of_v ? 1.f : a.scale;
         const uint64_t f2 = pack2(f, f);
-        const uint32_t from = mine + (out ? C::kColS : C::kColV) + half * 64;
+        const uint32_t from = mine + (of_v ? C::kColV : C::kColS) + c0;
         uint64_t rest = 0;  // z * 0 added up: NaN where some z is not finite
-        // a warp's 32 rows x 64 dims through shared memory (the owned tiles' place: every product is done), so that a
-        // store covers whole lines
-        uint8_t* stage = (out ? s2 : s1) + half * kTile * 128;
+        // a warp's 32 rows through shared memory (the ring's place: every product is done), so that a store covers
+        // whole lines
+        uint8_t* stage = ring + (part * C::kOut >> 6) * kTile * 128;
+        const int sc = part * C::kOut & 63;
 #pragma unroll
-        for (int c = 0; c < 2; ++c) {
+        for (int c = 0; c < C::kOut; c += 32) {
           uint32_t v[32];
           if (n > 0) {
-            tmem_ld32(from + c * 32, v);
+            tmem_ld32(from + c, v);
             tmem_wait_ld();
           } else {
 #pragma unroll
@@ -420,50 +527,97 @@ __global__ void __launch_bounds__(Cfg<D, KEYS>::kThreads, Cfg<D, KEYS>::kCtas)
               unpack2(z, z0, z1);
               w[k] = pack_bf16(z0, z1);
             }
-            *reinterpret_cast<uint4*>(stage + sw128(r, c * 32 + e * 8)) = make_uint4(w[0], w[1], w[2], w[3]);
+            *reinterpret_cast<uint4*>(stage + sw128(r, sc + c + e * 8)) = make_uint4(w[0], w[1], w[2], w[3]);
           }
         }
         __syncwarp();
+        constexpr int kPieces = C::kOut / 8;  // 16 bytes each
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          const int rr = quad * 32 + e * 4 + (lane >> 3), c = (lane & 7) * 8;
-          if (row0 + rr >= rows || (D == 64 && c >= d)) continue;
-          *reinterpret_cast<uint4*>(dst + rr * to.stride + half * 64 + c) = *reinterpret_cast<const uint4*>(stage + sw128(rr, c));
+        for (int e = 0; e < kPieces; ++e) {
+          const int x = e * 32 + lane, rr = quad * 32 + x / kPieces, c = x % kPieces * 8;
+          if (row0 + rr >= rows || (D == 64 && c0 + c >= d)) continue;
+          *reinterpret_cast<uint4*>(dst + rr * to.stride + c) = *reinterpret_cast<const uint4*>(stage + sw128(rr, sc + c));
         }
         float ra, rb;
         unpack2(rest, ra, rb);
         __syncwarp();
         for (uint32_t again = __ballot_sync(0xffffffffu, row < rows && !(ra + rb == 0.f)); again; again &= again - 1) {
           const int i = row0 + quad * 32 + __ffs(again) - 1;
-          const __nv_bfloat16 *q = static_cast<const __nv_bfloat16*>(a.q.p), *d_o = static_cast<const __nv_bfloat16*>(g.d_o.p);
-          const __nv_bfloat16 *k = static_cast<const __nv_bfloat16*>(a.k.p), *v = static_cast<const __nv_bfloat16*>(a.v.p);
           float x1[4], x2[4];
-          if constexpr (KEYS) {
-            const int64_t h0 = static_cast<int64_t>(head) * G * d, hk = static_cast<int64_t>(head) * d;
-            grad_key_row<__nv_bfloat16, D>(k + (k0 + i) * a.k.stride + hk, v + (k0 + i) * a.v.stride + hk,
-                                           q + q0 * a.q.stride + h0, a.q.stride, d_o + q0 * g.d_o.stride + h0, g.d_o.stride,
-                                           sums, g.blocks, G, max(i - off, 0), lq, d, a.scale, x1, x2);
-          } else {
-            const int64_t h0 = static_cast<int64_t>(head) * d, hk = static_cast<int64_t>(head / G) * d;
-            const float* s = sums + static_cast<int64_t>(i / kSumRows) * (2 * kSumRows) + i % kSumRows;
-            grad_query_row<__nv_bfloat16, D>(q + (q0 + i) * a.q.stride + h0, d_o + (q0 + i) * g.d_o.stride + h0, s[0],
-                                             s[kSumRows], k + k0 * a.k.stride + hk, a.k.stride, v + k0 * a.v.stride + hk,
-                                             a.v.stride, min(i + off + 1, lk), d, a.scale, x1);
-          }
+          compute_again(i, x1, x2);
           // this warp's part of the row
 #pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            const int c = half * 64 + e * 32 + lane, j = C::kSplit == 2 ? 2 * half + e : e;
-            float z = 0.f;
-#pragma unroll
-            for (int m = 0; m < 4; ++m)
-              if (m == j) z = KEYS && out == 0 ? x2[m] : x1[m];
-            if (c < d) dst[(i - row0) * to.stride + c] = __float2bfloat16_rn(z);
+          for (int m = 0; m < D / 32; ++m) {
+            const int c = m * 32 + lane;
+            if (m * 32 >= c0 && m * 32 < c0 + C::kOut && c < d)
+              dst[(i - row0) * to.stride + c - c0] = __float2bfloat16_rn(of_v ? x2[m] : x1[m]);
           }
         }
       }
+    } else {
+      // The sums in fp32 to shared memory (the ring's place and on: every product is done), 128 rows of dV, then of dK,
+      // 16-byte pieces swizzled by row; then each CTA adds up its share of the rows.
+      const bool of_v = part * C::kOut < D;
+      const int c0 = part * C::kOut % D;
+      const uint32_t from = mine + (of_v ? C::kColV : C::kColS) + c0;
+      uint8_t* dst = smem + (of_v ? 0 : kTile * D * 4) + r * D * 4;
+#pragma unroll
+      for (int c = 0; c < C::kOut; c += 32) {
+        uint32_t v[32];
+        if (n > 0 && ok) {
+          tmem_ld32(from + c, v);
+          tmem_wait_ld();
+        } else {
+#pragma unroll
+          for (int e = 0; e < 32; ++e) v[e] = 0;
+        }
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+          *reinterpret_cast<uint4*>(dst + ((((c0 + c) >> 2) + e) ^ (r & 7)) * 16) =
+              make_uint4(v[4 * e], v[4 * e + 1], v[4 * e + 2], v[4 * e + 3]);
+      }
+      cluster_barrier();
+      bool fine = true;
+      for (int s = 0; s < t.split; ++s) fine = fine && load_peer(peer_smem(smem_u32(&bar->failed), s)) == 0;
+      if (fine) {
+        const int share = kTile / t.split, rs = rank * share;
+        for (int x = tid; x < 2 * share * (D / 4); x += 32 * C::kWarps) {
+          const int c = x % (D / 4), rr = rs + x / (D / 4) % share, out = x / (D / 4) / share;  // out: dV, dK
+          if (row0 + rr >= rows || 4 * c >= d) continue;
+          const uint32_t at = smem_u32(smem) + out * (kTile * D * 4) + rr * (D * 4) + ((c ^ (rr & 7)) << 4);
+          float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
+          for (int s = 0; s < t.split; ++s) {
+            const float4 y = load_peer4(peer_smem(at, s));
+            sum.x += y.x, sum.y += y.y, sum.z += y.z, sum.w += y.w;
+          }
+          const float f = out ? a.scale : 1.f;
+          sum.x *= f, sum.y *= f, sum.z *= f, sum.w *= f;
+          const float rest = fmaf(sum.x, 0.f, fmaf(sum.y, 0.f, fmaf(sum.z, 0.f, sum.w * 0.f)));
+          if (!(rest == 0.f)) atomicOr(&bar->bad[out][rr >> 5], 1u << (rr & 31));
+          const RowsOut& to = out ? g.dk : g.dv;
+          *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(to.p) + (k0 + row0 + rr) * to.stride +
+                                    static_cast<int64_t>(head) * d + 4 * c) =
+              make_uint2(pack_bf16(sum.x, sum.y), pack_bf16(sum.z, sum.w));
+        }
+        named_bar(1, 32 * C::kWarps);
+        for (int x = warp; x < 2 * share; x += C::kWarps) {
+          const int rr = rs + x % share, out = x / share;
+          if (!(bar->bad[out][rr >> 5] >> (rr & 31) & 1)) continue;
+          float x1[4], x2[4];
+          compute_again(row0 + rr, x1, x2);
+          const RowsOut& to = out ? g.dk : g.dv;
+          store_row<__nv_bfloat16, D>(static_cast<__nv_bfloat16*>(to.p) + (k0 + row0 + rr) * to.stride +
+                                          static_cast<int64_t>(head) * d, out ? x1 : x2, d);
+        }
+      }
+      cluster_barrier();  // the others have read what lies here
     }
     tc_fence_before();
+  }
+  if (KEYS && t.split > 1 && warp >= C::kLoadWarp) {
+    __syncwarp();
+    cluster_barrier();
+    cluster_barrier();
   }
   __syncthreads();
   if (warp == C::kMmaWarp) {
@@ -474,12 +628,22 @@ __global__ void __launch_bounds__(Cfg<D, KEYS>::kThreads, Cfg<D, KEYS>::kCtas)
 
 template <int D, bool KEYS>
 int launch_kernel(TcGradArgs& t, int64_t grid, const CUtensorMap (&m)[4], cudaStream_t s) {
-  if (grid < 1 || grid > INT32_MAX) return FALCON_ERR_UNSUPPORTED;
+  if (grid < 1 || grid > INT32_MAX / t.split) return FALCON_ERR_UNSUPPORTED;
   t.stall = take_test_stall() ? 1 : 0;
   const auto kern = attn_grad_tc_kernel<D, KEYS>;
   if (!set_smem_limit(reinterpret_cast<const void*>(kern), smem_bytes<D, KEYS>())) return FALCON_ERR_CUDA;
-  kern<<<static_cast<unsigned>(grid), Cfg<D, KEYS>::kThreads, smem_bytes<D, KEYS>(), s>>>(m[0], m[1], m[2], m[3], t);
-  return cudaGetLastError() == cudaSuccess ? FALCON_OK : FALCON_ERR_CUDA;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(grid * t.split));
+  cfg.blockDim = dim3(Cfg<D, KEYS>::kThreads);
+  cfg.dynamicSmemBytes = smem_bytes<D, KEYS>();
+  cfg.stream = s;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = static_cast<unsigned>(t.split);
+  attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = t.split > 1 ? 1 : 0;
+  return cudaLaunchKernelEx(&cfg, kern, m[0], m[1], m[2], m[3], t) == cudaSuccess ? FALCON_OK : FALCON_ERR_CUDA;
 }
 
 template <int D>
@@ -487,7 +651,7 @@ int launch_d(const GradArgs& g, cudaStream_t s) {
   const PromptArgs& a = g.a;
   TcGradArgs t;
   t.g = g;
-  t.qblocks = 0, t.packed = false;
+  t.qblocks = 0, t.packed = false, t.split = 1;
   t.status = static_cast<uint32_t*>(a.ws);
   t.limit = wait_limit_ns();
   CUtensorMap m[4];
@@ -504,12 +668,16 @@ int launch_d(const GradArgs& g, cudaStream_t s) {
     if (st != FALCON_OK) return st;
   }
   if (g.dk.p) {
-    const int64_t blocks = a.k_tokens / kTile + a.B;
     constexpr int N = Cfg<D, true>::kN;
+    const int64_t blocks = a.k_tokens / kTile + a.B;
+    if (blocks > INT32_MAX / a.Hkv) return FALCON_ERR_UNSUPPORTED;
     if (!maps(a.k, a.k_tokens, a.Hkv, kTile, m) || !maps(a.v, a.k_tokens, a.Hkv, kTile, m + 1) ||
         !maps(a.q, a.tokens, a.Hq, N, m + 2) || !maps(g.d_o, a.tokens, a.Hq, N, m + 3))
       return FALCON_ERR_CUDA;
-    return blocks > INT32_MAX / a.Hkv ? FALCON_ERR_UNSUPPORTED : launch_kernel<D, true>(t, blocks * a.Hkv, m, s);
+    // clusters until there are two rounds of CTAs, as long as a CTA keeps some four tiles
+    const int64_t ctas = blocks * a.Hkv, tiles = std::max<int64_t>(a.tokens / a.B / (2 * N), 1) * (a.Hq / a.Hkv);
+    while (t.split < 8 && ctas * t.split < int64_t(2) * sm_count() * Cfg<D, true>::kCtas && tiles >= 8 * t.split) t.split *= 2;
+    return launch_kernel<D, true>(t, ctas, m, s);
   }
   return FALCON_OK;
 }

@@ -287,8 +287,8 @@ int falcon_attn_prompt(const falcon_attn_params_t* p, const void* q, const void*
 }
 
 size_t falcon_attn_prompt_backward_workspace_size(const falcon_attn_params_t* p) {
-  if (check_attn(p) != FALCON_OK || p->B < 1 || p->tokens > kMostRows) return 0;
-  return align_up(attn_grad_ws_bytes(p->tokens, p->B, p->Hq, p->dtype), 256);
+  if (check_attn(p) != FALCON_OK || p->B < 1 || p->tokens > kMostRows || p->k_tokens > kMostRows) return 0;
+  return align_up(attn_grad_ws_bytes(p->tokens, p->k_tokens, p->B, p->Hq, p->Hkv, p->d, p->dtype), 256);
 }
 
 int falcon_attn_prompt_backward(const falcon_attn_params_t* p, const void* q, const void* k, const void* v,

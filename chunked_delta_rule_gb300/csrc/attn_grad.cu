@@ -398,15 +398,16 @@ int launch_t(const GradArgs& g, cudaStream_t s) {
 
 }  // namespace
 
-size_t attn_grad_ws_bytes(int64_t tokens, int B, int Hq, int dtype) {
-  const size_t block = 2 * kSumRows * sizeof(float) + (dtype == FALCON_BF16 ? kImageBytes : 0);
-  return 256 + static_cast<size_t>(tokens / kSumRows + B) * Hq * block;
+size_t attn_grad_ws_bytes(int64_t tokens, int64_t k_tokens, int B, int Hq, int Hkv, int d, int dtype) {
+  const size_t blocks = static_cast<size_t>(tokens / kSumRows + B) * Hq, sums = blocks * (2 * kSumRows * sizeof(float));
+  return 256 + sums + (dtype == FALCON_BF16 ? blocks * kImageBytes : attn_grad_tc32_ws_bytes(tokens, k_tokens, B, Hq, Hkv, d));
 }
 
 int launch_attn_grad(const GradArgs& args, int dtype, cudaStream_t s) {
+  if (dtype == FALCON_F32) return launch_attn_grad_tc32(args, s);
   GradArgs g = args;
   g.images = attn_grad_tc_supported(g, dtype) ? reinterpret_cast<uint8_t*>(g.sums + row_sums(g.blocks, g.a.Hq, 0)) : nullptr;
-  return dtype == FALCON_BF16 ? launch_t<__nv_bfloat16>(g, s) : launch_t<float>(g, s);
+  return launch_t<__nv_bfloat16>(g, s);
 }
 
 }  // namespace falcon

@@ -18,10 +18,12 @@ struct GradArgs {
   uint8_t* images;      // the same as bf16 operand tiles, see kImageBytes; NULL: not wanted
   int64_t blocks;       // of 128 rows of queries, of a head, counted over the packed sequences
 };
-size_t attn_grad_ws_bytes(int64_t tokens, int B, int Hq, int dtype);
+size_t attn_grad_ws_bytes(int64_t tokens, int64_t k_tokens, int B, int Hq, int Hkv, int d, int dtype);
 int launch_attn_grad(const GradArgs& g, int dtype, cudaStream_t s);
 bool attn_grad_tc_supported(const GradArgs& g, int dtype);
 int launch_attn_grad_tc(const GradArgs& g, cudaStream_t s);
+size_t attn_grad_tc32_ws_bytes(int64_t tokens, int64_t k_tokens, int B, int Hq, int Hkv, int d);
+int launch_attn_grad_tc32(const GradArgs& g, cudaStream_t s);
 
 // The rows of query block j (of 128, counted from cu_q[b] / 128 + b on for sequence b) and head h: 128 times the
 // log sum of the scores (natural), then 128 times
@@ -37,6 +39,23 @@ __host__ __device__ __forceinline__ int64_t row_sums(int64_t blocks, int h, int6
 constexpr int kImageBytes = kSumRows * 32;
 // first block of a sequence whose rows begin at q0
 __device__ __forceinline__ int64_t first_block(int64_t q0, int b) { return q0 / kSumRows + b; }
+
+// packed_block by a whole warp: 32 sequences a look
+__device__ __forceinline__ int2 find_block(const int32_t* cu, int B, int rows, int j) {
+  const int lane = threadIdx.x & 31;
+  int lo = 0, n = B;
+  while (n > 1) {
+    const int step = (n + 31) / 32, i = lo + lane * step;
+    const bool begun = lane * step < n && static_cast<int64_t>(__ldg(cu + min(i, B))) / rows + i <= j;
+    const int c = max(__popc(__ballot_sync(0xffffffffu, begun)) - 1, 0);
+    lo += c * step;
+    n = min(step, n - c * step);
+  }
+  const int64_t first = static_cast<int64_t>(__ldg(cu + lo)) / rows + lo;
+  const int64_t next = static_cast<int64_t>(__ldg(cu + lo + 1)) / rows + lo + 1;
+  const int64_t row = (next - 1 - j) * rows;
+  return make_int2(lo, j < first || row > INT32_MAX ? -1 : static_cast<int>(row));
+}
 
 // Sums over the lanes, a few at a time.
 template <int N>

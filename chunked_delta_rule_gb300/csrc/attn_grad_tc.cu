@@ -122,23 +122,6 @@ __device__ __forceinline__ uint32_t load_peer(uint32_t addr) {
   asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(addr) : "memory");
   return v;
 }
-// packed_block by a whole warp: 32 sequences a look
-__device__ __forceinline__ int2 find_block(const int32_t* cu, int B, int rows, int j) {
-  const int lane = threadIdx.x & 31;
-  int lo = 0, n = B;
-  while (n > 1) {
-    const int step = (n + 31) / 32, i = lo + lane * step;
-    const bool begun = lane * step < n && static_cast<int64_t>(__ldg(cu + min(i, B))) / rows + i <= j;
-    const int c = max(__popc(__ballot_sync(0xffffffffu, begun)) - 1, 0);
-    lo += c * step;
-    n = min(step, n - c * step);
-  }
-  const int64_t first = static_cast<int64_t>(__ldg(cu + lo)) / rows + lo;
-  const int64_t next = static_cast<int64_t>(__ldg(cu + lo + 1)) / rows + lo + 1;
-  const int64_t row = (next - 1 - j) * rows;
-  return make_int2(lo, j < first || row > INT32_MAX ? -1 : static_cast<int>(row));
-}
-
 template <int D, bool KEYS>
 __global__ void __launch_bounds__(Cfg<D, KEYS>::kThreads, Cfg<D, KEYS>::kCtas)
     attn_grad_tc_kernel(const __grid_constant__ CUtensorMap own1, const __grid_constant__ CUtensorMap own2,

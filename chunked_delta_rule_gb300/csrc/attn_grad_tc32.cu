@@ -1,0 +1,786 @@
+// Gradient of causal attention over packed prompts on the tensor cores (fp32).
+//
+//   P = exp(scale Q K^T - log sum),  dS = P (dO V^T - D)
+//   dV = P^T dO,  dK = scale dS^T Q,  dQ = scale dS K
+//
+// An operand is held as two halves, x = s (hi + lo), each rounded to 11 bits, with a power of two s for
+// every row that brings the row's largest element to [2^14, 2^15): 22 bits, down to 2^-40
+// of the row's largest.  A product is hi hi + hi lo + lo hi, the small ones first; its sums stay
+// in the tensor cores, which cut them off, for one tile only (64 rows) and are added up in
+// fp32 registers.
+//
+// The first kernel splits q, k, v and dO into the workspace, 64 rows of a head at a time, laid out as
+// the operand tiles in shared memory, and forms D.  Two kernels from one template do the products, so
+// that every sum has one owner and one order.  A CTA owns 128 rows: of K and V (dK and dV; X = K Q^T,
+// Y = V dO^T, the queries of all heads of the group come past, 64 at a time) or of Q and dO (dQ;
+// X = Q K^T, Y = dO V^T, the keys come past).  A thread holds a row of a tile.  P and dS are split like the
+// operands, a power of two for every row of a tile, after the factors of the rows that the sum
+// runs over have been multiplied in; so no range of P or dS is out of reach.
+// dK and dV: one warpgroup forms P and holds dV, the other forms P again, then dS, and holds dK.
+//   tensor cores: ... X(i) dK(i - 1) Y(i) dV(i) X(i + 1) ...
+// dQ: the warpgroups take the tiles in turn, each with sums of its own.
+//
+// Masked scores are set to -inf after the product.  A masked weight is 0, but 0
+// times an infinite or NaN value of a row that the owner does not see would spoil
+// it: a row of a result that is not finite is computed again from the definition.
+
+#include <cuda_fp16.h>
+
+#include <type_traits>
+
+#include "attn_grad.cuh"
+#include "attn_tc.cuh"
+
+namespace falcon {
+namespace {
+
+using namespace tcu;
+
+constexpr int kPast = 64;  // rows of a tile that comes past, and of a block of the workspace
+
+// 2^k and 2^-k that bring the largest finite magnitude to [2^14, 2^15) and back
+__device__ __forceinline__ void row_factors(float amax, float& up, float& down) {
+  const int e = min(max(static_cast<int>(__float_as_uint(amax) >> 23), 16), 254);
+  up = __uint_as_float(static_cast<uint32_t>(268 - e) << 23);
+  down = __uint_as_float(static_cast<uint32_t>(e - 14) << 23);
+}
+__device__ __forceinline__ uint32_t pack_half(float lo, float hi) {
+  uint32_t r;
+  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+// a pair of scaled values: 11 bits to nearest, and the rest
+__device__ __forceinline__ void split2(uint64_t x, uint32_t& hi, uint32_t& lo) {
+  float a, b;
+  unpack2(x, a, b);
+  const float ha = __uint_as_float((__float_as_uint(a) + 0x1000u) & 0xFFFFE000u);
+  const float hb = __uint_as_float((__float_as_uint(b) + 0x1000u) & 0xFFFFE000u);
+  hi = pack_half(ha, hb);
+  lo = pack_half(a - ha, b - hb);
+}
+
+// ---------------------------------------------------------------- operands
+// 64 rows of one head's x (row `first` on, `rows` of them live) into an image: slabs of 64 columns, hi's and then lo's,
+// and the rows' factors.  dot: (sum of x o of each row) of the rows, by the row's first lane.
+template <int D, bool DOT, typename F>
+__device__ __forceinline__ void split_rows(const RowsIn& x, const RowsIn& o, int64_t row, int head, int rows, int d,
+                                           uint8_t* image, float* factor, F dot) {
+  constexpr int L = D / 8, kStep = 256 / L;
+  const int c = threadIdx.x % L;
+  for (int r = threadIdx.x / L; r < kPast; r += kStep) {
+    float v[8], w[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) v[e] = w[e] = 0.f;
+    if (r < rows && c * 8 < d) {
+      const float* p = static_cast<const float*>(x.p) + (row + r) * x.stride + static_cast<int64_t>(head) * d;
+      const Pieces at{c * 8, c * 8 + 4};
+      unpack8(x.vec ? load8<true, false>(p, at) : load8<false, false>(p, at), v);
+      if (DOT) {
+        p = static_cast<const float*>(o.p) + (row + r) * o.stride + static_cast<int64_t>(head) * d;
+        unpack8(o.vec ? load8<true, false>(p, at) : load8<false, false>(p, at), w);
+      }
+    }
+    float m = 0.f, s = 0.f;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      const float a = fabsf(v[e]);
+      m = fmaxf(m, a <= 3.402823466e38f ? a : 0.f);
+      if (DOT) s = fmaf(v[e], w[e], s);
+    }
+#pragma unroll
+    for (int i = 1; i < L; i <<= 1) {
+      m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, i));
+      if (DOT) s += __shfl_xor_sync(0xffffffffu, s, i);
+    }
+    float up, down;
+    row_factors(m, up, down);
+    uint32_t hi[4], lo[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) split2(mul2(pack2(v[2 * e], v[2 * e + 1]), pack2(up, up)), hi[e], lo[e]);
+    uint8_t* to = image + (c >> 3) * (kPast * 128) + tc::sw128(r, (c & 7) * 8);
+    *reinterpret_cast<uint4*>(to) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+    *reinterpret_cast<uint4*>(to + kPast * D * 2) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+    if (c == 0) {
+      factor[r] = down;
+      if (DOT) dot(r, s);
+    }
+  }
+}
+
+// Where the operands lie: 64-row blocks, a sequence's from cu[b] / 64 + b on.
+struct Operands {
+  uint8_t *q, *d_o, *k, *v;       // images of kPast * D * 4 bytes, a head's blocks behind one another
+  float *q_info, *o_info;         // 64 log sums and 64 factors; 64 D's and 64 factors; both sums negative
+  float *k_info, *v_info;         // 64 factors
+  int64_t q_blocks, k_blocks;     // of a head
+};
+__host__ __device__ __forceinline__ int64_t count_blocks(int64_t rows, int B) { return rows / kPast + B + 1; }
+__device__ __forceinline__ int64_t first64(int64_t q0, int b) { return q0 / kPast + b; }
+
+template <int D>
+__global__ void __launch_bounds__(256) attn_grad_split_kernel(GradArgs g, Operands w, unsigned q_ctas) {
+  const PromptArgs& a = g.a;
+  if (blockIdx.x == 0 && threadIdx.x == 0) *static_cast<uint32_t*>(a.ws) = 0;  // the call's status
+  const bool of_q = blockIdx.x < q_ctas;
+  const int H = of_q ? a.Hq : a.Hkv;
+  const unsigned at = of_q ? blockIdx.x : blockIdx.x - q_ctas;
+  const int h = static_cast<int>(at % H);
+  const int32_t* cu = of_q ? a.cu_q : a.cu_k;
+  const int2 x = find_block(cu, a.B, kPast, static_cast<int>(at / H));
+  const int64_t r0 = cu[x.x], r1 = cu[x.x + 1];
+  if (x.y < 0 || r0 < 0 || r1 > (of_q ? a.tokens : a.k_tokens) || x.y >= r1 - r0) return;
+  const int rows = static_cast<int>((of_q ? min(r1 - r0, static_cast<int64_t>(a.max_q)) : r1 - r0) - x.y);
+  const int64_t n = x.y / kPast, j = first64(r0, x.x) + n, row = r0 + x.y;
+  const auto none = [](int, float) {};
+  if (!of_q) {
+    const int64_t to = h * w.k_blocks + j;
+    split_rows<D, false>(a.k, a.k, row, h, rows, a.d, w.k + to * (kPast * D * 4), w.k_info + to * kPast, none);
+    split_rows<D, false>(a.v, a.v, row, h, rows, a.d, w.v + to * (kPast * D * 4), w.v_info + to * kPast, none);
+    return;
+  }
+  const int64_t to = h * w.q_blocks + j;
+  float *qi = w.q_info + to * (2 * kPast), *oi = w.o_info + to * (2 * kPast);
+  split_rows<D, false>(a.q, a.q, row, h, rows, a.d, w.q + to * (kPast * D * 4), qi + kPast, none);
+  // the log sums and D, for the tiles and for rows that are computed again; rows without a key have no weights
+  float* sums = g.sums + row_sums(g.blocks, h, first_block(r0, x.x) + n / 2) + n % 2 * kPast;
+  split_rows<D, true>(g.d_o, g.o, row, h, rows, a.d, w.d_o + to * (kPast * D * 4), oi + kPast, [&](int r, float s) {
+    float lse = INFINITY;
+    if (r < rows) {
+      const float l = g.lse[(row + r) * a.Hq + h];
+      if (g.dlse) s -= g.dlse[(row + r) * a.Hq + h];
+      lse = l == -INFINITY ? INFINITY : l == INFINITY ? __int_as_float(0x7fffffff) : l;
+      if (l == -INFINITY) s = 0.f;
+    }
+    sums[r] = lse, sums[kSumRows + r] = s;
+    qi[r] = -lse, oi[r] = -s;
+  });
+}
+
+// ---------------------------------------------------------------- products
+template <int D, bool KEYS>
+struct Cfg32 {
+  static constexpr int kWarps = 8;  // two warpgroups, a row of a tile a thread
+  // one more warp copies the tiles and issues the products; its warpgroup gives its registers to the others
+  static constexpr int kMmaWarp = kWarps, kThreads = 32 * kWarps + 128;
+  static constexpr int kOwnBytes = kTile * D * 4, kTileBytes = kPast * D * 4;
+  // places of the first tiles (Q; K), which are read until the tile's last product, and of the second ones (dO; V)
+  static constexpr int kP1 = D == 64 ? 4 : 2, kP2 = D == 64 ? 4 : 1;
+  // what the softmax threads need of the rows of a pair: with the first tile log sums and factors of Q, or factors of K
+  // and of V; with the second one (dK and dV) D and factors of dO
+  static constexpr int kInfo = 2 * kPast * 4, kInfo2 = KEYS ? kInfo : 0;
+  static constexpr int kRing = (kP1 + kP2) * kTileBytes;
+  // TMEM: dK and dV: X, P, Y (then dS over it), the tile's sums of dV and of dK;
+  // dQ: two of X (then dS over it), of Y and of the tile's sums
+  [[maybe_unused]] static constexpr uint32_t kColX = 0, kColP = kPast, kColY = 2 * kPast, kColV = KEYS ? 3 * kPast : 4 * kPast;
+  static constexpr int kSmem = 2 * kOwnBytes + kRing + kP1 * kInfo + kP2 * kInfo2 + 1024 + 256;
+};
+struct Bars32 {
+  uint64_t own, full1[4], empty1[4], full2[4], empty2[4], x[2], x_read, y, p, ds[2], drain, stall;
+  uint32_t tmem, failed;
+};
+static_assert(sizeof(Bars32) <= 256 && Cfg32<128, true>::kSmem <= 227 * 1024 && Cfg32<128, false>::kSmem <= 227 * 1024 &&
+                  Cfg32<64, true>::kSmem <= 227 * 1024, "shared memory");
+
+struct Tc32Args {
+  GradArgs g;
+  Operands w;
+  int qblocks;  // of a sequence
+  bool packed;
+  uint32_t* status;
+  uint64_t limit;
+  int stall;
+};
+
+__host__ __device__ constexpr uint32_t idesc_f16(int M, int N, bool b_mn = false) {
+  return idesc_bf16(M, N, false, b_mn) & ~((1u << 7) | (1u << 10));
+}
+// 16 columns of a thread's row
+__device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+      : "r"(taddr)
+      : "memory");
+}
+// two pairs of a row of factors, the same for every thread
+__device__ __forceinline__ void load_pairs(const float* p, uint64_t& a, uint64_t& b) {
+  const float4 v = *reinterpret_cast<const float4*>(p);
+  a = pack2(v.x, v.y), b = pack2(v.z, v.w);
+}
+// A thread's row of a tile of P or dS to TMEM: its own power of two, hi's in 32 columns, lo's in the next 32.  Returns the
+// factor that undoes the power.
+__device__ __forceinline__ float store_weights(uint32_t to, uint64_t (&x)[32]) {
+  float m = 0.f;
+#pragma unroll
+  for (int e = 0; e < 32; ++e) {
+    float a, b;
+    unpack2(x[e], a, b);
+    m = max3(m, fabsf(a), fabsf(b));
+  }
+  float up, down;
+  row_factors(m, up, down);
+  const uint64_t up2 = pack2(up, up);
+#pragma unroll
+  for (int c = 0; c < 2; ++c) {
+    uint32_t hi[16], lo[16];
+#pragma unroll
+    for (int e = 0; e < 16; ++e) split2(mul2(x[16 * c + e], up2), hi[e], lo[e]);
+    tmem_st16(to + 16 * c, hi);
+    tmem_st16(to + 32 + 16 * c, lo);
+  }
+  return down;
+}
+// acc += f times a thread's row of a tile's sums
+template <int D>
+__device__ __forceinline__ void add_sums(uint64_t (&acc)[D / 2], uint32_t from, float f) {
+  const uint64_t f2 = pack2(f, f);
+#pragma unroll
+  for (int c = 0; c < D / 16; ++c) {
+    uint32_t v[16];
+    tmem_ld16(from + 16 * c, v);
+    tmem_wait_ld();
+#pragma unroll
+    for (int e = 0; e < 8; ++e)
+      acc[8 * c + e] = fma2(pack2(__uint_as_float(v[2 * e]), __uint_as_float(v[2 * e + 1])), f2, acc[8 * c + e]);
+  }
+}
+
+template <int D, bool KEYS>
+__global__ void __launch_bounds__(Cfg32<D, KEYS>::kThreads, 1) attn_grad_tc32_kernel(const Tc32Args t) {
+  using C = Cfg32<D, KEYS>;
+  constexpr int N = kPast, P1 = C::kP1, P2 = C::kP2, kHalf = C::kTileBytes / 2;
+  const GradArgs& g = t.g;
+  const PromptArgs& a = g.a;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = align1024(smem_raw);
+  uint8_t *s1 = smem, *s2 = s1 + C::kOwnBytes, *ring1 = s2 + C::kOwnBytes, *ring2 = ring1 + P1 * C::kTileBytes;
+  uint8_t* infos = ring1 + C::kRing;  // of the first tiles, then of the second ones
+  Bars32* bar = reinterpret_cast<Bars32*>(infos + P1 * C::kInfo + P2 * C::kInfo2);
+  if (warp == C::kMmaWarp) {
+    tmem_alloc(&bar->tmem, 512);
+    tmem_relinquish();
+  }
+  if (tid == 0) {
+    mbar_init(&bar->own, 1);
+    for (int i = 0; i < 4; ++i) {
+      mbar_init(&bar->full1[i], 1);
+      mbar_init(&bar->empty1[i], 1);
+      mbar_init(&bar->full2[i], 1);
+      mbar_init(&bar->empty2[i], 1);
+    }
+    mbar_init(&bar->x[0], 1);
+    mbar_init(&bar->x[1], 1);
+    mbar_init(&bar->x_read, 4);
+    mbar_init(&bar->y, 1);
+    mbar_init(&bar->p, 4);
+    mbar_init(&bar->ds[0], 4);
+    mbar_init(&bar->ds[1], 4);
+    mbar_init(&bar->drain, 1);
+    mbar_init(&bar->stall, 1);
+    bar->failed = 0;
+    fence_mbar_init();
+  }
+
+  // whose rows
+  const int G = a.Hq / a.Hkv;
+  const uint32_t block = blockIdx.x;
+  int b, head, row0;
+  if (KEYS) {
+    const int2 x = find_block(a.cu_k, a.B, kTile, static_cast<int>(block / a.Hkv));
+    b = x.x, row0 = x.y, head = static_cast<int>(block % a.Hkv);
+  } else if (t.packed) {
+    const int2 x = find_block(a.cu_q, a.B, kTile, static_cast<int>(block / a.Hq));
+    b = x.x, row0 = x.y, head = static_cast<int>(block % a.Hq);
+  } else {
+    const uint32_t bh = static_cast<uint32_t>(a.B) * a.Hq, at = block % bh;
+    b = static_cast<int>(at) / a.Hq, head = static_cast<int>(at) % a.Hq;
+    row0 = (t.qblocks - 1 - static_cast<int>(block / bh)) * kTile;  // the longest rows first
+  }
+  const int64_t q0 = a.cu_q[b], k0 = a.cu_k[b];
+  const int lq_all = static_cast<int>(a.cu_q[b + 1] - q0), lk = static_cast<int>(a.cu_k[b + 1] - k0);
+  const int lq = min(lq_all, a.max_q), off = lk - lq_all, rows = KEYS ? lk : lq;
+  const bool valid = row0 >= 0 && row0 < rows && q0 >= 0 && k0 >= 0 && lq_all >= 0 && lk >= 0 && q0 + lq_all <= a.tokens &&
+                     k0 + lk <= a.k_tokens;
+  // a sequence's blocks are dealt out from its last; the first keys, which the most queries see, come first
+  if (KEYS) row0 = (lk - 1) / kTile * kTile - row0;
+  // the tiles that come past, [first, first + each N) of every head
+  const int first = KEYS ? max(row0 - off, 0) / N * N : 0;
+  const int end = KEYS ? lq : min(min(row0 + kTile, lq) + off, lk);
+  const int each = end > first ? (end - first + N - 1) / N : 0, n = KEYS ? each * G : each;
+  __syncthreads();
+  const uint32_t tmem = bar->tmem;
+  if (!valid) {
+    if (warp == C::kMmaWarp) tmem_dealloc(tmem, 512);
+    return;
+  }
+  auto wait = [&](uint64_t* m, uint32_t parity) {
+    if (mbar_wait_sleep(m, parity, t.limit)) return true;
+    atomicExch(t.status, kStatusTimeout);
+    *static_cast<volatile uint32_t*>(&bar->failed) = 1;
+    return false;
+  };
+  // blocks of the workspace: the owned rows' first one; tile i's
+  const int64_t own_block = (KEYS ? head * t.w.k_blocks + first64(k0, b) : head * t.w.q_blocks + first64(q0, b)) + row0 / kPast;
+  auto past_block = [&](int i) {
+    return (KEYS ? (head * G + i / each) * t.w.q_blocks + first64(q0, b) : head / G * t.w.k_blocks + first64(k0, b)) +
+           first / kPast + (KEYS ? i % each : i);
+  };
+
+  // 256 x 224 + 128 x 56 = 384 x 168
+  if (warp >= C::kMmaWarp) asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
+  if (warp == C::kMmaWarp) {
+    // The whole warp walks the loop, so that descriptors stay uniform; one lane issues.
+    constexpr uint32_t id_x = idesc_f16(kTile, N), id_s = idesc_f16(kTile, D, true);
+    const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);
+    const uint64_t a1 = sdesc_k128(smem_u32(s1)), a2 = sdesc_k128(smem_u32(s2));
+    const uint64_t bk1 = sdesc_k128(smem_u32(ring1)), bk2 = sdesc_k128(smem_u32(ring2));
+    const uint64_t bm1 = D == 64 ? sdesc_mn128(smem_u32(ring1)) : sdesc_mn128_wide(smem_u32(ring1), N * 128);
+    const uint64_t bm2 = D == 64 ? sdesc_mn128(smem_u32(ring2)) : sdesc_mn128_wide(smem_u32(ring2), N * 128);
+    auto arrived = [&](uint64_t* m, uint32_t parity) {  // one answer for the warp
+      const bool ok = __all_sync(0xffffffffu, wait(m, parity)) != 0;
+      tc_fence_after();
+      return ok;
+    };
+    auto full1 = [&](int i) { return arrived(&bar->full1[i % P1], (i / P1) & 1); };
+    auto full2 = [&](int i) { return arrived(&bar->full2[i % P2], (i / P2) & 1); };
+    // to = the owned rows times tile i's; lo hi, hi lo, hi hi
+    auto scores = [&](uint32_t to, int i, int second, uint64_t* then, uint64_t* frees) {
+      const uint64_t as = second ? a2 : a1, bs = second ? bk2 + i % P2 * (C::kTileBytes >> 4) : bk1 + i % P1 * (C::kTileBytes >> 4);
+      if (elect_one()) {
+#pragma unroll
+        for (int part = 0; part < 3; ++part) {
+          const uint64_t ap = as + (part == 0 ? C::kOwnBytes / 2 >> 4 : 0), bp = bs + (part == 1 ? kHalf >> 4 : 0);
+#pragma unroll
+          for (int ks = 0; ks < D / 16; ++ks)
+            umma_bf16(tm + to, ap + (((ks >> 2) * kTile * 128 + (ks & 3) * 32) >> 4),
+                      bp + (((ks >> 2) * N * 128 + (ks & 3) * 32) >> 4), id_x, part > 0 || ks > 0);
+        }
+        if (then) umma_commit(then);
+        if (frees) umma_commit(frees);
+      }
+      __syncwarp();
+    };
+    // sum = W (halves in TMEM) times tile i
+    auto weighted = [&](uint32_t sum, uint32_t w, int i, int second, uint64_t* frees) {
+      const uint64_t bs = second ? bm2 + i % P2 * (C::kTileBytes >> 4) : bm1 + i % P1 * (C::kTileBytes >> 4);
+      if (elect_one()) {
+#pragma unroll
+        for (int part = 0; part < 3; ++part)
+#pragma unroll
+          for (int ks = 0; ks < N / 16; ++ks)
+            umma_ts(tm + sum, tm + w + (part == 0 ? 32 : 0) + ks * 8, bs + (part == 1 ? kHalf >> 4 : 0) + ks * 128, id_s,
+                    part > 0 || ks > 0);
+        umma_commit(frees);
+      }
+      __syncwarp();
+    };
+    // copies of tile i's first and second part; by one lane
+    int loads1 = 0, loads2 = 0;
+    auto load1 = [&] {
+      const int i = loads1++, at = i % P1;
+      if (elect_one()) {
+        const int64_t blk = past_block(i);
+        uint8_t* info = infos + at * C::kInfo;
+        mbar_arrive_expect_tx(&bar->full1[at], C::kTileBytes + C::kInfo);
+        bulk_load(ring1 + at * C::kTileBytes, (KEYS ? t.w.q : t.w.k) + blk * C::kTileBytes, C::kTileBytes, &bar->full1[at]);
+        if (KEYS) {
+          bulk_load(info, t.w.q_info + blk * (2 * kPast), C::kInfo, &bar->full1[at]);
+        } else {
+          bulk_load(info, t.w.k_info + blk * kPast, C::kInfo / 2, &bar->full1[at]);
+          bulk_load(info + C::kInfo / 2, t.w.v_info + blk * kPast, C::kInfo / 2, &bar->full1[at]);
+        }
+      }
+      __syncwarp();
+    };
+    auto load2 = [&] {
+      const int i = loads2++, at = i % P2;
+      if (elect_one()) {
+        const int64_t blk = past_block(i);
+        mbar_arrive_expect_tx(&bar->full2[at], C::kTileBytes + C::kInfo2);
+        bulk_load(ring2 + at * C::kTileBytes, (KEYS ? t.w.d_o : t.w.v) + blk * C::kTileBytes, C::kTileBytes, &bar->full2[at]);
+        if (KEYS) bulk_load(infos + P1 * C::kInfo + at * C::kInfo2, t.w.o_info + blk * (2 * kPast), C::kInfo2, &bar->full2[at]);
+      }
+      __syncwarp();
+    };
+    // the place of tile i - P's is free
+    auto more1 = [&](int i) { return i >= n || (arrived(&bar->empty1[i % P1], (i / P1 - 1) & 1) && (load1(), true)); };
+    auto more2 = [&](int i) { return i >= n || (arrived(&bar->empty2[i % P2], (i / P2 - 1) & 1) && (load2(), true)); };
+    bool ok = n > 0 && (!t.stall || arrived(&bar->stall, 0));
+    const bool own = ok;
+    if (ok) {
+      if (elect_one()) {
+        // slabs of 128 rows from two blocks' of 64; the second block may not be there, no row of it counts then
+        const int halves = row0 + kPast < rows ? 2 : 1;
+        mbar_arrive_expect_tx(&bar->own, halves * 2 * C::kTileBytes);
+        for (int s = 0; s < 2 * halves; ++s) {
+          const uint8_t* from = ((s & 1) ? (KEYS ? t.w.v : t.w.d_o) : (KEYS ? t.w.k : t.w.q)) + (own_block + (s >> 1)) * C::kTileBytes;
+          uint8_t* to = ((s & 1) ? s2 : s1) + (s >> 1) * (kPast * 128);
+          for (int c = 0; c < D / 32; ++c) bulk_load(to + c * (kTile * 128), from + c * (kPast * 128), kPast * 128, &bar->own);
+        }
+      }
+      __syncwarp();
+      for (int i = 0; i < min(n, max(P1, P2)); ++i) {
+        if (i < P1) load1();
+        if (i < P2) load2();
+      }
+      ok = arrived(&bar->own, 0);
+    }
+    // A place's next copy waits for the place's last product while another one runs.
+    if constexpr (KEYS) {
+      if (ok && (ok = full1(0))) scores(C::kColX, 0, 0, &bar->x[0], nullptr);
+      for (int i = 0; i < n && ok; ++i) {
+        if (!(ok = full2(i))) break;
+        scores(C::kColY, i, 1, &bar->y, nullptr);
+        if (i > 0 && !(ok = more1(i - 1 + P1))) break;
+        if (!(ok = arrived(&bar->p, i & 1))) break;
+        weighted(C::kColV, C::kColP, i, 1, &bar->empty2[i % P2]);
+        if (i + 1 < n) {
+          if (!(ok = full1(i + 1) && arrived(&bar->x_read, i & 1))) break;
+          scores(C::kColX, i + 1, 0, &bar->x[0], nullptr);
+        }
+        if (!(ok = more2(i + P2))) break;
+        if (!(ok = arrived(&bar->ds[0], i & 1))) break;
+        weighted(C::kColV + D, C::kColY, i, 0, &bar->empty1[i % P1]);
+      }
+    } else {
+      // the warpgroups' dS of tiles i and i - 1 lie over X of them; Y of tile i + 1 over that of tile i - 1
+      for (int i = -1; i < n && ok; ++i) {
+        const uint32_t next = (i + 1) & 1;
+        if (i + 1 < n) {
+          if (P1 == 2 && i > 0 && !(ok = more1(i - 1 + P1))) break;  // tile i + 1 itself
+          if (!(ok = full1(i + 1))) break;
+          scores(C::kColX + next * N, i + 1, 0, nullptr, nullptr);
+          if (P1 > 2 && i > 0 && !(ok = more1(i - 1 + P1))) break;
+          if (!(ok = full2(i + 1))) break;
+          scores(C::kColY + next * N, i + 1, 1, &bar->x[next], &bar->empty2[(i + 1) % P2]);
+        }
+        if (i >= 0) {
+          if (!(ok = arrived(&bar->ds[i & 1], (i >> 1) & 1))) break;
+          weighted(C::kColV + (i & 1) * D, C::kColX + (i & 1) * N, i, 0, &bar->empty1[i % P1]);
+        }
+        if (i + 1 < n && !(ok = more2(i + 1 + P2))) break;
+      }
+    }
+    if (elect_one()) umma_commit(&bar->drain);  // products in flight end before the memory is freed
+    __syncwarp();
+    wait(&bar->drain, 0);
+    // every copy has landed before the CTA may end
+    if (own) wait(&bar->own, 0);
+    for (int i = max(0, loads1 - P1); i < loads1; ++i) wait(&bar->full1[i % P1], (i / P1) & 1);
+    for (int i = max(0, loads2 - P2); i < loads2; ++i) wait(&bar->full2[i % P2], (i / P2) & 1);
+    __syncwarp();
+  } else if (warp < C::kMmaWarp) {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 224;");
+    const int group = warp >> 2, quad = warp & 3, r = quad * 32 + lane;
+    const uint32_t mine = tmem + (static_cast<uint32_t>(quad * 32) << 16);
+    const int row = row0 + r;
+    auto arrive = [&](uint64_t* m) {
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(m);
+    };
+    auto waited = [&](uint64_t* m, uint32_t parity) {
+      const bool ok = __all_sync(0xffffffffu, wait(m, parity)) != 0;
+      tc_fence_after();
+      return ok;
+    };
+    bool ok = true;
+    uint64_t acc[D / 2];
+#pragma unroll
+    for (int e = 0; e < D / 2; ++e) acc[e] = 0;
+    // this row's factors; of rows past the sequence anything
+    const int64_t blk = own_block + (r >> 6);
+    const bool live = row < rows;
+    float f1 = 0.f, f2 = 0.f, lse = -INFINITY, delta = 0.f;  // lse, delta: negative
+    if (live && n > 0) {
+      const int at = r & 63;
+      f1 = a.scale * (KEYS ? t.w.k_info[blk * kPast + at] : t.w.q_info[blk * (2 * kPast) + kPast + at]);
+      f2 = KEYS ? t.w.v_info[blk * kPast + at] : t.w.o_info[blk * (2 * kPast) + kPast + at];
+      if (!KEYS) lse = t.w.q_info[blk * (2 * kPast) + at], delta = t.w.o_info[blk * (2 * kPast) + at];
+    }
+    const uint64_t f1p = pack2(f1, f1), f2p = pack2(f2, f2), l2e = pack2(kLog2e, kLog2e);
+    const uint64_t lse2 = pack2(lse, lse), delta2 = pack2(delta, delta);
+    // P of this row, columns 16 c on, from X in v: `ls` the log sums (dQ: lse2), `s` the columns' factors
+    auto weights = [&](const uint32_t (&v)[16], int c, const float* s, const float* ls, int lim, bool cut, uint64_t* x) {
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        uint64_t s0, s1, l0 = 0, l1 = 0;
+        load_pairs(s + 16 * c + 4 * e, s0, s1);
+        if (KEYS) load_pairs(ls + 16 * c + 4 * e, l0, l1);
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+          const int at = 4 * e + 2 * k;
+          uint64_t z = mul2(pack2(__uint_as_float(v[at]), __uint_as_float(v[at + 1])), f1p);
+          // the difference first: it is small where the weight is not
+          if (KEYS) z = fma2(z, k ? s1 : s0, k ? l1 : l0);
+          else z = fma2(z, k ? s1 : s0, lse2);
+          float z0, z1;
+          unpack2(mul2(z, l2e), z0, z1);
+          if (cut) {
+            if (KEYS ? 16 * c + at < lim : 16 * c + at >= lim) z0 = -INFINITY;
+            if (KEYS ? 16 * c + at + 1 < lim : 16 * c + at + 1 >= lim) z1 = -INFINITY;
+          }
+          x[2 * e + k] = pack2(ex2(z0), ex2(z1));
+        }
+      }
+    };
+    float down = 0.f;  // of the tile whose sums come next
+    if constexpr (KEYS) {
+      for (int i = 0; i < n; ++i) {
+        const int at = first + i % each * N, lim = row - off - at;
+        const bool cut = at + off < row0 + kTile - 1;  // some key is behind a query of these
+        const float* i1 = reinterpret_cast<const float*>(infos + i % P1 * C::kInfo);  // log sums, factors of Q
+        const float* i2 = reinterpret_cast<const float*>(infos + P1 * C::kInfo + i % P2 * C::kInfo2);  // D, factors of dO
+        uint64_t x[32];
+        if (!(ok = waited(&bar->full1[i % P1], (i / P1) & 1) && waited(&bar->x[0], i & 1))) break;
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          uint32_t v[16];
+          tmem_ld16(mine + C::kColX + 16 * c, v);
+          tmem_wait_ld();
+          weights(v, c, i1 + N, i1, lim, cut, x + 8 * c);
+        }
+        if (group) arrive(&bar->x_read);
+        if (!(ok = waited(&bar->full2[i % P2], (i / P2) & 1))) break;
+        if (group) {
+          if (!(ok = waited(&bar->y, i & 1))) break;
+#pragma unroll
+          for (int c = 0; c < 4; ++c) {
+            uint32_t v[16];
+            tmem_ld16(mine + C::kColY + 16 * c, v);
+            tmem_wait_ld();
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              uint64_t s[2], dd[2], sq[2];
+              load_pairs(i2 + N + 16 * c + 4 * e, s[0], s[1]);
+              load_pairs(i2 + 16 * c + 4 * e, dd[0], dd[1]);
+              load_pairs(i1 + N + 16 * c + 4 * e, sq[0], sq[1]);
+#pragma unroll
+              for (int k = 0; k < 2; ++k) {
+                const uint64_t y = mul2(pack2(__uint_as_float(v[4 * e + 2 * k]), __uint_as_float(v[4 * e + 2 * k + 1])), f2p);
+                const uint64_t z = fma2(y, s[k], dd[k]);
+                x[8 * c + 2 * e + k] = mul2(mul2(x[8 * c + 2 * e + k], z), sq[k]);
+              }
+            }
+          }
+        } else {
+#pragma unroll
+          for (int e = 0; e < 16; ++e) {
+            uint64_t s0, s1;
+            load_pairs(i2 + N + 4 * e, s0, s1);
+            x[2 * e] = mul2(x[2 * e], s0);
+            x[2 * e + 1] = mul2(x[2 * e + 1], s1);
+          }
+        }
+        // X and Y of this tile came after the products of the one before: its sums are there, its P and dS are read
+        const float was = down;
+        down = store_weights(mine + (group ? C::kColY : C::kColP), x);
+        if (i > 0) add_sums<D>(acc, mine + C::kColV + group * D, was);
+        tmem_wait_st();
+        arrive(group ? &bar->ds[0] : &bar->p);
+      }
+    } else {
+      for (int i = group; i < n; i += 2) {
+        const int at = i * N, lim = min(row + off + 1, lk) - at;
+        const bool cut = at + N > min(row0 + off + 1, lk);
+        const float* i1 = reinterpret_cast<const float*>(infos + i % P1 * C::kInfo);  // factors of K, of V
+        const uint32_t tx = mine + C::kColX + group * N, ty = mine + C::kColY + group * N;
+        uint64_t x[32];
+        if (!(ok = waited(&bar->full1[i % P1], (i / P1) & 1) && waited(&bar->x[group], (i >> 1) & 1))) break;
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          uint32_t v[16];
+          tmem_ld16(tx + 16 * c, v);
+          tmem_wait_ld();
+          weights(v, c, i1, nullptr, lim, cut, x + 8 * c);
+        }
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          uint32_t v[16];
+          tmem_ld16(ty + 16 * c, v);
+          tmem_wait_ld();
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            uint64_t s[2], sk[2];
+            load_pairs(i1 + N + 16 * c + 4 * e, s[0], s[1]);
+            load_pairs(i1 + 16 * c + 4 * e, sk[0], sk[1]);
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+              const uint64_t y = mul2(pack2(__uint_as_float(v[4 * e + 2 * k]), __uint_as_float(v[4 * e + 2 * k + 1])), f2p);
+              const uint64_t z = fma2(y, s[k], delta2);
+              x[8 * c + 2 * e + k] = mul2(mul2(x[8 * c + 2 * e + k], z), sk[k]);
+            }
+          }
+        }
+        const float was = down;
+        down = store_weights(tx, x);
+        if (i > 1) add_sums<D>(acc, mine + C::kColV + group * D, was);
+        tmem_wait_st();
+        arrive(&bar->ds[group]);
+      }
+    }
+    // the last tile's sums
+    if (ok && n > 0) {
+      ok = waited(&bar->drain, 0);
+      if (ok && (KEYS || n > group)) add_sums<D>(acc, mine + C::kColV + group * D, down);
+    }
+    const int d = D == 64 ? a.d : D;  // of the rows
+    // this thread's part of its row of a result, dims c0 to c0 + 2 M of it; which: dV (0), dK or dQ (1)
+    auto finish = [&](const auto& z, auto pairs, int c0, int which) {
+      constexpr int M = decltype(pairs)::value;
+      const RowsOut& to = KEYS ? (which ? g.dk : g.dv) : g.dq;
+      float* out = static_cast<float*>(to.p) + ((KEYS ? k0 : q0) + row0) * to.stride + static_cast<int64_t>(head) * d;
+      const float f = which ? a.scale : 1.f;
+      const uint64_t fp = pack2(f, f);
+      uint64_t rest = 0;  // z * 0 added up: NaN where some z is not finite
+#pragma unroll
+      for (int e = 0; e < M / 2; ++e) {
+        const uint64_t z0 = mul2(z[2 * e], fp), z1 = mul2(z[2 * e + 1], fp);
+        rest = fma2(z0, 0, fma2(z1, 0, rest));
+        const int c = c0 + 4 * e;
+        if (!live || c >= d) continue;
+        float4 v;
+        unpack2(z0, v.x, v.y);
+        unpack2(z1, v.z, v.w);
+        float* dst = out + r * to.stride + c;
+        if (to.vec) *reinterpret_cast<float4*>(dst) = v;
+        else dst[0] = v.x, dst[1] = v.y, dst[2] = v.z, dst[3] = v.w;
+      }
+      float ra, rb;
+      unpack2(rest, ra, rb);
+      __syncwarp();
+      for (uint32_t again = __ballot_sync(0xffffffffu, live && !(ra + rb == 0.f)); again; again &= again - 1) {
+        const int i = row0 + quad * 32 + __ffs(again) - 1;
+        float x1[4], x2[4];
+        const float *q = static_cast<const float*>(a.q.p), *d_o = static_cast<const float*>(g.d_o.p);
+        const float *k = static_cast<const float*>(a.k.p), *v = static_cast<const float*>(a.v.p);
+        const float* sums = g.sums + row_sums(g.blocks, KEYS ? head * G : head, first_block(q0, b));
+        if constexpr (KEYS) {
+          const int64_t h0 = static_cast<int64_t>(head) * G * d, hk = static_cast<int64_t>(head) * d;
+          grad_key_row<float, D>(k + (k0 + i) * a.k.stride + hk, v + (k0 + i) * a.v.stride + hk, q + q0 * a.q.stride + h0,
+                                 a.q.stride, d_o + q0 * g.d_o.stride + h0, g.d_o.stride, sums, g.blocks, G, max(i - off, 0),
+                                 lq, d, a.scale, x1, x2);
+        } else {
+          const int64_t h0 = static_cast<int64_t>(head) * d, hk = static_cast<int64_t>(head / G) * d;
+          const float* s = sums + static_cast<int64_t>(i / kSumRows) * (2 * kSumRows) + i % kSumRows;
+          grad_query_row<float, D>(q + (q0 + i) * a.q.stride + h0, d_o + (q0 + i) * g.d_o.stride + h0, s[0], s[kSumRows],
+                                   k + k0 * a.k.stride + hk, a.k.stride, v + k0 * a.v.stride + hk, a.v.stride,
+                                   min(i + off + 1, lk), d, a.scale, x1);
+        }
+#pragma unroll
+        for (int m = 0; m < D / 32; ++m) {
+          const int c = m * 32 + lane;
+          if (m * 32 >= c0 && m * 32 < c0 + 2 * M && c < d) out[(i - row0) * to.stride + c] = KEYS && !which ? x2[m] : x1[m];
+        }
+      }
+    };
+    if constexpr (KEYS) {
+      if (__all_sync(0xffffffffu, ok)) finish(acc, std::integral_constant<int, D / 2>{}, 0, group);
+    } else {
+      // each warpgroup gives the other its sums of half of the dims, through the owned tiles' place (every product is
+      // done), 16-byte pieces swizzled by row
+      uint8_t *theirs = smem + (1 - group) * (kTile * D * 2) + r * (D * 2), *ours = smem + group * (kTile * D * 2) + r * (D * 2);
+#pragma unroll
+      for (int e = 0; e < D / 8; ++e) {
+        const uint64_t z0 = group ? acc[2 * e] : acc[D / 4 + 2 * e], z1 = group ? acc[2 * e + 1] : acc[D / 4 + 2 * e + 1];
+        *reinterpret_cast<ulonglong2*>(theirs + ((e ^ (r & 7)) << 4)) = make_ulonglong2(z0, z1);
+      }
+      named_bar(1, 32 * C::kWarps);
+      if (*static_cast<volatile uint32_t*>(&bar->failed) == 0) {
+        uint64_t z[D / 4];
+#pragma unroll
+        for (int e = 0; e < D / 8; ++e) {
+          const ulonglong2 y = *reinterpret_cast<const ulonglong2*>(ours + ((e ^ (r & 7)) << 4));
+          const uint64_t z0 = group ? acc[D / 4 + 2 * e] : acc[2 * e], z1 = group ? acc[D / 4 + 2 * e + 1] : acc[2 * e + 1];
+          z[2 * e] = add2(z0, y.x);
+          z[2 * e + 1] = add2(z1, y.y);
+        }
+        finish(z, std::integral_constant<int, D / 4>{}, group * (D / 2), 1);
+      }
+    }
+    tc_fence_before();
+  }
+  __syncthreads();
+  if (warp == C::kMmaWarp) {
+    tc_fence_after();
+    tmem_dealloc(tmem, 512);
+  }
+}
+
+template <int D, bool KEYS>
+int launch_kernel(Tc32Args& t, int64_t grid, cudaStream_t s) {
+  if (grid < 1 || grid > INT32_MAX) return FALCON_ERR_UNSUPPORTED;
+  t.stall = take_test_stall() ? 1 : 0;
+  const auto kern = attn_grad_tc32_kernel<D, KEYS>;
+  if (!set_smem_limit(reinterpret_cast<const void*>(kern), Cfg32<D, KEYS>::kSmem)) return FALCON_ERR_CUDA;
+  kern<<<static_cast<unsigned>(grid), Cfg32<D, KEYS>::kThreads, Cfg32<D, KEYS>::kSmem, s>>>(t);
+  return cudaGetLastError() == cudaSuccess ? FALCON_OK : FALCON_ERR_CUDA;
+}
+
+// The parts of the workspace from `base` on; bytes: all of them.
+Operands operands(uint8_t* base, const PromptArgs& a, int D, size_t* bytes) {
+  Operands w;
+  w.q_blocks = count_blocks(a.tokens, a.B);
+  w.k_blocks = count_blocks(a.k_tokens, a.B);
+  size_t at = 0;
+  auto part = [&](int64_t blocks, size_t size) {
+    uint8_t* p = base + at;
+    at += static_cast<size_t>(blocks) * size;
+    return p;
+  };
+  const int64_t nq = w.q_blocks * a.Hq, nk = w.k_blocks * a.Hkv;
+  const size_t image = static_cast<size_t>(kPast) * D * 4, row = kPast * sizeof(float);
+  w.q = part(nq, image), w.d_o = part(nq, image), w.k = part(nk, image), w.v = part(nk, image);
+  w.q_info = reinterpret_cast<float*>(part(nq, 2 * row)), w.o_info = reinterpret_cast<float*>(part(nq, 2 * row));
+  w.k_info = reinterpret_cast<float*>(part(nk, row)), w.v_info = reinterpret_cast<float*>(part(nk, row));
+  *bytes = at;
+  return w;
+}
+
+template <int D>
+int launch_d(const GradArgs& g, cudaStream_t s) {
+  const PromptArgs& a = g.a;
+  Tc32Args t;
+  t.g = g;
+  size_t bytes;
+  t.w = operands(reinterpret_cast<uint8_t*>(g.sums + row_sums(g.blocks, a.Hq, 0)), a, D, &bytes);
+  t.qblocks = 0, t.packed = false;
+  t.status = static_cast<uint32_t*>(a.ws);
+  t.limit = wait_limit_ns();
+  const int64_t q_ctas = a.tokens > 0 && a.max_q > 0 ? (a.tokens / kPast + a.B) * a.Hq : 0;
+  const int64_t k_ctas = a.k_tokens > 0 ? (a.k_tokens / kPast + a.B) * a.Hkv : 0;
+  if (q_ctas + k_ctas > INT32_MAX) return FALCON_ERR_UNSUPPORTED;
+  attn_grad_split_kernel<D><<<static_cast<unsigned>(q_ctas + k_ctas), 256, 0, s>>>(g, t.w, static_cast<unsigned>(q_ctas));
+  if (cudaGetLastError() != cudaSuccess) return FALCON_ERR_CUDA;
+  if (g.dq.p && q_ctas) {
+    const PromptGrid pg = prompt_grid(a, kTile);
+    t.qblocks = static_cast<int>(pg.blocks / a.B);
+    t.packed = pg.packed;
+    const int st = pg.blocks > INT32_MAX / a.Hq ? FALCON_ERR_UNSUPPORTED : launch_kernel<D, false>(t, pg.blocks * a.Hq, s);
+    if (st != FALCON_OK) return st;
+  }
+  if (g.dk.p && k_ctas) {
+    const int64_t blocks = a.k_tokens / kTile + a.B;
+    return blocks > INT32_MAX / a.Hkv ? FALCON_ERR_UNSUPPORTED : launch_kernel<D, true>(t, blocks * a.Hkv, s);
+  }
+  return FALCON_OK;
+}
+
+}  // namespace
+
+size_t attn_grad_tc32_ws_bytes(int64_t tokens, int64_t k_tokens, int B, int Hq, int Hkv, int d) {
+  PromptArgs a = {};
+  a.B = B, a.Hq = Hq, a.Hkv = Hkv, a.tokens = tokens, a.k_tokens = k_tokens;
+  size_t bytes;
+  operands(nullptr, a, d <= 64 ? 64 : 128, &bytes);
+  return bytes;
+}
+
+int launch_attn_grad_tc32(const GradArgs& g, cudaStream_t s) {
+  return g.a.d <= 64 ? launch_d<64>(g, s) : launch_d<128>(g, s);
+}
+
+}  // namespace falcon

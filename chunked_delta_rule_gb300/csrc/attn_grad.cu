@@ -33,6 +33,7 @@ __device__ __forceinline__ uint2 three_parts(float x) {
 template <typename T>
 __global__ void __launch_bounds__(256) attn_grad_sums_kernel(GradArgs g) {
   const PromptArgs& a = g.a;
+  launch_dependents();
   if (blockIdx.x == 0 && threadIdx.x == 0) *static_cast<uint32_t*>(a.ws) = 0;  // the call's status
   const int h = static_cast<int>(blockIdx.x % a.Hq);
   const int64_t j = blockIdx.x / a.Hq;
@@ -43,41 +44,52 @@ __global__ void __launch_bounds__(256) attn_grad_sums_kernel(GradArgs g) {
   // packed_block deals a sequence's blocks out from the last; here block n of a sequence holds its rows 128 n ..
   const int64_t n = x.y / kSumRows, at = first_block(q0, x.x) + n;
   float* out = g.sums + row_sums(g.blocks, h, at);
-  const int ls = 28 - __clz(a.d), li = threadIdx.x & ((1 << ls) - 1);
-  for (int r = threadIdx.x >> ls; r < kSumRows; r += 256 >> ls) {
-    const int i = x.y + r;
-    const bool live = i < lq;
-    float s = 0.f;
-    if (live) {
+  const int ls = 28 - __clz(a.d), li = threadIdx.x & ((1 << ls) - 1), step = 256 >> ls;
+  const Pieces p{li * 8, li * 8 + 4};
+  for (int r0 = threadIdx.x >> ls; r0 < kSumRows; r0 += 4 * step) {
+    // up to four rows' loads under way at once
+    Raw8<T> u[4], v[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const int i = x.y + r0 + k * step;
+      if (r0 + k * step >= kSumRows || i >= lq) continue;
       const T* o = static_cast<const T*>(g.o.p) + (q0 + i) * g.o.stride + h * a.d;
       const T* d_o = static_cast<const T*>(g.d_o.p) + (q0 + i) * g.d_o.stride + h * a.d;
-      float u[8], v[8];
-      const Pieces p{li * 8, li * 8 + 4};
-      if (g.o.vec) unpack8(load8<true, false>(o, p), u);
-      else unpack8(load8<false, false>(o, p), u);
-      if (g.d_o.vec) unpack8(load8<true, false>(d_o, p), v);
-      else unpack8(load8<false, false>(d_o, p), v);
-#pragma unroll
-      for (int e = 0; e < 8; ++e) s = fmaf(u[e], v[e], s);
+      u[k] = g.o.vec ? load8<true, false>(o, p) : load8<false, false>(o, p);
+      v[k] = g.d_o.vec ? load8<true, false>(d_o, p) : load8<false, false>(d_o, p);
     }
-    for (int m = 1; m < 1 << ls; m <<= 1) s += __shfl_xor_sync(0xffffffffu, s, m);
-    if (li == 0) {
-      float lse = INFINITY;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const int r = r0 + k * step, i = x.y + r;
+      if (r >= kSumRows) break;
+      const bool live = i < lq;
+      float s = 0.f;
       if (live) {
-        const float l = g.lse[(q0 + i) * a.Hq + h];
-        if (g.dlse) s -= g.dlse[(q0 + i) * a.Hq + h];
-        lse = l == -INFINITY ? INFINITY : l == INFINITY ? __int_as_float(0x7fffffff) : l;
-        if (l == -INFINITY) s = 0.f;
+        float y[8], z[8];
+        unpack8(u[k], y);
+        unpack8(v[k], z);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) s = fmaf(y[e], z[e], s);
       }
-      out[r] = lse;
-      out[kSumRows + r] = s;
-      if (g.images) {
-        // no weight: as far down as bf16 goes short of an infinity, which would spoil the columns' zeros
-        const uint2 x = lse == INFINITY ? make_uint2(0xFF7Fu, 0u) : three_parts(-lse / a.scale), y = three_parts(-s);
-        uint4* to = reinterpret_cast<uint4*>(g.images + (static_cast<int64_t>(h) * g.blocks + at) * kImageBytes +
-                                             (r >> 3) * 256 + (r & 7) * 16);
-        to[0] = make_uint4(x.x, x.y, y.x, y.y);
-        to[8] = make_uint4(0u, 0u, 0u, 0u);
+      for (int m = 1; m < 1 << ls; m <<= 1) s += __shfl_xor_sync(0xffffffffu, s, m);
+      if (li == 0) {
+        float lse = INFINITY;
+        if (live) {
+          const float l = g.lse[(q0 + i) * a.Hq + h];
+          if (g.dlse) s -= g.dlse[(q0 + i) * a.Hq + h];
+          lse = l == -INFINITY ? INFINITY : l == INFINITY ? __int_as_float(0x7fffffff) : l;
+          if (l == -INFINITY) s = 0.f;
+        }
+        out[r] = lse;
+        out[kSumRows + r] = s;
+        if (g.images) {
+          // no weight: as far down as bf16 goes short of an infinity, which would spoil the columns' zeros
+          const uint2 x = lse == INFINITY ? make_uint2(0xFF7Fu, 0u) : three_parts(-lse / a.scale), y = three_parts(-s);
+          uint4* to = reinterpret_cast<uint4*>(g.images + (static_cast<int64_t>(h) * g.blocks + at) * kImageBytes +
+                                               (r >> 3) * 256 + (r & 7) * 16);
+          to[0] = make_uint4(x.x, x.y, y.x, y.y);
+          to[8] = make_uint4(0u, 0u, 0u, 0u);
+        }
       }
     }
   }

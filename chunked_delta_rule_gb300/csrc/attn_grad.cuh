@@ -40,6 +40,18 @@ constexpr int kImageBytes = kSumRows * 32;
 // first block of a sequence whose rows begin at q0
 __device__ __forceinline__ int64_t first_block(int64_t q0, int b) { return q0 / kSumRows + b; }
 
+// The kernels of a call overlap: the products' first kernel is launched while the rows' sums are formed, which it waits for
+// before it reads them; the second one (the two do not depend on one another) once the last CTAs of the first have
+// begun, so that its CTAs take the SMs as these fall free.  It ends no sooner than the first: a thread of its last CTA
+// waits for that.
+__device__ __forceinline__ void launch_dependents() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+__device__ __forceinline__ void wait_for_previous() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+inline cudaLaunchAttribute overlap_attribute() {
+  cudaLaunchAttribute a;
+  a.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  a.val.programmaticStreamSerializationAllowed = 1;
+  return a;
+}
 // packed_block by a whole warp: 32 sequences a look
 __device__ __forceinline__ int2 find_block(const int32_t* cu, int B, int rows, int j) {
   const int lane = threadIdx.x & 31;

@@ -85,6 +85,7 @@ struct TcGradArgs {
   GradArgs g;
   int qblocks;  // of a sequence
   bool packed;
+  bool second;  // of the call's two kernels
   int split;    // CTAs of a cluster
   uint32_t* status;
   uint64_t limit;
@@ -206,8 +207,14 @@ __global__ void __launch_bounds__(Cfg<D, KEYS>::kThreads, Cfg<D, KEYS>::kCtas)
   }
   __syncthreads();
   const uint32_t tmem = bar->tmem;
+  if (!t.second) {  // what the sums' kernel wrote is there
+    wait_for_previous();
+    launch_dependents();
+  }
+  const bool last = t.second && blockIdx.x == gridDim.x - 1 && tid == C::kThreads - 1;  // ends no sooner than the first kernel
   if (!valid) {  // (the whole cluster)
     if (warp == C::kMmaWarp) tmem_dealloc(tmem, C::kCols);
+    if (last) wait_for_previous();
     return;
   }
   auto wait = [&](uint64_t* m, uint32_t parity) {
@@ -226,6 +233,8 @@ __global__ void __launch_bounds__(Cfg<D, KEYS>::kThreads, Cfg<D, KEYS>::kCtas)
   if (warp >= C::kLoadWarp) {
     if (D == 64) asm volatile("setmaxnreg.dec.sync.aligned.u32 48;");
     else asm volatile("setmaxnreg.dec.sync.aligned.u32 64;");
+    if (last) wait_for_previous();
+    __syncwarp();
   }
   if (warp == C::kLoadWarp) {
     if (lane == 0 && n > 0) {
@@ -620,12 +629,13 @@ int launch_kernel(TcGradArgs& t, int64_t grid, const CUtensorMap (&m)[4], cudaSt
   cfg.blockDim = dim3(Cfg<D, KEYS>::kThreads);
   cfg.dynamicSmemBytes = smem_bytes<D, KEYS>();
   cfg.stream = s;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = static_cast<unsigned>(t.split);
-  attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+  cudaLaunchAttribute attr[2];
+  attr[0] = overlap_attribute();
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = static_cast<unsigned>(t.split);
+  attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
-  cfg.numAttrs = t.split > 1 ? 1 : 0;
+  cfg.numAttrs = t.split > 1 ? 2 : 1;
   return cudaLaunchKernelEx(&cfg, kern, m[0], m[1], m[2], m[3], t) == cudaSuccess ? FALCON_OK : FALCON_ERR_CUDA;
 }
 
@@ -639,18 +649,8 @@ int launch_d(const GradArgs& g, cudaStream_t s) {
   t.limit = wait_limit_ns();
   CUtensorMap m[4];
   auto maps = [&](const RowsIn& x, int64_t n, int H, int rows, CUtensorMap* to) { return make_rows_map(to, x, n, H, a.d, rows); };
-  if (g.dq.p) {
-    const PromptGrid pg = prompt_grid(a, kTile);
-    t.qblocks = static_cast<int>(pg.blocks / a.B);
-    t.packed = pg.packed;
-    constexpr int N = Cfg<D, false>::kN;
-    if (!maps(a.q, a.tokens, a.Hq, kTile, m) || !maps(g.d_o, a.tokens, a.Hq, kTile, m + 1) ||
-        !maps(a.k, a.k_tokens, a.Hkv, N, m + 2) || !maps(a.v, a.k_tokens, a.Hkv, N, m + 3))
-      return FALCON_ERR_CUDA;
-    const int st = pg.blocks > INT32_MAX / a.Hq ? FALCON_ERR_UNSUPPORTED : launch_kernel<D, false>(t, pg.blocks * a.Hq, m, s);
-    if (st != FALCON_OK) return st;
-  }
-  if (g.dk.p) {
+  t.second = false;
+  if (g.dk.p) {  // first: its CTAs run longest
     constexpr int N = Cfg<D, true>::kN;
     const int64_t blocks = a.k_tokens / kTile + a.B;
     if (blocks > INT32_MAX / a.Hkv) return FALCON_ERR_UNSUPPORTED;
@@ -660,7 +660,20 @@ int launch_d(const GradArgs& g, cudaStream_t s) {
     // clusters until there are two rounds of CTAs, as long as a CTA keeps some four tiles
     const int64_t ctas = blocks * a.Hkv, tiles = std::max<int64_t>(a.tokens / a.B / (2 * N), 1) * (a.Hq / a.Hkv);
     while (t.split < 8 && ctas * t.split < int64_t(2) * sm_count() * Cfg<D, true>::kCtas && tiles >= 8 * t.split) t.split *= 2;
-    return launch_kernel<D, true>(t, ctas, m, s);
+    const int st = launch_kernel<D, true>(t, ctas, m, s);
+    if (st != FALCON_OK) return st;
+    t.split = 1;
+    t.second = true;
+  }
+  if (g.dq.p) {
+    const PromptGrid pg = prompt_grid(a, kTile);
+    t.qblocks = static_cast<int>(pg.blocks / a.B);
+    t.packed = pg.packed;
+    constexpr int N = Cfg<D, false>::kN;
+    if (!maps(a.q, a.tokens, a.Hq, kTile, m) || !maps(g.d_o, a.tokens, a.Hq, kTile, m + 1) ||
+        !maps(a.k, a.k_tokens, a.Hkv, N, m + 2) || !maps(a.v, a.k_tokens, a.Hkv, N, m + 3))
+      return FALCON_ERR_CUDA;
+    return pg.blocks > INT32_MAX / a.Hq ? FALCON_ERR_UNSUPPORTED : launch_kernel<D, false>(t, pg.blocks * a.Hq, m, s);
   }
   return FALCON_OK;
 }

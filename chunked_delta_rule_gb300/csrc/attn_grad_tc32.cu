@@ -120,6 +120,7 @@ __device__ __forceinline__ int64_t first64(int64_t q0, int b) { return q0 / kPas
 template <int D>
 __global__ void __launch_bounds__(256) attn_grad_split_kernel(GradArgs g, Operands w, unsigned q_ctas) {
   const PromptArgs& a = g.a;
+  launch_dependents();
   if (blockIdx.x == 0 && threadIdx.x == 0) *static_cast<uint32_t*>(a.ws) = 0;  // the call's status
   const bool of_q = blockIdx.x < q_ctas;
   const int H = of_q ? a.Hq : a.Hkv;
@@ -171,7 +172,7 @@ struct Cfg32 {
   static constexpr int kRing = (kP1 + kP2) * kTileBytes;
   // TMEM: dK and dV: X, P, Y (then dS over it), the tile's sums of dV and of dK;
   // dQ: two of X (then dS over it), of Y and of the tile's sums
-  [[maybe_unused]] static constexpr uint32_t kColX = 0, kColP = kPast, kColY = 2 * kPast, kColV = KEYS ? 3 * kPast : 4 * kPast;
+  [[maybe_unused]] static constexpr uint32_t kColX = 0, kColP = KEYS ? kPast : 0, kColY = 2 * kPast, kColV = kColY + (KEYS ? 1 : 2) * kPast;
   static constexpr int kSmem = 2 * kOwnBytes + kRing + kP1 * kInfo + kP2 * kInfo2 + 1024 + 256;
 };
 struct Bars32 {
@@ -186,6 +187,7 @@ struct Tc32Args {
   Operands w;
   int qblocks;  // of a sequence
   bool packed;
+  bool second;  // of the call's two kernels
   uint32_t* status;
   uint64_t limit;
   int stall;
@@ -193,15 +195,6 @@ struct Tc32Args {
 
 __host__ __device__ constexpr uint32_t idesc_f16(int M, int N, bool b_mn = false) {
   return idesc_bf16(M, N, false, b_mn) & ~((1u << 7) | (1u << 10));
-}
-// 16 columns of a thread's row
-__device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t (&r)[16]) {
-  asm volatile(
-      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
-      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
-        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
-      : "r"(taddr)
-      : "memory");
 }
 // two pairs of a row of factors, the same for every thread
 __device__ __forceinline__ void load_pairs(const float* p, uint64_t& a, uint64_t& b) {
@@ -236,13 +229,15 @@ template <int D>
 __device__ __forceinline__ void add_sums(uint64_t (&acc)[D / 2], uint32_t from, float f) {
   const uint64_t f2 = pack2(f, f);
 #pragma unroll
-  for (int c = 0; c < D / 16; ++c) {
-    uint32_t v[16];
-    tmem_ld16(from + 16 * c, v);
+  for (int c = 0; c < D / 64; ++c) {
+    uint32_t v[2][32];
+    tmem_ld32(from + 64 * c, v[0]);
+    tmem_ld32(from + 64 * c + 32, v[1]);
     tmem_wait_ld();
 #pragma unroll
-    for (int e = 0; e < 8; ++e)
-      acc[8 * c + e] = fma2(pack2(__uint_as_float(v[2 * e]), __uint_as_float(v[2 * e + 1])), f2, acc[8 * c + e]);
+    for (int e = 0; e < 32; ++e)
+      acc[32 * c + e] = fma2(pack2(__uint_as_float(v[e >> 4][(2 * e) & 31]), __uint_as_float(v[e >> 4][(2 * e + 1) & 31])), f2,
+                             acc[32 * c + e]);
   }
 }
 
@@ -312,8 +307,14 @@ __global__ void __launch_bounds__(Cfg32<D, KEYS>::kThreads, 1) attn_grad_tc32_ke
   const int each = end > first ? (end - first + N - 1) / N : 0, n = KEYS ? each * G : each;
   __syncthreads();
   const uint32_t tmem = bar->tmem;
+  if (!t.second) {  // the operands are there
+    wait_for_previous();
+    launch_dependents();
+  }
+  const bool last = t.second && blockIdx.x == gridDim.x - 1 && tid == C::kThreads - 1;  // ends no sooner than the first kernel
   if (!valid) {
     if (warp == C::kMmaWarp) tmem_dealloc(tmem, 512);
+    if (last) wait_for_previous();
     return;
   }
   auto wait = [&](uint64_t* m, uint32_t parity) {
@@ -330,7 +331,11 @@ __global__ void __launch_bounds__(Cfg32<D, KEYS>::kThreads, 1) attn_grad_tc32_ke
   };
 
   // 256 x 224 + 128 x 56 = 384 x 168
-  if (warp >= C::kMmaWarp) asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
+  if (warp >= C::kMmaWarp) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
+    if (last) wait_for_previous();
+    __syncwarp();
+  }
   if (warp == C::kMmaWarp) {
     // The whole warp walks the loop, so that descriptors stay uniform; one lane issues.
     constexpr uint32_t id_x = idesc_f16(kTile, N), id_s = idesc_f16(kTile, D, true);
@@ -503,69 +508,87 @@ __global__ void __launch_bounds__(Cfg32<D, KEYS>::kThreads, 1) attn_grad_tc32_ke
     }
     const uint64_t f1p = pack2(f1, f1), f2p = pack2(f2, f2), l2e = pack2(kLog2e, kLog2e);
     const uint64_t lse2 = pack2(lse, lse), delta2 = pack2(delta, delta);
-    // P of this row, columns 16 c on, from X in v: `ls` the log sums (dQ: lse2), `s` the columns' factors
-    auto weights = [&](const uint32_t (&v)[16], int c, const float* s, const float* ls, int lim, bool cut, uint64_t* x) {
+    // P of this row from X: `ls` the log sums (dQ: lse2), `s` the columns' factors
+    auto weights = [&](uint32_t from, const float* s, const float* ls, int lim, bool cut, uint64_t (&x)[32]) {
+      {
+        uint32_t v[2][32];
+        tmem_ld32(from, v[0]);
+        tmem_ld32(from + 32, v[1]);
+        tmem_wait_ld();
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        uint64_t s0, s1, l0 = 0, l1 = 0;
-        load_pairs(s + 16 * c + 4 * e, s0, s1);
-        if (KEYS) load_pairs(ls + 16 * c + 4 * e, l0, l1);
+        for (int e = 0; e < 32; ++e)
+          x[e] = pack2(__uint_as_float(v[e >> 4][(2 * e) & 31]), __uint_as_float(v[e >> 4][(2 * e + 1) & 31]));
+      }
+      if (KEYS && group) arrive(&bar->x_read);
 #pragma unroll
-        for (int k = 0; k < 2; ++k) {
-          const int at = 4 * e + 2 * k;
-          uint64_t z = mul2(pack2(__uint_as_float(v[at]), __uint_as_float(v[at + 1])), f1p);
-          // the difference first: it is small where the weight is not
-          if (KEYS) z = fma2(z, k ? s1 : s0, k ? l1 : l0);
-          else z = fma2(z, k ? s1 : s0, lse2);
+      for (int e = 0; e < 16; ++e) {
+        uint64_t s0, s1, l0 = lse2, l1 = lse2;
+        load_pairs(s + 4 * e, s0, s1);
+        if (KEYS) load_pairs(ls + 4 * e, l0, l1);
+        // the difference first: it is small where the weight is not
+        x[2 * e] = mul2(fma2(mul2(x[2 * e], f1p), s0, l0), l2e);
+        x[2 * e + 1] = mul2(fma2(mul2(x[2 * e + 1], f1p), s1, l1), l2e);
+      }
+      if (cut) {
+#pragma unroll
+        for (int e = 0; e < 32; ++e) {
           float z0, z1;
-          unpack2(mul2(z, l2e), z0, z1);
-          if (cut) {
-            if (KEYS ? 16 * c + at < lim : 16 * c + at >= lim) z0 = -INFINITY;
-            if (KEYS ? 16 * c + at + 1 < lim : 16 * c + at + 1 >= lim) z1 = -INFINITY;
+          unpack2(x[e], z0, z1);
+          if (KEYS ? 2 * e < lim : 2 * e >= lim) z0 = -INFINITY;
+          if (KEYS ? 2 * e + 1 < lim : 2 * e + 1 >= lim) z1 = -INFINITY;
+          x[e] = pack2(z0, z1);
+        }
+      }
+#pragma unroll
+      for (int e = 0; e < 32; ++e) {
+        float z0, z1;
+        unpack2(x[e], z0, z1);
+        x[e] = pack2(ex2(z0), ex2(z1));
+      }
+    };
+    // dS from P and Y, times the factors w of the rows that the sum runs over: s the columns' factors, ds their D (dQ: delta2)
+    auto differences = [&](uint32_t from, const float* s, const float* ds, const float* w, uint64_t (&x)[32]) {
+#pragma unroll
+      for (int c = 0; c < 2; ++c) {
+        uint32_t v[32];
+        tmem_ld32(from + 32 * c, v);
+        tmem_wait_ld();
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          uint64_t s2[2], d2[2] = {delta2, delta2}, w2[2];
+          load_pairs(s + 32 * c + 4 * e, s2[0], s2[1]);
+          if (KEYS) load_pairs(ds + 32 * c + 4 * e, d2[0], d2[1]);
+          load_pairs(w + 32 * c + 4 * e, w2[0], w2[1]);
+#pragma unroll
+          for (int k = 0; k < 2; ++k) {
+            const uint64_t y = mul2(pack2(__uint_as_float(v[4 * e + 2 * k]), __uint_as_float(v[4 * e + 2 * k + 1])), f2p);
+            uint64_t& to = x[16 * c + 2 * e + k];
+            to = mul2(mul2(to, fma2(y, s2[k], d2[k])), w2[k]);
           }
-          x[2 * e + k] = pack2(ex2(z0), ex2(z1));
         }
       }
     };
     float down = 0.f;  // of the tile whose sums come next
     if constexpr (KEYS) {
       for (int i = 0; i < n; ++i) {
-        const int at = first + i % each * N, lim = row - off - at;
-        const bool cut = at + off < row0 + kTile - 1;  // some key is behind a query of these
+        const int at = first + i % each * N;
         const float* i1 = reinterpret_cast<const float*>(infos + i % P1 * C::kInfo);  // log sums, factors of Q
         const float* i2 = reinterpret_cast<const float*>(infos + P1 * C::kInfo + i % P2 * C::kInfo2);  // D, factors of dO
         uint64_t x[32];
-        if (!(ok = waited(&bar->full1[i % P1], (i / P1) & 1) && waited(&bar->x[0], i & 1))) break;
-#pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          uint32_t v[16];
-          tmem_ld16(mine + C::kColX + 16 * c, v);
-          tmem_wait_ld();
-          weights(v, c, i1 + N, i1, lim, cut, x + 8 * c);
+        // the sums of the tile before, while X (Y) of this one is formed
+        if (i > 0) {
+          if (!(ok = group ? waited(&bar->empty1[(i - 1) % P1], ((i - 1) / P1) & 1)
+                           : waited(&bar->empty2[(i - 1) % P2], ((i - 1) / P2) & 1)))
+            break;
+          add_sums<D>(acc, mine + C::kColV + group * D, down);
         }
-        if (group) arrive(&bar->x_read);
+        if (!(ok = waited(&bar->full1[i % P1], (i / P1) & 1) && waited(&bar->x[0], i & 1))) break;
+        // cut: some key is behind a query of these
+        weights(mine + C::kColX, i1 + N, i1, row - off - at, at + off < row0 + kTile - 1, x);
         if (!(ok = waited(&bar->full2[i % P2], (i / P2) & 1))) break;
         if (group) {
           if (!(ok = waited(&bar->y, i & 1))) break;
-#pragma unroll
-          for (int c = 0; c < 4; ++c) {
-            uint32_t v[16];
-            tmem_ld16(mine + C::kColY + 16 * c, v);
-            tmem_wait_ld();
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              uint64_t s[2], dd[2], sq[2];
-              load_pairs(i2 + N + 16 * c + 4 * e, s[0], s[1]);
-              load_pairs(i2 + 16 * c + 4 * e, dd[0], dd[1]);
-              load_pairs(i1 + N + 16 * c + 4 * e, sq[0], sq[1]);
-#pragma unroll
-              for (int k = 0; k < 2; ++k) {
-                const uint64_t y = mul2(pack2(__uint_as_float(v[4 * e + 2 * k]), __uint_as_float(v[4 * e + 2 * k + 1])), f2p);
-                const uint64_t z = fma2(y, s[k], dd[k]);
-                x[8 * c + 2 * e + k] = mul2(mul2(x[8 * c + 2 * e + k], z), sq[k]);
-              }
-            }
-          }
+          differences(mine + C::kColY, i2 + N, i2, i1 + N, x);
         } else {
 #pragma unroll
           for (int e = 0; e < 16; ++e) {
@@ -575,49 +598,25 @@ __global__ void __launch_bounds__(Cfg32<D, KEYS>::kThreads, 1) attn_grad_tc32_ke
             x[2 * e + 1] = mul2(x[2 * e + 1], s1);
           }
         }
-        // X and Y of this tile came after the products of the one before: its sums are there, its P and dS are read
-        const float was = down;
+        // the products that read P and dS of the tile before are done
         down = store_weights(mine + (group ? C::kColY : C::kColP), x);
-        if (i > 0) add_sums<D>(acc, mine + C::kColV + group * D, was);
         tmem_wait_st();
         arrive(group ? &bar->ds[0] : &bar->p);
       }
     } else {
       for (int i = group; i < n; i += 2) {
-        const int at = i * N, lim = min(row + off + 1, lk) - at;
-        const bool cut = at + N > min(row0 + off + 1, lk);
+        const int at = i * N;
         const float* i1 = reinterpret_cast<const float*>(infos + i % P1 * C::kInfo);  // factors of K, of V
-        const uint32_t tx = mine + C::kColX + group * N, ty = mine + C::kColY + group * N;
+        const uint32_t tx = mine + C::kColX + group * N;
         uint64_t x[32];
+        if (i > 1) {  // the sums of this warpgroup's last tile
+          if (!(ok = waited(&bar->empty1[(i - 2) % P1], ((i - 2) / P1) & 1))) break;
+          add_sums<D>(acc, mine + C::kColV + group * D, down);
+        }
         if (!(ok = waited(&bar->full1[i % P1], (i / P1) & 1) && waited(&bar->x[group], (i >> 1) & 1))) break;
-#pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          uint32_t v[16];
-          tmem_ld16(tx + 16 * c, v);
-          tmem_wait_ld();
-          weights(v, c, i1, nullptr, lim, cut, x + 8 * c);
-        }
-#pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          uint32_t v[16];
-          tmem_ld16(ty + 16 * c, v);
-          tmem_wait_ld();
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            uint64_t s[2], sk[2];
-            load_pairs(i1 + N + 16 * c + 4 * e, s[0], s[1]);
-            load_pairs(i1 + 16 * c + 4 * e, sk[0], sk[1]);
-#pragma unroll
-            for (int k = 0; k < 2; ++k) {
-              const uint64_t y = mul2(pack2(__uint_as_float(v[4 * e + 2 * k]), __uint_as_float(v[4 * e + 2 * k + 1])), f2p);
-              const uint64_t z = fma2(y, s[k], delta2);
-              x[8 * c + 2 * e + k] = mul2(mul2(x[8 * c + 2 * e + k], z), sk[k]);
-            }
-          }
-        }
-        const float was = down;
+        weights(tx, i1, nullptr, min(row + off + 1, lk) - at, at + N > min(row0 + off + 1, lk), x);
+        differences(mine + C::kColY + group * N, i1 + N, nullptr, i1, x);
         down = store_weights(tx, x);
-        if (i > 1) add_sums<D>(acc, mine + C::kColV + group * D, was);
         tmem_wait_st();
         arrive(&bar->ds[group]);
       }
@@ -716,8 +715,15 @@ int launch_kernel(Tc32Args& t, int64_t grid, cudaStream_t s) {
   t.stall = take_test_stall() ? 1 : 0;
   const auto kern = attn_grad_tc32_kernel<D, KEYS>;
   if (!set_smem_limit(reinterpret_cast<const void*>(kern), Cfg32<D, KEYS>::kSmem)) return FALCON_ERR_CUDA;
-  kern<<<static_cast<unsigned>(grid), Cfg32<D, KEYS>::kThreads, Cfg32<D, KEYS>::kSmem, s>>>(t);
-  return cudaGetLastError() == cudaSuccess ? FALCON_OK : FALCON_ERR_CUDA;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(grid));
+  cfg.blockDim = dim3(Cfg32<D, KEYS>::kThreads);
+  cfg.dynamicSmemBytes = Cfg32<D, KEYS>::kSmem;
+  cfg.stream = s;
+  cudaLaunchAttribute attr[1] = {overlap_attribute()};
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kern, t) == cudaSuccess ? FALCON_OK : FALCON_ERR_CUDA;
 }
 
 // The parts of the workspace from `base` on; bytes: all of them.
@@ -755,16 +761,18 @@ int launch_d(const GradArgs& g, cudaStream_t s) {
   if (q_ctas + k_ctas > INT32_MAX) return FALCON_ERR_UNSUPPORTED;
   attn_grad_split_kernel<D><<<static_cast<unsigned>(q_ctas + k_ctas), 256, 0, s>>>(g, t.w, static_cast<unsigned>(q_ctas));
   if (cudaGetLastError() != cudaSuccess) return FALCON_ERR_CUDA;
+  t.second = false;
+  if (g.dk.p && k_ctas) {  // first: its CTAs run longest
+    const int64_t blocks = a.k_tokens / kTile + a.B;
+    const int st = blocks > INT32_MAX / a.Hkv ? FALCON_ERR_UNSUPPORTED : launch_kernel<D, true>(t, blocks * a.Hkv, s);
+    if (st != FALCON_OK) return st;
+    t.second = true;
+  }
   if (g.dq.p && q_ctas) {
     const PromptGrid pg = prompt_grid(a, kTile);
     t.qblocks = static_cast<int>(pg.blocks / a.B);
     t.packed = pg.packed;
-    const int st = pg.blocks > INT32_MAX / a.Hq ? FALCON_ERR_UNSUPPORTED : launch_kernel<D, false>(t, pg.blocks * a.Hq, s);
-    if (st != FALCON_OK) return st;
-  }
-  if (g.dk.p && k_ctas) {
-    const int64_t blocks = a.k_tokens / kTile + a.B;
-    return blocks > INT32_MAX / a.Hkv ? FALCON_ERR_UNSUPPORTED : launch_kernel<D, true>(t, blocks * a.Hkv, s);
+    return pg.blocks > INT32_MAX / a.Hq ? FALCON_ERR_UNSUPPORTED : launch_kernel<D, false>(t, pg.blocks * a.Hq, s);
   }
   return FALCON_OK;
 }

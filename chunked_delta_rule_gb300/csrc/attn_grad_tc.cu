@@ -37,6 +37,7 @@
 // after the pipeline has ended.
 
 #include <algorithm>
+#include <cmath>
 
 #include "attn_grad.cuh"
 #include "attn_tc.cuh"
@@ -401,8 +402,10 @@ __global__ void __launch_bounds__(Cfg<D, KEYS>::kThreads, Cfg<D, KEYS>::kCtas)
         arrive(&bar->ready);
       }
     }
+    int past = KEYS && n > 0 ? i0 % each : 0;  // the tile's place among a head's
     for (int i = 0; i < n && ok; ++i) {
-      const int at = first + (KEYS ? (i0 + i) % each : i) * N + part * 32;  // of the first column
+      const int at = first + past * N + part * 32;  // of the first column
+      if (++past == each) past = 0;
       const uint32_t tx = mine + C::kColX + part * 32, ty = mine + C::kColY + part * 32;
       if (!(ok = waited(&bar->x, i & 1))) break;
       tc_fence_after();
@@ -657,9 +660,14 @@ int launch_d(const GradArgs& g, cudaStream_t s) {
     if (!maps(a.k, a.k_tokens, a.Hkv, kTile, m) || !maps(a.v, a.k_tokens, a.Hkv, kTile, m + 1) ||
         !maps(a.q, a.tokens, a.Hq, N, m + 2) || !maps(g.d_o, a.tokens, a.Hq, N, m + 3))
       return FALCON_ERR_CUDA;
-    // clusters until there are two rounds of CTAs, as long as a CTA keeps some four tiles
-    const int64_t ctas = blocks * a.Hkv, tiles = std::max<int64_t>(a.tokens / a.B / (2 * N), 1) * (a.Hq / a.Hkv);
-    while (t.split < 8 && ctas * t.split < int64_t(2) * sm_count() * Cfg<D, true>::kCtas && tiles >= 8 * t.split) t.split *= 2;
+    // Clusters until the longest CTA (the keys that every query of all heads sees) takes no longer than all tiles of both
+    // kernels dealt out evenly, sequences taken as of one length; a tile of dQ costs some 0.7 of one of dK and dV.
+    const int64_t ctas = blocks * a.Hkv;
+    const double lq = static_cast<double>(a.tokens) / a.B, lk = static_cast<double>(a.k_tokens) / a.B;
+    const double longest = std::ceil(lq / N) * (a.Hq / a.Hkv);
+    const double seen = lk >= lq ? 1.0 - 0.5 * lq / lk : 0.5 * lk / lq;  // of all pairs
+    const double even = 1.7 * longest * seen * std::ceil(lk / kTile) * a.B * a.Hkv / (sm_count() * Cfg<D, true>::kCtas);
+    while (t.split < 8 && longest > even * t.split && longest >= 8 * t.split) t.split *= 2;
     const int st = launch_kernel<D, true>(t, ctas, m, s);
     if (st != FALCON_OK) return st;
     t.split = 1;

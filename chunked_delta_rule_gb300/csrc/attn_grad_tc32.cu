@@ -18,6 +18,7 @@
 // runs over have been multiplied in; so no range of P or dS is out of reach.
 // dK and dV: one warpgroup forms P and holds dV, the other forms P again, then dS, and holds dK.
 //   tensor cores: ... X(i) dK(i - 1) Y(i) dV(i) X(i + 1) ...
+// (X's owned operand lies in shared memory, Y's in TMEM, which gives the ring its room.)
 // dQ: the warpgroups take the tiles in turn, each with sums of its own.
 //
 // Masked scores are set to -inf after the product.  A masked weight is 0, but 0
@@ -64,7 +65,7 @@ __device__ __forceinline__ void split2(uint64_t x, uint32_t& hi, uint32_t& lo) {
 // and the rows' factors.  dot: (sum of x o of each row) of the rows, by the row's first lane.
 template <int D, bool DOT, typename F>
 __device__ __forceinline__ void split_rows(const RowsIn& x, const RowsIn& o, int64_t row, int head, int rows, int d,
-                                           uint8_t* image, float* factor, F dot) {
+                                           uint8_t* image, __nv_bfloat16* factor, F dot) {
   constexpr int L = D / 8, kStep = 256 / L;
   const int c = threadIdx.x % L;
   for (int r = threadIdx.x / L; r < kPast; r += kStep) {
@@ -101,7 +102,7 @@ __device__ __forceinline__ void split_rows(const RowsIn& x, const RowsIn& o, int
     *reinterpret_cast<uint4*>(to) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
     *reinterpret_cast<uint4*>(to + kPast * D * 2) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
     if (c == 0) {
-      factor[r] = down;
+      factor[r] = __float2bfloat16_rn(down);  // exact
       if (DOT) dot(r, s);
     }
   }
@@ -109,11 +110,16 @@ __device__ __forceinline__ void split_rows(const RowsIn& x, const RowsIn& o, int
 
 // Where the operands lie: 64-row blocks, a sequence's from cu[b] / 64 + b on.
 struct Operands {
-  uint8_t *q, *d_o, *k, *v;       // images of kPast * D * 4 bytes, a head's blocks behind one another
-  float *q_info, *o_info;         // 64 log sums and 64 factors; 64 D's and 64 factors; both sums negative
-  float *k_info, *v_info;         // 64 factors
+  uint8_t *q, *d_o, *k, *v;    // images of kPast * D * 4 bytes, a head's blocks behind one another
+  // What the softmax threads need of a block's rows.  Queries: -log sum, -D (fp32), the factors of q and of dO; keys: the
+  // factors of k and of v (bf16: powers of two).
+  uint8_t *q_info, *k_info;
   int64_t q_blocks, k_blocks;     // of a head
 };
+constexpr int kQInfo = kPast * 12, kKInfo = kPast * 4;
+__device__ __forceinline__ float factor_at(const uint8_t* factors, int i) {
+  return __bfloat162float(reinterpret_cast<const __nv_bfloat16*>(factors)[i]);
+}
 __host__ __device__ __forceinline__ int64_t count_blocks(int64_t rows, int B) { return rows / kPast + B + 1; }
 __device__ __forceinline__ int64_t first64(int64_t q0, int b) { return q0 / kPast + b; }
 
@@ -135,16 +141,18 @@ __global__ void __launch_bounds__(256) attn_grad_split_kernel(GradArgs g, Operan
   const auto none = [](int, float) {};
   if (!of_q) {
     const int64_t to = h * w.k_blocks + j;
-    split_rows<D, false>(a.k, a.k, row, h, rows, a.d, w.k + to * (kPast * D * 4), w.k_info + to * kPast, none);
-    split_rows<D, false>(a.v, a.v, row, h, rows, a.d, w.v + to * (kPast * D * 4), w.v_info + to * kPast, none);
+    __nv_bfloat16* factors = reinterpret_cast<__nv_bfloat16*>(w.k_info + to * kKInfo);
+    split_rows<D, false>(a.k, a.k, row, h, rows, a.d, w.k + to * (kPast * D * 4), factors, none);
+    split_rows<D, false>(a.v, a.v, row, h, rows, a.d, w.v + to * (kPast * D * 4), factors + kPast, none);
     return;
   }
   const int64_t to = h * w.q_blocks + j;
-  float *qi = w.q_info + to * (2 * kPast), *oi = w.o_info + to * (2 * kPast);
-  split_rows<D, false>(a.q, a.q, row, h, rows, a.d, w.q + to * (kPast * D * 4), qi + kPast, none);
+  float* info = reinterpret_cast<float*>(w.q_info + to * kQInfo);
+  __nv_bfloat16* factors = reinterpret_cast<__nv_bfloat16*>(info + 2 * kPast);
+  split_rows<D, false>(a.q, a.q, row, h, rows, a.d, w.q + to * (kPast * D * 4), factors, none);
   // the log sums and D, for the tiles and for rows that are computed again; rows without a key have no weights
   float* sums = g.sums + row_sums(g.blocks, h, first_block(r0, x.x) + n / 2) + n % 2 * kPast;
-  split_rows<D, true>(g.d_o, g.o, row, h, rows, a.d, w.d_o + to * (kPast * D * 4), oi + kPast, [&](int r, float s) {
+  split_rows<D, true>(g.d_o, g.o, row, h, rows, a.d, w.d_o + to * (kPast * D * 4), factors + kPast, [&](int r, float s) {
     float lse = INFINITY;
     if (r < rows) {
       const float l = g.lse[(row + r) * a.Hq + h];
@@ -153,7 +161,7 @@ __global__ void __launch_bounds__(256) attn_grad_split_kernel(GradArgs g, Operan
       if (l == -INFINITY) s = 0.f;
     }
     sums[r] = lse, sums[kSumRows + r] = s;
-    qi[r] = -lse, oi[r] = -s;
+    info[r] = -lse, info[kPast + r] = -s;
   });
 }
 
@@ -164,23 +172,23 @@ struct Cfg32 {
   // one more warp copies the tiles and issues the products; its warpgroup gives its registers to the others
   static constexpr int kMmaWarp = kWarps, kThreads = 32 * kWarps + 128;
   static constexpr int kOwnBytes = kTile * D * 4, kTileBytes = kPast * D * 4;
-  // places of the first tiles (Q; K), which are read until the tile's last product, and of the second ones (dO; V)
-  static constexpr int kP1 = D == 64 ? 4 : 2, kP2 = D == 64 ? 4 : 1;
-  // what the softmax threads need of the rows of a pair: with the first tile log sums and factors of Q, or factors of K
-  // and of V; with the second one (dK and dV) D and factors of dO
-  static constexpr int kInfo = 2 * kPast * 4, kInfo2 = KEYS ? kInfo : 0;
+  // places of the first tiles (Q; K), which are read until the tile's last product, and of the second ones (dO; V); the
+  // second owned tile (V; dO) lies in the first tiles' places 1 and 2 until it is in TMEM
+  static constexpr int kP1 = D == 64 ? 4 : 3, kP2 = D == 64 ? 4 : 2;
   static constexpr int kRing = (kP1 + kP2) * kTileBytes;
-  // TMEM: dK and dV: X, P, Y (then dS over it), the tile's sums of dV and of dK;
-  // dQ: two of X (then dS over it), of Y and of the tile's sums
-  [[maybe_unused]] static constexpr uint32_t kColX = 0, kColP = KEYS ? kPast : 0, kColY = 2 * kPast, kColV = kColY + (KEYS ? 1 : 2) * kPast;
-  static constexpr int kSmem = 2 * kOwnBytes + kRing + kP1 * kInfo + kP2 * kInfo2 + 1024 + 256;
+  static constexpr int kInfo = KEYS ? kQInfo : kKInfo;
+  // TMEM: dK and dV: X (then P over it), Y (then dS), the tile's sums of dV and of dK; dQ: two of X (then dS), two of Y,
+  // the tile's sums.  Then the second owned tile.
+  static constexpr uint32_t kColX = 0, kColY = KEYS ? kPast : 2 * kPast, kColV = 2 * kColY, kColA = kColV + (KEYS ? 2 : 1) * D;
+  static constexpr int kSmem = kOwnBytes + kRing + 2 * kInfo + 1024 + 256;
 };
 struct Bars32 {
-  uint64_t own, full1[4], empty1[4], full2[4], empty2[4], x[2], x_read, y, p, ds[2], drain, stall;
+  uint64_t own, ready, full1[4], empty1[4], full2[4], empty2[4], info[2], x[2], x_read, y, p, ds[2], added, drain, stall;
   uint32_t tmem, failed;
 };
 static_assert(sizeof(Bars32) <= 256 && Cfg32<128, true>::kSmem <= 227 * 1024 && Cfg32<128, false>::kSmem <= 227 * 1024 &&
-                  Cfg32<64, true>::kSmem <= 227 * 1024, "shared memory");
+                  Cfg32<64, true>::kSmem <= 227 * 1024 && Cfg32<128, true>::kColA + 128 <= 512 &&
+                  Cfg32<128, false>::kColA + 128 <= 512, "shared memory and TMEM");
 
 struct Tc32Args {
   GradArgs g;
@@ -196,10 +204,16 @@ struct Tc32Args {
 __host__ __device__ constexpr uint32_t idesc_f16(int M, int N, bool b_mn = false) {
   return idesc_bf16(M, N, false, b_mn) & ~((1u << 7) | (1u << 10));
 }
-// two pairs of a row of factors, the same for every thread
+// two pairs of a row of numbers, the same for every thread; four pairs of a row of factors
 __device__ __forceinline__ void load_pairs(const float* p, uint64_t& a, uint64_t& b) {
   const float4 v = *reinterpret_cast<const float4*>(p);
   a = pack2(v.x, v.y), b = pack2(v.z, v.w);
+}
+__device__ __forceinline__ void load_factors(const uint8_t* p, uint64_t (&f)[4]) {
+  const uint4 v = *reinterpret_cast<const uint4*>(p);
+  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) f[i] = pack2(__uint_as_float(w[i] << 16), __uint_as_float(w[i] & 0xFFFF0000u));
 }
 // A thread's row of a tile of P or dS to TMEM: its own power of two, hi's in 32 columns, lo's in the next 32.  Returns the
 // factor that undoes the power.
@@ -251,15 +265,19 @@ __global__ void __launch_bounds__(Cfg32<D, KEYS>::kThreads, 1) attn_grad_tc32_ke
 
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = align1024(smem_raw);
-  uint8_t *s1 = smem, *s2 = s1 + C::kOwnBytes, *ring1 = s2 + C::kOwnBytes, *ring2 = ring1 + P1 * C::kTileBytes;
-  uint8_t* infos = ring1 + C::kRing;  // of the first tiles, then of the second ones
-  Bars32* bar = reinterpret_cast<Bars32*>(infos + P1 * C::kInfo + P2 * C::kInfo2);
+  uint8_t *s1 = smem, *ring1 = s1 + C::kOwnBytes, *ring2 = ring1 + P1 * C::kTileBytes, *s2 = ring1 + C::kTileBytes;
+  uint8_t* infos = ring1 + C::kRing;
+  Bars32* bar = reinterpret_cast<Bars32*>(infos + 2 * C::kInfo);
   if (warp == C::kMmaWarp) {
     tmem_alloc(&bar->tmem, 512);
     tmem_relinquish();
   }
   if (tid == 0) {
     mbar_init(&bar->own, 1);
+    mbar_init(&bar->ready, C::kWarps);
+    mbar_init(&bar->info[0], 1);
+    mbar_init(&bar->info[1], 1);
+    mbar_init(&bar->added, 4);
     for (int i = 0; i < 4; ++i) {
       mbar_init(&bar->full1[i], 1);
       mbar_init(&bar->empty1[i], 1);
@@ -340,7 +358,7 @@ __global__ void __launch_bounds__(Cfg32<D, KEYS>::kThreads, 1) attn_grad_tc32_ke
     // The whole warp walks the loop, so that descriptors stay uniform; one lane issues.
     constexpr uint32_t id_x = idesc_f16(kTile, N), id_s = idesc_f16(kTile, D, true);
     const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);
-    const uint64_t a1 = sdesc_k128(smem_u32(s1)), a2 = sdesc_k128(smem_u32(s2));
+    const uint64_t a1 = sdesc_k128(smem_u32(s1));
     const uint64_t bk1 = sdesc_k128(smem_u32(ring1)), bk2 = sdesc_k128(smem_u32(ring2));
     const uint64_t bm1 = D == 64 ? sdesc_mn128(smem_u32(ring1)) : sdesc_mn128_wide(smem_u32(ring1), N * 128);
     const uint64_t bm2 = D == 64 ? sdesc_mn128(smem_u32(ring2)) : sdesc_mn128_wide(smem_u32(ring2), N * 128);
@@ -353,16 +371,19 @@ __global__ void __launch_bounds__(Cfg32<D, KEYS>::kThreads, 1) attn_grad_tc32_ke
     auto full2 = [&](int i) { return arrived(&bar->full2[i % P2], (i / P2) & 1); };
     // to = the owned rows times tile i's; lo hi, hi lo, hi hi
     auto scores = [&](uint32_t to, int i, int second, uint64_t* then, uint64_t* frees) {
-      const uint64_t as = second ? a2 : a1, bs = second ? bk2 + i % P2 * (C::kTileBytes >> 4) : bk1 + i % P1 * (C::kTileBytes >> 4);
+      const uint64_t bs = second ? bk2 + i % P2 * (C::kTileBytes >> 4) : bk1 + i % P1 * (C::kTileBytes >> 4);
       if (elect_one()) {
 #pragma unroll
-        for (int part = 0; part < 3; ++part) {
-          const uint64_t ap = as + (part == 0 ? C::kOwnBytes / 2 >> 4 : 0), bp = bs + (part == 1 ? kHalf >> 4 : 0);
+        for (int part = 0; part < 3; ++part)
 #pragma unroll
-          for (int ks = 0; ks < D / 16; ++ks)
-            umma_bf16(tm + to, ap + (((ks >> 2) * kTile * 128 + (ks & 3) * 32) >> 4),
-                      bp + (((ks >> 2) * N * 128 + (ks & 3) * 32) >> 4), id_x, part > 0 || ks > 0);
-        }
+          for (int ks = 0; ks < D / 16; ++ks) {
+            const uint64_t bd = bs + (part == 1 ? kHalf >> 4 : 0) + (((ks >> 2) * N * 128 + (ks & 3) * 32) >> 4);
+            if (second)
+              umma_ts(tm + to, tm + C::kColA + (part == 0 ? D / 2 : 0) + ks * 8, bd, id_x, part > 0 || ks > 0);
+            else
+              umma_bf16(tm + to, a1 + (part == 0 ? C::kOwnBytes / 2 >> 4 : 0) + (((ks >> 2) * kTile * 128 + (ks & 3) * 32) >> 4),
+                        bd, id_x, part > 0 || ks > 0);
+          }
         if (then) umma_commit(then);
         if (frees) umma_commit(frees);
       }
@@ -382,36 +403,36 @@ __global__ void __launch_bounds__(Cfg32<D, KEYS>::kThreads, 1) attn_grad_tc32_ke
       }
       __syncwarp();
     };
-    // copies of tile i's first and second part; by one lane
-    int loads1 = 0, loads2 = 0;
-    auto load1 = [&] {
-      const int i = loads1++, at = i % P1;
+    // copies of the next tile's first and second part, and of its rows' numbers; by one lane
+    int loads1 = 0, loads2 = 0, infos_in = 0;
+    auto load = [&](uint8_t* to, const uint8_t* from, int bytes, uint64_t* full) {
       if (elect_one()) {
-        const int64_t blk = past_block(i);
-        uint8_t* info = infos + at * C::kInfo;
-        mbar_arrive_expect_tx(&bar->full1[at], C::kTileBytes + C::kInfo);
-        bulk_load(ring1 + at * C::kTileBytes, (KEYS ? t.w.q : t.w.k) + blk * C::kTileBytes, C::kTileBytes, &bar->full1[at]);
-        if (KEYS) {
-          bulk_load(info, t.w.q_info + blk * (2 * kPast), C::kInfo, &bar->full1[at]);
-        } else {
-          bulk_load(info, t.w.k_info + blk * kPast, C::kInfo / 2, &bar->full1[at]);
-          bulk_load(info + C::kInfo / 2, t.w.v_info + blk * kPast, C::kInfo / 2, &bar->full1[at]);
-        }
+        mbar_arrive_expect_tx(full, bytes);
+        bulk_load(to, from, bytes, full);
       }
       __syncwarp();
+    };
+    auto load1 = [&] {
+      const int i = loads1++, at = i % P1;
+      load(ring1 + at * C::kTileBytes, (KEYS ? t.w.q : t.w.k) + past_block(i) * C::kTileBytes, C::kTileBytes, &bar->full1[at]);
     };
     auto load2 = [&] {
       const int i = loads2++, at = i % P2;
-      if (elect_one()) {
-        const int64_t blk = past_block(i);
-        mbar_arrive_expect_tx(&bar->full2[at], C::kTileBytes + C::kInfo2);
-        bulk_load(ring2 + at * C::kTileBytes, (KEYS ? t.w.d_o : t.w.v) + blk * C::kTileBytes, C::kTileBytes, &bar->full2[at]);
-        if (KEYS) bulk_load(infos + P1 * C::kInfo + at * C::kInfo2, t.w.o_info + blk * (2 * kPast), C::kInfo2, &bar->full2[at]);
-      }
-      __syncwarp();
+      load(ring2 + at * C::kTileBytes, (KEYS ? t.w.d_o : t.w.v) + past_block(i) * C::kTileBytes, C::kTileBytes, &bar->full2[at]);
     };
-    // the place of tile i - P's is free
-    auto more1 = [&](int i) { return i >= n || (arrived(&bar->empty1[i % P1], (i / P1 - 1) & 1) && (load1(), true)); };
+    auto load_info = [&] {
+      const int i = infos_in++;
+      load(infos + (i & 1) * C::kInfo, (KEYS ? t.w.q_info : t.w.k_info) + past_block(i) * C::kInfo, C::kInfo, &bar->info[i & 1]);
+    };
+    // The place of tile i - P's is free.  Its last product is that of dK or dQ, which also ends the use of the tile's numbers.
+    auto more1 = [&](int i) {
+      const int done = i - P1;
+      if (done + 2 >= n && i >= n) return true;
+      if (!arrived(&bar->empty1[i % P1], (i / P1 - 1) & 1)) return false;
+      if (done + 2 < n) load_info();
+      if (i < n) load1();
+      return true;
+    };
     auto more2 = [&](int i) { return i >= n || (arrived(&bar->empty2[i % P2], (i / P2 - 1) & 1) && (load2(), true)); };
     bool ok = n > 0 && (!t.stall || arrived(&bar->stall, 0));
     const bool own = ok;
@@ -427,23 +448,26 @@ __global__ void __launch_bounds__(Cfg32<D, KEYS>::kThreads, 1) attn_grad_tc32_ke
         }
       }
       __syncwarp();
-      for (int i = 0; i < min(n, max(P1, P2)); ++i) {
-        if (i < P1) load1();
-        if (i < P2) load2();
-      }
-      ok = arrived(&bar->own, 0);
+      load1();
+      for (int i = 0; i < min(n, P2); ++i) load2();
+      for (int i = 0; i < min(n, 2); ++i) load_info();
+      ok = arrived(&bar->own, 0) && full1(0);
+    }
+    if (ok) {
+      scores(C::kColX, 0, 0, KEYS ? &bar->x[0] : nullptr, nullptr);
+      ok = arrived(&bar->ready, 0);
+      for (int i = 1; i < min(n, P1) && ok; ++i) load1();
     }
     // A place's next copy waits for the place's last product while another one runs.
     if constexpr (KEYS) {
-      if (ok && (ok = full1(0))) scores(C::kColX, 0, 0, &bar->x[0], nullptr);
       for (int i = 0; i < n && ok; ++i) {
         if (!(ok = full2(i))) break;
         scores(C::kColY, i, 1, &bar->y, nullptr);
         if (i > 0 && !(ok = more1(i - 1 + P1))) break;
         if (!(ok = arrived(&bar->p, i & 1))) break;
-        weighted(C::kColV, C::kColP, i, 1, &bar->empty2[i % P2]);
+        weighted(C::kColV, C::kColX, i, 1, &bar->empty2[i % P2]);
         if (i + 1 < n) {
-          if (!(ok = full1(i + 1) && arrived(&bar->x_read, i & 1))) break;
+          if (!(ok = full1(i + 1))) break;
           scores(C::kColX, i + 1, 0, &bar->x[0], nullptr);
         }
         if (!(ok = more2(i + P2))) break;
@@ -452,20 +476,20 @@ __global__ void __launch_bounds__(Cfg32<D, KEYS>::kThreads, 1) attn_grad_tc32_ke
       }
     } else {
       // the warpgroups' dS of tiles i and i - 1 lie over X of them; Y of tile i + 1 over that of tile i - 1
-      for (int i = -1; i < n && ok; ++i) {
+      if (ok && (ok = full2(0))) scores(C::kColY, 0, 1, &bar->x[0], &bar->empty2[0]);
+      if (ok) ok = more2(P2);
+      for (int i = 0; i < n && ok; ++i) {
         const uint32_t next = (i + 1) & 1;
         if (i + 1 < n) {
-          if (P1 == 2 && i > 0 && !(ok = more1(i - 1 + P1))) break;  // tile i + 1 itself
           if (!(ok = full1(i + 1))) break;
           scores(C::kColX + next * N, i + 1, 0, nullptr, nullptr);
-          if (P1 > 2 && i > 0 && !(ok = more1(i - 1 + P1))) break;
+          if (i > 0 && !(ok = more1(i - 1 + P1))) break;
           if (!(ok = full2(i + 1))) break;
           scores(C::kColY + next * N, i + 1, 1, &bar->x[next], &bar->empty2[(i + 1) % P2]);
         }
-        if (i >= 0) {
-          if (!(ok = arrived(&bar->ds[i & 1], (i >> 1) & 1))) break;
-          weighted(C::kColV + (i & 1) * D, C::kColX + (i & 1) * N, i, 0, &bar->empty1[i % P1]);
-        }
+        // the sums of the tile before are read
+        if (!(ok = arrived(&bar->ds[i & 1], (i >> 1) & 1) && (i == 0 || arrived(&bar->added, (i - 1) & 1)))) break;
+        weighted(C::kColV, C::kColX + (i & 1) * N, i, 0, &bar->empty1[i % P1]);
         if (i + 1 < n && !(ok = more2(i + 1 + P2))) break;
       }
     }
@@ -476,6 +500,7 @@ __global__ void __launch_bounds__(Cfg32<D, KEYS>::kThreads, 1) attn_grad_tc32_ke
     if (own) wait(&bar->own, 0);
     for (int i = max(0, loads1 - P1); i < loads1; ++i) wait(&bar->full1[i % P1], (i / P1) & 1);
     for (int i = max(0, loads2 - P2); i < loads2; ++i) wait(&bar->full2[i % P2], (i / P2) & 1);
+    for (int i = max(0, infos_in - 2); i < infos_in; ++i) wait(&bar->info[i & 1], (i >> 1) & 1);
     __syncwarp();
   } else if (warp < C::kMmaWarp) {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 224;");
@@ -502,14 +527,35 @@ __global__ void __launch_bounds__(Cfg32<D, KEYS>::kThreads, 1) attn_grad_tc32_ke
     float f1 = 0.f, f2 = 0.f, lse = -INFINITY, delta = 0.f;  // lse, delta: negative
     if (live && n > 0) {
       const int at = r & 63;
-      f1 = a.scale * (KEYS ? t.w.k_info[blk * kPast + at] : t.w.q_info[blk * (2 * kPast) + kPast + at]);
-      f2 = KEYS ? t.w.v_info[blk * kPast + at] : t.w.o_info[blk * (2 * kPast) + kPast + at];
-      if (!KEYS) lse = t.w.q_info[blk * (2 * kPast) + at], delta = t.w.o_info[blk * (2 * kPast) + at];
+      if (KEYS) {
+        const uint8_t* info = t.w.k_info + blk * kKInfo;
+        f1 = a.scale * factor_at(info, at), f2 = factor_at(info, kPast + at);
+      } else {
+        const uint8_t* info = t.w.q_info + blk * kQInfo;
+        f1 = a.scale * factor_at(info + 8 * kPast, at), f2 = factor_at(info + 8 * kPast, kPast + at);
+        lse = reinterpret_cast<const float*>(info)[at], delta = reinterpret_cast<const float*>(info)[kPast + at];
+      }
+    }
+    // this row of the second owned tile to TMEM: the hi's by one warpgroup, the lo's by the other
+    if (n > 0 && (ok = waited(&bar->own, 0))) {
+#pragma unroll
+      for (int s = 0; s < D / 64; ++s) {
+        const uint8_t* from = s2 + group * (C::kOwnBytes / 2) + s * (kTile * 128);
+        uint32_t w[32];
+#pragma unroll
+        for (int c = 0; c < 8; ++c) {
+          const uint4 x = *reinterpret_cast<const uint4*>(from + sw128(r, c * 8));
+          w[4 * c] = x.x, w[4 * c + 1] = x.y, w[4 * c + 2] = x.z, w[4 * c + 3] = x.w;
+        }
+        tmem_st32(mine + C::kColA + group * (D / 2) + s * 32, w);
+      }
+      tmem_wait_st();
+      arrive(&bar->ready);
     }
     const uint64_t f1p = pack2(f1, f1), f2p = pack2(f2, f2), l2e = pack2(kLog2e, kLog2e);
     const uint64_t lse2 = pack2(lse, lse), delta2 = pack2(delta, delta);
-    // P of this row from X: `ls` the log sums (dQ: lse2), `s` the columns' factors
-    auto weights = [&](uint32_t from, const float* s, const float* ls, int lim, bool cut, uint64_t (&x)[32]) {
+    // P of this row from X: ls the log sums (dQ: lse2), s the columns' factors
+    auto weights = [&](uint32_t from, const uint8_t* s, const float* ls, int lim, bool cut, uint64_t (&x)[32]) {
       {
         uint32_t v[2][32];
         tmem_ld32(from, v[0]);
@@ -521,13 +567,13 @@ __global__ void __launch_bounds__(Cfg32<D, KEYS>::kThreads, 1) attn_grad_tc32_ke
       }
       if (KEYS && group) arrive(&bar->x_read);
 #pragma unroll
-      for (int e = 0; e < 16; ++e) {
-        uint64_t s0, s1, l0 = lse2, l1 = lse2;
-        load_pairs(s + 4 * e, s0, s1);
-        if (KEYS) load_pairs(ls + 4 * e, l0, l1);
+      for (int e = 0; e < 8; ++e) {
+        uint64_t s4[4], l4[4] = {lse2, lse2, lse2, lse2};
+        load_factors(s + 16 * e, s4);
+        if (KEYS) load_pairs(ls + 8 * e, l4[0], l4[1]), load_pairs(ls + 8 * e + 4, l4[2], l4[3]);
         // the difference first: it is small where the weight is not
-        x[2 * e] = mul2(fma2(mul2(x[2 * e], f1p), s0, l0), l2e);
-        x[2 * e + 1] = mul2(fma2(mul2(x[2 * e + 1], f1p), s1, l1), l2e);
+#pragma unroll
+        for (int k = 0; k < 4; ++k) x[4 * e + k] = mul2(fma2(mul2(x[4 * e + k], f1p), s4[k], l4[k]), l2e);
       }
       if (cut) {
 #pragma unroll
@@ -547,33 +593,35 @@ __global__ void __launch_bounds__(Cfg32<D, KEYS>::kThreads, 1) attn_grad_tc32_ke
       }
     };
     // dS from P and Y, times the factors w of the rows that the sum runs over: s the columns' factors, ds their D (dQ: delta2)
-    auto differences = [&](uint32_t from, const float* s, const float* ds, const float* w, uint64_t (&x)[32]) {
+    auto differences = [&](uint32_t from, const uint8_t* s, const float* ds, const uint8_t* w, uint64_t (&x)[32]) {
 #pragma unroll
       for (int c = 0; c < 2; ++c) {
         uint32_t v[32];
         tmem_ld32(from + 32 * c, v);
         tmem_wait_ld();
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          uint64_t s2[2], d2[2] = {delta2, delta2}, w2[2];
-          load_pairs(s + 32 * c + 4 * e, s2[0], s2[1]);
-          if (KEYS) load_pairs(ds + 32 * c + 4 * e, d2[0], d2[1]);
-          load_pairs(w + 32 * c + 4 * e, w2[0], w2[1]);
+        for (int e = 0; e < 4; ++e) {
+          uint64_t s4[4], d4[4] = {delta2, delta2, delta2, delta2}, w4[4];
+          load_factors(s + 64 * c + 16 * e, s4);
+          load_factors(w + 64 * c + 16 * e, w4);
+          if (KEYS) load_pairs(ds + 32 * c + 8 * e, d4[0], d4[1]), load_pairs(ds + 32 * c + 8 * e + 4, d4[2], d4[3]);
 #pragma unroll
-          for (int k = 0; k < 2; ++k) {
-            const uint64_t y = mul2(pack2(__uint_as_float(v[4 * e + 2 * k]), __uint_as_float(v[4 * e + 2 * k + 1])), f2p);
-            uint64_t& to = x[16 * c + 2 * e + k];
-            to = mul2(mul2(to, fma2(y, s2[k], d2[k])), w2[k]);
+          for (int k = 0; k < 4; ++k) {
+            const uint64_t y = mul2(pack2(__uint_as_float(v[8 * e + 2 * k]), __uint_as_float(v[8 * e + 2 * k + 1])), f2p);
+            uint64_t& to = x[16 * c + 4 * e + k];
+            to = mul2(mul2(to, fma2(y, s4[k], d4[k])), w4[k]);
           }
         }
       }
     };
     float down = 0.f;  // of the tile whose sums come next
     if constexpr (KEYS) {
-      for (int i = 0; i < n; ++i) {
-        const int at = first + i % each * N;
-        const float* i1 = reinterpret_cast<const float*>(infos + i % P1 * C::kInfo);  // log sums, factors of Q
-        const float* i2 = reinterpret_cast<const float*>(infos + P1 * C::kInfo + i % P2 * C::kInfo2);  // D, factors of dO
+      for (int i = 0, past = 0; i < n; ++i) {
+        const int at = first + past * N;
+        if (++past == each) past = 0;
+        const uint8_t* info = infos + (i & 1) * C::kInfo;
+        const float* numbers = reinterpret_cast<const float*>(info);  // log sums, D
+        const uint8_t* factors = info + 8 * kPast;                   // of Q, of dO
         uint64_t x[32];
         // the sums of the tile before, while X (Y) of this one is formed
         if (i > 0) {
@@ -582,49 +630,48 @@ __global__ void __launch_bounds__(Cfg32<D, KEYS>::kThreads, 1) attn_grad_tc32_ke
             break;
           add_sums<D>(acc, mine + C::kColV + group * D, down);
         }
-        if (!(ok = waited(&bar->full1[i % P1], (i / P1) & 1) && waited(&bar->x[0], i & 1))) break;
+        if (!(ok = waited(&bar->info[i & 1], (i >> 1) & 1) && waited(&bar->x[0], i & 1))) break;
         // cut: some key is behind a query of these
-        weights(mine + C::kColX, i1 + N, i1, row - off - at, at + off < row0 + kTile - 1, x);
-        if (!(ok = waited(&bar->full2[i % P2], (i / P2) & 1))) break;
+        weights(mine + C::kColX, factors, numbers, row - off - at, at + off < row0 + kTile - 1, x);
         if (group) {
           if (!(ok = waited(&bar->y, i & 1))) break;
-          differences(mine + C::kColY, i2 + N, i2, i1 + N, x);
+          differences(mine + C::kColY, factors + 2 * kPast, numbers + kPast, factors, x);
         } else {
 #pragma unroll
-          for (int e = 0; e < 16; ++e) {
-            uint64_t s0, s1;
-            load_pairs(i2 + N + 4 * e, s0, s1);
-            x[2 * e] = mul2(x[2 * e], s0);
-            x[2 * e + 1] = mul2(x[2 * e + 1], s1);
+          for (int e = 0; e < 8; ++e) {
+            uint64_t s4[4];
+            load_factors(factors + 2 * kPast + 16 * e, s4);
+#pragma unroll
+            for (int k = 0; k < 4; ++k) x[4 * e + k] = mul2(x[4 * e + k], s4[k]);
           }
+          if (!(ok = waited(&bar->x_read, i & 1))) break;  // P lies over X, which the other warpgroup reads too
         }
         // the products that read P and dS of the tile before are done
-        down = store_weights(mine + (group ? C::kColY : C::kColP), x);
+        down = store_weights(mine + (group ? C::kColY : C::kColX), x);
         tmem_wait_st();
         arrive(group ? &bar->ds[0] : &bar->p);
       }
     } else {
       for (int i = group; i < n; i += 2) {
         const int at = i * N;
-        const float* i1 = reinterpret_cast<const float*>(infos + i % P1 * C::kInfo);  // factors of K, of V
+        const uint8_t* factors = infos + (i & 1) * C::kInfo;  // of K, of V
         const uint32_t tx = mine + C::kColX + group * N;
         uint64_t x[32];
-        if (i > 1) {  // the sums of this warpgroup's last tile
-          if (!(ok = waited(&bar->empty1[(i - 2) % P1], ((i - 2) / P1) & 1))) break;
-          add_sums<D>(acc, mine + C::kColV + group * D, down);
-        }
-        if (!(ok = waited(&bar->full1[i % P1], (i / P1) & 1) && waited(&bar->x[group], (i >> 1) & 1))) break;
-        weights(tx, i1, nullptr, min(row + off + 1, lk) - at, at + N > min(row0 + off + 1, lk), x);
-        differences(mine + C::kColY + group * N, i1 + N, nullptr, i1, x);
+        if (!(ok = waited(&bar->info[i & 1], (i >> 1) & 1) && waited(&bar->x[group], (i >> 1) & 1))) break;
+        weights(tx, factors, nullptr, min(row + off + 1, lk) - at, at + N > min(row0 + off + 1, lk), x);
+        differences(mine + C::kColY + group * N, factors + 2 * kPast, nullptr, factors, x);
         down = store_weights(tx, x);
         tmem_wait_st();
         arrive(&bar->ds[group]);
+        if (!(ok = waited(&bar->empty1[i % P1], (i / P1) & 1))) break;
+        add_sums<D>(acc, mine + C::kColV, down);
+        arrive(&bar->added);
       }
     }
     // the last tile's sums
     if (ok && n > 0) {
       ok = waited(&bar->drain, 0);
-      if (ok && (KEYS || n > group)) add_sums<D>(acc, mine + C::kColV + group * D, down);
+      if (KEYS && ok) add_sums<D>(acc, mine + C::kColV + group * D, down);
     }
     const int d = D == 64 ? a.d : D;  // of the rows
     // this thread's part of its row of a result, dims c0 to c0 + 2 M of it; which: dV (0), dK or dQ (1)
@@ -738,10 +785,9 @@ Operands operands(uint8_t* base, const PromptArgs& a, int D, size_t* bytes) {
     return p;
   };
   const int64_t nq = w.q_blocks * a.Hq, nk = w.k_blocks * a.Hkv;
-  const size_t image = static_cast<size_t>(kPast) * D * 4, row = kPast * sizeof(float);
+  const size_t image = static_cast<size_t>(kPast) * D * 4;
   w.q = part(nq, image), w.d_o = part(nq, image), w.k = part(nk, image), w.v = part(nk, image);
-  w.q_info = reinterpret_cast<float*>(part(nq, 2 * row)), w.o_info = reinterpret_cast<float*>(part(nq, 2 * row));
-  w.k_info = reinterpret_cast<float*>(part(nk, row)), w.v_info = reinterpret_cast<float*>(part(nk, row));
+  w.q_info = part(nq, kQInfo), w.k_info = part(nk, kKInfo);
   *bytes = at;
   return w;
 }

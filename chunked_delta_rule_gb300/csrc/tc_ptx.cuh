@@ -61,7 +61,7 @@ __device__ __forceinline__ bool mbar_wait(uint64_t* bar, uint32_t parity,
 __device__ __forceinline__ bool mbar_wait_sleep(uint64_t* bar, uint32_t parity,
                                                 uint64_t limit_ns = kWaitLimitNs) {
   if (mbar_try_wait(bar, parity)) return true;
-  const uint64_t t0 = globaltimer();
+  uint64_t t0 = 0;  // read after the first sleep: no wait of a healthy kernel is as long
   for (;;) {
     uint32_t ok;
     asm volatile(
@@ -72,7 +72,9 @@ __device__ __forceinline__ bool mbar_wait_sleep(uint64_t* bar, uint32_t parity,
         : "r"(smem_u32(bar)), "r"(parity), "r"(2000u)
         : "memory");
     if (ok) return true;
-    if (globaltimer() - t0 > limit_ns) return false;
+    const uint64_t now = globaltimer();
+    if (t0 == 0) t0 = now;
+    else if (now - t0 > limit_ns) return false;
   }
 }
 

@@ -13,21 +13,19 @@
 // the operand tiles in shared memory, and forms D.  Two kernels from one template do the products, so
 // that every sum has one owner and one order.  A CTA owns 128 rows: of K and V (dK and dV; X = K Q^T,
 // Y = V dO^T, the queries of all heads of the group come past, 64 at a time) or of Q and dO (dQ;
-// X = Q K^T, Y = dO V^T, the keys come past).  A thread holds a row of a tile.  P and dS are split like the
-// operands, a power of two for every row of a tile, after the factors of the rows that the sum
-// runs over have been multiplied in; so no range of P or dS is out of reach.
-// dK and dV: one warpgroup forms P and holds dV, the other forms P again, then dS, and holds dK.
-//   tensor cores: ... X(i) dK(i - 1) Y(i) dV(i) X(i + 1) ...
+// X = Q K^T, Y = dO V^T, the keys come past).  Two lanes of a warp hold a row of a tile, 32
+// columns each.  P and dS are split like the operands, a power of two for every row of a
+// tile, after the factors of the rows that the sum runs over have been multiplied in: no range
+// of P or dS is out of reach.
+//   dK and dV: ... X(i) dK(i - 1) Y(i) dV(i) X(i + 1) ...
+//   dQ:        ... X(i + 1) Y(i + 1) dQ(i) X(i + 2) ...
 // (X's owned operand lies in shared memory, Y's in TMEM, which gives the ring its room.)
-// dQ: the warpgroups take the tiles in turn, each with sums of its own.
 //
 // Masked scores are set to -inf after the product.  A masked weight is 0, but 0
 // times an infinite or NaN value of a row that the owner does not see would spoil
 // it: a row of a result that is not finite is computed again from the definition.
 
 #include <cuda_fp16.h>
-
-#include <type_traits>
 
 #include "attn_grad.cuh"
 #include "attn_tc.cuh"
@@ -168,7 +166,7 @@ __global__ void __launch_bounds__(256) attn_grad_split_kernel(GradArgs g, Operan
 // ---------------------------------------------------------------- products
 template <int D, bool KEYS>
 struct Cfg32 {
-  static constexpr int kWarps = 8;  // two warpgroups, a row of a tile a thread
+  static constexpr int kWarps = 8;  // of softmax threads
   // one more warp copies the tiles and issues the products; its warpgroup gives its registers to the others
   static constexpr int kMmaWarp = kWarps, kThreads = 32 * kWarps + 128;
   static constexpr int kOwnBytes = kTile * D * 4, kTileBytes = kPast * D * 4;
@@ -183,7 +181,7 @@ struct Cfg32 {
   static constexpr int kSmem = kOwnBytes + kRing + 2 * kInfo + 1024 + 256;
 };
 struct Bars32 {
-  uint64_t own, ready, full1[4], empty1[4], full2[4], empty2[4], info[2], x[2], x_read, y, p, ds[2], added, drain, stall;
+  uint64_t own, ready, full1[4], empty1[4], full2[4], empty2[4], info[2], x[2], y, p, ds, drain, stall;
   uint32_t tmem, failed;
 };
 static_assert(sizeof(Bars32) <= 256 && Cfg32<128, true>::kSmem <= 227 * 1024 && Cfg32<128, false>::kSmem <= 227 * 1024 &&
@@ -204,6 +202,27 @@ struct Tc32Args {
 __host__ __device__ constexpr uint32_t idesc_f16(int M, int N, bool b_mn = false) {
   return idesc_bf16(M, N, false, b_mn) & ~((1u << 7) | (1u << 10));
 }
+// A warp's 16 rows, two lanes a row: lane t < 16 holds columns c to c + 31 (or 15) of row t, lane t + 16 those OFF later.
+template <int OFF>
+__device__ __forceinline__ void tmem_ld_rows16(uint32_t taddr, uint32_t (&r)[32]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.16x32bx2.x32.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
+      "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32], %33;"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]), "=r"(r[17]),
+        "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]), "=r"(r[25]), "=r"(r[26]),
+        "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+      : "r"(taddr), "n"(OFF)
+      : "memory");
+}
+__device__ __forceinline__ void tmem_st_rows16(uint32_t taddr, const uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.16x32bx2.x16.b32 [%0], 16, {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, "
+      "%15, %16};" ::"r"(taddr),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
+      "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+      : "memory");
+}
 // two pairs of a row of numbers, the same for every thread; four pairs of a row of factors
 __device__ __forceinline__ void load_pairs(const float* p, uint64_t& a, uint64_t& b) {
   const float4 v = *reinterpret_cast<const float4*>(p);
@@ -215,44 +234,38 @@ __device__ __forceinline__ void load_factors(const uint8_t* p, uint64_t (&f)[4])
 #pragma unroll
   for (int i = 0; i < 4; ++i) f[i] = pack2(__uint_as_float(w[i] << 16), __uint_as_float(w[i] & 0xFFFF0000u));
 }
-// A thread's row of a tile of P or dS to TMEM: its own power of two, hi's in 32 columns, lo's in the next 32.  Returns the
+// Rows of a tile of P or dS to TMEM: each with its own power of two, hi's in 32 columns, lo's in the next 32.  Returns the
 // factor that undoes the power.
-__device__ __forceinline__ float store_weights(uint32_t to, uint64_t (&x)[32]) {
+__device__ __forceinline__ float store_weights(uint32_t to, const uint64_t (&x)[16]) {
   float m = 0.f;
 #pragma unroll
-  for (int e = 0; e < 32; ++e) {
+  for (int e = 0; e < 16; ++e) {
     float a, b;
     unpack2(x[e], a, b);
     m = max3(m, fabsf(a), fabsf(b));
   }
+  m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 16));
   float up, down;
   row_factors(m, up, down);
   const uint64_t up2 = pack2(up, up);
+  uint32_t hi[16], lo[16];
 #pragma unroll
-  for (int c = 0; c < 2; ++c) {
-    uint32_t hi[16], lo[16];
-#pragma unroll
-    for (int e = 0; e < 16; ++e) split2(mul2(x[16 * c + e], up2), hi[e], lo[e]);
-    tmem_st16(to + 16 * c, hi);
-    tmem_st16(to + 32 + 16 * c, lo);
-  }
+  for (int e = 0; e < 16; ++e) split2(mul2(x[e], up2), hi[e], lo[e]);
+  tmem_st_rows16(to, hi);
+  tmem_st_rows16(to + 32, lo);
   return down;
 }
-// acc += f times a thread's row of a tile's sums
+// acc += f times this lane's half of a row of a tile's sums
 template <int D>
-__device__ __forceinline__ void add_sums(uint64_t (&acc)[D / 2], uint32_t from, float f) {
+__device__ __forceinline__ void add_sums(uint64_t (&acc)[D / 4], uint32_t from, float f) {
   const uint64_t f2 = pack2(f, f);
+  uint32_t v[D / 64][32];
 #pragma unroll
-  for (int c = 0; c < D / 64; ++c) {
-    uint32_t v[2][32];
-    tmem_ld32(from + 64 * c, v[0]);
-    tmem_ld32(from + 64 * c + 32, v[1]);
-    tmem_wait_ld();
+  for (int c = 0; c < D / 64; ++c) tmem_ld_rows16<D / 2>(from + 32 * c, v[c]);
+  tmem_wait_ld();
 #pragma unroll
-    for (int e = 0; e < 32; ++e)
-      acc[32 * c + e] = fma2(pack2(__uint_as_float(v[e >> 4][(2 * e) & 31]), __uint_as_float(v[e >> 4][(2 * e + 1) & 31])), f2,
-                             acc[32 * c + e]);
-  }
+  for (int e = 0; e < D / 4; ++e)
+    acc[e] = fma2(pack2(__uint_as_float(v[e >> 4][(2 * e) & 31]), __uint_as_float(v[e >> 4][(2 * e + 1) & 31])), f2, acc[e]);
 }
 
 template <int D, bool KEYS>
@@ -277,7 +290,6 @@ __global__ void __launch_bounds__(Cfg32<D, KEYS>::kThreads, 1) attn_grad_tc32_ke
     mbar_init(&bar->ready, C::kWarps);
     mbar_init(&bar->info[0], 1);
     mbar_init(&bar->info[1], 1);
-    mbar_init(&bar->added, 4);
     for (int i = 0; i < 4; ++i) {
       mbar_init(&bar->full1[i], 1);
       mbar_init(&bar->empty1[i], 1);
@@ -286,11 +298,9 @@ __global__ void __launch_bounds__(Cfg32<D, KEYS>::kThreads, 1) attn_grad_tc32_ke
     }
     mbar_init(&bar->x[0], 1);
     mbar_init(&bar->x[1], 1);
-    mbar_init(&bar->x_read, 4);
     mbar_init(&bar->y, 1);
-    mbar_init(&bar->p, 4);
-    mbar_init(&bar->ds[0], 4);
-    mbar_init(&bar->ds[1], 4);
+    mbar_init(&bar->p, C::kWarps);
+    mbar_init(&bar->ds, C::kWarps);
     mbar_init(&bar->drain, 1);
     mbar_init(&bar->stall, 1);
     bar->failed = 0;
@@ -471,11 +481,11 @@ __global__ void __launch_bounds__(Cfg32<D, KEYS>::kThreads, 1) attn_grad_tc32_ke
           scores(C::kColX, i + 1, 0, &bar->x[0], nullptr);
         }
         if (!(ok = more2(i + P2))) break;
-        if (!(ok = arrived(&bar->ds[0], i & 1))) break;
+        if (!(ok = arrived(&bar->ds, i & 1))) break;
         weighted(C::kColV + D, C::kColY, i, 0, &bar->empty1[i % P1]);
       }
     } else {
-      // the warpgroups' dS of tiles i and i - 1 lie over X of them; Y of tile i + 1 over that of tile i - 1
+      // dS of tiles i and i - 1 lie over X of them; Y of tile i + 1 over that of tile i - 1
       if (ok && (ok = full2(0))) scores(C::kColY, 0, 1, &bar->x[0], &bar->empty2[0]);
       if (ok) ok = more2(P2);
       for (int i = 0; i < n && ok; ++i) {
@@ -487,8 +497,7 @@ __global__ void __launch_bounds__(Cfg32<D, KEYS>::kThreads, 1) attn_grad_tc32_ke
           if (!(ok = full2(i + 1))) break;
           scores(C::kColY + next * N, i + 1, 1, &bar->x[next], &bar->empty2[(i + 1) % P2]);
         }
-        // the sums of the tile before are read
-        if (!(ok = arrived(&bar->ds[i & 1], (i >> 1) & 1) && (i == 0 || arrived(&bar->added, (i - 1) & 1)))) break;
+        if (!(ok = arrived(&bar->ds, i & 1))) break;
         weighted(C::kColV, C::kColX + (i & 1) * N, i, 0, &bar->empty1[i % P1]);
         if (i + 1 < n && !(ok = more2(i + 1 + P2))) break;
       }
@@ -504,8 +513,9 @@ __global__ void __launch_bounds__(Cfg32<D, KEYS>::kThreads, 1) attn_grad_tc32_ke
     __syncwarp();
   } else if (warp < C::kMmaWarp) {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 224;");
-    const int group = warp >> 2, quad = warp & 3, r = quad * 32 + lane;
-    const uint32_t mine = tmem + (static_cast<uint32_t>(quad * 32) << 16);
+    // A warp takes 16 rows, two lanes a row: 32 of a tile's columns each, half of the dims of the row's sums each.
+    const int group = warp >> 2, quad = warp & 3, r = quad * 32 + group * 16 + (lane & 15), half = lane >> 4;
+    const uint32_t mine = tmem + (static_cast<uint32_t>(quad * 32 + group * 16) << 16);
     const int row = row0 + r;
     auto arrive = [&](uint64_t* m) {
       tc_fence_before();
@@ -518,9 +528,9 @@ __global__ void __launch_bounds__(Cfg32<D, KEYS>::kThreads, 1) attn_grad_tc32_ke
       return ok;
     };
     bool ok = true;
-    uint64_t acc[D / 2];
+    uint64_t acc[D / 4], acc_v[KEYS ? D / 4 : 1];  // dK or dQ; dV
 #pragma unroll
-    for (int e = 0; e < D / 2; ++e) acc[e] = 0;
+    for (int e = 0; e < D / 4; ++e) acc[e] = acc_v[KEYS ? e : 0] = 0;
     // this row's factors; of rows past the sequence anything
     const int64_t blk = own_block + (r >> 6);
     const bool live = row < rows;
@@ -536,7 +546,7 @@ __global__ void __launch_bounds__(Cfg32<D, KEYS>::kThreads, 1) attn_grad_tc32_ke
         lse = reinterpret_cast<const float*>(info)[at], delta = reinterpret_cast<const float*>(info)[kPast + at];
       }
     }
-    // this row of the second owned tile to TMEM: the hi's by one warpgroup, the lo's by the other
+    // the second owned tile to TMEM, a row a thread: the hi's by one warpgroup, the lo's by the other
     if (n > 0 && (ok = waited(&bar->own, 0))) {
 #pragma unroll
       for (int s = 0; s < D / 64; ++s) {
@@ -544,40 +554,40 @@ __global__ void __launch_bounds__(Cfg32<D, KEYS>::kThreads, 1) attn_grad_tc32_ke
         uint32_t w[32];
 #pragma unroll
         for (int c = 0; c < 8; ++c) {
-          const uint4 x = *reinterpret_cast<const uint4*>(from + sw128(r, c * 8));
+          const uint4 x = *reinterpret_cast<const uint4*>(from + sw128(quad * 32 + lane, c * 8));
           w[4 * c] = x.x, w[4 * c + 1] = x.y, w[4 * c + 2] = x.z, w[4 * c + 3] = x.w;
         }
-        tmem_st32(mine + C::kColA + group * (D / 2) + s * 32, w);
+        tmem_st32(tmem + (static_cast<uint32_t>(quad * 32) << 16) + C::kColA + group * (D / 2) + s * 32, w);
       }
       tmem_wait_st();
       arrive(&bar->ready);
     }
     const uint64_t f1p = pack2(f1, f1), f2p = pack2(f2, f2), l2e = pack2(kLog2e, kLog2e);
     const uint64_t lse2 = pack2(lse, lse), delta2 = pack2(delta, delta);
-    // P of this row from X: ls the log sums (dQ: lse2), s the columns' factors
-    auto weights = [&](uint32_t from, const uint8_t* s, const float* ls, int lim, bool cut, uint64_t (&x)[32]) {
-      {
-        uint32_t v[2][32];
-        tmem_ld32(from, v[0]);
-        tmem_ld32(from + 32, v[1]);
-        tmem_wait_ld();
+    // P from X: ls the log sums (dQ: lse2), s the columns' factors
+    auto weights = [&](uint32_t from, const uint8_t* s, const float* ls, int lim, bool cut, uint64_t (&x)[16]) {
+      uint32_t v[32];
+      tmem_ld_rows16<32>(from, v);
+      tmem_wait_ld();
 #pragma unroll
-        for (int e = 0; e < 32; ++e)
-          x[e] = pack2(__uint_as_float(v[e >> 4][(2 * e) & 31]), __uint_as_float(v[e >> 4][(2 * e + 1) & 31]));
-      }
-      if (KEYS && group) arrive(&bar->x_read);
-#pragma unroll
-      for (int e = 0; e < 8; ++e) {
+      for (int e = 0; e < 4; ++e) {
         uint64_t s4[4], l4[4] = {lse2, lse2, lse2, lse2};
-        load_factors(s + 16 * e, s4);
-        if (KEYS) load_pairs(ls + 8 * e, l4[0], l4[1]), load_pairs(ls + 8 * e + 4, l4[2], l4[3]);
+        load_factors(s + half * 64 + 16 * e, s4);
+        if (KEYS) {
+          load_pairs(ls + half * 32 + 8 * e, l4[0], l4[1]);
+          load_pairs(ls + half * 32 + 8 * e + 4, l4[2], l4[3]);
+        }
         // the difference first: it is small where the weight is not
 #pragma unroll
-        for (int k = 0; k < 4; ++k) x[4 * e + k] = mul2(fma2(mul2(x[4 * e + k], f1p), s4[k], l4[k]), l2e);
+        for (int k = 0; k < 4; ++k) {
+          const uint64_t y = mul2(pack2(__uint_as_float(v[8 * e + 2 * k]), __uint_as_float(v[8 * e + 2 * k + 1])), f1p);
+          x[4 * e + k] = mul2(fma2(y, s4[k], l4[k]), l2e);
+        }
       }
       if (cut) {
+        lim -= half * 32;
 #pragma unroll
-        for (int e = 0; e < 32; ++e) {
+        for (int e = 0; e < 16; ++e) {
           float z0, z1;
           unpack2(x[e], z0, z1);
           if (KEYS ? 2 * e < lim : 2 * e >= lim) z0 = -INFINITY;
@@ -586,107 +596,102 @@ __global__ void __launch_bounds__(Cfg32<D, KEYS>::kThreads, 1) attn_grad_tc32_ke
         }
       }
 #pragma unroll
-      for (int e = 0; e < 32; ++e) {
+      for (int e = 0; e < 16; ++e) {
         float z0, z1;
         unpack2(x[e], z0, z1);
         x[e] = pack2(ex2(z0), ex2(z1));
       }
     };
     // dS from P and Y, times the factors w of the rows that the sum runs over: s the columns' factors, ds their D (dQ: delta2)
-    auto differences = [&](uint32_t from, const uint8_t* s, const float* ds, const uint8_t* w, uint64_t (&x)[32]) {
+    auto differences = [&](uint32_t from, const uint8_t* s, const float* ds, const uint8_t* w, uint64_t (&x)[16]) {
+      uint32_t v[32];
+      tmem_ld_rows16<32>(from, v);
+      tmem_wait_ld();
 #pragma unroll
-      for (int c = 0; c < 2; ++c) {
-        uint32_t v[32];
-        tmem_ld32(from + 32 * c, v);
-        tmem_wait_ld();
+      for (int e = 0; e < 4; ++e) {
+        uint64_t s4[4], d4[4] = {delta2, delta2, delta2, delta2}, w4[4];
+        load_factors(s + half * 64 + 16 * e, s4);
+        load_factors(w + half * 64 + 16 * e, w4);
+        if (KEYS) {
+          load_pairs(ds + half * 32 + 8 * e, d4[0], d4[1]);
+          load_pairs(ds + half * 32 + 8 * e + 4, d4[2], d4[3]);
+        }
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          uint64_t s4[4], d4[4] = {delta2, delta2, delta2, delta2}, w4[4];
-          load_factors(s + 64 * c + 16 * e, s4);
-          load_factors(w + 64 * c + 16 * e, w4);
-          if (KEYS) load_pairs(ds + 32 * c + 8 * e, d4[0], d4[1]), load_pairs(ds + 32 * c + 8 * e + 4, d4[2], d4[3]);
-#pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            const uint64_t y = mul2(pack2(__uint_as_float(v[8 * e + 2 * k]), __uint_as_float(v[8 * e + 2 * k + 1])), f2p);
-            uint64_t& to = x[16 * c + 4 * e + k];
-            to = mul2(mul2(to, fma2(y, s4[k], d4[k])), w4[k]);
-          }
+        for (int k = 0; k < 4; ++k) {
+          const uint64_t y = mul2(pack2(__uint_as_float(v[8 * e + 2 * k]), __uint_as_float(v[8 * e + 2 * k + 1])), f2p);
+          x[4 * e + k] = mul2(mul2(x[4 * e + k], fma2(y, s4[k], d4[k])), w4[k]);
         }
       }
     };
-    float down = 0.f;  // of the tile whose sums come next
-    if constexpr (KEYS) {
-      for (int i = 0, past = 0; i < n; ++i) {
-        const int at = first + past * N;
-        if (++past == each) past = 0;
-        const uint8_t* info = infos + (i & 1) * C::kInfo;
+    float down = 0.f, down_v = 0.f;  // of the tile whose sums come next
+    for (int i = 0, past = 0; i < n; ++i) {
+      const int at = first + past * N;
+      if (KEYS && ++past == each) past = 0;
+      if (!KEYS) past = i + 1;
+      const uint8_t* info = infos + (i & 1) * C::kInfo;
+      uint64_t x[16];
+      if constexpr (KEYS) {
         const float* numbers = reinterpret_cast<const float*>(info);  // log sums, D
         const uint8_t* factors = info + 8 * kPast;                   // of Q, of dO
-        uint64_t x[32];
-        // the sums of the tile before, while X (Y) of this one is formed
+        // the sums of the tile before, while X and Y of this one are formed
         if (i > 0) {
-          if (!(ok = group ? waited(&bar->empty1[(i - 1) % P1], ((i - 1) / P1) & 1)
-                           : waited(&bar->empty2[(i - 1) % P2], ((i - 1) / P2) & 1)))
-            break;
-          add_sums<D>(acc, mine + C::kColV + group * D, down);
+          if (!(ok = waited(&bar->empty2[(i - 1) % P2], ((i - 1) / P2) & 1))) break;
+          add_sums<D>(acc_v, mine + C::kColV, down_v);
         }
         if (!(ok = waited(&bar->info[i & 1], (i >> 1) & 1) && waited(&bar->x[0], i & 1))) break;
         // cut: some key is behind a query of these
         weights(mine + C::kColX, factors, numbers, row - off - at, at + off < row0 + kTile - 1, x);
-        if (group) {
-          if (!(ok = waited(&bar->y, i & 1))) break;
-          differences(mine + C::kColY, factors + 2 * kPast, numbers + kPast, factors, x);
-        } else {
+        uint64_t z[16];
 #pragma unroll
-          for (int e = 0; e < 8; ++e) {
-            uint64_t s4[4];
-            load_factors(factors + 2 * kPast + 16 * e, s4);
+        for (int e = 0; e < 4; ++e) {
+          uint64_t s4[4];
+          load_factors(factors + 2 * kPast + half * 64 + 16 * e, s4);
 #pragma unroll
-            for (int k = 0; k < 4; ++k) x[4 * e + k] = mul2(x[4 * e + k], s4[k]);
-          }
-          if (!(ok = waited(&bar->x_read, i & 1))) break;  // P lies over X, which the other warpgroup reads too
+          for (int k = 0; k < 4; ++k) z[4 * e + k] = mul2(x[4 * e + k], s4[k]);
         }
-        // the products that read P and dS of the tile before are done
-        down = store_weights(mine + (group ? C::kColY : C::kColX), x);
+        down_v = store_weights(mine + C::kColX, z);
         tmem_wait_st();
-        arrive(group ? &bar->ds[0] : &bar->p);
-      }
-    } else {
-      for (int i = group; i < n; i += 2) {
-        const int at = i * N;
-        const uint8_t* factors = infos + (i & 1) * C::kInfo;  // of K, of V
-        const uint32_t tx = mine + C::kColX + group * N;
-        uint64_t x[32];
-        if (!(ok = waited(&bar->info[i & 1], (i >> 1) & 1) && waited(&bar->x[group], (i >> 1) & 1))) break;
-        weights(tx, factors, nullptr, min(row + off + 1, lk) - at, at + N > min(row0 + off + 1, lk), x);
-        differences(mine + C::kColY + group * N, factors + 2 * kPast, nullptr, factors, x);
+        arrive(&bar->p);
+        if (i > 0) {
+          if (!(ok = waited(&bar->empty1[(i - 1) % P1], ((i - 1) / P1) & 1))) break;
+          add_sums<D>(acc, mine + C::kColV + D, down);
+        }
+        if (!(ok = waited(&bar->y, i & 1))) break;
+        differences(mine + C::kColY, factors + 2 * kPast, numbers + kPast, factors, x);
+        down = store_weights(mine + C::kColY, x);
+      } else {
+        const uint32_t tx = mine + C::kColX + (i & 1) * N;
+        if (!(ok = waited(&bar->info[i & 1], (i >> 1) & 1) && waited(&bar->x[i & 1], (i >> 1) & 1))) break;
+        weights(tx, info, nullptr, min(row + off + 1, lk) - at, at + N > min(row0 + off + 1, lk), x);  // info: factors of K, of V
+        differences(mine + C::kColY + (i & 1) * N, info + 2 * kPast, nullptr, info, x);
+        const float was = down;
         down = store_weights(tx, x);
-        tmem_wait_st();
-        arrive(&bar->ds[group]);
-        if (!(ok = waited(&bar->empty1[i % P1], (i / P1) & 1))) break;
-        add_sums<D>(acc, mine + C::kColV, down);
-        arrive(&bar->added);
+        if (i > 0) {  // the sums of the tile before
+          if (!(ok = waited(&bar->empty1[(i - 1) % P1], ((i - 1) / P1) & 1))) break;
+          add_sums<D>(acc, mine + C::kColV, was);
+        }
       }
+      tmem_wait_st();
+      arrive(&bar->ds);
     }
     // the last tile's sums
-    if (ok && n > 0) {
-      ok = waited(&bar->drain, 0);
-      if (KEYS && ok) add_sums<D>(acc, mine + C::kColV + group * D, down);
+    if (ok && n > 0 && (ok = waited(&bar->drain, 0))) {
+      if constexpr (KEYS) add_sums<D>(acc_v, mine + C::kColV, down_v);
+      add_sums<D>(acc, mine + C::kColV + (KEYS ? D : 0), down);
     }
     const int d = D == 64 ? a.d : D;  // of the rows
-    // this thread's part of its row of a result, dims c0 to c0 + 2 M of it; which: dV (0), dK or dQ (1)
-    auto finish = [&](const auto& z, auto pairs, int c0, int which) {
-      constexpr int M = decltype(pairs)::value;
+    // this lane's half of its row of a result; which: dV (0), dK or dQ (1)
+    auto finish = [&](const uint64_t (&z)[D / 4], int which) {
       const RowsOut& to = KEYS ? (which ? g.dk : g.dv) : g.dq;
       float* out = static_cast<float*>(to.p) + ((KEYS ? k0 : q0) + row0) * to.stride + static_cast<int64_t>(head) * d;
       const float f = which ? a.scale : 1.f;
       const uint64_t fp = pack2(f, f);
       uint64_t rest = 0;  // z * 0 added up: NaN where some z is not finite
 #pragma unroll
-      for (int e = 0; e < M / 2; ++e) {
+      for (int e = 0; e < D / 8; ++e) {
         const uint64_t z0 = mul2(z[2 * e], fp), z1 = mul2(z[2 * e + 1], fp);
         rest = fma2(z0, 0, fma2(z1, 0, rest));
-        const int c = c0 + 4 * e;
+        const int c = half * (D / 2) + 4 * e;
         if (!live || c >= d) continue;
         float4 v;
         unpack2(z0, v.x, v.y);
@@ -699,7 +704,7 @@ __global__ void __launch_bounds__(Cfg32<D, KEYS>::kThreads, 1) attn_grad_tc32_ke
       unpack2(rest, ra, rb);
       __syncwarp();
       for (uint32_t again = __ballot_sync(0xffffffffu, live && !(ra + rb == 0.f)); again; again &= again - 1) {
-        const int i = row0 + quad * 32 + __ffs(again) - 1;
+        const int from = __ffs(again) - 1, i = row0 + quad * 32 + group * 16 + (from & 15);
         float x1[4], x2[4];
         const float *q = static_cast<const float*>(a.q.p), *d_o = static_cast<const float*>(g.d_o.p);
         const float *k = static_cast<const float*>(a.k.p), *v = static_cast<const float*>(a.v.p);
@@ -719,33 +724,13 @@ __global__ void __launch_bounds__(Cfg32<D, KEYS>::kThreads, 1) attn_grad_tc32_ke
 #pragma unroll
         for (int m = 0; m < D / 32; ++m) {
           const int c = m * 32 + lane;
-          if (m * 32 >= c0 && m * 32 < c0 + 2 * M && c < d) out[(i - row0) * to.stride + c] = KEYS && !which ? x2[m] : x1[m];
+          if (m / (D / 64) == from >> 4 && c < d) out[(i - row0) * to.stride + c] = KEYS && !which ? x2[m] : x1[m];
         }
       }
     };
-    if constexpr (KEYS) {
-      if (__all_sync(0xffffffffu, ok)) finish(acc, std::integral_constant<int, D / 2>{}, 0, group);
-    } else {
-      // each warpgroup gives the other its sums of half of the dims, through the owned tiles' place (every product is
-      // done), 16-byte pieces swizzled by row
-      uint8_t *theirs = smem + (1 - group) * (kTile * D * 2) + r * (D * 2), *ours = smem + group * (kTile * D * 2) + r * (D * 2);
-#pragma unroll
-      for (int e = 0; e < D / 8; ++e) {
-        const uint64_t z0 = group ? acc[2 * e] : acc[D / 4 + 2 * e], z1 = group ? acc[2 * e + 1] : acc[D / 4 + 2 * e + 1];
-        *reinterpret_cast<ulonglong2*>(theirs + ((e ^ (r & 7)) << 4)) = make_ulonglong2(z0, z1);
-      }
-      named_bar(1, 32 * C::kWarps);
-      if (*static_cast<volatile uint32_t*>(&bar->failed) == 0) {
-        uint64_t z[D / 4];
-#pragma unroll
-        for (int e = 0; e < D / 8; ++e) {
-          const ulonglong2 y = *reinterpret_cast<const ulonglong2*>(ours + ((e ^ (r & 7)) << 4));
-          const uint64_t z0 = group ? acc[D / 4 + 2 * e] : acc[2 * e], z1 = group ? acc[D / 4 + 2 * e + 1] : acc[2 * e + 1];
-          z[2 * e] = add2(z0, y.x);
-          z[2 * e + 1] = add2(z1, y.y);
-        }
-        finish(z, std::integral_constant<int, D / 4>{}, group * (D / 2), 1);
-      }
+    if (ok) {  // the same in all lanes
+      if constexpr (KEYS) finish(acc_v, 0);
+      finish(acc, 1);
     }
     tc_fence_before();
   }

@@ -3,7 +3,10 @@
 // warp, straight from the definition.
 #pragma once
 
+#include <cmath>
+
 #include "attn_row.cuh"
+#include "tc_util.cuh"
 
 namespace falcon {
 
@@ -50,6 +53,13 @@ inline cudaLaunchAttribute overlap_attribute() {
   cudaLaunchAttribute a;
   a.id = cudaLaunchAttributeProgrammaticStreamSerialization;
   a.val.programmaticStreamSerializationAllowed = 1;
+  return a;
+}
+inline cudaLaunchAttribute cluster_attribute(int ctas) {
+  cudaLaunchAttribute a;
+  a.id = cudaLaunchAttributeClusterDimension;
+  a.val.clusterDim.x = static_cast<unsigned>(ctas);
+  a.val.clusterDim.y = a.val.clusterDim.z = 1;
   return a;
 }
 // packed_block by a whole warp: 32 sequences a look
@@ -189,6 +199,90 @@ __device__ __forceinline__ void store_row(T* out, const float (&x)[4], int d) {
 #pragma unroll
   for (int j = 0; j < (D + 31) / 32; ++j)
     if (lane + 32 * j < d) out[lane + 32 * j] = from_f32<T>(x[j]);
+}
+
+// ---------------------------------------------------------------- a block's dK and dV by a cluster of CTAs
+// Clusters until the longest CTA (the keys that every query of all heads sees) takes no longer than all tiles of N queries
+// of both kernels dealt out evenly over `slots` CTAs, sequences taken as of one length; a tile of dQ costs some 0.7 of
+// one of dK and dV.
+inline int keys_split(const PromptArgs& a, int N, int slots) {
+  const double lq = static_cast<double>(a.tokens) / a.B, lk = static_cast<double>(a.k_tokens) / a.B;
+  const double longest = std::ceil(lq / N) * (a.Hq / a.Hkv);
+  const double seen = lk >= lq ? 1.0 - 0.5 * lq / lk : 0.5 * lk / lq;  // of all pairs
+  const double even = 1.7 * longest * seen * std::ceil(lk / kSumRows) * a.B * a.Hkv / slots;
+  int split = 1;
+  while (split < 8 && longest > even * split && longest >= 8 * split) split *= 2;
+  return split;
+}
+// every thread of the cluster's CTAs
+__device__ __forceinline__ void cluster_barrier() {
+  asm volatile("barrier.cluster.arrive.release;\n\tbarrier.cluster.wait.acquire;" ::: "memory");
+}
+__device__ __forceinline__ uint32_t peer_smem(uint32_t addr, uint32_t rank) {
+  uint32_t r;
+  asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(addr), "r"(rank));
+  return r;
+}
+__device__ __forceinline__ float4 load_peer4(uint32_t addr) {
+  float4 v;
+  asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+               : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+               : "r"(addr)
+               : "memory");
+  return v;
+}
+__device__ __forceinline__ uint32_t load_peer(uint32_t addr) {
+  uint32_t v;
+  asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(addr) : "memory");
+  return v;
+}
+// The sums of a block of 128 keys from the cluster's CTAs, which each left theirs in fp32 at `smem`: rows of dV, then of dK,
+// D numbers each, 16-byte pieces swizzled by row.  Added in the CTAs' order, an equal share of the rows by each CTA;
+// by `threads` threads, all others of the CTA pass two cluster barriers meanwhile.  again(i, dk, dv): row i from the
+// definition.
+template <typename T, int D, int THREADS, typename F>
+__device__ __forceinline__ void cluster_sums(const GradArgs& g, const uint8_t* smem, const uint32_t* failed,
+                                             uint32_t (&bad)[2][4], int split, int rank, int row0, int rows, int64_t k0,
+                                             int head, int d, F again) {
+  const int tid = threadIdx.x;
+  cluster_barrier();
+  bool fine = true;
+  for (int s = 0; s < split; ++s) fine = fine && load_peer(peer_smem(tc::smem_u32(failed), s)) == 0;
+  if (fine) {
+    const int share = kSumRows / split, rs = rank * share;
+    for (int x = tid; x < 2 * share * (D / 4); x += THREADS) {
+      const int c = x % (D / 4), rr = rs + x / (D / 4) % share, out = x / (D / 4) / share;  // out: dV, dK
+      if (row0 + rr >= rows || 4 * c >= d) continue;
+      const uint32_t at = tc::smem_u32(smem) + out * (kSumRows * D * 4) + rr * (D * 4) + ((c ^ (rr & 7)) << 4);
+      float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
+      for (int s = 0; s < split; ++s) {
+        const float4 y = load_peer4(peer_smem(at, s));
+        sum.x += y.x, sum.y += y.y, sum.z += y.z, sum.w += y.w;
+      }
+      const float f = out ? g.a.scale : 1.f;
+      sum.x *= f, sum.y *= f, sum.z *= f, sum.w *= f;
+      const float rest = fmaf(sum.x, 0.f, fmaf(sum.y, 0.f, fmaf(sum.z, 0.f, sum.w * 0.f)));
+      if (!(rest == 0.f)) atomicOr(&bad[out][rr >> 5], 1u << (rr & 31));
+      const RowsOut& to = out ? g.dk : g.dv;
+      T* dst = static_cast<T*>(to.p) + (k0 + row0 + rr) * to.stride + static_cast<int64_t>(head) * d + 4 * c;
+      if constexpr (sizeof(T) == 2)
+        *reinterpret_cast<uint2*>(dst) = make_uint2(tcu::pack_bf16(sum.x, sum.y), tcu::pack_bf16(sum.z, sum.w));
+      else if (to.vec)
+        *reinterpret_cast<float4*>(dst) = sum;
+      else
+        dst[0] = sum.x, dst[1] = sum.y, dst[2] = sum.z, dst[3] = sum.w;
+    }
+    tcu::named_bar(1, THREADS);
+    for (int x = tid >> 5; x < 2 * share; x += THREADS / 32) {
+      const int rr = rs + x % share, out = x / share;
+      if (!(bad[out][rr >> 5] >> (rr & 31) & 1)) continue;
+      float x1[4], x2[4];
+      again(row0 + rr, x1, x2);
+      const RowsOut& to = out ? g.dk : g.dv;
+      store_row<T, D>(static_cast<T*>(to.p) + (k0 + row0 + rr) * to.stride + static_cast<int64_t>(head) * d, out ? x1 : x2, d);
+    }
+  }
+  cluster_barrier();  // the others have read what lies here
 }
 
 }  // namespace falcon

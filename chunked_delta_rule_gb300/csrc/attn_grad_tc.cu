@@ -37,7 +37,6 @@
 // after the pipeline has ended.
 
 #include <algorithm>
-#include <cmath>
 
 #include "attn_grad.cuh"
 #include "attn_tc.cuh"
@@ -101,28 +100,6 @@ __device__ __forceinline__ uint64_t sdesc_plain16(uint32_t saddr) {
   d |= static_cast<uint64_t>(256 >> 4) << 32;
   d |= static_cast<uint64_t>(1) << 46;
   return d;
-}
-// every thread of the cluster's CTAs
-__device__ __forceinline__ void cluster_barrier() {
-  asm volatile("barrier.cluster.arrive.release;\n\tbarrier.cluster.wait.acquire;" ::: "memory");
-}
-__device__ __forceinline__ uint32_t peer_smem(uint32_t addr, uint32_t rank) {
-  uint32_t r;
-  asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(addr), "r"(rank));
-  return r;
-}
-__device__ __forceinline__ float4 load_peer4(uint32_t addr) {
-  float4 v;
-  asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
-               : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
-               : "r"(addr)
-               : "memory");
-  return v;
-}
-__device__ __forceinline__ uint32_t load_peer(uint32_t addr) {
-  uint32_t v;
-  asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(addr) : "memory");
-  return v;
 }
 template <int D, bool KEYS>
 __global__ void __launch_bounds__(Cfg<D, KEYS>::kThreads, Cfg<D, KEYS>::kCtas)
@@ -571,41 +548,7 @@ __global__ void __launch_bounds__(Cfg<D, KEYS>::kThreads, Cfg<D, KEYS>::kCtas)
           *reinterpret_cast<uint4*>(dst + ((((c0 + c) >> 2) + e) ^ (r & 7)) * 16) =
               make_uint4(v[4 * e], v[4 * e + 1], v[4 * e + 2], v[4 * e + 3]);
       }
-      cluster_barrier();
-      bool fine = true;
-      for (int s = 0; s < t.split; ++s) fine = fine && load_peer(peer_smem(smem_u32(&bar->failed), s)) == 0;
-      if (fine) {
-        const int share = kTile / t.split, rs = rank * share;
-        for (int x = tid; x < 2 * share * (D / 4); x += 32 * C::kWarps) {
-          const int c = x % (D / 4), rr = rs + x / (D / 4) % share, out = x / (D / 4) / share;  // out: dV, dK
-          if (row0 + rr >= rows || 4 * c >= d) continue;
-          const uint32_t at = smem_u32(smem) + out * (kTile * D * 4) + rr * (D * 4) + ((c ^ (rr & 7)) << 4);
-          float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
-          for (int s = 0; s < t.split; ++s) {
-            const float4 y = load_peer4(peer_smem(at, s));
-            sum.x += y.x, sum.y += y.y, sum.z += y.z, sum.w += y.w;
-          }
-          const float f = out ? a.scale : 1.f;
-          sum.x *= f, sum.y *= f, sum.z *= f, sum.w *= f;
-          const float rest = fmaf(sum.x, 0.f, fmaf(sum.y, 0.f, fmaf(sum.z, 0.f, sum.w * 0.f)));
-          if (!(rest == 0.f)) atomicOr(&bar->bad[out][rr >> 5], 1u << (rr & 31));
-          const RowsOut& to = out ? g.dk : g.dv;
-          *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(to.p) + (k0 + row0 + rr) * to.stride +
-                                    static_cast<int64_t>(head) * d + 4 * c) =
-              make_uint2(pack_bf16(sum.x, sum.y), pack_bf16(sum.z, sum.w));
-        }
-        named_bar(1, 32 * C::kWarps);
-        for (int x = warp; x < 2 * share; x += C::kWarps) {
-          const int rr = rs + x % share, out = x / share;
-          if (!(bar->bad[out][rr >> 5] >> (rr & 31) & 1)) continue;
-          float x1[4], x2[4];
-          compute_again(row0 + rr, x1, x2);
-          const RowsOut& to = out ? g.dk : g.dv;
-          store_row<__nv_bfloat16, D>(static_cast<__nv_bfloat16*>(to.p) + (k0 + row0 + rr) * to.stride +
-                                          static_cast<int64_t>(head) * d, out ? x1 : x2, d);
-        }
-      }
-      cluster_barrier();  // the others have read what lies here
+      cluster_sums<__nv_bfloat16, D, 32 * C::kWarps>(g, smem, &bar->failed, bar->bad, t.split, rank, row0, rows, k0, head, d, compute_again);
     }
     tc_fence_before();
   }
@@ -632,11 +575,7 @@ int launch_kernel(TcGradArgs& t, int64_t grid, const CUtensorMap (&m)[4], cudaSt
   cfg.blockDim = dim3(Cfg<D, KEYS>::kThreads);
   cfg.dynamicSmemBytes = smem_bytes<D, KEYS>();
   cfg.stream = s;
-  cudaLaunchAttribute attr[2];
-  attr[0] = overlap_attribute();
-  attr[1].id = cudaLaunchAttributeClusterDimension;
-  attr[1].val.clusterDim.x = static_cast<unsigned>(t.split);
-  attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+  cudaLaunchAttribute attr[2] = {overlap_attribute(), cluster_attribute(t.split)};
   cfg.attrs = attr;
   cfg.numAttrs = t.split > 1 ? 2 : 1;
   return cudaLaunchKernelEx(&cfg, kern, m[0], m[1], m[2], m[3], t) == cudaSuccess ? FALCON_OK : FALCON_ERR_CUDA;
@@ -660,14 +599,8 @@ int launch_d(const GradArgs& g, cudaStream_t s) {
     if (!maps(a.k, a.k_tokens, a.Hkv, kTile, m) || !maps(a.v, a.k_tokens, a.Hkv, kTile, m + 1) ||
         !maps(a.q, a.tokens, a.Hq, N, m + 2) || !maps(g.d_o, a.tokens, a.Hq, N, m + 3))
       return FALCON_ERR_CUDA;
-    // Clusters until the longest CTA (the keys that every query of all heads sees) takes no longer than all tiles of both
-    // kernels dealt out evenly, sequences taken as of one length; a tile of dQ costs some 0.7 of one of dK and dV.
     const int64_t ctas = blocks * a.Hkv;
-    const double lq = static_cast<double>(a.tokens) / a.B, lk = static_cast<double>(a.k_tokens) / a.B;
-    const double longest = std::ceil(lq / N) * (a.Hq / a.Hkv);
-    const double seen = lk >= lq ? 1.0 - 0.5 * lq / lk : 0.5 * lk / lq;  // of all pairs
-    const double even = 1.7 * longest * seen * std::ceil(lk / kTile) * a.B * a.Hkv / (sm_count() * Cfg<D, true>::kCtas);
-    while (t.split < 8 && longest > even * t.split && longest >= 8 * t.split) t.split *= 2;
+    t.split = keys_split(a, N, sm_count() * Cfg<D, true>::kCtas);
     const int st = launch_kernel<D, true>(t, ctas, m, s);
     if (st != FALCON_OK) return st;
     t.split = 1;

@@ -183,6 +183,7 @@ struct Cfg32 {
 struct Bars32 {
   uint64_t own, ready, full1[4], empty1[4], full2[4], empty2[4], info[2], x[2], y, p, ds, drain, stall;
   uint32_t tmem, failed;
+  uint32_t bad[2][4];  // rows that are not finite, a bit each
 };
 static_assert(sizeof(Bars32) <= 256 && Cfg32<128, true>::kSmem <= 227 * 1024 && Cfg32<128, false>::kSmem <= 227 * 1024 &&
                   Cfg32<64, true>::kSmem <= 227 * 1024 && Cfg32<128, true>::kColA + 128 <= 512 &&
@@ -194,6 +195,7 @@ struct Tc32Args {
   int qblocks;  // of a sequence
   bool packed;
   bool second;  // of the call's two kernels
+  int split;    // CTAs of a cluster
   uint32_t* status;
   uint64_t limit;
   int stall;
@@ -304,12 +306,14 @@ __global__ void __launch_bounds__(Cfg32<D, KEYS>::kThreads, 1) attn_grad_tc32_ke
     mbar_init(&bar->drain, 1);
     mbar_init(&bar->stall, 1);
     bar->failed = 0;
+    for (int i = 0; i < 8; ++i) bar->bad[i >> 2][i & 3] = 0;
     fence_mbar_init();
   }
 
   // whose rows
   const int G = a.Hq / a.Hkv;
-  const uint32_t block = blockIdx.x;
+  const uint32_t block = KEYS ? blockIdx.x / t.split : blockIdx.x;
+  const int rank = KEYS ? static_cast<int>(blockIdx.x % t.split) : 0;
   int b, head, row0;
   if (KEYS) {
     const int2 x = find_block(a.cu_k, a.B, kTile, static_cast<int>(block / a.Hkv));
@@ -332,7 +336,13 @@ __global__ void __launch_bounds__(Cfg32<D, KEYS>::kThreads, 1) attn_grad_tc32_ke
   // the tiles that come past, [first, first + each N) of every head
   const int first = KEYS ? max(row0 - off, 0) / N * N : 0;
   const int end = KEYS ? lq : min(min(row0 + kTile, lq) + off, lk);
-  const int each = end > first ? (end - first + N - 1) / N : 0, n = KEYS ? each * G : each;
+  const int each = end > first ? (end - first + N - 1) / N : 0;
+  int i0 = 0, n = each;  // this CTA's
+  if (KEYS) {
+    const int64_t all = static_cast<int64_t>(each) * G;
+    i0 = static_cast<int>(all * rank / t.split);
+    n = static_cast<int>(all * (rank + 1) / t.split) - i0;
+  }
   __syncthreads();
   const uint32_t tmem = bar->tmem;
   if (!t.second) {  // the operands are there
@@ -340,7 +350,7 @@ __global__ void __launch_bounds__(Cfg32<D, KEYS>::kThreads, 1) attn_grad_tc32_ke
     launch_dependents();
   }
   const bool last = t.second && blockIdx.x == gridDim.x - 1 && tid == C::kThreads - 1;  // ends no sooner than the first kernel
-  if (!valid) {
+  if (!valid) {  // (the whole cluster)
     if (warp == C::kMmaWarp) tmem_dealloc(tmem, 512);
     if (last) wait_for_previous();
     return;
@@ -354,8 +364,8 @@ __global__ void __launch_bounds__(Cfg32<D, KEYS>::kThreads, 1) attn_grad_tc32_ke
   // blocks of the workspace: the owned rows' first one; tile i's
   const int64_t own_block = (KEYS ? head * t.w.k_blocks + first64(k0, b) : head * t.w.q_blocks + first64(q0, b)) + row0 / kPast;
   auto past_block = [&](int i) {
-    return (KEYS ? (head * G + i / each) * t.w.q_blocks + first64(q0, b) : head / G * t.w.k_blocks + first64(k0, b)) +
-           first / kPast + (KEYS ? i % each : i);
+    return (KEYS ? (head * G + (i0 + i) / each) * t.w.q_blocks + first64(q0, b) : head / G * t.w.k_blocks + first64(k0, b)) +
+           first / kPast + (KEYS ? (i0 + i) % each : i);
   };
 
   // 256 x 224 + 128 x 56 = 384 x 168
@@ -624,7 +634,7 @@ __global__ void __launch_bounds__(Cfg32<D, KEYS>::kThreads, 1) attn_grad_tc32_ke
       }
     };
     float down = 0.f, down_v = 0.f;  // of the tile whose sums come next
-    for (int i = 0, past = 0; i < n; ++i) {
+    for (int i = 0, past = KEYS && n > 0 ? i0 % each : 0; i < n; ++i) {
       const int at = first + past * N;
       if (KEYS && ++past == each) past = 0;
       if (!KEYS) past = i + 1;
@@ -680,6 +690,24 @@ __global__ void __launch_bounds__(Cfg32<D, KEYS>::kThreads, 1) attn_grad_tc32_ke
       add_sums<D>(acc, mine + C::kColV + (KEYS ? D : 0), down);
     }
     const int d = D == 64 ? a.d : D;  // of the rows
+    // a row of a result (x1: dK or dQ, x2: dV) from the definition
+    auto compute_again = [&](int i, float (&x1)[4], float (&x2)[4]) {
+      const float *q = static_cast<const float*>(a.q.p), *d_o = static_cast<const float*>(g.d_o.p);
+      const float *k = static_cast<const float*>(a.k.p), *v = static_cast<const float*>(a.v.p);
+      const float* sums = g.sums + row_sums(g.blocks, KEYS ? head * G : head, first_block(q0, b));
+      if constexpr (KEYS) {
+        const int64_t h0 = static_cast<int64_t>(head) * G * d, hk = static_cast<int64_t>(head) * d;
+        grad_key_row<float, D>(k + (k0 + i) * a.k.stride + hk, v + (k0 + i) * a.v.stride + hk, q + q0 * a.q.stride + h0,
+                               a.q.stride, d_o + q0 * g.d_o.stride + h0, g.d_o.stride, sums, g.blocks, G, max(i - off, 0), lq,
+                               d, a.scale, x1, x2);
+      } else {
+        const int64_t h0 = static_cast<int64_t>(head) * d, hk = static_cast<int64_t>(head / G) * d;
+        const float* s = sums + static_cast<int64_t>(i / kSumRows) * (2 * kSumRows) + i % kSumRows;
+        grad_query_row<float, D>(q + (q0 + i) * a.q.stride + h0, d_o + (q0 + i) * g.d_o.stride + h0, s[0], s[kSumRows],
+                                 k + k0 * a.k.stride + hk, a.k.stride, v + k0 * a.v.stride + hk, a.v.stride,
+                                 min(i + off + 1, lk), d, a.scale, x1);
+      }
+    };
     // this lane's half of its row of a result; which: dV (0), dK or dQ (1)
     auto finish = [&](const uint64_t (&z)[D / 4], int which) {
       const RowsOut& to = KEYS ? (which ? g.dk : g.dv) : g.dq;
@@ -706,21 +734,7 @@ __global__ void __launch_bounds__(Cfg32<D, KEYS>::kThreads, 1) attn_grad_tc32_ke
       for (uint32_t again = __ballot_sync(0xffffffffu, live && !(ra + rb == 0.f)); again; again &= again - 1) {
         const int from = __ffs(again) - 1, i = row0 + quad * 32 + group * 16 + (from & 15);
         float x1[4], x2[4];
-        const float *q = static_cast<const float*>(a.q.p), *d_o = static_cast<const float*>(g.d_o.p);
-        const float *k = static_cast<const float*>(a.k.p), *v = static_cast<const float*>(a.v.p);
-        const float* sums = g.sums + row_sums(g.blocks, KEYS ? head * G : head, first_block(q0, b));
-        if constexpr (KEYS) {
-          const int64_t h0 = static_cast<int64_t>(head) * G * d, hk = static_cast<int64_t>(head) * d;
-          grad_key_row<float, D>(k + (k0 + i) * a.k.stride + hk, v + (k0 + i) * a.v.stride + hk, q + q0 * a.q.stride + h0,
-                                 a.q.stride, d_o + q0 * g.d_o.stride + h0, g.d_o.stride, sums, g.blocks, G, max(i - off, 0),
-                                 lq, d, a.scale, x1, x2);
-        } else {
-          const int64_t h0 = static_cast<int64_t>(head) * d, hk = static_cast<int64_t>(head / G) * d;
-          const float* s = sums + static_cast<int64_t>(i / kSumRows) * (2 * kSumRows) + i % kSumRows;
-          grad_query_row<float, D>(q + (q0 + i) * a.q.stride + h0, d_o + (q0 + i) * g.d_o.stride + h0, s[0], s[kSumRows],
-                                   k + k0 * a.k.stride + hk, a.k.stride, v + k0 * a.v.stride + hk, a.v.stride,
-                                   min(i + off + 1, lk), d, a.scale, x1);
-        }
+        compute_again(i, x1, x2);
 #pragma unroll
         for (int m = 0; m < D / 32; ++m) {
           const int c = m * 32 + lane;
@@ -728,11 +742,28 @@ __global__ void __launch_bounds__(Cfg32<D, KEYS>::kThreads, 1) attn_grad_tc32_ke
         }
       }
     };
-    if (ok) {  // the same in all lanes
-      if constexpr (KEYS) finish(acc_v, 0);
-      finish(acc, 1);
+    if (!KEYS || t.split == 1) {
+      if (ok) {  // the same in all lanes
+        if constexpr (KEYS) finish(acc_v, 0);
+        finish(acc, 1);
+      }
+    } else if constexpr (KEYS) {
+      // the owned tile's and the ring's place: every product is done
+      uint8_t* dst = smem + r * (D * 4);
+#pragma unroll
+      for (int e = 0; e < D / 8; ++e) {
+        const int c = ((half * (D / 8) + e) ^ (r & 7)) << 4;
+        *reinterpret_cast<ulonglong2*>(dst + c) = make_ulonglong2(acc_v[2 * e], acc_v[2 * e + 1]);
+        *reinterpret_cast<ulonglong2*>(dst + kTile * D * 4 + c) = make_ulonglong2(acc[2 * e], acc[2 * e + 1]);
+      }
+      cluster_sums<float, D, 32 * C::kWarps>(g, smem, &bar->failed, bar->bad, t.split, rank, row0, rows, k0, head, d, compute_again);
     }
     tc_fence_before();
+  }
+  if (KEYS && t.split > 1 && warp >= C::kMmaWarp) {
+    __syncwarp();
+    cluster_barrier();
+    cluster_barrier();
   }
   __syncthreads();
   if (warp == C::kMmaWarp) {
@@ -743,18 +774,18 @@ __global__ void __launch_bounds__(Cfg32<D, KEYS>::kThreads, 1) attn_grad_tc32_ke
 
 template <int D, bool KEYS>
 int launch_kernel(Tc32Args& t, int64_t grid, cudaStream_t s) {
-  if (grid < 1 || grid > INT32_MAX) return FALCON_ERR_UNSUPPORTED;
+  if (grid < 1 || grid > INT32_MAX / t.split) return FALCON_ERR_UNSUPPORTED;
   t.stall = take_test_stall() ? 1 : 0;
   const auto kern = attn_grad_tc32_kernel<D, KEYS>;
   if (!set_smem_limit(reinterpret_cast<const void*>(kern), Cfg32<D, KEYS>::kSmem)) return FALCON_ERR_CUDA;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>(grid));
+  cfg.gridDim = dim3(static_cast<unsigned>(grid * t.split));
   cfg.blockDim = dim3(Cfg32<D, KEYS>::kThreads);
   cfg.dynamicSmemBytes = Cfg32<D, KEYS>::kSmem;
   cfg.stream = s;
-  cudaLaunchAttribute attr[1] = {overlap_attribute()};
+  cudaLaunchAttribute attr[2] = {overlap_attribute(), cluster_attribute(t.split)};
   cfg.attrs = attr;
-  cfg.numAttrs = 1;
+  cfg.numAttrs = t.split > 1 ? 2 : 1;
   return cudaLaunchKernelEx(&cfg, kern, t) == cudaSuccess ? FALCON_OK : FALCON_ERR_CUDA;
 }
 
@@ -793,10 +824,13 @@ int launch_d(const GradArgs& g, cudaStream_t s) {
   attn_grad_split_kernel<D><<<static_cast<unsigned>(q_ctas + k_ctas), 256, 0, s>>>(g, t.w, static_cast<unsigned>(q_ctas));
   if (cudaGetLastError() != cudaSuccess) return FALCON_ERR_CUDA;
   t.second = false;
+  t.split = 1;
   if (g.dk.p && k_ctas) {  // first: its CTAs run longest
     const int64_t blocks = a.k_tokens / kTile + a.B;
+    t.split = keys_split(a, kPast, sm_count());
     const int st = blocks > INT32_MAX / a.Hkv ? FALCON_ERR_UNSUPPORTED : launch_kernel<D, true>(t, blocks * a.Hkv, s);
     if (st != FALCON_OK) return st;
+    t.split = 1;
     t.second = true;
   }
   if (g.dq.p && q_ctas) {

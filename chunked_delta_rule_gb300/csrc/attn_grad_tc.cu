@@ -70,7 +70,9 @@ struct Cfg {
 };
 constexpr int kMostPairs = 5;
 struct Bars {
-  uint64_t own, ready, full[2 * kMostPairs], empty[2 * kMostPairs], x, x_read, y, p, ds, drain, stall;
+  uint64_t own, ready, full[2 * kMostPairs], empty[2 * kMostPairs], x, y;
+  uint64_t p;  // dK and dV: P is there; dQ: X has been read
+  uint64_t ds, drain, stall;
   uint32_t tmem, failed;
   uint32_t bad[2][4];  // rows that are not finite, a bit each
 };
@@ -130,10 +132,9 @@ __global__ void __launch_bounds__(Cfg<D, KEYS>::kThreads, Cfg<D, KEYS>::kCtas)
       mbar_init(&bar->empty[i], 1);
     }
     mbar_init(&bar->x, 1);
-    mbar_init(&bar->x_read, C::kWarps);
     mbar_init(&bar->y, 1);
-    mbar_init(&bar->p, C::kWarps);
-    mbar_init(&bar->ds, C::kWarps);
+    mbar_init(&bar->p, C::kWarps + 1);
+    mbar_init(&bar->ds, C::kWarps + 1);
     mbar_init(&bar->drain, 1);
     mbar_init(&bar->stall, 1);
     bar->failed = 0;
@@ -253,22 +254,24 @@ __global__ void __launch_bounds__(Cfg<D, KEYS>::kThreads, Cfg<D, KEYS>::kCtas)
     }
     __syncwarp();
   } else if (warp == C::kMmaWarp) {
-    // The whole warp walks the loop, so that descriptors stay uniform; one lane issues.
-    constexpr uint32_t id_x = idesc_bf16(kTile, N), id_s = idesc_bf16(kTile, D, false, true);
+    // One lane walks the loop: it issues a product in 16 cycles (the whole warp with an elected lane in 46) and a wait that
+    // has come true costs it 66; the tensor cores' queue hides some 250 cycles between two batches.
     const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);
-    const uint64_t a1 = sdesc_k128(smem_u32(s1)), a2 = sdesc_k128(smem_u32(s2)), bk = sdesc_k128(smem_u32(ring));
-    const uint64_t bm = D == 64 ? sdesc_mn128(smem_u32(ring)) : sdesc_mn128_wide(smem_u32(ring), N * 128);
-    const uint64_t one = sdesc_plain16(smem_u32(ones)), img = sdesc_plain16(smem_u32(images));
-    auto arrived = [&](uint64_t* m, uint32_t parity) {  // one answer for the warp
-      return __all_sync(0xffffffffu, wait(m, parity)) != 0;
-    };
-    auto full = [&](int i, int second) { return arrived(&bar->full[place(i, second)], (i / P) & 1); };
-    // X (second = 0) or Y of tile i, with what its completion tells
-    auto scores = [&](int i, int second, uint64_t* then, bool frees) {
-      const int slot = place(i, second);
-      const uint64_t bs = bk + slot * (C::kTileBytes >> 4);
-      const uint32_t to = tm + (second ? C::kColY : C::kColX);
-      if (elect_one()) {
+    if (elect_one()) {
+      constexpr uint32_t id_x = idesc_bf16(kTile, N), id_s = idesc_bf16(kTile, D, false, true);
+      const uint64_t a1 = sdesc_k128(smem_u32(s1)), a2 = sdesc_k128(smem_u32(s2)), bk = sdesc_k128(smem_u32(ring));
+      const uint64_t bm = D == 64 ? sdesc_mn128(smem_u32(ring)) : sdesc_mn128_wide(smem_u32(ring), N * 128);
+      const uint64_t one = sdesc_plain16(smem_u32(ones)), img = sdesc_plain16(smem_u32(images));
+      auto arrived = [&](uint64_t* m, uint32_t parity) {
+        const bool ok = wait(m, parity);
+        tc_fence_after();
+        return ok;
+      };
+      // X (second = 0) or Y of tile i, with what its completion tells
+      auto scores = [&](int i, int second, uint64_t* then, bool frees) {
+        const int slot = place(i, second);
+        const uint64_t bs = bk + slot * (C::kTileBytes >> 4);
+        const uint32_t to = tm + (second ? C::kColY : C::kColX);
 #pragma unroll
         for (int ks = 0; ks < D / 16; ++ks) {
           const uint64_t bd = bs + (((ks >> 2) * N * 128 + (ks & 3) * 32) >> 4);
@@ -278,69 +281,49 @@ __global__ void __launch_bounds__(Cfg<D, KEYS>::kThreads, Cfg<D, KEYS>::kCtas)
         if (KEYS) umma_bf16(to, one + second * (kImageBytes >> 4), img + i % P * (C::kImage >> 4), id_x, 1);
         umma_commit(then);
         if (frees) umma_commit(&bar->empty[slot]);
-      }
-      __syncwarp();
-    };
-    // sum += W (bf16, in TMEM) times the first or second tile of pair i
-    auto add = [&](uint32_t sum, uint32_t w, int i, int second) {
-      const int slot = place(i, second);
-      const uint64_t bs = bm + slot * (C::kTileBytes >> 4);
-      if (elect_one()) {
+      };
+      // sum += W (bf16, in TMEM) times the first or second tile of pair i
+      auto add = [&](uint32_t sum, uint32_t w, int i, int second) {
+        const int slot = place(i, second);
+        const uint64_t bs = bm + slot * (C::kTileBytes >> 4);
 #pragma unroll
         for (int ks = 0; ks < N / 16; ++ks)
           umma_ts(tm + sum, tm + w + (ks >> 1) * 32 + (ks & 1) * 8, bs + ks * 128, id_s, i > 0 || ks > 0);
         umma_commit(&bar->empty[slot]);
+      };
+      bool ok = n > 0 && arrived(KEYS ? &bar->own : &bar->ready, 0) && arrived(&bar->full[place(0, 0)], 0);
+      if (ok) {
+        scores(0, 0, &bar->x, false);
+        if ((ok = arrived(&bar->full[place(0, 1)], 0))) scores(0, 1, &bar->y, !KEYS);
       }
-      __syncwarp();
-    };
-    bool ok = n > 0 && arrived(KEYS ? &bar->own : &bar->ready, 0);
-    if (ok && (ok = full(0, 0))) {
-      tc_fence_after();
-      scores(0, 0, &bar->x, false);
-    }
-    if constexpr (KEYS) {
-      // ... X(i) dK(i - 1) Y(i) dV(i) X(i + 1) ...: P(i) is formed under dK(i - 1) and Y(i), dS(i) under dV(i) and X(i + 1)
+      // dK and dV: ... X(i) dK(i - 1) Y(i) dV(i) X(i + 1) ...: P(i) is formed under dK(i - 1) and Y(i), dS(i) under dV(i)
+      // and X(i + 1).  dQ: ... Y(i) X(i + 1) dQ(i) Y(i + 1) ...: P(i + 1) is formed under dQ(i) and Y(i + 1), dS(i) under
+      // X(i + 1).  What these wait for holds the next tile's copies too.
       for (int i = 0; i < n && ok; ++i) {
-        if (!(ok = full(i, 1))) break;
-        tc_fence_after();
-        scores(i, 1, &bar->y, false);
         if (!(ok = arrived(&bar->p, i & 1))) break;
-        tc_fence_after();
-        add(C::kColV, C::kColX, i, 1);
-        if (i + 1 < n) {
-          if (!(ok = full(i + 1, 0))) break;
-          tc_fence_after();
-          scores(i + 1, 0, &bar->x, false);
-        }
+        if (KEYS) add(C::kColV, C::kColX, i, 1);
+        if (i + 1 < n) scores(i + 1, 0, &bar->x, false);
         if (!(ok = arrived(&bar->ds, i & 1))) break;
-        tc_fence_after();
         add(C::kColS, C::kColY, i, 0);
+        if (i + 1 < n) scores(i + 1, 1, &bar->y, !KEYS);
       }
-    } else {
-      // ... Y(i) X(i + 1) dQ(i) Y(i + 1) ...: P(i + 1) is formed under dQ(i) and Y(i + 1), dS(i) under X(i + 1)
-      if (ok && (ok = full(0, 1))) {
-        tc_fence_after();
-        scores(0, 1, &bar->y, true);
-      }
-      for (int i = 0; i < n && ok; ++i) {
-        if (i + 1 < n) {
-          if (!(ok = full(i + 1, 0) && arrived(&bar->x_read, i & 1))) break;
-          tc_fence_after();
-          scores(i + 1, 0, &bar->x, false);
-        }
-        if (!(ok = arrived(&bar->ds, i & 1))) break;
-        tc_fence_after();
-        add(C::kColS, C::kColY, i, 0);
-        if (i + 1 < n) {
-          if (!(ok = full(i + 1, 1))) break;
-          tc_fence_after();
-          scores(i + 1, 1, &bar->y, true);
-        }
-      }
+      umma_commit(&bar->drain);  // products in flight end before the memory is freed
+      wait(&bar->drain, 0);
     }
-    if (elect_one()) umma_commit(&bar->drain);  // products in flight end before the memory is freed
     __syncwarp();
-    wait(&bar->drain, 0);
+  } else if (warp == C::kMmaWarp + 1) {
+    // waits for the next tile's copies in the MMA warp's place, and joins the softmax warps' arrivals
+    if (lane == 0) {
+      bool ok = true;
+      for (int i = 0; i < n && ok; ++i)
+        for (int second = 0; second < 2 && ok; ++second) {
+          uint64_t* m = second ? &bar->ds : &bar->p;
+          if (i + 1 < n) ok = wait(&bar->full[place(i + 1, second)], ((i + 1) / P) & 1);
+          if (!ok) break;
+          mbar_arrive(m);
+          ok = wait(m, i & 1);  // so that the next arrival counts for the next tile
+        }
+    }
     __syncwarp();
   } else if (warp < C::kLoadWarp) {
     if (D == 64) asm volatile("setmaxnreg.inc.sync.aligned.u32 96;");
@@ -386,37 +369,38 @@ __global__ void __launch_bounds__(Cfg<D, KEYS>::kThreads, Cfg<D, KEYS>::kCtas)
       const uint32_t tx = mine + C::kColX + part * 32, ty = mine + C::kColY + part * 32;
       if (!(ok = waited(&bar->x, i & 1))) break;
       tc_fence_after();
-      float p[32];
-      uint32_t v[32], u[16];
-      tmem_ld32(tx, v);
-      tmem_wait_ld();
-      if (!KEYS) {
-        tc_fence_before();
-        arrive(&bar->x_read);
-      }
-#pragma unroll
-      for (int e = 0; e < 32; ++e) p[e] = __uint_as_float(v[e]);
-      if constexpr (KEYS) {
-        if (at + off < row0 + kTile - 1) {  // some key is behind a query of these
-          const int lim = row - off - at;
-#pragma unroll
-          for (int e = 0; e < 32; ++e)
-            if (e < lim) p[e] = -INFINITY;
+      uint64_t x[16];  // X, then P
+      uint32_t u[16];
+      {
+        uint32_t v[32];
+        tmem_ld32(tx, v);
+        tmem_wait_ld();
+        if (!KEYS) {
+          tc_fence_before();
+          arrive(&bar->p);
         }
-      } else {
-        if (at + 32 > min(row0 + off + 1, lk)) {
-          const int lim = min(row + off + 1, lk) - at;
 #pragma unroll
-          for (int e = 0; e < 32; ++e)
-            if (e >= lim) p[e] = -INFINITY;
+        for (int e = 0; e < 16; ++e) x[e] = pack2(__uint_as_float(v[2 * e]), __uint_as_float(v[2 * e + 1]));
+      }
+      // keys behind a query of these, or past the last
+      if (KEYS ? at + off < row0 + kTile - 1 : at + 32 > min(row0 + off + 1, lk)) {
+        const int lim = KEYS ? row - off - at : min(row + off + 1, lk) - at;
+#pragma unroll
+        for (int e = 0; e < 16; ++e) {
+          float z0, z1;
+          unpack2(x[e], z0, z1);
+          if (KEYS ? 2 * e < lim : 2 * e >= lim) z0 = -INFINITY;
+          if (KEYS ? 2 * e + 1 < lim : 2 * e + 1 >= lim) z1 = -INFINITY;
+          x[e] = pack2(z0, z1);
         }
       }
 #pragma unroll
       for (int e = 0; e < 16; ++e) {
-        const uint64_t x = pack2(p[2 * e], p[2 * e + 1]);
-        unpack2(KEYS ? mul2(x, scale2) : fma2(x, scale2, lse2), p[2 * e], p[2 * e + 1]);
-        p[2 * e] = ex2(p[2 * e]), p[2 * e + 1] = ex2(p[2 * e + 1]);
-        if (KEYS) u[e] = pack_bf16(p[2 * e], p[2 * e + 1]);
+        float z0, z1;
+        unpack2(KEYS ? mul2(x[e], scale2) : fma2(x[e], scale2, lse2), z0, z1);
+        z0 = ex2(z0), z1 = ex2(z1);
+        x[e] = pack2(z0, z1);
+        if (KEYS) u[e] = pack_bf16(z0, z1);
       }
       if (KEYS) {
         tmem_st16(tx, u);
@@ -426,15 +410,18 @@ __global__ void __launch_bounds__(Cfg<D, KEYS>::kThreads, Cfg<D, KEYS>::kCtas)
       }
       if (!(ok = waited(&bar->y, i & 1))) break;
       tc_fence_after();
-      tmem_ld32(ty, v);
-      tmem_wait_ld();
+      {
+        uint32_t v[32];
+        tmem_ld32(ty, v);
+        tmem_wait_ld();
 #pragma unroll
-      for (int e = 0; e < 16; ++e) {
-        uint64_t z = pack2(__uint_as_float(v[2 * e]), __uint_as_float(v[2 * e + 1]));
-        if (!KEYS) z = add2(z, delta2);
-        float z0, z1;
-        unpack2(mul2(pack2(p[2 * e], p[2 * e + 1]), z), z0, z1);
-        u[e] = pack_bf16(z0, z1);
+        for (int e = 0; e < 16; ++e) {
+          uint64_t z = pack2(__uint_as_float(v[2 * e]), __uint_as_float(v[2 * e + 1]));
+          if (!KEYS) z = add2(z, delta2);
+          float z0, z1;
+          unpack2(mul2(x[e], z), z0, z1);
+          u[e] = pack_bf16(z0, z1);
+        }
       }
       tmem_st16(ty, u);
       tmem_wait_st();

@@ -125,6 +125,8 @@ __global__ void __launch_bounds__(Cfg<D, KEYS>::kThreads, Cfg<D, KEYS>::kCtas)
     tmem_relinquish();
   }
   if (warp == C::kLoadWarp && lane == 0) {
+    for (const CUtensorMap* m : {&own1, &own2, &past1, &past2})
+      asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(m)) : "memory");
     mbar_init(&bar->own, 1);
     mbar_init(&bar->ready, C::kWarps);
     for (int i = 0; i < 2 * P; ++i) {

@@ -375,24 +375,24 @@ __global__ void __launch_bounds__(Cfg32<D, KEYS>::kThreads, 1) attn_grad_tc32_ke
     __syncwarp();
   }
   if (warp == C::kMmaWarp) {
-    // The whole warp walks the loop, so that descriptors stay uniform; one lane issues.
-    constexpr uint32_t id_x = idesc_f16(kTile, N), id_s = idesc_f16(kTile, D, true);
+    // One lane walks the loop, see the bf16 kernels.
     const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);
-    const uint64_t a1 = sdesc_k128(smem_u32(s1));
-    const uint64_t bk1 = sdesc_k128(smem_u32(ring1)), bk2 = sdesc_k128(smem_u32(ring2));
-    const uint64_t bm1 = D == 64 ? sdesc_mn128(smem_u32(ring1)) : sdesc_mn128_wide(smem_u32(ring1), N * 128);
-    const uint64_t bm2 = D == 64 ? sdesc_mn128(smem_u32(ring2)) : sdesc_mn128_wide(smem_u32(ring2), N * 128);
-    auto arrived = [&](uint64_t* m, uint32_t parity) {  // one answer for the warp
-      const bool ok = __all_sync(0xffffffffu, wait(m, parity)) != 0;
-      tc_fence_after();
-      return ok;
-    };
-    auto full1 = [&](int i) { return arrived(&bar->full1[i % P1], (i / P1) & 1); };
-    auto full2 = [&](int i) { return arrived(&bar->full2[i % P2], (i / P2) & 1); };
-    // to = the owned rows times tile i's; lo hi, hi lo, hi hi
-    auto scores = [&](uint32_t to, int i, int second, uint64_t* then, uint64_t* frees) {
-      const uint64_t bs = second ? bk2 + i % P2 * (C::kTileBytes >> 4) : bk1 + i % P1 * (C::kTileBytes >> 4);
-      if (elect_one()) {
+    if (elect_one()) {
+      constexpr uint32_t id_x = idesc_f16(kTile, N), id_s = idesc_f16(kTile, D, true);
+      const uint64_t a1 = sdesc_k128(smem_u32(s1));
+      const uint64_t bk1 = sdesc_k128(smem_u32(ring1)), bk2 = sdesc_k128(smem_u32(ring2));
+      const uint64_t bm1 = D == 64 ? sdesc_mn128(smem_u32(ring1)) : sdesc_mn128_wide(smem_u32(ring1), N * 128);
+      const uint64_t bm2 = D == 64 ? sdesc_mn128(smem_u32(ring2)) : sdesc_mn128_wide(smem_u32(ring2), N * 128);
+      auto arrived = [&](uint64_t* m, uint32_t parity) {
+        const bool ok = wait(m, parity);
+        tc_fence_after();
+        return ok;
+      };
+      auto full1 = [&](int i) { return arrived(&bar->full1[i % P1], (i / P1) & 1); };
+      auto full2 = [&](int i) { return arrived(&bar->full2[i % P2], (i / P2) & 1); };
+      // to = the owned rows times tile i's; lo hi, hi lo, hi hi
+      auto scores = [&](uint32_t to, int i, int second, uint64_t* then, uint64_t* frees) {
+        const uint64_t bs = second ? bk2 + i % P2 * (C::kTileBytes >> 4) : bk1 + i % P1 * (C::kTileBytes >> 4);
 #pragma unroll
         for (int part = 0; part < 3; ++part)
 #pragma unroll
@@ -406,13 +406,10 @@ __global__ void __launch_bounds__(Cfg32<D, KEYS>::kThreads, 1) attn_grad_tc32_ke
           }
         if (then) umma_commit(then);
         if (frees) umma_commit(frees);
-      }
-      __syncwarp();
-    };
-    // sum = W (halves in TMEM) times tile i
-    auto weighted = [&](uint32_t sum, uint32_t w, int i, int second, uint64_t* frees) {
-      const uint64_t bs = second ? bm2 + i % P2 * (C::kTileBytes >> 4) : bm1 + i % P1 * (C::kTileBytes >> 4);
-      if (elect_one()) {
+      };
+      // sum = W (halves in TMEM) times tile i
+      auto weighted = [&](uint32_t sum, uint32_t w, int i, int second, uint64_t* frees) {
+        const uint64_t bs = second ? bm2 + i % P2 * (C::kTileBytes >> 4) : bm1 + i % P1 * (C::kTileBytes >> 4);
 #pragma unroll
         for (int part = 0; part < 3; ++part)
 #pragma unroll
@@ -420,44 +417,38 @@ __global__ void __launch_bounds__(Cfg32<D, KEYS>::kThreads, 1) attn_grad_tc32_ke
             umma_ts(tm + sum, tm + w + (part == 0 ? 32 : 0) + ks * 8, bs + (part == 1 ? kHalf >> 4 : 0) + ks * 128, id_s,
                     part > 0 || ks > 0);
         umma_commit(frees);
-      }
-      __syncwarp();
-    };
-    // copies of the next tile's first and second part, and of its rows' numbers; by one lane
-    int loads1 = 0, loads2 = 0, infos_in = 0;
-    auto load = [&](uint8_t* to, const uint8_t* from, int bytes, uint64_t* full) {
-      if (elect_one()) {
+      };
+      // copies of the next tile's first and second part, and of its rows' numbers
+      int loads1 = 0, loads2 = 0, infos_in = 0;
+      auto load = [&](uint8_t* to, const uint8_t* from, int bytes, uint64_t* full) {
         mbar_arrive_expect_tx(full, bytes);
         bulk_load(to, from, bytes, full);
-      }
-      __syncwarp();
-    };
-    auto load1 = [&] {
-      const int i = loads1++, at = i % P1;
-      load(ring1 + at * C::kTileBytes, (KEYS ? t.w.q : t.w.k) + past_block(i) * C::kTileBytes, C::kTileBytes, &bar->full1[at]);
-    };
-    auto load2 = [&] {
-      const int i = loads2++, at = i % P2;
-      load(ring2 + at * C::kTileBytes, (KEYS ? t.w.d_o : t.w.v) + past_block(i) * C::kTileBytes, C::kTileBytes, &bar->full2[at]);
-    };
-    auto load_info = [&] {
-      const int i = infos_in++;
-      load(infos + (i & 1) * C::kInfo, (KEYS ? t.w.q_info : t.w.k_info) + past_block(i) * C::kInfo, C::kInfo, &bar->info[i & 1]);
-    };
-    // The place of tile i - P's is free.  Its last product is that of dK or dQ, which also ends the use of the tile's numbers.
-    auto more1 = [&](int i) {
-      const int done = i - P1;
-      if (done + 2 >= n && i >= n) return true;
-      if (!arrived(&bar->empty1[i % P1], (i / P1 - 1) & 1)) return false;
-      if (done + 2 < n) load_info();
-      if (i < n) load1();
-      return true;
-    };
-    auto more2 = [&](int i) { return i >= n || (arrived(&bar->empty2[i % P2], (i / P2 - 1) & 1) && (load2(), true)); };
-    bool ok = n > 0 && (!t.stall || arrived(&bar->stall, 0));
-    const bool own = ok;
-    if (ok) {
-      if (elect_one()) {
+      };
+      auto load1 = [&] {
+        const int i = loads1++, at = i % P1;
+        load(ring1 + at * C::kTileBytes, (KEYS ? t.w.q : t.w.k) + past_block(i) * C::kTileBytes, C::kTileBytes, &bar->full1[at]);
+      };
+      auto load2 = [&] {
+        const int i = loads2++, at = i % P2;
+        load(ring2 + at * C::kTileBytes, (KEYS ? t.w.d_o : t.w.v) + past_block(i) * C::kTileBytes, C::kTileBytes, &bar->full2[at]);
+      };
+      auto load_info = [&] {
+        const int i = infos_in++;
+        load(infos + (i & 1) * C::kInfo, (KEYS ? t.w.q_info : t.w.k_info) + past_block(i) * C::kInfo, C::kInfo, &bar->info[i & 1]);
+      };
+      // The place of tile i - P's is free.  Its last product is that of dK or dQ, which also ends the use of the tile's numbers.
+      auto more1 = [&](int i) {
+        const int done = i - P1;
+        if (done + 2 >= n && i >= n) return true;
+        if (!arrived(&bar->empty1[i % P1], (i / P1 - 1) & 1)) return false;
+        if (done + 2 < n) load_info();
+        if (i < n) load1();
+        return true;
+      };
+      auto more2 = [&](int i) { return i >= n || (arrived(&bar->empty2[i % P2], (i / P2 - 1) & 1) && (load2(), true)); };
+      bool ok = n > 0 && (!t.stall || arrived(&bar->stall, 0));
+      const bool own = ok;
+      if (ok) {
         // slabs of 128 rows from two blocks' of 64; the second block may not be there, no row of it counts then
         const int halves = row0 + kPast < rows ? 2 : 1;
         mbar_arrive_expect_tx(&bar->own, halves * 2 * C::kTileBytes);
@@ -466,60 +457,58 @@ __global__ void __launch_bounds__(Cfg32<D, KEYS>::kThreads, 1) attn_grad_tc32_ke
           uint8_t* to = ((s & 1) ? s2 : s1) + (s >> 1) * (kPast * 128);
           for (int c = 0; c < D / 32; ++c) bulk_load(to + c * (kTile * 128), from + c * (kPast * 128), kPast * 128, &bar->own);
         }
+        load1();
+        for (int i = 0; i < min(n, P2); ++i) load2();
+        for (int i = 0; i < min(n, 2); ++i) load_info();
+        ok = arrived(&bar->own, 0) && full1(0);
       }
-      __syncwarp();
-      load1();
-      for (int i = 0; i < min(n, P2); ++i) load2();
-      for (int i = 0; i < min(n, 2); ++i) load_info();
-      ok = arrived(&bar->own, 0) && full1(0);
-    }
-    if (ok) {
-      scores(C::kColX, 0, 0, KEYS ? &bar->x[0] : nullptr, nullptr);
-      ok = arrived(&bar->ready, 0);
-      for (int i = 1; i < min(n, P1) && ok; ++i) load1();
-    }
-    // A place's next copy waits for the place's last product while another one runs.
-    if constexpr (KEYS) {
-      for (int i = 0; i < n && ok; ++i) {
-        if (!(ok = full2(i))) break;
-        scores(C::kColY, i, 1, &bar->y, nullptr);
-        if (i > 0 && !(ok = more1(i - 1 + P1))) break;
-        if (!(ok = arrived(&bar->p, i & 1))) break;
-        weighted(C::kColV, C::kColX, i, 1, &bar->empty2[i % P2]);
-        if (i + 1 < n) {
-          if (!(ok = full1(i + 1))) break;
-          scores(C::kColX, i + 1, 0, &bar->x[0], nullptr);
-        }
-        if (!(ok = more2(i + P2))) break;
-        if (!(ok = arrived(&bar->ds, i & 1))) break;
-        weighted(C::kColV + D, C::kColY, i, 0, &bar->empty1[i % P1]);
+      if (ok) {
+        scores(C::kColX, 0, 0, KEYS ? &bar->x[0] : nullptr, nullptr);
+        ok = arrived(&bar->ready, 0);
+        for (int i = 1; i < min(n, P1) && ok; ++i) load1();
       }
-    } else {
-      // dS of tiles i and i - 1 lie over X of them; Y of tile i + 1 over that of tile i - 1
-      if (ok && (ok = full2(0))) scores(C::kColY, 0, 1, &bar->x[0], &bar->empty2[0]);
-      if (ok) ok = more2(P2);
-      for (int i = 0; i < n && ok; ++i) {
-        const uint32_t next = (i + 1) & 1;
-        if (i + 1 < n) {
-          if (!(ok = full1(i + 1))) break;
-          scores(C::kColX + next * N, i + 1, 0, nullptr, nullptr);
+      // A place's next copy waits for the place's last product while another one runs.
+      if constexpr (KEYS) {
+        for (int i = 0; i < n && ok; ++i) {
+          if (!(ok = full2(i))) break;
+          scores(C::kColY, i, 1, &bar->y, nullptr);
           if (i > 0 && !(ok = more1(i - 1 + P1))) break;
-          if (!(ok = full2(i + 1))) break;
-          scores(C::kColY + next * N, i + 1, 1, &bar->x[next], &bar->empty2[(i + 1) % P2]);
+          if (!(ok = arrived(&bar->p, i & 1))) break;
+          weighted(C::kColV, C::kColX, i, 1, &bar->empty2[i % P2]);
+          if (i + 1 < n) {
+            if (!(ok = full1(i + 1))) break;
+            scores(C::kColX, i + 1, 0, &bar->x[0], nullptr);
+          }
+          if (!(ok = more2(i + P2))) break;
+          if (!(ok = arrived(&bar->ds, i & 1))) break;
+          weighted(C::kColV + D, C::kColY, i, 0, &bar->empty1[i % P1]);
         }
-        if (!(ok = arrived(&bar->ds, i & 1))) break;
-        weighted(C::kColV, C::kColX + (i & 1) * N, i, 0, &bar->empty1[i % P1]);
-        if (i + 1 < n && !(ok = more2(i + 1 + P2))) break;
+      } else {
+        // dS of tiles i and i - 1 lie over X of them; Y of tile i + 1 over that of tile i - 1
+        if (ok && (ok = full2(0))) scores(C::kColY, 0, 1, &bar->x[0], &bar->empty2[0]);
+        if (ok) ok = more2(P2);
+        for (int i = 0; i < n && ok; ++i) {
+          const uint32_t next = (i + 1) & 1;
+          if (i + 1 < n) {
+            if (!(ok = full1(i + 1))) break;
+            scores(C::kColX + next * N, i + 1, 0, nullptr, nullptr);
+            if (i > 0 && !(ok = more1(i - 1 + P1))) break;
+            if (!(ok = full2(i + 1))) break;
+            scores(C::kColY + next * N, i + 1, 1, &bar->x[next], &bar->empty2[(i + 1) % P2]);
+          }
+          if (!(ok = arrived(&bar->ds, i & 1))) break;
+          weighted(C::kColV, C::kColX + (i & 1) * N, i, 0, &bar->empty1[i % P1]);
+          if (i + 1 < n && !(ok = more2(i + 1 + P2))) break;
+        }
       }
+      umma_commit(&bar->drain);  // products in flight end before the memory is freed
+      wait(&bar->drain, 0);
+      // every copy has landed before the CTA may end
+      if (own) wait(&bar->own, 0);
+      for (int i = max(0, loads1 - P1); i < loads1; ++i) wait(&bar->full1[i % P1], (i / P1) & 1);
+      for (int i = max(0, loads2 - P2); i < loads2; ++i) wait(&bar->full2[i % P2], (i / P2) & 1);
+      for (int i = max(0, infos_in - 2); i < infos_in; ++i) wait(&bar->info[i & 1], (i >> 1) & 1);
     }
-    if (elect_one()) umma_commit(&bar->drain);  // products in flight end before the memory is freed
-    __syncwarp();
-    wait(&bar->drain, 0);
-    // every copy has landed before the CTA may end
-    if (own) wait(&bar->own, 0);
-    for (int i = max(0, loads1 - P1); i < loads1; ++i) wait(&bar->full1[i % P1], (i / P1) & 1);
-    for (int i = max(0, loads2 - P2); i < loads2; ++i) wait(&bar->full2[i % P2], (i / P2) & 1);
-    for (int i = max(0, infos_in - 2); i < infos_in; ++i) wait(&bar->info[i & 1], (i >> 1) & 1);
     __syncwarp();
   } else if (warp < C::kMmaWarp) {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 224;");

@@ -10,8 +10,9 @@
 // one set of shuffles.  A warp walks tokens with the stride of the grid and adds its
 // dw up in registers; the CTAs' sums go through the workspace to a second kernel, launched
 // under the first, which adds them in one order.
-// 32768 tokens of 20 heads of 128, bf16: 111 us, 4.6 TB/s (176 us with loads just
-// ahead of their use, 126 with four passes' loads at once in registers).
+// 32768 tokens of 20 heads of 128, bf16: 103 us, 5.0 TB/s (176 us with loads just
+// ahead of their use, 126 with four passes' loads at once in registers, 110 with a pass at a time
+// from the ring).
 
 #include <algorithm>
 
@@ -23,9 +24,13 @@ namespace {
 
 constexpr int kWarps = 8;
 constexpr int kMostCtas = 1024;  // whose sums the workspace holds
-constexpr int kResident = 2;  // CTAs of an SM: with three the registers spill (the same call: 154 us)
+// CTAs of an SM: with three of the norm's the registers spill (the call above: 154 us); of the others' three take 20.5
+// us for 16384 x 24 x 64 bf16, two 21.6
+template <bool NORM>
+constexpr int kResident = NORM ? 2 : 3;
+constexpr int kPasses = 2;  // of a stage
 template <typename T, bool NORM>
-constexpr int kStages = (sizeof(T) == 2 ? 8 : 4) * (NORM ? 1 : 2);  // 8 KB a warp
+constexpr int kStages = NORM ? (sizeof(T) == 2 ? 4 : 3) : (sizeof(T) == 2 ? 8 : 4);  // 8 or 12 KB a warp
 
 using tcu::fma2, tcu::mul2, tcu::pack2, tcu::unpack2;
 
@@ -67,9 +72,9 @@ __device__ __forceinline__ void rotate_back8(uint64_t (&y)[4], const uint64_t (&
 }
 
 // An item is a token's rows [part * passes * rows, ...): its query rows first, then its key rows.  A warp walks the
-// passes of its items, whose rows come through a ring of its own in shared memory, kStages passes ahead.
+// passes of its items, whose rows come through a ring of its own in shared memory, kStages times kPasses passes.
 template <typename T, bool VEC, int MODE, bool NORM>
-__global__ void __launch_bounds__(32 * kWarps, MODE == kRotAny ? 1 : kResident)
+__global__ void __launch_bounds__(32 * kWarps, MODE == kRotAny ? 1 : kResident<NORM>)
     qk_norm_rope_grad_kernel(NormGradArgs a, int passes, int parts) {
   const HeadArgs& h = a.h;
   if (NORM && a.partial) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
@@ -78,10 +83,11 @@ __global__ void __launch_bounds__(32 * kWarps, MODE == kRotAny ? 1 : kResident)
   const int li = lane & ((1 << ls) - 1);
   const Pieces at = pieces_of<MODE>(h, li);
   constexpr bool kSplit = MODE == kRotHalf, kRot = MODE == kRotHalf || MODE == kRotInterleaved;
-  constexpr int S = kStages<T, NORM>;
+  constexpr int S = kStages<T, NORM>, K = MODE == kRotAny ? 1 : kPasses;
+  constexpr int kPass = NORM ? 512 : 256;  // elements of a pass: 256 of dy, 256 of x
   const int Hq = a.H[0], all = a.H[0] + a.H[1];
   extern __shared__ float4 ring_smem[];
-  T* ring = reinterpret_cast<T*>(ring_smem) + warp * (S * (NORM ? 512 : 256));  // a stage: 256 elements of dy, 256 of x
+  T* ring = reinterpret_cast<T*>(ring_smem) + warp * (S * K * kPass);
   __shared__ float4 weights[2][32][2];  // a lane's 8 of the queries' and of the keys' (the same in every warp)
   uint64_t dwq[4], dwk[4];
 #pragma unroll
@@ -123,14 +129,17 @@ __global__ void __launch_bounds__(32 * kWarps, MODE == kRotAny ? 1 : kResident)
         ahead_r = ahead_part * passes * rows + (lane >> ls);
         ahead_end = min((ahead_part + 1) * passes * rows, all);
       }
-      // a lane past the rows: zeros
-      const bool live = ahead_r < ahead_end, of_q = live ? ahead_r < Hq : Hq > 0;
-      const uint32_t to = to0 + ahead_st * ((NORM ? 512 : 256) * sizeof(T));
-      const int64_t off = (live ? ahead_r : of_q ? 0 : Hq) * row_bytes + own;
-      copy8<T>(to, (of_q ? yq : yk) + off, live ? 16 : 0);
-      if (NORM) copy8<T>(to + 256 * sizeof(T), (of_q ? xq : xk) + off, live ? 16 : 0);
-      ahead_r += rows;
-      if (++ahead_p == passes) ahead_p = 0, advance(ahead, ahead_part);
+#pragma unroll
+      for (int k = 0; k < K; ++k) {
+        // a lane past the rows: zeros
+        const bool live = ahead_r < ahead_end, of_q = live ? ahead_r < Hq : Hq > 0;
+        const uint32_t to = to0 + (ahead_st * K + k) * (kPass * sizeof(T));
+        const int64_t off = (live ? ahead_r : of_q ? 0 : Hq) * row_bytes + own;
+        copy8<T>(to, (of_q ? yq : yk) + off, live ? 16 : 0);
+        if (NORM) copy8<T>(to + 256 * sizeof(T), (of_q ? xq : xk) + off, live ? 16 : 0);
+        ahead_r += rows;
+      }
+      if ((ahead_p += K) >= passes) ahead_p = 0, advance(ahead, ahead_part);
     }
     asm volatile("cp.async.commit_group;" ::: "memory");
     if (++ahead_st == S) ahead_st = 0;
@@ -167,86 +176,92 @@ __global__ void __launch_bounds__(32 * kWarps, MODE == kRotAny ? 1 : kResident)
     tok = tok1, part = part1;
     advance(tok1, part1);
     pos1 = position(tok1);
-    for (int p = 0; p < passes; ++p) {
-      const int r = first + p * rows + (lane >> ls);
-      const bool live = r < end, of_q = r < Hq;
-      uint64_t x[4] = {0, 0, 0, 0}, y[4] = {0, 0, 0, 0};
-      if constexpr (MODE == kRotAny) {
-        const int s = of_q ? 0 : 1;
-        if (live) {
-          unpack8(load8<VEC, kSplit>(reinterpret_cast<const T*>(row0(a.dy[s], tok0, s)) + r * h.d, at), y);
-          if (NORM) unpack8(load8<VEC, kSplit>(reinterpret_cast<const T*>(row0(a.x[s], tok0, s)) + r * h.d, at), x);
-        }
-      } else {
+    for (int p = 0; p < passes; p += K) {
+      const T* from = nullptr;
+      if constexpr (MODE != kRotAny) {
         asm volatile("cp.async.wait_group %0;" ::"n"(S - 2) : "memory");
         __syncwarp();  // the others' copies are there, and they have read the stage that is copied into next
-        const T* from = ring + st * (NORM ? 512 : 256) + (lane >> ls) * h.d;
+        from = ring + st * (K * kPass) + (lane >> ls) * h.d;
         if (++st == S) st = 0;
         copy();
-        unpack8(load8<true, kSplit>(from, at), y);
-        if (NORM) unpack8(load8<true, kSplit>(from + 256, at), x);
       }
-      if constexpr (MODE == kRotAny) {
-        const T* src = reinterpret_cast<const T*>(row0(a.dy[of_q ? 0 : 1], tok0, of_q ? 0 : 1)) + r * h.d;
-        const int half = h.rot >> 1;
-        const bool hl = h.layout == FALCON_ROPE_HALF;
-        float z[8];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const int c = (i < 4 ? at.a : at.b - 4) + i, j = hl ? (c < half ? c : c - half) : c >> 1;  // element, its pair
-          const bool low = hl ? c < half : !(c & 1);
-          float mine[2];
-          unpack2(y[i >> 1], mine[0], mine[1]);
-          z[i] = mine[i & 1];
-          if (live && c < h.rot) {
-            const float other = to_f32(src[hl ? (low ? c + half : c - half) : c ^ 1]);
-            const float2 t = row ? __ldg(row + j) : make_float2(__int_as_float(0x7fffffff), 0.f);
-            z[i] = z[i] * t.x + (low ? t.y : -t.y) * other;
+      for (int k = 0; k < K; ++k) {
+        const int r = first + (p + k) * rows + (lane >> ls);
+        const bool live = r < end, of_q = r < Hq;
+        uint64_t x[4] = {0, 0, 0, 0}, y[4] = {0, 0, 0, 0};
+        if constexpr (MODE == kRotAny) {
+          const int s = of_q ? 0 : 1;
+          if (live) {
+            unpack8(load8<VEC, kSplit>(reinterpret_cast<const T*>(row0(a.dy[s], tok0, s)) + r * h.d, at), y);
+            if (NORM) unpack8(load8<VEC, kSplit>(reinterpret_cast<const T*>(row0(a.x[s], tok0, s)) + r * h.d, at), x);
+          }
+        } else {
+          unpack8(load8<true, kSplit>(from + k * kPass, at), y);
+          if (NORM) unpack8(load8<true, kSplit>(from + k * kPass + 256, at), x);
+        }
+        if constexpr (MODE == kRotAny) {
+          const T* src = reinterpret_cast<const T*>(row0(a.dy[of_q ? 0 : 1], tok0, of_q ? 0 : 1)) + r * h.d;
+          const int half = h.rot >> 1;
+          const bool hl = h.layout == FALCON_ROPE_HALF;
+          float z[8];
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            const int c = (i < 4 ? at.a : at.b - 4) + i, j = hl ? (c < half ? c : c - half) : c >> 1;  // element, its pair
+            const bool low = hl ? c < half : !(c & 1);
+            float mine[2];
+            unpack2(y[i >> 1], mine[0], mine[1]);
+            z[i] = mine[i & 1];
+            if (live && c < h.rot) {
+              const float other = to_f32(src[hl ? (low ? c + half : c - half) : c ^ 1]);
+              const float2 t = row ? __ldg(row + j) : make_float2(__int_as_float(0x7fffffff), 0.f);
+              z[i] = z[i] * t.x + (low ? t.y : -t.y) * other;
+            }
+          }
+          __syncwarp();  // read before any lane writes the row in place
+#pragma unroll
+          for (int i = 0; i < 4; ++i) y[i] = pack2(z[2 * i], z[2 * i + 1]);
+        } else if (kRot && at.a < h.rot) {
+          rotate_back8<MODE>(y, co, si, ns);
+        }
+        if (NORM) {
+          const float4 w0 = weights[of_q ? 0 : 1][lane][0], w1 = weights[of_q ? 0 : 1][lane][1];
+          const uint64_t w[4] = {pack2(w0.x, w0.y), pack2(w0.z, w0.w), pack2(w1.x, w1.y), pack2(w1.z, w1.w)};
+          uint64_t v[4], xx = mul2(x[0], x[0]), vx;
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            v[i] = mul2(y[i], w[i]);
+            vx = i ? fma2(v[i], x[i], vx) : mul2(v[i], x[i]);
+            if (i) xx = fma2(x[i], x[i], xx);
+          }
+          float s0, s1, t0, t1;
+          unpack2(xx, s0, t0);
+          unpack2(vx, s1, t1);
+          s0 += t0, s1 += t1;
+          // over the d / 8 lanes: 2, 4, 8 or 16
+#pragma unroll
+          for (int m = 1; m < 16; m <<= 1) {
+            if (m >= 1 << ls) break;
+            s0 += __shfl_xor_sync(0xffffffffu, s0, m);
+            s1 += __shfl_xor_sync(0xffffffffu, s1, m);
+          }
+          const float rs = live ? rsqrtf(fmaf(s0, h.inv_d, h.eps)) : 0.f;
+          const float c = rs == 0.f ? 0.f : s1 * rs * h.inv_d;
+          const uint64_t rs2 = pack2(rs, rs), nc = pack2(-c, -c);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const uint64_t xr = mul2(x[i], rs2);
+            if (of_q) dwq[i] = fma2(y[i], xr, dwq[i]);
+            else dwk[i] = fma2(y[i], xr, dwk[i]);
+            y[i] = mul2(rs2, fma2(xr, nc, v[i]));
           }
         }
-        __syncwarp();  // read before any lane writes the row in place
+        if (live) {
+          float z[8];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) y[i] = pack2(z[2 * i], z[2 * i + 1]);
-      } else if (kRot && at.a < h.rot) {
-        rotate_back8<MODE>(y, co, si, ns);
-      }
-      if (NORM) {
-        const float4 w0 = weights[of_q ? 0 : 1][lane][0], w1 = weights[of_q ? 0 : 1][lane][1];
-        const uint64_t w[4] = {pack2(w0.x, w0.y), pack2(w0.z, w0.w), pack2(w1.x, w1.y), pack2(w1.z, w1.w)};
-        uint64_t v[4], xx = mul2(x[0], x[0]), vx;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          v[i] = mul2(y[i], w[i]);
-          vx = i ? fma2(v[i], x[i], vx) : mul2(v[i], x[i]);
-          if (i) xx = fma2(x[i], x[i], xx);
+          for (int i = 0; i < 4; ++i) unpack2(y[i], z[2 * i], z[2 * i + 1]);
+          store8<VEC, kSplit>(reinterpret_cast<T*>((of_q ? oq : ok) + static_cast<int64_t>(r) * row_bytes), at, z);
         }
-        float s0, s1, t0, t1;
-        unpack2(xx, s0, t0);
-        unpack2(vx, s1, t1);
-        s0 += t0, s1 += t1;
-        // over the d / 8 lanes: 2, 4, 8 or 16
-#pragma unroll
-        for (int m = 1; m < 16; m <<= 1) {
-          if (m >= 1 << ls) break;
-          s0 += __shfl_xor_sync(0xffffffffu, s0, m);
-          s1 += __shfl_xor_sync(0xffffffffu, s1, m);
-        }
-        const float rs = live ? rsqrtf(fmaf(s0, h.inv_d, h.eps)) : 0.f;
-        const float c = rs == 0.f ? 0.f : s1 * rs * h.inv_d;
-        const uint64_t rs2 = pack2(rs, rs), nc = pack2(-c, -c);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const uint64_t xr = mul2(x[i], rs2);
-          if (of_q) dwq[i] = fma2(y[i], xr, dwq[i]);
-          else dwk[i] = fma2(y[i], xr, dwk[i]);
-          y[i] = mul2(rs2, fma2(xr, nc, v[i]));
-        }
-      }
-      if (live) {
-        float z[8];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) unpack2(y[i], z[2 * i], z[2 * i + 1]);
-        store8<VEC, kSplit>(reinterpret_cast<T*>((of_q ? oq : ok) + static_cast<int64_t>(r) * row_bytes), at, z);
       }
     }
     row = row1;
@@ -314,13 +329,13 @@ int launch(NormGradArgs a, cudaStream_t s) {
     const int parts = static_cast<int>(a.tokens >= int64_t(32) * tcu::sm_count() ? 1 : (all_passes + 1) / 2);
     const int passes = static_cast<int>((all_passes + parts - 1) / parts);
     const int64_t want = (a.tokens * parts + kWarps - 1) / kWarps;
-    ctas = static_cast<int>(std::min<int64_t>(want, std::min(kResident * tcu::sm_count(), kMostCtas)));
+    ctas = static_cast<int>(std::min<int64_t>(want, std::min(kResident<NORM> * tcu::sm_count(), kMostCtas)));
     const RotMode mode = vec ? rot_mode(a.h) : kRotAny;
     const auto kern = mode == kRotNone ? qk_norm_rope_grad_kernel<T, true, kRotNone, NORM>
                       : mode == kRotHalf ? qk_norm_rope_grad_kernel<T, true, kRotHalf, NORM>
                       : mode == kRotInterleaved ? qk_norm_rope_grad_kernel<T, true, kRotInterleaved, NORM>
                                                 : qk_norm_rope_grad_kernel<T, false, kRotAny, NORM>;
-    const size_t smem = static_cast<size_t>(kWarps) * kStages<T, NORM> * (NORM ? 512 : 256) * sizeof(T);
+    const size_t smem = static_cast<size_t>(kWarps) * kStages<T, NORM> * kPasses * (NORM ? 512 : 256) * sizeof(T);
     if (!set_smem_limit(reinterpret_cast<const void*>(kern), smem)) return FALCON_ERR_CUDA;
     kern<<<ctas, 32 * kWarps, smem, s>>>(a, passes, parts);
     if (cudaGetLastError() != cudaSuccess) return FALCON_ERR_CUDA;

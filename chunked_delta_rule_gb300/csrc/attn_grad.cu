@@ -29,42 +29,45 @@ __device__ __forceinline__ uint2 three_parts(float x) {
   const float hi = __bfloat162float(__float2bfloat16_rn(x)), mid = __bfloat162float(__float2bfloat16_rn(x - hi));
   return make_uint2(tcu::pack_bf16(x, x - hi), tcu::pack_bf16(x - hi - mid, 0.f));
 }
-// A CTA takes 128 rows of one head: d / 8 lanes a row.
+// A CTA takes 128 rows of one head: d / 8 lanes a row, two rows' loads of each under way at once; then a thread a row.
+// Bound by memory: 13906 x 16 x 128 bf16, 26 us, 4.3 TB/s.
 template <typename T>
-__global__ void __launch_bounds__(256) attn_grad_sums_kernel(GradArgs g) {
+__global__ void __launch_bounds__(256, 6) attn_grad_sums_kernel(GradArgs g) {
   const PromptArgs& a = g.a;
   launch_dependents();
   if (blockIdx.x == 0 && threadIdx.x == 0) *static_cast<uint32_t*>(a.ws) = 0;  // the call's status
   const int h = static_cast<int>(blockIdx.x % a.Hq);
   const int64_t j = blockIdx.x / a.Hq;
-  const int2 x = packed_block(a.cu_q, a.B, kSumRows, static_cast<int>(j));
+  const int2 x = find_block(a.cu_q, a.B, kSumRows, static_cast<int>(j));
   const int64_t q0 = a.cu_q[x.x], q1 = a.cu_q[x.x + 1];
   if (x.y < 0 || q0 < 0 || q1 > a.tokens || x.y >= q1 - q0) return;
   const int lq = static_cast<int>(min(q1 - q0, static_cast<int64_t>(a.max_q)));
-  // packed_block deals a sequence's blocks out from the last; here block n of a sequence holds its rows 128 n ..
-  const int64_t n = x.y / kSumRows, at = first_block(q0, x.x) + n;
-  float* out = g.sums + row_sums(g.blocks, h, at);
+  const int rows = min(lq - x.y, kSumRows);  // live ones
+  __shared__ float dots[kSumRows];
+  float l = -INFINITY, dl = 0.f;  // of the thread's row
+  if (static_cast<int>(threadIdx.x) < rows) {
+    const int64_t i = (q0 + x.y + threadIdx.x) * a.Hq + h;
+    l = g.lse[i];
+    if (g.dlse) dl = g.dlse[i];
+  }
   const int ls = 28 - __clz(a.d), li = threadIdx.x & ((1 << ls) - 1), step = 256 >> ls;
   const Pieces p{li * 8, li * 8 + 4};
-  for (int r0 = threadIdx.x >> ls; r0 < kSumRows; r0 += 4 * step) {
-    // up to four rows' loads under way at once
-    Raw8<T> u[4], v[4];
+  const T* o = static_cast<const T*>(g.o.p) + (q0 + x.y) * g.o.stride + h * a.d;
+  const T* d_o = static_cast<const T*>(g.d_o.p) + (q0 + x.y) * g.d_o.stride + h * a.d;
+  for (int r0 = threadIdx.x >> ls; r0 < kSumRows; r0 += 2 * step) {
+    Raw8<T> u[2], v[2];
 #pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      const int i = x.y + r0 + k * step;
-      if (r0 + k * step >= kSumRows || i >= lq) continue;
-      const T* o = static_cast<const T*>(g.o.p) + (q0 + i) * g.o.stride + h * a.d;
-      const T* d_o = static_cast<const T*>(g.d_o.p) + (q0 + i) * g.d_o.stride + h * a.d;
-      u[k] = g.o.vec ? load8<true, false>(o, p) : load8<false, false>(o, p);
-      v[k] = g.d_o.vec ? load8<true, false>(d_o, p) : load8<false, false>(d_o, p);
+    for (int k = 0; k < 2; ++k) {
+      const int r = r0 + k * step;
+      if (r >= rows) continue;
+      u[k] = g.o.vec ? load8<true, false>(o + r * g.o.stride, p) : load8<false, false>(o + r * g.o.stride, p);
+      v[k] = g.d_o.vec ? load8<true, false>(d_o + r * g.d_o.stride, p) : load8<false, false>(d_o + r * g.d_o.stride, p);
     }
 #pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      const int r = r0 + k * step, i = x.y + r;
-      if (r >= kSumRows) break;
-      const bool live = i < lq;
+    for (int k = 0; k < 2; ++k) {
+      const int r = r0 + k * step;
       float s = 0.f;
-      if (live) {
+      if (r < rows) {
         float y[8], z[8];
         unpack8(u[k], y);
         unpack8(v[k], z);
@@ -72,27 +75,24 @@ __global__ void __launch_bounds__(256) attn_grad_sums_kernel(GradArgs g) {
         for (int e = 0; e < 8; ++e) s = fmaf(y[e], z[e], s);
       }
       for (int m = 1; m < 1 << ls; m <<= 1) s += __shfl_xor_sync(0xffffffffu, s, m);
-      if (li == 0) {
-        float lse = INFINITY;
-        if (live) {
-          const float l = g.lse[(q0 + i) * a.Hq + h];
-          if (g.dlse) s -= g.dlse[(q0 + i) * a.Hq + h];
-          lse = l == -INFINITY ? INFINITY : l == INFINITY ? __int_as_float(0x7fffffff) : l;
-          if (l == -INFINITY) s = 0.f;
-        }
-        out[r] = lse;
-        out[kSumRows + r] = s;
-        if (g.images) {
-          // no weight: as far down as bf16 goes short of an infinity, which would spoil the columns' zeros
-          const uint2 x = lse == INFINITY ? make_uint2(0xFF7Fu, 0u) : three_parts(-lse / a.scale), y = three_parts(-s);
-          uint4* to = reinterpret_cast<uint4*>(g.images + (static_cast<int64_t>(h) * g.blocks + at) * kImageBytes +
-                                               (r >> 3) * 256 + (r & 7) * 16);
-          to[0] = make_uint4(x.x, x.y, y.x, y.y);
-          to[8] = make_uint4(0u, 0u, 0u, 0u);
-        }
-      }
+      if (li == 0 && r < kSumRows) dots[r] = s;
     }
   }
+  __syncthreads();
+  const int r = threadIdx.x;
+  if (r >= kSumRows) return;
+  // find_block deals a sequence's blocks out from the last; here block n of a sequence holds its rows 128 n ..
+  const int64_t at = h * g.blocks + first_block(q0, x.x) + x.y / kSumRows;
+  const float lse = l == -INFINITY ? INFINITY : l == INFINITY ? __int_as_float(0x7fffffff) : l;
+  const float delta = l == -INFINITY ? 0.f : dots[r] - dl;
+  g.sums[row_sums(1, 0, at) + r] = lse;
+  g.sums[row_sums(1, 0, at) + kSumRows + r] = delta;
+  if (!g.images) return;
+  // no weight: as far down as bf16 goes short of an infinity, which would spoil the columns' zeros
+  const uint2 y = lse == INFINITY ? make_uint2(0xFF7Fu, 0u) : three_parts(-lse / a.scale), z = three_parts(-delta);
+  uint4* to = reinterpret_cast<uint4*>(g.images + at * kImageBytes + (r >> 3) * 256 + (r & 7) * 16);
+  to[0] = make_uint4(y.x, y.y, z.x, z.y);
+  to[8] = make_uint4(0u, 0u, 0u, 0u);
 }
 
 // ---------------------------------------------------------------- warp-level kernels

@@ -3,6 +3,7 @@
 // warp, straight from the definition.
 #pragma once
 
+#include <algorithm>
 #include <cmath>
 
 #include "attn_row.cuh"
@@ -202,16 +203,24 @@ __device__ __forceinline__ void store_row(T* out, const float (&x)[4], int d) {
 }
 
 // ---------------------------------------------------------------- a block's dK and dV by a cluster of CTAs
-// Clusters until the longest CTA (the keys that every query of all heads sees) takes no longer than all tiles of N queries
-// of both kernels dealt out evenly over `slots` CTAs, sequences taken as of one length; a tile of dQ costs some 0.7 of
-// one of dK and dV.
-inline int keys_split(const PromptArgs& a, int N, int slots) {
+// How many CTAs take a block of 128 keys together.  In units of a tile of N queries: the call takes as long as its longest
+// CTA (the keys that every query of all heads sees; sequences taken as half as long again as their mean) or as all
+// tiles of both kernels dealt out over `slots` CTAs, a tile of dQ at 0.7 of one of dK and dV.  A CTA costs `begin` tiles to begin
+// and end, one of a cluster `join`.
+// (us, unsplit and 2, 4, 8 CTAs: 2048 tokens, 12 heads of 64: 41, 52; 2048 tokens, 16 over 4 heads of 128: 93, 60, 71;
+// 4 x 300 after 500 keys, 8 over 1 heads of 32: 41, 31, 25, 21; 8 x 300: 49, 37, 34, 35.)
+inline int keys_split(const PromptArgs& a, int N, int slots, double begin, double join) {
   const double lq = static_cast<double>(a.tokens) / a.B, lk = static_cast<double>(a.k_tokens) / a.B;
-  const double longest = std::ceil(lq / N) * (a.Hq / a.Hkv);
+  const double G = a.Hq / a.Hkv, longest = std::ceil((a.B > 1 ? 1.5 : 1.0) * lq / N) * G;
   const double seen = lk >= lq ? 1.0 - 0.5 * lq / lk : 0.5 * lk / lq;  // of all pairs
-  const double even = 1.7 * longest * seen * std::ceil(lk / kSumRows) * a.B * a.Hkv / slots;
+  const double blocks = std::ceil(lk / kSumRows) * a.B * a.Hkv;
+  const double tiles = 1.7 * blocks * std::ceil(lq / N) * G * seen + begin * std::ceil(lq / kSumRows) * a.B * a.Hq;
   int split = 1;
-  while (split < 8 && longest > even * split && longest >= 8 * split) split *= 2;
+  double best = std::max(longest + begin, (tiles + blocks * begin) / slots);
+  for (int s = 2; s <= 8; s *= 2) {
+    const double cost = std::max(longest / s + join, (tiles + blocks * s * join) / slots);
+    if (cost < best) best = cost, split = s;
+  }
   return split;
 }
 // every thread of the cluster's CTAs
@@ -236,29 +245,36 @@ __device__ __forceinline__ uint32_t load_peer(uint32_t addr) {
   asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(addr) : "memory");
   return v;
 }
-// The sums of a block of 128 keys from the cluster's CTAs, which each left theirs in fp32 at `smem`: rows of dV, then of dK,
-// D numbers each, 16-byte pieces swizzled by row.  Added in the CTAs' order, an equal share of the rows by each CTA;
-// by `threads` threads, all others of the CTA pass two cluster barriers meanwhile.  again(i, dk, dv): row i from the
-// definition.
-template <typename T, int D, int THREADS, typename F>
-__device__ __forceinline__ void cluster_sums(const GradArgs& g, const uint8_t* smem, const uint32_t* failed,
-                                             uint32_t (&bad)[2][4], int split, int rank, int row0, int rows, int64_t k0,
-                                             int head, int d, F again) {
-  const int tid = threadIdx.x;
-  cluster_barrier();
-  bool fine = true;
-  for (int s = 0; s < split; ++s) fine = fine && load_peer(peer_smem(tc::smem_u32(failed), s)) == 0;
-  if (fine) {
-    const int share = kSumRows / split, rs = rank * share;
-    for (int x = tid; x < 2 * share * (D / 4); x += THREADS) {
-      const int c = x % (D / 4), rr = rs + x / (D / 4) % share, out = x / (D / 4) / share;  // out: dV, dK
-      if (row0 + rr >= rows || 4 * c >= d) continue;
-      const uint32_t at = tc::smem_u32(smem) + out * (kSumRows * D * 4) + rr * (D * 4) + ((c ^ (rr & 7)) << 4);
-      float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
-      for (int s = 0; s < split; ++s) {
-        const float4 y = load_peer4(peer_smem(at, s));
-        sum.x += y.x, sum.y += y.y, sum.z += y.z, sum.w += y.w;
-      }
+// This CTA's share of the rows of a block's dV and dK, added up over the SPLIT CTAs in their order; eight loads of a thread
+// are under way at once (the CTAs' shared memory is far: one after another they took some 5 us).
+template <typename T, int D, int THREADS, int SPLIT>
+__device__ __forceinline__ void add_cluster(const GradArgs& g, uint32_t smem, uint32_t (&bad)[2][4], int rank, int row0,
+                                            int rows, int64_t k0, int head, int d) {
+  constexpr int kShare = kSumRows / SPLIT, kPieces = D / 4, kItems = 2 * kShare * kPieces / THREADS, U = 8 / SPLIT;
+  static_assert(kItems * THREADS == 2 * kShare * kPieces && (kItems % U == 0 || kItems < U), "whole rounds");
+  const int rs = rank * kShare;
+  uint32_t peer[SPLIT];
+#pragma unroll
+  for (int s = 0; s < SPLIT; ++s) peer[s] = peer_smem(smem, s);
+#pragma unroll 1
+  for (int i0 = 0; i0 < kItems; i0 += U) {
+    float4 y[U][SPLIT];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      if (i0 + u >= kItems) break;
+      const int x = (i0 + u) * THREADS + threadIdx.x, c = x % kPieces, rr = rs + x / kPieces % kShare, out = x / kPieces / kShare;
+      const uint32_t at = out * (kSumRows * D * 4) + rr * (D * 4) + ((c ^ (rr & 7)) << 4);
+#pragma unroll
+      for (int s = 0; s < SPLIT; ++s) y[u][s] = load_peer4(peer[s] + at);
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      if (i0 + u >= kItems) break;
+      const int x = (i0 + u) * THREADS + threadIdx.x, c = x % kPieces, rr = rs + x / kPieces % kShare, out = x / kPieces / kShare;
+      if (row0 + rr >= rows || 4 * c >= d) continue;  // out: dV, dK
+      float4 sum = y[u][0];
+#pragma unroll
+      for (int s = 1; s < SPLIT; ++s) sum.x += y[u][s].x, sum.y += y[u][s].y, sum.z += y[u][s].z, sum.w += y[u][s].w;
       const float f = out ? g.a.scale : 1.f;
       sum.x *= f, sum.y *= f, sum.z *= f, sum.w *= f;
       const float rest = fmaf(sum.x, 0.f, fmaf(sum.y, 0.f, fmaf(sum.z, 0.f, sum.w * 0.f)));
@@ -272,6 +288,25 @@ __device__ __forceinline__ void cluster_sums(const GradArgs& g, const uint8_t* s
       else
         dst[0] = sum.x, dst[1] = sum.y, dst[2] = sum.z, dst[3] = sum.w;
     }
+  }
+}
+// The sums of a block of 128 keys from the cluster's CTAs, which each left theirs in fp32 at `smem`: rows of dV, then of dK,
+// D numbers each, 16-byte pieces swizzled by row.  By `THREADS` threads, all others of the CTA pass two cluster barriers
+// meanwhile.  again(i, dk, dv): row i from the definition.
+template <typename T, int D, int THREADS, typename F>
+__device__ __forceinline__ void cluster_sums(const GradArgs& g, const uint8_t* smem, const uint32_t* failed,
+                                             uint32_t (&bad)[2][4], int split, int rank, int row0, int rows, int64_t k0,
+                                             int head, int d, F again) {
+  const int tid = threadIdx.x;
+  cluster_barrier();
+  bool fine = true;
+  for (int s = 0; s < split; ++s) fine = fine && load_peer(peer_smem(tc::smem_u32(failed), s)) == 0;
+  if (fine) {
+    const int share = kSumRows / split, rs = rank * share;
+    const uint32_t at = tc::smem_u32(smem);
+    if (split == 2) add_cluster<T, D, THREADS, 2>(g, at, bad, rank, row0, rows, k0, head, d);
+    else if (split == 4) add_cluster<T, D, THREADS, 4>(g, at, bad, rank, row0, rows, k0, head, d);
+    else add_cluster<T, D, THREADS, 8>(g, at, bad, rank, row0, rows, k0, head, d);
     tcu::named_bar(1, THREADS);
     for (int x = tid >> 5; x < 2 * share; x += THREADS / 32) {
       const int rr = rs + x % share, out = x / share;

@@ -589,7 +589,7 @@ int launch_d(const GradArgs& g, cudaStream_t s) {
         !maps(a.q, a.tokens, a.Hq, N, m + 2) || !maps(g.d_o, a.tokens, a.Hq, N, m + 3))
       return FALCON_ERR_CUDA;
     const int64_t ctas = blocks * a.Hkv;
-    t.split = keys_split(a, N, sm_count() * Cfg<D, true>::kCtas);
+    t.split = keys_split(a, N, sm_count() * Cfg<D, true>::kCtas, D == 64 ? 4 : 2, D == 64 ? 14 : 9);
     const int st = launch_kernel<D, true>(t, ctas, m, s);
     if (st != FALCON_OK) return st;
     t.split = 1;

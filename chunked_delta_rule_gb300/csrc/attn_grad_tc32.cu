@@ -816,7 +816,7 @@ int launch_d(const GradArgs& g, cudaStream_t s) {
   t.split = 1;
   if (g.dk.p && k_ctas) {  // first: its CTAs run longest
     const int64_t blocks = a.k_tokens / kTile + a.B;
-    t.split = keys_split(a, kPast, sm_count());
+    t.split = keys_split(a, kPast, sm_count(), 3, 8);
     const int st = blocks > INT32_MAX / a.Hkv ? FALCON_ERR_UNSUPPORTED : launch_kernel<D, true>(t, blocks * a.Hkv, s);
     if (st != FALCON_OK) return st;
     t.split = 1;

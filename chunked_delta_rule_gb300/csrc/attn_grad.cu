@@ -1,6 +1,6 @@
-// Gradient of causal attention over packed prompts where the tcgen05 kernels do not
-// go (fp32, rows off the 16-byte boundaries, a few short prompts), and the rows'
-// sums that every kernel of the gradient reads.
+// Gradient of causal attention over packed prompts: the rows' sums that the bf16
+// kernels read, and the products where the tcgen05 kernels do not go (bf16 rows off
+// the 16-byte boundaries).
 //
 //   P = exp(scale Q K^T - log sum),  dS = P (dO V^T - D),  D = sum_c dO_c o_c - dlse
 //   dV = P^T dO,  dK = scale dS^T Q,  dQ = scale dS K
@@ -10,8 +10,8 @@
 // of one head and walks their keys (dQ), one of the second 64 keys of a key head and
 // walks the queries of all its heads (dK by four of its warps, dV by the other four).
 // Rows of the tile that a CTA owns lie in shared memory throughout, the others come 64 at a
-// time.  Products are warp-level tf32 MMAs as in the forward: fp32 operands in two
-// parts, a tile's products in sums of their own; bf16 weights are rounded to 11 bits.
+// time.  Products are warp-level tf32 MMAs as in the forward; P and dS are rounded to 11
+// bits.  Bound by the instructions around the MMAs: 8 x 2048 tokens, 12 heads of 64, 2.3 ms.
 //
 // A masked weight is 0, but 0 times an infinite or NaN value of a row that the
 // owner does not see would spoil it.  A row of a result that is not finite is
@@ -23,6 +23,8 @@
 namespace falcon {
 namespace {
 
+using T = __nv_bfloat16;
+
 // ---------------------------------------------------------------- sums of the rows
 // x as three bf16 numbers (24 bits), packed in pairs
 __device__ __forceinline__ uint2 three_parts(float x) {
@@ -31,7 +33,6 @@ __device__ __forceinline__ uint2 three_parts(float x) {
 }
 // A CTA takes 128 rows of one head: d / 8 lanes a row, two rows' loads of each under way at once; then a thread a row.
 // Bound by memory: 13906 x 16 x 128 bf16, 26 us, 4.3 TB/s.
-template <typename T>
 __global__ void __launch_bounds__(256, 6) attn_grad_sums_kernel(GradArgs g) {
   const PromptArgs& a = g.a;
   launch_dependents();
@@ -99,98 +100,47 @@ __global__ void __launch_bounds__(256, 6) attn_grad_sums_kernel(GradArgs g) {
 constexpr int kRows = kMmaRows, NT = kRows / 8;
 
 // x (16 rows of a warp x 64) = A B^T, A and B rows of D in shared memory
-template <int NP, int D>
+template <int D>
 __device__ __forceinline__ void rows_product(float (&x)[NT][4], const float* A, const float* Bm, int gid, int tig) {
   constexpr int LD = D + 4;
-  float low[NT][4];  // fp32: the small products apart
 #pragma unroll
   for (int t = 0; t < NT; ++t)
 #pragma unroll
-    for (int e = 0; e < 4; ++e) x[t][e] = low[t][e] = 0.f;
+    for (int e = 0; e < 4; ++e) x[t][e] = 0.f;
 #pragma unroll 2
   for (int ks = 0; ks < D / 8; ++ks) {
-    uint32_t af[NP][4];
     const float* qa = A + gid * LD + ks * 8 + tig;
-    const float av[4] = {qa[0], qa[8 * LD], qa[4], qa[8 * LD + 4]};
-#pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      uint32_t w[NP];
-      split<NP>(av[e], w);
-#pragma unroll
-      for (int p = 0; p < NP; ++p) af[p][e] = w[p];
-    }
+    const uint32_t af[4] = {__float_as_uint(qa[0]), __float_as_uint(qa[8 * LD]), __float_as_uint(qa[4]),
+                            __float_as_uint(qa[8 * LD + 4])};
 #pragma unroll
     for (int t = 0; t < NT; ++t) {
       const float* kb = Bm + (t * 8 + gid) * LD + ks * 8 + tig;
-      uint32_t bf[NP][2];
-#pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        uint32_t w[NP];
-        split<NP>(kb[4 * e], w);
-#pragma unroll
-        for (int p = 0; p < NP; ++p) bf[p][e] = w[p];
-      }
-      tc::mma_tf32_16x8x8(x[t], af[0], bf[0]);
-      if (NP == 2) {
-        tc::mma_tf32_16x8x8(low[t], af[0], bf[NP - 1]);
-        tc::mma_tf32_16x8x8(low[t], af[NP - 1], bf[0]);
-      }
+      const uint32_t bf[2] = {__float_as_uint(kb[0]), __float_as_uint(kb[4])};
+      tc::mma_tf32_16x8x8(x[t], af, bf);
     }
-  }
-  if (NP == 2) {
-#pragma unroll
-    for (int t = 0; t < NT; ++t)
-#pragma unroll
-      for (int e = 0; e < 4; ++e) x[t][e] += low[t][e];
   }
 }
 
 // acc (16 rows x D) += W B: W the warp's 16 x 64 weights as rows_product leaves them, B 64 rows of D.  Column 2c of a
 // group of 8 takes the place of column c, 2c + 1 that of c + 4, in both operands.
-template <int NP, int D>
+template <int D>
 __device__ __forceinline__ void add_product(float (&acc)[D / 8][4], const float (&w)[NT][4], const float* Bm, int gid,
                                             int tig) {
   constexpr int LD = D + 4;
-  float part[D / 8][4];  // fp32: a tile's products in sums of their own
-#pragma unroll
-  for (int i = 0; i < D / 8; ++i)
-#pragma unroll
-    for (int e = 0; e < 4; ++e) part[i][e] = 0.f;
 #pragma unroll
   for (int t = 0; t < NT; ++t) {
-    uint32_t pf[NP][4];
-    const float pv[4] = {w[t][0], w[t][2], w[t][1], w[t][3]};
-#pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      uint32_t x[NP];
-      split<NP>(NP == 1 ? __uint_as_float(tc::to_tf32(pv[e])) : pv[e], x);
-#pragma unroll
-      for (int p = 0; p < NP; ++p) pf[p][e] = x[p];
-    }
+    const uint32_t pf[4] = {tc::to_tf32(w[t][0]), tc::to_tf32(w[t][2]), tc::to_tf32(w[t][1]), tc::to_tf32(w[t][3])};
 #pragma unroll
     for (int i = 0; i < D / 8; ++i) {
       const float* vb = Bm + (t * 8 + 2 * tig) * LD + i * 8 + gid;
-      uint32_t bf[NP][2];
-#pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        uint32_t x[NP];
-        split<NP>(vb[e * LD], x);
-#pragma unroll
-        for (int p = 0; p < NP; ++p) bf[p][e] = x[p];
-      }
-      product<NP>(NP == 2 ? part[i] : acc[i], pf, bf);
+      const uint32_t bf[2] = {__float_as_uint(vb[0]), __float_as_uint(vb[LD])};
+      tc::mma_tf32_16x8x8(acc[i], pf, bf);
     }
-  }
-  if (NP == 2) {
-#pragma unroll
-    for (int i = 0; i < D / 8; ++i)
-#pragma unroll
-      for (int e = 0; e < 4; ++e) acc[i][e] += part[i][e];
   }
 }
 
 // Rows of a warp's sums to their places (out: row 0 of the block's), and which of this thread's two rows are not finite.
-template <typename T, int D>
+template <int D>
 __device__ __forceinline__ void store_sums(const float (&acc)[D / 8][4], float f, T* out, int64_t stride, int rows, int r0,
                                            int tig, bool (&bad)[2]) {
 #pragma unroll
@@ -210,9 +160,9 @@ __device__ __forceinline__ void store_sums(const float (&acc)[D / 8][4], float f
 }
 
 // dQ: a CTA takes 64 queries of one head
-template <typename T, int D>
+template <int D>
 __global__ void __launch_bounds__(128) attn_grad_queries_kernel(GradArgs g, int qblocks, bool packed) {
-  constexpr int NP = sizeof(T) == 4 ? 2 : 1, LD = D + 4;
+  constexpr int LD = D + 4;
   const PromptArgs& a = g.a;
   extern __shared__ float smem[];
   float *sq = smem, *sg = sq + kRows * LD, *sk = sg + kRows * LD, *sv = sk + kRows * LD;
@@ -253,8 +203,8 @@ __global__ void __launch_bounds__(128) attn_grad_queries_kernel(GradArgs g, int 
     stage_rows<T, D, 128>(sv, v, a.v.stride, a.v.vec, j0, lk);
     __syncthreads();
     float p[NT][4], y[NT][4];
-    rows_product<NP, D>(p, sq + warp * 16 * LD, sk, gid, tig);
-    rows_product<NP, D>(y, sg + warp * 16 * LD, sv, gid, tig);
+    rows_product<D>(p, sq + warp * 16 * LD, sk, gid, tig);
+    rows_product<D>(y, sg + warp * 16 * LD, sv, gid, tig);
 #pragma unroll
     for (int t = 0; t < NT; ++t)
 #pragma unroll
@@ -264,11 +214,11 @@ __global__ void __launch_bounds__(128) attn_grad_queries_kernel(GradArgs g, int 
         const float w = ex2(fmaf(p[t][e], a.scale, -lse[i]) * kLog2e);
         y[t][e] = c < min(row0 + r0 + 8 * i + off + 1, lk) ? w * (y[t][e] - delta[i]) : 0.f;
       }
-    add_product<NP, D>(acc, y, sk, gid, tig);
+    add_product<D>(acc, y, sk, gid, tig);
   }
   bool bad[2];
   T* out = static_cast<T*>(g.dq.p) + (q0 + row0) * g.dq.stride + static_cast<int64_t>(h) * D;
-  store_sums<T, D>(acc, a.scale, out, g.dq.stride, lq - row0, r0, tig, bad);
+  store_sums<D>(acc, a.scale, out, g.dq.stride, lq - row0, r0, tig, bad);
   __syncwarp();
 #pragma unroll
   for (int i = 0; i < 2; ++i)
@@ -283,9 +233,9 @@ __global__ void __launch_bounds__(128) attn_grad_queries_kernel(GradArgs g, int 
 }
 
 // dK and dV: a CTA takes 64 keys of a key head; warps 0 to 3 form dV, 4 to 7 dK
-template <typename T, int D>
+template <int D>
 __global__ void __launch_bounds__(256) attn_grad_keys_kernel(GradArgs g) {
-  constexpr int NP = sizeof(T) == 4 ? 2 : 1, LD = D + 4;
+  constexpr int LD = D + 4;
   const PromptArgs& a = g.a;
   extern __shared__ float smem[];
   float *sk = smem, *sv = sk + kRows * LD, *sq = sv + kRows * LD, *sg = sq + kRows * LD, *ss = sg + kRows * LD;
@@ -327,7 +277,7 @@ __global__ void __launch_bounds__(256) attn_grad_keys_kernel(GradArgs g) {
       }
       __syncthreads();
       float p[NT][4];
-      rows_product<NP, D>(p, sk + warp * 16 * LD, sq, gid, tig);
+      rows_product<D>(p, sk + warp * 16 * LD, sq, gid, tig);
 #pragma unroll
       for (int t = 0; t < NT; ++t)
 #pragma unroll
@@ -338,7 +288,7 @@ __global__ void __launch_bounds__(256) attn_grad_keys_kernel(GradArgs g) {
         }
       if (of_k) {
         float y[NT][4];
-        rows_product<NP, D>(y, sv + warp * 16 * LD, sg, gid, tig);
+        rows_product<D>(y, sv + warp * 16 * LD, sg, gid, tig);
 #pragma unroll
         for (int t = 0; t < NT; ++t)
 #pragma unroll
@@ -347,12 +297,12 @@ __global__ void __launch_bounds__(256) attn_grad_keys_kernel(GradArgs g) {
             p[t][e] = row0 + r0 + 8 * (e >> 1) <= i0 + c + off && i0 + c < lq ? p[t][e] * (y[t][e] - ss[kRows + c]) : 0.f;
           }
       }
-      add_product<NP, D>(acc, p, of_k ? sq : sg, gid, tig);
+      add_product<D>(acc, p, of_k ? sq : sg, gid, tig);
     }
   bool bad[2];
   const RowsOut& to = of_k ? g.dk : g.dv;
   T* out = static_cast<T*>(to.p) + (k0 + row0) * to.stride + static_cast<int64_t>(hk) * D;
-  store_sums<T, D>(acc, of_k ? a.scale : 1.f, out, to.stride, lk - row0, r0, tig, bad);
+  store_sums<D>(acc, of_k ? a.scale : 1.f, out, to.stride, lk - row0, r0, tig, bad);
   __syncwarp();
 #pragma unroll
   for (int i = 0; i < 2; ++i)
@@ -366,7 +316,7 @@ __global__ void __launch_bounds__(256) attn_grad_keys_kernel(GradArgs g) {
     }
 }
 
-template <typename T, int D>
+template <int D>
 int launch(const GradArgs& g, cudaStream_t s) {
   const PromptArgs& a = g.a;
   constexpr int LD = D + 4;
@@ -374,7 +324,7 @@ int launch(const GradArgs& g, cudaStream_t s) {
     const PromptGrid pg = prompt_grid(a, kRows);
     if (pg.blocks < 1 || pg.blocks > INT32_MAX / a.Hq) return FALCON_ERR_UNSUPPORTED;
     constexpr size_t smem = static_cast<size_t>(4 * kRows * LD) * 4;
-    const auto kern = attn_grad_queries_kernel<T, D>;
+    const auto kern = attn_grad_queries_kernel<D>;
     if (!set_smem_limit(reinterpret_cast<const void*>(kern), smem)) return FALCON_ERR_CUDA;
     kern<<<static_cast<unsigned>(pg.blocks * a.Hq), 128, smem, s>>>(g, static_cast<int>(pg.blocks / a.B), pg.packed);
     if (cudaGetLastError() != cudaSuccess) return FALCON_ERR_CUDA;
@@ -383,7 +333,7 @@ int launch(const GradArgs& g, cudaStream_t s) {
     const int64_t blocks = a.k_tokens / kRows + a.B;
     if (blocks > INT32_MAX / a.Hkv) return FALCON_ERR_UNSUPPORTED;
     constexpr size_t smem = static_cast<size_t>(4 * kRows * LD + 2 * kRows) * 4;
-    const auto kern = attn_grad_keys_kernel<T, D>;
+    const auto kern = attn_grad_keys_kernel<D>;
     if (!set_smem_limit(reinterpret_cast<const void*>(kern), smem)) return FALCON_ERR_CUDA;
     kern<<<static_cast<unsigned>(blocks * a.Hkv), 256, smem, s>>>(g);
     if (cudaGetLastError() != cudaSuccess) return FALCON_ERR_CUDA;
@@ -391,20 +341,19 @@ int launch(const GradArgs& g, cudaStream_t s) {
   return FALCON_OK;
 }
 
-template <typename T>
-int launch_t(const GradArgs& g, cudaStream_t s) {
+int launch_bf16(const GradArgs& g, cudaStream_t s) {
   const PromptArgs& a = g.a;
   if (a.tokens > 0 && a.max_q > 0) {
     if (g.blocks > INT32_MAX / a.Hq) return FALCON_ERR_UNSUPPORTED;
-    attn_grad_sums_kernel<T><<<static_cast<unsigned>(g.blocks * a.Hq), 256, 0, s>>>(g);
+    attn_grad_sums_kernel<<<static_cast<unsigned>(g.blocks * a.Hq), 256, 0, s>>>(g);
     if (cudaGetLastError() != cudaSuccess) return FALCON_ERR_CUDA;
   }
   if (g.images) return launch_attn_grad_tc(g, s);
   switch (a.d) {
-    case 16: return launch<T, 16>(g, s);
-    case 32: return launch<T, 32>(g, s);
-    case 64: return launch<T, 64>(g, s);
-    default: return launch<T, 128>(g, s);
+    case 16: return launch<16>(g, s);
+    case 32: return launch<32>(g, s);
+    case 64: return launch<64>(g, s);
+    default: return launch<128>(g, s);
   }
 }
 
@@ -419,7 +368,7 @@ int launch_attn_grad(const GradArgs& args, int dtype, cudaStream_t s) {
   if (dtype == FALCON_F32) return launch_attn_grad_tc32(args, s);
   GradArgs g = args;
   g.images = attn_grad_tc_supported(g, dtype) ? reinterpret_cast<uint8_t*>(g.sums + row_sums(g.blocks, g.a.Hq, 0)) : nullptr;
-  return launch_t<__nv_bfloat16>(g, s);
+  return launch_bf16(g, s);
 }
 
 }  // namespace falcon

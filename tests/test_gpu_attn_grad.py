@@ -4,8 +4,8 @@ Tolerances follow from the number formats, u = half a step: 2^-8 for bf16.  A is
 the sum of the absolute values of what an element of a gradient is the sum of
 (tests/attn_grad_ref.py).  bf16: the weights P are rounded once (u), dS once (u),
 o, which D is formed from, was rounded by the forward (u), the result is
-rounded once (u of itself): at most 3 u A + u |x|.  fp32: scores and dP are sums of up to
-128 products, each off by up to 2^-22 of the sum of absolute values; the
+rounded once (u of itself): at most 3 u A + u |x|.  fp32: operands, P and dS keep 22 bits (down to 2^-40 of
+their row's largest); scores and dP are sums of up to 128 products, each off by up to 2^-22 of the sum of absolute values; the
 scores' enter P through the exponential, times the largest sum of absolute values
 of a score, S: at most 2^-22 (2 S + 8) A for all of it, and 2^-21 A for the
 gradients' own sums over a tile and 2^-24 a tile after that.  Over a whole tensor roundings do
@@ -137,7 +137,7 @@ def test_large_and_small_scores(F, dtype, scale, size):
 
 def test_bits_do_not_change(F):
     """The same call twice, on another stream, and its halves alone."""
-    for dtype, d in (("bf16", 64), ("bf16", 128), ("f32", 64)):
+    for dtype, d in (("bf16", 64), ("bf16", 128), ("f32", 64), ("f32", 128)):
         lens = [700, 333, 128]
         q, k, v, dO = _inputs(lens, lens, 8, 2, d, dtype, 3)
         cu = _dev(_cu(lens))
@@ -181,13 +181,15 @@ def test_slices_of_fused_projections_and_gaps(F):
         assert (grad[:2] == 5).all() and (grad[-2:] == 5).all() and (grad[:, -1] == 5).all()
 
 
-@pytest.mark.parametrize("d", [64, 128])
-def test_odd_addresses(F, d):
-    """bf16 rows off the 16-byte boundaries, each operand in turn, agree with the aligned call's tolerances."""
-    lens, Hq, Hkv = [200, 77], 4, 2
-    q, k, v, dO = _inputs(lens, lens, Hq, Hkv, d, "bf16", 8)
+@pytest.mark.parametrize("dtype,lens,Hq,Hkv,d", [
+    ("bf16", [200, 77], 4, 2, 64), ("bf16", [200, 77], 4, 2, 128), ("bf16", [70], 2, 1, 16),
+    ("f32", [200, 77], 4, 2, 64), ("f32", [130], 2, 2, 128), ("f32", [700], 8, 1, 32),
+])
+def test_odd_addresses(F, dtype, lens, Hq, Hkv, d):
+    """Rows off the 16-byte boundaries, each operand in turn, agree with the aligned call's tolerances."""
+    q, k, v, dO = _inputs(lens, lens, Hq, Hkv, d, dtype, 8)
     cu = _cu(lens)
-    o, lse = _forward(F, q, k, v, _dev(cu), _dev(cu), 200)
+    o, lse = _forward(F, q, k, v, _dev(cu), _dev(cu), max(lens))
     _, _, want, A = attention_grad(q, k, v, cu, cu, d ** -0.5, dO)
 
     def odd(x):
@@ -199,8 +201,8 @@ def test_odd_addresses(F, d):
         args = [odd(x) if which == i else x for i, x in enumerate((q, k, v, o))]
         g = odd(dO) if which == 4 else dO
         out = {n: odd(torch.zeros_like(x)) for n, x in (("dq", q), ("dk", k), ("dv", v))} if which == 5 else None
-        got = F.attn_prompt_backward(*args, lse, g, _dev(cu), max_q=200, out=out)
-        _check(got, want, A, "bf16", _S(q, k, d ** -0.5))
+        got = F.attn_prompt_backward(*args, lse, g, _dev(cu), max_q=max(lens), out=out)
+        _check(got, want, A, dtype, _S(q, k, d ** -0.5))
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
@@ -237,12 +239,14 @@ def test_rows_behind_the_last_sequence_and_past_max_q(F, dtype):
     _check(got, want, A, dtype, _S(q[:-9], k[:-9], d ** -0.5))
 
 
-@pytest.mark.parametrize("dtype,d", [("bf16", 64), ("bf16", 128), ("bf16", 32), ("f32", 64)])
+@pytest.mark.parametrize("dtype,d,Hq,Hkv", [("bf16", 64, 2, 1), ("bf16", 128, 2, 1), ("bf16", 32, 2, 1), ("f32", 64, 2, 1),
+                                              ("f32", 128, 2, 1), ("f32", 16, 16, 1), ("f32", 128, 16, 1),
+                                              ("bf16", 64, 16, 1), ("bf16", 128, 16, 1)])
 @pytest.mark.parametrize("value", [math.nan, math.inf])
-def test_infinities_and_nan_reach_only_what_sees_them(F, dtype, d, value):
+def test_infinities_and_nan_reach_only_what_sees_them(F, dtype, d, Hq, Hkv, value):
     """A key's row at 60 of 150 is not finite: queries before it see none of it.  A query's gradient at 100 is not finite:
     keys after it are not touched by it.  And the next sequence's first rows are not finite."""
-    lens, Hq, Hkv = [150, 40], 2, 1
+    lens = [150, 40]
     cu = _cu(lens)
     for what in ("k", "v", "dO", "q", "next"):
         q, k, v, dO = _inputs(lens, lens, Hq, Hkv, d, dtype, 6)
@@ -271,6 +275,97 @@ def test_infinities_and_nan_reach_only_what_sees_them(F, dtype, d, value):
             assert ok[:first].all(), (what, name, (~ok).nonzero()[:4].tolist())
             if what == "k":
                 assert fine[:60].all() == (name == "dq"), name
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("lq,lk,Hq,Hkv,d", [
+    ([1500], [1500], 8, 1, 64), ([900], [1700], 16, 1, 128), ([700, 20, 333], [700, 20, 333], 12, 1, 32),
+    ([1100], [600], 8, 1, 128), ([300], [5], 16, 1, 64),
+])
+def test_keys_shared_by_several_ctas(F, dtype, lq, lk, Hq, Hkv, d):
+    """One key head: the queries of a block of keys are dealt out over a cluster, some of whose CTAs may have none."""
+    q, k, v, dO = _inputs(lq, lk, Hq, Hkv, d, dtype, 31)
+    cu_q, cu_k = _cu(lq), _cu(lk)
+    o, lse = _forward(F, q, k, v, _dev(cu_q), _dev(cu_k), max(lq))
+    got = F.attn_prompt_backward(q, k, v, o, lse, dO, _dev(cu_q), _dev(cu_k), max(lq))
+    _, _, want, A = attention_grad(q, k, v, cu_q, cu_k, d ** -0.5, dO)
+    _check(got, want, A, dtype, _S(q, k, d ** -0.5))
+    again = F.attn_prompt_backward(q, k, v, o, lse, dO, _dev(cu_q), _dev(cu_k), max(lq))
+    assert all(torch.equal(got[n], again[n]) for n in got)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("d", [64, 128])
+def test_rows_of_very_different_sizes(F, dtype, d):
+    """Rows of dO and of v scaled by powers of two between 2^-30 and 2^30, some rows of dO zero with a gradient of their log
+    sum: an error stays relative to what a sum is formed of.  (fp32's 2^-40 of a row's largest, times the largest of 64
+    terms, is below 2^-22 of A but for elements 2^-12 below their row's largest, which have 2^-20.)"""
+    lens = [260, 77]
+    q, k, v, dO = _inputs(lens, lens, 4, 2, d, dtype, 12)
+    g = torch.Generator().manual_seed(5)
+    for x in (v, dO):
+        x *= torch.exp2(torch.randint(-30, 31, (x.shape[0], 1, 1), generator=g).float()).cuda().to(x.dtype)
+    dO[5::7] = 0
+    dlse = _rand(q.shape[:2], "f32", 9)
+    cu = _cu(lens)
+    o, lse = _forward(F, q, k, v, _dev(cu), _dev(cu), 260)
+    got = F.attn_prompt_backward(q, k, v, o, lse, dO, _dev(cu), max_q=260, dlse=dlse)
+    _, _, want, A = attention_grad(q, k, v, cu, cu, d ** -0.5, dO, dlse)
+    S = _S(q, k, d ** -0.5)
+    for n in want:
+        tol = 3 * U * A[n] + U * want[n].abs() if dtype == "bf16" else (2.0 ** -22 * (2 * S + 8) + 2.0 ** -19) * A[n]
+        worst = ((got[n].double() - want[n]).abs() / (tol + 1e-30)).max().item()
+        assert worst <= 1.0, (n, worst)
+
+
+@pytest.mark.parametrize("dtype,d", [("bf16", 64), ("bf16", 128), ("f32", 64), ("f32", 128)])
+def test_calls_behind_one_another_over_one_workspace(F, dtype, d):
+    """Calls of different sizes queued without a wait between them: the kernels of a call overlap, those of two do not."""
+    calls, most = [], 0
+    for lens, Hq, Hkv in (([900], 8, 1), ([33, 150], 4, 4), ([512, 300], 6, 2), ([1], 2, 2)):
+        n = sum(lens)
+        q, k, v, dO = _inputs(lens, lens, Hq, Hkv, d, dtype, n)
+        cu = _dev(_cu(lens))
+        o, lse = _forward(F, q, k, v, cu, cu, max(lens))
+        p = F.AttnParams(B=len(lens), Hq=Hq, Hkv=Hkv, d=d, dtype=F.FALCON_BF16 if dtype == "bf16" else F.FALCON_F32,
+                         max_q=max(lens), tokens=n, k_tokens=n)
+        most = max(most, F.falcon_attn_prompt_backward_workspace_size(p))
+        want = F.attn_prompt_backward(q, k, v, o, lse, dO, cu, max_q=max(lens))
+        calls.append((p, (q, k, v, cu, cu, o, lse, dO, None), want, {m: torch.zeros_like(x) for m, x in want.items()}))
+    ws = F.alloc_workspace(most)
+    torch.cuda.synchronize()
+    for _ in range(6):
+        for p, args, _, out in calls:
+            F.falcon_attn_prompt_backward(p, *args, out, ws)
+            ws.fill_(0xFF)  # what the next call does not write itself is of no use to it
+    for _, _, want, out in calls:
+        assert all(torch.equal(out[m], want[m]) for m in want)
+
+
+@pytest.mark.parametrize("dtype,d", [("bf16", 64), ("bf16", 128), ("f32", 64), ("f32", 128)])
+@pytest.mark.parametrize("Hq,Hkv", [(2, 2), (16, 1)])
+def test_a_wait_that_runs_out_is_reported(F, dtype, d, Hq, Hkv):
+    """The copies of the first kernel never begin: the call ends with a timeout, and the next one is right."""
+    lens = [700]
+    q, k, v, dO = _inputs(lens, lens, Hq, Hkv, d, dtype, 2)
+    cu = _dev(_cu(lens))
+    o, lse = _forward(F, q, k, v, cu, cu, 700)
+    p = F.AttnParams(B=1, Hq=Hq, Hkv=Hkv, d=d, dtype=F.FALCON_BF16 if dtype == "bf16" else F.FALCON_F32, max_q=700,
+                     tokens=700, k_tokens=700)
+    ws = F.alloc_workspace(F.falcon_attn_prompt_backward_workspace_size(p))
+    out = {m: torch.full_like(x, 3.0) for m, x in (("dq", q), ("dk", k), ("dv", v))}
+    run = lambda: F.falcon_attn_prompt_backward(p, q, k, v, cu, cu, o, lse, dO, None, out, ws)  # noqa: E731
+    try:
+        F.falcon_test_hooks(wait_limit_ns=2_000_000, stall=True)
+        run()
+        assert F.falcon_workspace_status(ws) == F.FALCON_ERR_TIMEOUT
+    finally:
+        F.falcon_test_hooks(0, False)
+    assert (out["dk"] == 3).all() and (out["dv"] == 3).all()
+    run()
+    assert F.falcon_workspace_status(ws) == F.FALCON_OK
+    want = F.attn_prompt_backward(q, k, v, o, lse, dO, cu, max_q=700)
+    assert all(torch.equal(out[m], want[m]) for m in want)
 
 
 def test_no_queries_and_no_keys(F):

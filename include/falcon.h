@@ -494,7 +494,8 @@ typedef struct {
   int64_t do_stride; /* of dO; attn_prompt_backward only */
 } falcon_attn_grads_t;
 
-/* Bytes of workspace falcon_attn_prompt_backward needs (0 when the params are invalid). */
+/* Bytes of workspace falcon_attn_prompt_backward needs (0 when the params are invalid).  In fp32 it holds q, dO, k and
+ * v once more, each sequence rounded up to 64 rows and rows of 16 and 32 dims to 64. */
 size_t falcon_attn_prompt_backward_workspace_size(const falcon_attn_params_t* p);
 
 /* Gradient of falcon_attn_prompt(p, q, k, v, cu_q, cu_k) with results o and lse,
@@ -511,10 +512,11 @@ size_t falcon_attn_prompt_backward_workspace_size(const falcon_attn_params_t* p)
  * max_q of their sequence have no gradient: their dq is left as it is and they
  * add nothing.  So are rows of dq, dk and dv behind the last sequence.  What
  * lies in rows that a row does not see (infinities, NaN) does not reach it.
- * Every sum has one order: the same call gives the same bits.  Products as in
- * falcon_attn_prompt; sums are fp32, P and dS rounded to 11 bits (bf16 rows on 16-byte
- * boundaries: 8, on the tensor cores, whose bounded waits are reported through
- * falcon_workspace_status(workspace, stream)); fp32 keeps 22 bits.
+ * Every sum has one order: the same call gives the same bits.  Sums are
+ * fp32.  bf16: P and dS are rounded to 8 bits (rows off the 16-byte boundaries: 11);
+ * fp32: operands, P and dS keep 22 bits, down to 2^-40 of the largest magnitude of
+ * their row.  Bounded waits that run out are reported through
+ * falcon_workspace_status(workspace, stream).
  * Errors: FALCON_ERR_INVALID_ARG, FALCON_ERR_UNSUPPORTED,
  * FALCON_ERR_WORKSPACE, FALCON_ERR_CUDA. */
 int falcon_attn_prompt_backward(const falcon_attn_params_t* p, const void* q, const void* k, const void* v,

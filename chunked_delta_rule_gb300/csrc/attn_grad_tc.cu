@@ -596,7 +596,7 @@ int launch_d(const GradArgs& g, cudaStream_t s) {
     t.second = true;
   }
   if (g.dq.p) {
-    const PromptGrid pg = prompt_grid(a, kTile);
+    const PromptGrid pg = query_grid(a);
     t.qblocks = static_cast<int>(pg.blocks / a.B);
     t.packed = pg.packed;
     constexpr int N = Cfg<D, false>::kN;

@@ -823,7 +823,7 @@ int launch_d(const GradArgs& g, cudaStream_t s) {
     t.second = true;
   }
   if (g.dq.p && q_ctas) {
-    const PromptGrid pg = prompt_grid(a, kTile);
+    const PromptGrid pg = query_grid(a);
     t.qblocks = static_cast<int>(pg.blocks / a.B);
     t.packed = pg.packed;
     return pg.blocks > INT32_MAX / a.Hq ? FALCON_ERR_UNSUPPORTED : launch_kernel<D, false>(t, pg.blocks * a.Hq, s);

@@ -387,15 +387,17 @@ def test_no_queries_and_no_keys(F):
         F.attn_prompt_backward(e(q), e(k), e(v), e(o), e(lse), e(dO), _dev([0, 0]))
 
 
-def test_captured_calls_share_a_workspace(F):
+@pytest.mark.parametrize("dtype,d", [("bf16", 64), ("bf16", 128), ("f32", 64), ("f32", 128)])
+def test_captured_calls_share_a_workspace(F, dtype, d):
     """Two graphs of different sizes over one workspace, replayed in turn with new inputs."""
-    d, Hq, Hkv, calls = 64, 4, 2, []
+    Hq, Hkv, calls = 4, 2, []
     most = 0
     for lens in ([300, 100], [129]):
         n = sum(lens)
         cu = _dev(_cu(lens))
-        q, k, v, dO = _inputs(lens, lens, Hq, Hkv, d, "bf16", n)
-        p = F.AttnParams(B=len(lens), Hq=Hq, Hkv=Hkv, d=d, dtype=F.FALCON_BF16, max_q=max(lens), tokens=n, k_tokens=n)
+        q, k, v, dO = _inputs(lens, lens, Hq, Hkv, d, dtype, n)
+        p = F.AttnParams(B=len(lens), Hq=Hq, Hkv=Hkv, d=d, dtype=F.FALCON_BF16 if dtype == "bf16" else F.FALCON_F32,
+                         max_q=max(lens), tokens=n, k_tokens=n)
         most = max(most, F.falcon_attn_prompt_backward_workspace_size(p))
         g = {name: torch.zeros_like(x) for name, x in (("dq", q), ("dk", k), ("dv", v))}
         calls.append((p, lens, cu, q, k, v, dO, g))
@@ -412,7 +414,7 @@ def test_captured_calls_share_a_workspace(F):
         graphs.append((graph, o, lse))
     for seed in (100, 200):
         for (p, lens, cu, q, k, v, dO, g), (graph, o, lse) in zip(calls, graphs):
-            for t, x in zip((q, k, v, dO), _inputs(lens, lens, Hq, Hkv, d, "bf16", seed)):
+            for t, x in zip((q, k, v, dO), _inputs(lens, lens, Hq, Hkv, d, dtype, seed)):
                 t.copy_(x)
             for t, x in zip((o, lse), _forward(F, q, k, v, cu, cu, max(lens))):
                 t.copy_(x)

@@ -13,10 +13,10 @@
 //   load warp    TMA: the two tiles, through a ring of pairs
 //   MMA warp     X, Y and the sums' products in the order that keeps the tensor
 //                cores ahead of the softmax warps, see the loops
-//   softmax      32 columns of a row a thread: P from X, dS from P and Y.  They go back
-//   warps        to TMEM in bf16 over the scores that they came from, as the A operand
-//                of the sums' products.
-// dK and dV: a thread holds one key and 32 queries, so that log sums and D would be
+//   softmax      64 columns of a row a thread (32: 290 us for 281 in the packed case): P
+//   warps        from X, dS from P and Y.  They go back to TMEM in bf16 over the scores
+//                that they came from, as the A operand of the sums' products.
+// dK and dV: a thread holds one key and 64 queries, so that log sums and D would be
 // loads for every element; they come out of the products instead, one more step of 16
 // columns: [K | 1] [Q | -log sum / scale]^T and [V | 1] [dO | -D]^T, in three bf16
 // parts (24 bits).
@@ -50,7 +50,8 @@ template <int D, bool KEYS>
 struct Cfg {
   static constexpr int kCtas = D == 64 ? 2 : 1;           // CTAs of an SM
   static constexpr int kN = D == 64 ? 64 : 128;           // rows of a tile that comes past
-  static constexpr int kSplit = kN / 32;                  // softmax threads of a row, 32 columns each
+  static constexpr int kW = 2;                            // times 32 columns of a row: a softmax thread's
+  static constexpr int kSplit = kN / (32 * kW);           // softmax threads of a row
   static constexpr int kOut = (KEYS ? 2 : 1) * D / kSplit;  // columns of the sums that each of them writes
   static constexpr int kWarps = 4 * kSplit;
   static constexpr int kLoadWarp = kWarps, kMmaWarp = kWarps + 1;
@@ -210,10 +211,10 @@ __global__ void __launch_bounds__(Cfg<D, KEYS>::kThreads, Cfg<D, KEYS>::kCtas)
   auto place = [&](int i, int second) { return 2 * (i % P) + (KEYS ? (i / P + second) & 1 : second); };
 
   // registers: the softmax threads take what the last warpgroup gives up
-  // (256 x 96 + 128 x 48 = 384 x 80; 512 x 104 + 128 x 64 = 640 x 96)
+  // (128 x 200 + 128 x 56 = 256 x 128; 256 x 208 + 128 x 88 = 384 x 168)
   if (warp >= C::kLoadWarp) {
-    if (D == 64) asm volatile("setmaxnreg.dec.sync.aligned.u32 48;");
-    else asm volatile("setmaxnreg.dec.sync.aligned.u32 64;");
+    if (D == 64) asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
+    else asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
     if (last) wait_for_previous();
     __syncwarp();
   }
@@ -328,8 +329,8 @@ __global__ void __launch_bounds__(Cfg<D, KEYS>::kThreads, Cfg<D, KEYS>::kCtas)
     }
     __syncwarp();
   } else if (warp < C::kLoadWarp) {
-    if (D == 64) asm volatile("setmaxnreg.inc.sync.aligned.u32 96;");
-    else asm volatile("setmaxnreg.inc.sync.aligned.u32 104;");
+    if (D == 64) asm volatile("setmaxnreg.inc.sync.aligned.u32 200;");
+    else asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
     const int part = warp >> 2, quad = warp & 3, r = quad * 32 + lane;
     const uint32_t mine = tmem + (static_cast<uint32_t>(quad * 32) << 16);
     const int row = row0 + r;
@@ -349,16 +350,19 @@ __global__ void __launch_bounds__(Cfg<D, KEYS>::kThreads, Cfg<D, KEYS>::kCtas)
       delta2 = pack2(-at[kSumRows], -at[kSumRows]);
       // the owned rows to TMEM, a share of the columns each; rows past the sequence are some others', or zeros
       if ((ok = waited(&bar->own, 0))) {
-        constexpr int kShare = 2 * D / C::kSplit;  // of the 2 D elements of a row of Q and dO: 64
-        static_assert(kShare == 64, "a slab of 64 columns a thread");
-        const uint8_t* from = s1 + part * kTile * 128;
-        uint32_t w[32];
+        constexpr int kSlabs = 2 * D / 64 / C::kSplit;  // of 64 of the 2 D elements of a row of Q and dO
+        static_assert(kSlabs * C::kSplit * 64 == 2 * D, "whole slabs a thread");
 #pragma unroll
-        for (int c = 0; c < 8; ++c) {
-          const uint4 x = *reinterpret_cast<const uint4*>(from + sw128(r, c * 8));
-          w[4 * c] = x.x, w[4 * c + 1] = x.y, w[4 * c + 2] = x.z, w[4 * c + 3] = x.w;
+        for (int sl = 0; sl < kSlabs; ++sl) {
+          const uint8_t* from = s1 + (part * kSlabs + sl) * kTile * 128;
+          uint32_t w[32];
+#pragma unroll
+          for (int c = 0; c < 8; ++c) {
+            const uint4 x = *reinterpret_cast<const uint4*>(from + sw128(r, c * 8));
+            w[4 * c] = x.x, w[4 * c + 1] = x.y, w[4 * c + 2] = x.z, w[4 * c + 3] = x.w;
+          }
+          tmem_st32(mine + C::kColA1 + (part * kSlabs + sl) * 32, w);
         }
-        tmem_st32(mine + C::kColA1 + part * 32, w);
         tmem_wait_st();
         tc_fence_before();
         arrive(&bar->ready);
@@ -366,46 +370,56 @@ __global__ void __launch_bounds__(Cfg<D, KEYS>::kThreads, Cfg<D, KEYS>::kCtas)
     }
     int past = KEYS && n > 0 ? i0 % each : 0;  // the tile's place among a head's
     for (int i = 0; i < n && ok; ++i) {
-      const int at = first + past * N + part * 32;  // of the first column
+      constexpr int W = C::kW;
+      const int at = first + past * N + part * (32 * W);  // of the first column
       if (++past == each) past = 0;
-      const uint32_t tx = mine + C::kColX + part * 32, ty = mine + C::kColY + part * 32;
+      const uint32_t tx = mine + C::kColX + part * (32 * W), ty = mine + C::kColY + part * (32 * W);
       if (!(ok = waited(&bar->x, i & 1))) break;
       tc_fence_after();
-      uint64_t x[16];  // X, then P
-      uint32_t u[16];
+      uint64_t x[W][16];  // X, then P
       {
-        uint32_t v[32];
-        tmem_ld32(tx, v);
+        uint32_t v[W][32];
+#pragma unroll
+        for (int c = 0; c < W; ++c) tmem_ld32(tx + 32 * c, v[c]);
         tmem_wait_ld();
         if (!KEYS) {
           tc_fence_before();
           arrive(&bar->p);
         }
 #pragma unroll
-        for (int e = 0; e < 16; ++e) x[e] = pack2(__uint_as_float(v[2 * e]), __uint_as_float(v[2 * e + 1]));
+        for (int c = 0; c < W; ++c)
+#pragma unroll
+          for (int e = 0; e < 16; ++e) x[c][e] = pack2(__uint_as_float(v[c][2 * e]), __uint_as_float(v[c][2 * e + 1]));
       }
       // keys behind a query of these, or past the last
-      if (KEYS ? at + off < row0 + kTile - 1 : at + 32 > min(row0 + off + 1, lk)) {
+      if (KEYS ? at + off < row0 + kTile - 1 : at + 32 * W > min(row0 + off + 1, lk)) {
         const int lim = KEYS ? row - off - at : min(row + off + 1, lk) - at;
+#pragma unroll
+        for (int c = 0; c < W; ++c)
+#pragma unroll
+          for (int e = 0; e < 16; ++e) {
+            const int first_of = 32 * c + 2 * e;
+            float z0, z1;
+            unpack2(x[c][e], z0, z1);
+            if (KEYS ? first_of < lim : first_of >= lim) z0 = -INFINITY;
+            if (KEYS ? first_of + 1 < lim : first_of + 1 >= lim) z1 = -INFINITY;
+            x[c][e] = pack2(z0, z1);
+          }
+      }
+#pragma unroll
+      for (int c = 0; c < W; ++c) {
+        uint32_t u[16];
 #pragma unroll
         for (int e = 0; e < 16; ++e) {
           float z0, z1;
-          unpack2(x[e], z0, z1);
-          if (KEYS ? 2 * e < lim : 2 * e >= lim) z0 = -INFINITY;
-          if (KEYS ? 2 * e + 1 < lim : 2 * e + 1 >= lim) z1 = -INFINITY;
-          x[e] = pack2(z0, z1);
+          unpack2(KEYS ? mul2(x[c][e], scale2) : fma2(x[c][e], scale2, lse2), z0, z1);
+          z0 = ex2(z0), z1 = ex2(z1);
+          x[c][e] = pack2(z0, z1);
+          if (KEYS) u[e] = pack_bf16(z0, z1);
         }
-      }
-#pragma unroll
-      for (int e = 0; e < 16; ++e) {
-        float z0, z1;
-        unpack2(KEYS ? mul2(x[e], scale2) : fma2(x[e], scale2, lse2), z0, z1);
-        z0 = ex2(z0), z1 = ex2(z1);
-        x[e] = pack2(z0, z1);
-        if (KEYS) u[e] = pack_bf16(z0, z1);
+        if (KEYS) tmem_st16(tx + 32 * c, u);
       }
       if (KEYS) {
-        tmem_st16(tx, u);
         tmem_wait_st();
         tc_fence_before();
         arrive(&bar->p);
@@ -413,19 +427,24 @@ __global__ void __launch_bounds__(Cfg<D, KEYS>::kThreads, Cfg<D, KEYS>::kCtas)
       if (!(ok = waited(&bar->y, i & 1))) break;
       tc_fence_after();
       {
-        uint32_t v[32];
-        tmem_ld32(ty, v);
+        uint32_t v[W][32];
+#pragma unroll
+        for (int c = 0; c < W; ++c) tmem_ld32(ty + 32 * c, v[c]);
         tmem_wait_ld();
 #pragma unroll
-        for (int e = 0; e < 16; ++e) {
-          uint64_t z = pack2(__uint_as_float(v[2 * e]), __uint_as_float(v[2 * e + 1]));
-          if (!KEYS) z = add2(z, delta2);
-          float z0, z1;
-          unpack2(mul2(x[e], z), z0, z1);
-          u[e] = pack_bf16(z0, z1);
+        for (int c = 0; c < W; ++c) {
+          uint32_t u[16];
+#pragma unroll
+          for (int e = 0; e < 16; ++e) {
+            uint64_t z = pack2(__uint_as_float(v[c][2 * e]), __uint_as_float(v[c][2 * e + 1]));
+            if (!KEYS) z = add2(z, delta2);
+            float z0, z1;
+            unpack2(mul2(x[c][e], z), z0, z1);
+            u[e] = pack_bf16(z0, z1);
+          }
+          tmem_st16(ty + 32 * c, u);
         }
       }
-      tmem_st16(ty, u);
       tmem_wait_st();
       tc_fence_before();
       arrive(&bar->ds);
@@ -453,80 +472,82 @@ __global__ void __launch_bounds__(Cfg<D, KEYS>::kThreads, Cfg<D, KEYS>::kCtas)
     };
     if (!KEYS || t.split == 1) {
       if (__all_sync(0xffffffffu, ok)) {
-        // this thread's columns of a row: of dV (the first ones) or dK; of dQ
-        const bool of_v = KEYS && part * C::kOut < D;
-        const int c0 = part * C::kOut % D;
-        const RowsOut& to = KEYS ? (of_v ? g.dv : g.dk) : g.dq;
-        __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(to.p) + ((KEYS ? k0 : q0) + row0) * to.stride +
-                             static_cast<int64_t>(head) * d + c0;
-        const float f = of_v ? 1.f : a.scale;
-        const uint64_t f2 = pack2(f, f);
-        const uint32_t from = mine + (of_v ? C::kColV : C::kColS) + c0;
-        uint64_t rest = 0;  // z * 0 added up: NaN where some z is not finite
-        // a warp's 32 rows through shared memory (the ring's place: every product is done), so that a store covers
-        // whole lines
-        uint8_t* stage = ring + (part * C::kOut >> 6) * kTile * 128;
-        const int sc = part * C::kOut & 63;
+        // this thread's columns of a row, of dV and then dK, or of dQ, up to 64 at a time
+        constexpr int PW = C::kOut < 64 ? C::kOut : 64;
+#pragma unroll 1
+        for (int start = part * C::kOut; start < (part + 1) * C::kOut; start += PW) {
+          const bool of_v = KEYS && start < D;
+          const int c0 = start % D;
+          const RowsOut& to = KEYS ? (of_v ? g.dv : g.dk) : g.dq;
+          __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(to.p) + ((KEYS ? k0 : q0) + row0) * to.stride +
+                               static_cast<int64_t>(head) * d + c0;
+          const float f = of_v ? 1.f : a.scale;
+          const uint64_t f2 = pack2(f, f);
+          const uint32_t from = mine + (of_v ? C::kColV : C::kColS) + c0;
+          uint64_t rest = 0;  // z * 0 added up: NaN where some z is not finite
+          // a warp's 32 rows through shared memory (the ring's place: every product is done), so that a store covers
+          // whole lines
+          uint8_t* stage = ring + (start >> 6) * kTile * 128;
+          const int sc = start & 63;
 #pragma unroll
-        for (int c = 0; c < C::kOut; c += 32) {
-          uint32_t v[32];
-          if (n > 0) {
-            tmem_ld32(from + c, v);
-            tmem_wait_ld();
-          } else {
+          for (int c = 0; c < PW; c += 32) {
+            uint32_t v[32];
+            if (n > 0) {
+              tmem_ld32(from + c, v);
+              tmem_wait_ld();
+            } else {
 #pragma unroll
-            for (int e = 0; e < 32; ++e) v[e] = 0;
-          }
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            uint32_t w[4];
-#pragma unroll
-            for (int k = 0; k < 4; ++k) {
-              const uint64_t z = mul2(pack2(__uint_as_float(v[8 * e + 2 * k]), __uint_as_float(v[8 * e + 2 * k + 1])), f2);
-              float z0, z1;
-              rest = fma2(z, 0, rest);
-              unpack2(z, z0, z1);
-              w[k] = pack_bf16(z0, z1);
+              for (int e = 0; e < 32; ++e) v[e] = 0;
             }
-            *reinterpret_cast<uint4*>(stage + sw128(r, sc + c + e * 8)) = make_uint4(w[0], w[1], w[2], w[3]);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              uint32_t w[4];
+#pragma unroll
+              for (int k = 0; k < 4; ++k) {
+                const uint64_t z = mul2(pack2(__uint_as_float(v[8 * e + 2 * k]), __uint_as_float(v[8 * e + 2 * k + 1])), f2);
+                float z0, z1;
+                rest = fma2(z, 0, rest);
+                unpack2(z, z0, z1);
+                w[k] = pack_bf16(z0, z1);
+              }
+              *reinterpret_cast<uint4*>(stage + sw128(r, sc + c + e * 8)) = make_uint4(w[0], w[1], w[2], w[3]);
+            }
           }
-        }
-        __syncwarp();
-        constexpr int kPieces = C::kOut / 8;  // 16 bytes each
+          __syncwarp();
+          constexpr int kPieces = PW / 8;  // 16 bytes each
 #pragma unroll
-        for (int e = 0; e < kPieces; ++e) {
-          const int x = e * 32 + lane, rr = quad * 32 + x / kPieces, c = x % kPieces * 8;
-          if (row0 + rr >= rows || (D == 64 && c0 + c >= d)) continue;
-          *reinterpret_cast<uint4*>(dst + rr * to.stride + c) = *reinterpret_cast<const uint4*>(stage + sw128(rr, sc + c));
-        }
-        float ra, rb;
-        unpack2(rest, ra, rb);
-        __syncwarp();
-        for (uint32_t again = __ballot_sync(0xffffffffu, row < rows && !(ra + rb == 0.f)); again; again &= again - 1) {
-          const int i = row0 + quad * 32 + __ffs(again) - 1;
-          float x1[4], x2[4];
-          compute_again(i, x1, x2);
-          // this warp's part of the row
+          for (int e = 0; e < kPieces; ++e) {
+            const int x = e * 32 + lane, rr = quad * 32 + x / kPieces, c = x % kPieces * 8;
+            if (row0 + rr >= rows || (D == 64 && c0 + c >= d)) continue;
+            *reinterpret_cast<uint4*>(dst + rr * to.stride + c) = *reinterpret_cast<const uint4*>(stage + sw128(rr, sc + c));
+          }
+          float ra, rb;
+          unpack2(rest, ra, rb);
+          __syncwarp();
+          for (uint32_t again = __ballot_sync(0xffffffffu, row < rows && !(ra + rb == 0.f)); again; again &= again - 1) {
+            const int i = row0 + quad * 32 + __ffs(again) - 1;
+            float x1[4], x2[4];
+            compute_again(i, x1, x2);
+            // this warp's part of the row
 #pragma unroll
-          for (int m = 0; m < D / 32; ++m) {
-            const int c = m * 32 + lane;
-            if (m * 32 >= c0 && m * 32 < c0 + C::kOut && c < d)
-              dst[(i - row0) * to.stride + c - c0] = __float2bfloat16_rn(of_v ? x2[m] : x1[m]);
+            for (int m = 0; m < D / 32; ++m) {
+              const int c = m * 32 + lane;
+              if (m * 32 >= c0 && m * 32 < c0 + PW && c < d)
+                dst[(i - row0) * to.stride + c - c0] = __float2bfloat16_rn(of_v ? x2[m] : x1[m]);
+            }
           }
         }
       }
     } else {
       // The sums in fp32 to shared memory (the ring's place and on: every product is done), 128 rows of dV, then of dK,
       // 16-byte pieces swizzled by row; then each CTA adds up its share of the rows.
-      const bool of_v = part * C::kOut < D;
-      const int c0 = part * C::kOut % D;
-      const uint32_t from = mine + (of_v ? C::kColV : C::kColS) + c0;
-      uint8_t* dst = smem + (of_v ? 0 : kTile * D * 4) + r * D * 4;
-#pragma unroll
-      for (int c = 0; c < C::kOut; c += 32) {
+#pragma unroll 1
+      for (int start = part * C::kOut; start < (part + 1) * C::kOut; start += 32) {
+        const int c0 = start % D;
+        uint8_t* dst = smem + start / D * (kTile * D * 4) + r * D * 4;
         uint32_t v[32];
         if (n > 0 && ok) {
-          tmem_ld32(from + c, v);
+          tmem_ld32(mine + C::kColV + start, v);  // the sums of dK lie behind those of dV
           tmem_wait_ld();
         } else {
 #pragma unroll
@@ -534,7 +555,7 @@ __global__ void __launch_bounds__(Cfg<D, KEYS>::kThreads, Cfg<D, KEYS>::kCtas)
         }
 #pragma unroll
         for (int e = 0; e < 8; ++e)
-          *reinterpret_cast<uint4*>(dst + ((((c0 + c) >> 2) + e) ^ (r & 7)) * 16) =
+          *reinterpret_cast<uint4*>(dst + (((c0 >> 2) + e) ^ (r & 7)) * 16) =
               make_uint4(v[4 * e], v[4 * e + 1], v[4 * e + 2], v[4 * e + 3]);
       }
       cluster_sums<__nv_bfloat16, D, 32 * C::kWarps>(g, smem, &bar->failed, bar->bad, t.split, rank, row0, rows, k0, head, d, compute_again);

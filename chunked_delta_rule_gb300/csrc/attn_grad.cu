@@ -36,7 +36,8 @@ __device__ __forceinline__ uint2 three_parts(float x) {
 __global__ void __launch_bounds__(256, 6) attn_grad_sums_kernel(GradArgs g) {
   const PromptArgs& a = g.a;
   launch_dependents();
-  if (blockIdx.x == 0 && threadIdx.x == 0) *static_cast<uint32_t*>(a.ws) = 0;  // the call's status
+  // the call's status, and the blocks of dQ that have begun
+  if (blockIdx.x == 0 && threadIdx.x == 0) *static_cast<uint2*>(a.ws) = make_uint2(0u, 0u);
   const int h = static_cast<int>(blockIdx.x % a.Hq);
   const int64_t j = blockIdx.x / a.Hq;
   const int2 x = find_block(a.cu_q, a.B, kSumRows, static_cast<int>(j));

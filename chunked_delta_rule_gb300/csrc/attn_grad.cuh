@@ -26,6 +26,7 @@ size_t attn_grad_ws_bytes(int64_t tokens, int64_t k_tokens, int B, int Hq, int H
 int launch_attn_grad(const GradArgs& g, int dtype, cudaStream_t s);
 bool attn_grad_tc_supported(const GradArgs& g, int dtype);
 int launch_attn_grad_tc(const GradArgs& g, cudaStream_t s);
+int launch_attn_grad_dq_tc(const GradArgs& g, bool second, cudaStream_t s);
 size_t attn_grad_tc32_ws_bytes(int64_t tokens, int64_t k_tokens, int B, int Hq, int Hkv, int d);
 int launch_attn_grad_tc32(const GradArgs& g, cudaStream_t s);
 

@@ -616,16 +616,7 @@ int launch_d(const GradArgs& g, cudaStream_t s) {
     t.split = 1;
     t.second = true;
   }
-  if (g.dq.p) {
-    const PromptGrid pg = query_grid(a);
-    t.qblocks = static_cast<int>(pg.blocks / a.B);
-    t.packed = pg.packed;
-    constexpr int N = Cfg<D, false>::kN;
-    if (!maps(a.q, a.tokens, a.Hq, kTile, m) || !maps(g.d_o, a.tokens, a.Hq, kTile, m + 1) ||
-        !maps(a.k, a.k_tokens, a.Hkv, N, m + 2) || !maps(a.v, a.k_tokens, a.Hkv, N, m + 3))
-      return FALCON_ERR_CUDA;
-    return pg.blocks > INT32_MAX / a.Hq ? FALCON_ERR_UNSUPPORTED : launch_kernel<D, false>(t, pg.blocks * a.Hq, m, s);
-  }
+  if (g.dq.p) return launch_attn_grad_dq_tc(g, t.second, s);
   return FALCON_OK;
 }
 

@@ -204,9 +204,8 @@ __device__ __forceinline__ void store_row(T* out, const float (&x)[4], int d) {
 }
 
 // ---------------------------------------------------------------- a block's dK and dV by a cluster of CTAs
-// The grid of dQ, blocks of 128 rows, as prompt_grid: but a block without rows costs a CTA that has an SM (or half of it) to
-// itself its start, so that the packed grid is taken from an eighth more blocks on.  (12 documents of 205 .. 2048 tokens, 16
-// heads of 128: 296 us the other way, 290 this way.)
+// The grid of fp32's dQ, blocks of 128 rows, as prompt_grid: but a block without rows costs a CTA that has an SM to itself its
+// start, so that the packed grid is taken from an eighth more blocks on.
 inline PromptGrid query_grid(const PromptArgs& a) {
   const int64_t each = (static_cast<int64_t>(a.max_q) + kSumRows - 1) / kSumRows * a.B, packed = a.tokens / kSumRows + a.B;
   return each > packed + packed / 8 ? PromptGrid{packed, true} : PromptGrid{each, false};

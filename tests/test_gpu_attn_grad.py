@@ -368,6 +368,26 @@ def test_a_wait_that_runs_out_is_reported(F, dtype, d, Hq, Hkv):
     assert all(torch.equal(out[m], want[m]) for m in want)
 
 
+@pytest.mark.parametrize("dtype,d", [("bf16", 64), ("bf16", 128), ("f32", 32), ("f32", 128)])
+def test_many_short_sequences(F, dtype, d):
+    """Several blocks a CTA, most of them a few rows, some sequences empty, some with keys alone; rows before the first one."""
+    g = torch.Generator().manual_seed(d)
+    lq = torch.randint(0, 10, (260,), generator=g).tolist()
+    lk = [n if i % 3 else max(0, n + i % 7 - 3) for i, n in enumerate(lq)]
+    lq[7], lk[7] = 300, 410
+    cu_q, cu_k = ([5 + x for x in _cu(n)] for n in (lq, lk))
+    n, m, Hq, Hkv = cu_q[-1], cu_k[-1], 8, 4
+    q, k, v, dO = (_rand((rows, H, d), dtype, seed, seed < 3) for seed, rows, H in
+                   ((1, n, Hq), (2, m, Hkv), (3, m, Hkv), (4, n, Hq)))
+    o, lse = _forward(F, q, k, v, _dev(cu_q), _dev(cu_k), max(lq))
+    out = {name: torch.full_like(x, 3.0) for name, x in (("dq", q), ("dk", k), ("dv", v))}
+    got = F.attn_prompt_backward(q, k, v, o, lse, dO, _dev(cu_q), _dev(cu_k), max(lq), out=out)
+    _, _, want, A = attention_grad(q, k, v, cu_q, cu_k, d ** -0.5, dO)
+    assert all((x[:5] == 3).all() for x in got.values())
+    cut = lambda xs: {name: x[5:] for name, x in xs.items()}  # noqa: E731
+    _check(cut(got), cut(want), cut(A), dtype, _S(q, k, d ** -0.5))
+
+
 def test_no_queries_and_no_keys(F):
     """Keys that no query sees get zeros; queries without keys too; empty calls write nothing."""
     d = 64

@@ -501,7 +501,9 @@ int launch_d(const GradArgs& g, bool second, cudaStream_t s) {
   t.second = second;
   t.status = static_cast<uint32_t*>(a.ws);
   t.counter = t.status + 1;
-  t.limit = wait_limit_ns();
+  // Rows that are computed again hold up the CTA's next block, so that no wait may run out before a warp's 32 rows are done: 2 us
+  // a key and row, several times what it takes.  (A look at a count of such rows in the waits: 222 us for 205 at 8 x 2048.)
+  t.limit = wait_limit_ns() + static_cast<uint64_t>(a.k_tokens) * 32 * 2000;
   t.stall = take_test_stall() ? 1 : 0;
   const auto kern = attn_grad_dq_tc_kernel<D>;
   if (!set_smem_limit(reinterpret_cast<const void*>(kern), smem_bytes<D>())) return FALCON_ERR_CUDA;

@@ -388,6 +388,32 @@ def test_many_short_sequences(F, dtype, d):
     _check(cut(got), cut(want), cut(A), dtype, _S(q, k, d ** -0.5))
 
 
+@pytest.mark.parametrize("d,Hq", [(64, 8), (128, 4)])
+def test_rows_computed_again_outlast_the_waits(F, d, Hq):
+    """An infinite key at 2000 of 3000: the queries before it in its tile are computed again, milliseconds of work, while the
+    CTA's next blocks wait with a limit of half a millisecond."""
+    lens = [3000] * 4
+    cu = _dev(_cu(lens))
+    n = sum(lens)
+    q, k, v, dO = _inputs(lens, lens, Hq, Hq, d, "bf16", 3)
+    o, lse = _forward(F, q, k, v, cu, cu, 3000)
+    for b in range(4):
+        v[3000 * b + 2000] = math.inf
+    p = F.AttnParams(B=4, Hq=Hq, Hkv=Hq, d=d, dtype=F.FALCON_BF16, max_q=3000, tokens=n, k_tokens=n)
+    ws = F.alloc_workspace(F.falcon_attn_prompt_backward_workspace_size(p))
+    got = [{"dq": torch.full_like(q, 3.0)} for _ in range(2)]
+    try:
+        for out, limit in zip(got, (0, 500_000)):
+            F.falcon_test_hooks(wait_limit_ns=limit)
+            F.falcon_attn_prompt_backward(p, q, k, v, cu, cu, o, lse, dO, None, out, ws)
+            assert F.falcon_workspace_status(ws) == F.FALCON_OK
+    finally:
+        F.falcon_test_hooks(0, False)
+    x = got[0]["dq"].view(4, 3000, Hq, d)
+    assert torch.isfinite(x[:, :2000]).all() and not torch.isfinite(x[:, 2000:]).any()
+    assert torch.equal(got[1]["dq"].view(torch.int16), got[0]["dq"].view(torch.int16))
+
+
 def test_no_queries_and_no_keys(F):
     """Keys that no query sees get zeros; queries without keys too; empty calls write nothing."""
     d = 64

@@ -1,6 +1,6 @@
 // Gradient of causal attention over packed prompts: the rows' sums that the bf16
 // kernels read, and the products where the tcgen05 kernels do not go (bf16 rows off
-// the 16-byte boundaries).
+// the 16-byte boundaries, scales below 2^-100).
 //
 //   P = exp(scale Q K^T - log sum),  dS = P (dO V^T - D),  D = sum_c dO_c o_c - dlse
 //   dV = P^T dO,  dK = scale dS^T Q,  dQ = scale dS K
@@ -90,8 +90,9 @@ __global__ void __launch_bounds__(256, 6) attn_grad_sums_kernel(GradArgs g) {
   g.sums[row_sums(1, 0, at) + r] = lse;
   g.sums[row_sums(1, 0, at) + kSumRows + r] = delta;
   if (!g.images) return;
-  // no weight: as far down as bf16 goes short of an infinity, which would spoil the columns' zeros
-  const uint2 y = lse == INFINITY ? make_uint2(0xFF7Fu, 0u) : three_parts(-lse / a.scale), z = three_parts(-delta);
+  // no weight: bf16's lowest number (an infinity would spoil the columns' zeros) in all three parts, so that whatever
+  // finite score they are added to, the sum is -inf or fp32's lowest number: see attn_grad_tc_supported for the scale
+  const uint2 y = lse == INFINITY ? make_uint2(0xFF7FFF7Fu, 0xFF7Fu) : three_parts(-lse / a.scale), z = three_parts(-delta);
   uint4* to = reinterpret_cast<uint4*>(g.images + at * kImageBytes + (r >> 3) * 256 + (r & 7) * 16);
   to[0] = make_uint4(y.x, y.y, z.x, z.y);
   to[8] = make_uint4(0u, 0u, 0u, 0u);

@@ -519,10 +519,12 @@ int launch_d(const GradArgs& g, cudaStream_t s) {
 }  // namespace
 
 // The tensor-core kernels take bf16 rows on 16-byte boundaries (their TMA copies and stores), with token strides below
-// the maps' 2^40 bytes.
+// the maps' 2^40 bytes, and scales from 2^-100 on: the scale comes after the log sums, and a row without weight has -3.4e38
+// there at least, which 2^-100 leaves at -2.7e8 (weight 0), while 2^-126 would make a weight of 0.02 of it.
 bool attn_grad_tc_supported(const GradArgs& g, int dtype) {
   const PromptArgs& a = g.a;
   if (dtype != FALCON_BF16 || a.k_tokens == 0 || a.tokens == 0 || a.max_q == 0) return false;
+  if (!(a.scale >= 0x1p-100f)) return false;
   if (!a.q.vec || !a.k.vec || !a.v.vec || !g.d_o.vec) return false;
   for (const RowsOut& x : {g.dq, g.dk, g.dv})
     if (x.p && !x.vec) return false;

@@ -513,7 +513,8 @@ size_t falcon_attn_prompt_backward_workspace_size(const falcon_attn_params_t* p)
  * add nothing.  So are rows of dq, dk and dv behind the last sequence.  What
  * lies in rows that a row does not see (infinities, NaN) does not reach it.
  * Every sum has one order: the same call gives the same bits.  Sums are
- * fp32.  bf16: P and dS are rounded to 8 bits (rows off the 16-byte boundaries: 11);
+ * fp32.  bf16: P and dS are rounded to 8 bits (rows off the 16-byte boundaries and
+ * scales below 2^-100: 11);
  * fp32: operands, P and dS keep 22 bits, down to 2^-40 of the largest magnitude of
  * their row.  Bounded waits that run out are reported through
  * falcon_workspace_status(workspace, stream) (in the bf16 kernel of dq after 64 us a

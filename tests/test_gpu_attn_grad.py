@@ -135,6 +135,25 @@ def test_large_and_small_scores(F, dtype, scale, size):
     _check(got, want, A, dtype, _S(q, k, scale))
 
 
+@pytest.mark.parametrize("dtype,d,Hq,Hkv", [("bf16", 64, 2, 1), ("bf16", 128, 2, 2), ("bf16", 16, 16, 1), ("bf16", 128, 16, 1),
+                                            ("f32", 64, 2, 1)])
+@pytest.mark.parametrize("power", [-126, -113, -101, -100, -99, -60, 100])
+def test_scales_at_the_ends_of_the_range(F, dtype, d, Hq, Hkv, power):
+    """Scales down to fp32's smallest normal number, with queries and keys whose scores are of ordinary size all the same:
+    rows past the end of a sequence (the next one's) have no weight at any scale."""
+    scale = 2.0 ** power
+    lens = [1, 3, 2, 40]
+    q, k, v, dO = _inputs(lens, lens, Hq, Hkv, d, dtype, 21)
+    q, k = q * 2.0 ** (-power // 2 - 2), k * 2.0 ** (-power - -power // 2 - 3)
+    cu = _cu(lens)
+    o, lse, want, A = attention_grad(q, k, v, cu, cu, scale, dO)
+    got = F.attn_prompt_backward(q, k, v, o.to(q.dtype), lse.float(), dO, _dev(cu), None, 40, scale)
+    # the sizes of dq and dk back to those of ordinary scores
+    for name, f in (("dq", 2.0 ** (-power // 2 - 2)), ("dk", 2.0 ** (-power - -power // 2 - 3))):
+        got[name], want[name], A[name] = got[name].double() * f, want[name] * f, A[name] * f
+    _check(got, want, A, dtype, _S(q, k, scale))
+
+
 def test_bits_do_not_change(F):
     """The same call twice, on another stream, and its halves alone."""
     for dtype, d in (("bf16", 64), ("bf16", 128), ("f32", 64), ("f32", 128)):

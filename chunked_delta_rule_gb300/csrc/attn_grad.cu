@@ -1,6 +1,6 @@
 // Gradient of causal attention over packed prompts: the rows' sums that the bf16
 // kernels read, and the products where the tcgen05 kernels do not go (bf16 rows off
-// the 16-byte boundaries, scales below 2^-100).
+// the 16-byte boundaries, scales below 2^-100, calls without query rows).
 //
 //   P = exp(scale Q K^T - log sum),  dS = P (dO V^T - D),  D = sum_c dO_c o_c - dlse
 //   dV = P^T dO,  dK = scale dS^T Q,  dQ = scale dS K
@@ -239,6 +239,8 @@ template <int D>
 __global__ void __launch_bounds__(256) attn_grad_keys_kernel(GradArgs g) {
   constexpr int LD = D + 4;
   const PromptArgs& a = g.a;
+  // the call's status: a call without queries has no rows' sums, whose kernel clears it otherwise
+  if (blockIdx.x == 0 && threadIdx.x == 0) *static_cast<uint32_t*>(a.ws) = 0;
   extern __shared__ float smem[];
   float *sk = smem, *sv = sk + kRows * LD, *sq = sv + kRows * LD, *sg = sq + kRows * LD, *ss = sg + kRows * LD;
   const int lane = threadIdx.x & 31, warp = (threadIdx.x >> 5) & 3, gid = lane >> 2, tig = lane & 3;

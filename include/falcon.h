@@ -565,8 +565,9 @@ int falcon_qk_norm_rope_backward(const falcon_attn_params_t* p, const void* q, c
  * and clears it.  Returns FALCON_OK, FALCON_ERR_TIMEOUT (the outputs and
  * carry of that call are incomplete), FALCON_ERR_WORKSPACE (workspace not
  * 256-byte aligned) or FALCON_ERR_CUDA.  The chunked backward (Falcon-1 /
- * 1A, d = 64) and falcon_attn_decode / _prompt keep their words in the same
- * place (a call without rows launches nothing and leaves the word alone).
+ * 1A, d = 64) and falcon_attn_decode / _prompt / _prompt_backward keep their
+ * words in the same place (a call without rows to write launches nothing and
+ * leaves the word alone).
  * Other kernel families have no device-side waits and do not write the word. */
 int falcon_workspace_status(const void* workspace, void* stream);
 
@@ -576,7 +577,8 @@ int falcon_workspace_status(const void* workspace, void* stream);
  * and of the chunked backward and the softmax-attention operators launched
  * from now on in this process (0 restores 2 s; the Falcon-2 kernel keeps 2 s).
  * stall != 0 makes the next forward call's per-chunk kernel (or the next
- * falcon_attn_decode, or tensor-core falcon_attn_prompt) wait once, before it loads anything, on a barrier
+ * falcon_attn_decode, or tensor-core falcon_attn_prompt, or the first tensor-core kernel of
+ * products of falcon_attn_prompt_backward) wait once, before it loads anything, on a barrier
  * that nothing completes: that wait runs out after the limit, the timeout is
  * recorded as described at falcon_workspace_status and the call's later
  * kernels skip their work.  No fault, trap or unbounded wait is involved;

@@ -452,6 +452,22 @@ def test_no_queries_and_no_keys(F):
         F.attn_prompt_backward(e(q), e(k), e(v), e(o), e(lse), e(dO), _dev([0, 0]))
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("d", [16, 64, 128])
+def test_calls_without_queries_clear_the_status(F, dtype, d):
+    q, k, v, dO = _inputs([5], [70], 2, 1, d, dtype)
+    lse = torch.zeros(5, 2, device="cuda")
+    for tokens, max_q in ((0, 3), (5, 0)):
+        p = F.AttnParams(B=1, Hq=2, Hkv=1, d=d, dtype=F.FALCON_BF16 if dtype == "bf16" else F.FALCON_F32, max_q=max_q,
+                         tokens=tokens, k_tokens=70)
+        ws = F.alloc_workspace(F.falcon_attn_prompt_backward_workspace_size(p))
+        ws.fill_(0xFF)
+        out = {n: torch.full_like(k, 3.0) for n in ("dk", "dv")}
+        F.falcon_attn_prompt_backward(p, q, k, v, _dev([0, tokens]), _dev([0, 70]), q, lse, dO, None, out, ws)
+        assert F.falcon_workspace_status(ws) == F.FALCON_OK
+        assert not out["dk"].any() and not out["dv"].any()
+
+
 @pytest.mark.parametrize("dtype,d", [("bf16", 64), ("bf16", 128), ("f32", 64), ("f32", 128)])
 def test_captured_calls_share_a_workspace(F, dtype, d):
     """Two graphs of different sizes over one workspace, replayed in turn with new inputs."""

@@ -576,11 +576,12 @@ __global__ void __launch_bounds__(Cfg32<D, KEYS>::kThreads, 1) attn_grad_tc32_ke
           load_pairs(ls + half * 32 + 8 * e, l4[0], l4[1]);
           load_pairs(ls + half * 32 + 8 * e + 4, l4[2], l4[3]);
         }
-        // the difference first: it is small where the weight is not
+        // The difference first: it is small where the weight is not.  The two factors first: X times one of them may pass
+        // fp32's range where the score does not (an infinite score of the wrong size would be a weight of 0, unnoticed).
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
-          const uint64_t y = mul2(pack2(__uint_as_float(v[8 * e + 2 * k]), __uint_as_float(v[8 * e + 2 * k + 1])), f1p);
-          x[4 * e + k] = mul2(fma2(y, s4[k], l4[k]), l2e);
+          const uint64_t y = pack2(__uint_as_float(v[8 * e + 2 * k]), __uint_as_float(v[8 * e + 2 * k + 1]));
+          x[4 * e + k] = mul2(fma2(y, mul2(f1p, s4[k]), l4[k]), l2e);
         }
       }
       if (cut) {

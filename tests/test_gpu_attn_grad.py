@@ -337,6 +337,31 @@ def test_rows_of_very_different_sizes(F, dtype, d):
         assert worst <= 1.0, (n, worst)
 
 
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("up", [110, -110])
+def test_rows_at_the_ends_of_fp32(F, d, up):
+    """Queries of 2^110 against keys of 2^-110 and the other way round; scores of -60 and 60 from rows that are each other's
+    negative or the same.  Such a score's products have one sign, and the tensor cores cut their sum off eight times (16 dims
+    at a time, high halves; the other parts are below 2^-10 of it): 2^-23 S each, 2^-20 S of a weight on top of the
+    tolerance of the other tests, whose products cancel.  The small operand's gradient lies at 2^-110 and below: dS times
+    that row's factor (2^-15 of its largest element, or more) is off by 2^-150 where it is not a normal number, times 2^15
+    for each of 90 terms, together below fp32's smallest normal number, 2^-126."""
+    lens = [1, 1, 90, 2]
+    q, k, v, dO = _inputs(lens, lens, 2, 2, d, "f32", 14)
+    k[:2] = -q[:2]
+    k[-2:] = q[-2:]
+    scale = 60.0 / d
+    q, k = q * 2.0 ** up, k * 2.0 ** -up
+    cu = _cu(lens)
+    o, lse, want, A = attention_grad(q, k, v, cu, cu, scale, dO)
+    got = F.attn_prompt_backward(q, k, v, o.float(), lse.float(), dO, _dev(cu), None, 90, scale)
+    S = _S(q, k, scale)
+    for name, f in (("dq", 2.0 ** up), ("dk", 2.0 ** -up), ("dv", 1.0)):
+        tol = (2.0 ** -22 * (2 * S + 8) + 2.0 ** -20 * S + 2.0 ** -20) * (A[name] * f) + 2.0 ** -126 * f
+        worst = ((got[name].double() - want[name]).abs() * f / tol).max().item()
+        assert worst <= 1.0, (name, worst)
+
+
 @pytest.mark.parametrize("dtype,d", [("bf16", 64), ("bf16", 128), ("f32", 64), ("f32", 128)])
 def test_calls_behind_one_another_over_one_workspace(F, dtype, d):
     """Calls of different sizes queued without a wait between them: the kernels of a call overlap, those of two do not."""

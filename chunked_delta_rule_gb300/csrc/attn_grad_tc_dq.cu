@@ -53,6 +53,7 @@ struct Block {
 struct BarsQ {
   uint64_t ready, full[10], empty[10], x, x_read, y, ds, drain, stall, told[2], heard[2];
   Block next[2];  // what the loading warp tells the others
+  uint64_t held;  // until when rows that are computed again may hold up the CTA's next block
   uint32_t tmem;
 };
 template <int D>
@@ -108,6 +109,7 @@ __global__ void __launch_bounds__(CfgQ<D>::kThreads, CfgQ<D>::kCtas)
       mbar_init(&bar->told[i], 1);
       mbar_init(&bar->heard[i], C::kWarps + 2);
     }
+    bar->held = 0;
     fence_mbar_init();
   }
   __syncthreads();
@@ -118,7 +120,7 @@ __global__ void __launch_bounds__(CfgQ<D>::kThreads, CfgQ<D>::kCtas)
   }
   const bool last = t.second && blockIdx.x == gridDim.x - 1 && tid == C::kThreads - 1;  // ends no sooner than the first kernel
   auto wait = [&](uint64_t* m, uint32_t parity) {
-    if (mbar_wait_sleep(m, parity, t.limit)) return true;
+    if (mbar_wait_sleep(m, parity, t.limit, &bar->held)) return true;
     atomicExch(t.status, kStatusTimeout);
     return false;
   };
@@ -456,7 +458,13 @@ __global__ void __launch_bounds__(CfgQ<D>::kThreads, CfgQ<D>::kCtas)
       float ra, rb;
       unpack2(rest, ra, rb);
       __syncwarp();
-      for (uint32_t again = __ballot_sync(0xffffffffu, row < x.lq && !(ra + rb == 0.f)); again; again &= again - 1) {
+      uint32_t again = __ballot_sync(0xffffffffu, row < x.lq && !(ra + rb == 0.f));
+      // They hold up the CTA's next block: no wait runs out meanwhile.  2 us a key and row, several times what it takes.
+      // (Counts of the warps that begin and end, looked at where a wait runs out: 212 us for 205 at 8 x 2048.)
+      if (again && lane == 0)
+        atomicMax(reinterpret_cast<unsigned long long*>(&bar->held),
+                  globaltimer() + static_cast<uint64_t>(__popc(again)) * x.lk * 2000);
+      for (; again; again &= again - 1) {
         const int i = x.row0 + quad * 32 + __ffs(again) - 1;
         float z[4];
         const __nv_bfloat16 *q = static_cast<const __nv_bfloat16*>(a.q.p), *d_o = static_cast<const __nv_bfloat16*>(g.d_o.p);
@@ -501,9 +509,7 @@ int launch_d(const GradArgs& g, bool second, cudaStream_t s) {
   t.second = second;
   t.status = static_cast<uint32_t*>(a.ws);
   t.counter = t.status + 1;
-  // Rows that are computed again hold up the CTA's next block, so that no wait may run out before a warp's 32 rows are done: 2 us
-  // a key and row, several times what it takes.  (A look at a count of such rows in the waits: 222 us for 205 at 8 x 2048.)
-  t.limit = wait_limit_ns() + static_cast<uint64_t>(a.k_tokens) * 32 * 2000;
+  t.limit = wait_limit_ns();
   t.stall = take_test_stall() ? 1 : 0;
   const auto kern = attn_grad_dq_tc_kernel<D>;
   if (!set_smem_limit(reinterpret_cast<const void*>(kern), smem_bytes<D>())) return FALCON_ERR_CUDA;

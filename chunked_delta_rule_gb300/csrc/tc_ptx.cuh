@@ -57,9 +57,11 @@ __device__ __forceinline__ bool mbar_wait(uint64_t* bar, uint32_t parity,
   return true;
 }
 // The same bound for warps that share their scheduler with busy ones: the
-// thread sleeps in the hardware for up to 2 us a try instead of polling.
+// thread sleeps in the hardware for up to 2 us a try instead of polling.  held: a
+// time up to which what is waited for may be held up; the limit counts from there.
 __device__ __forceinline__ bool mbar_wait_sleep(uint64_t* bar, uint32_t parity,
-                                                uint64_t limit_ns = kWaitLimitNs) {
+                                                uint64_t limit_ns = kWaitLimitNs,
+                                                const volatile uint64_t* held = nullptr) {
   if (mbar_try_wait(bar, parity)) return true;
   uint64_t t0 = 0;  // read after the first sleep: no wait of a healthy kernel is as long
   for (;;) {
@@ -74,7 +76,7 @@ __device__ __forceinline__ bool mbar_wait_sleep(uint64_t* bar, uint32_t parity,
     if (ok) return true;
     const uint64_t now = globaltimer();
     if (t0 == 0) t0 = now;
-    else if (now - t0 > limit_ns) return false;
+    else if (now - t0 > limit_ns && (!held || now > *held + limit_ns)) return false;
   }
 }
 

@@ -517,8 +517,9 @@ size_t falcon_attn_prompt_backward_workspace_size(const falcon_attn_params_t* p)
  * scales below 2^-100: 11);
  * fp32: operands, P and dS keep 22 bits, down to 2^-40 of the largest magnitude of
  * their row.  Bounded waits that run out are reported through
- * falcon_workspace_status(workspace, stream) (in the bf16 kernel of dq after 64 us a
- * key of the call on top of the limit, since rows computed again hold it up).
+ * falcon_workspace_status(workspace, stream) (in the bf16 kernel of dq, where a
+ * block has rows that are computed again, up to 2 us a key and such row later: they
+ * hold up the next block).
  * Errors: FALCON_ERR_INVALID_ARG, FALCON_ERR_UNSUPPORTED,
  * FALCON_ERR_WORKSPACE, FALCON_ERR_CUDA. */
 int falcon_attn_prompt_backward(const falcon_attn_params_t* p, const void* q, const void* k, const void* v,

@@ -16,6 +16,7 @@ many terms add up) or 1e-5 (fp32) times 2 of the norm.
 from __future__ import annotations
 
 import math
+import time
 
 import numpy as np
 import pytest
@@ -410,6 +411,37 @@ def test_a_wait_that_runs_out_is_reported(F, dtype, d, Hq, Hkv):
     assert F.falcon_workspace_status(ws) == F.FALCON_OK
     want = F.attn_prompt_backward(q, k, v, o, lse, dO, cu, max_q=700)
     assert all(torch.equal(out[m], want[m]) for m in want)
+
+
+@pytest.mark.parametrize("dtype,d", [("bf16", 32), ("bf16", 64), ("bf16", 128), ("f32", 64), ("f32", 128)])
+@pytest.mark.parametrize("lens", [[700], [2000] * 12])
+def test_a_wait_of_dq_alone_that_runs_out_is_reported(F, dtype, d, lens):
+    """The copies of dQ's kernel never begin: reported after the limit, however many keys the call has; the next call is right."""
+    n = sum(lens)
+    q, k, v, dO = _inputs(lens, lens, 4, 2, d, dtype, 2)
+    cu = _dev(_cu(lens))
+    o, lse = _forward(F, q, k, v, cu, cu, lens[0])
+    want = F.attn_prompt_backward(q, k, v, o, lse, dO, cu, max_q=lens[0])["dq"]
+    p = F.AttnParams(B=len(lens), Hq=4, Hkv=2, d=d, dtype=F.FALCON_BF16 if dtype == "bf16" else F.FALCON_F32, max_q=lens[0],
+                     tokens=n, k_tokens=n)
+    ws = F.alloc_workspace(F.falcon_attn_prompt_backward_workspace_size(p))
+    out = {"dq": torch.full_like(q, 3.0)}
+    run = lambda: F.falcon_attn_prompt_backward(p, q, k, v, cu, cu, o, lse, dO, None, out, ws)  # noqa: E731
+    torch.cuda.synchronize()
+    try:
+        F.falcon_test_hooks(wait_limit_ns=2_000_000, stall=True)
+        begin = time.perf_counter()
+        run()
+        assert F.falcon_workspace_status(ws) == F.FALCON_ERR_TIMEOUT
+        took = time.perf_counter() - begin
+    finally:
+        F.falcon_test_hooks(0, False)
+    # a CTA waits for the limit in at most five places after one another; at most 12 x 16 x 4 CTAs in 152 places
+    assert took < 0.25, took
+    assert (out["dq"] == 3).all()
+    run()
+    assert F.falcon_workspace_status(ws) == F.FALCON_OK
+    assert torch.equal(out["dq"], want)
 
 
 @pytest.mark.parametrize("dtype,d", [("bf16", 64), ("bf16", 128), ("f32", 32), ("f32", 128)])

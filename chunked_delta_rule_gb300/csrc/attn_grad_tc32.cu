@@ -116,7 +116,7 @@ struct Operands {
 };
 constexpr int kQInfo = kPast * 12, kKInfo = kPast * 4;
 __device__ __forceinline__ float factor_at(const uint8_t* factors, int i) {
-  return __bfloat162float(reinterpret_cast<const __nv_bfloat16*>(factors)[i]);
+  return __bfloat162float(__ldcg(reinterpret_cast<const __nv_bfloat16*>(factors) + i));
 }
 __host__ __device__ __forceinline__ int64_t count_blocks(int64_t rows, int B) { return rows / kPast + B + 1; }
 __device__ __forceinline__ int64_t first64(int64_t q0, int b) { return q0 / kPast + b; }
@@ -542,7 +542,8 @@ __global__ void __launch_bounds__(Cfg32<D, KEYS>::kThreads, 1) attn_grad_tc32_ke
       } else {
         const uint8_t* info = t.w.q_info + blk * kQInfo;
         f1 = a.scale * factor_at(info + 8 * kPast, at), f2 = factor_at(info + 8 * kPast, kPast + at);
-        lse = reinterpret_cast<const float*>(info)[at], delta = reinterpret_cast<const float*>(info)[kPast + at];
+        const float* sums = reinterpret_cast<const float*>(info) + at;
+        lse = load_past_l1(sums), delta = load_past_l1(sums + kPast);
       }
     }
     // the second owned tile to TMEM, a row a thread: the hi's by one warpgroup, the lo's by the other
@@ -693,9 +694,9 @@ __global__ void __launch_bounds__(Cfg32<D, KEYS>::kThreads, 1) attn_grad_tc32_ke
       } else {
         const int64_t h0 = static_cast<int64_t>(head) * d, hk = static_cast<int64_t>(head / G) * d;
         const float* s = sums + static_cast<int64_t>(i / kSumRows) * (2 * kSumRows) + i % kSumRows;
-        grad_query_row<float, D>(q + (q0 + i) * a.q.stride + h0, d_o + (q0 + i) * g.d_o.stride + h0, s[0], s[kSumRows],
-                                 k + k0 * a.k.stride + hk, a.k.stride, v + k0 * a.v.stride + hk, a.v.stride,
-                                 min(i + off + 1, lk), d, a.scale, x1);
+        grad_query_row<float, D>(q + (q0 + i) * a.q.stride + h0, d_o + (q0 + i) * g.d_o.stride + h0, load_past_l1(s),
+                                 load_past_l1(s + kSumRows), k + k0 * a.k.stride + hk, a.k.stride,
+                                 v + k0 * a.v.stride + hk, a.v.stride, min(i + off + 1, lk), d, a.scale, x1);
       }
     };
     // this lane's half of its row of a result; which: dV (0), dK or dQ (1)

@@ -341,7 +341,7 @@ __global__ void __launch_bounds__(CfgQ<D>::kThreads, CfgQ<D>::kCtas)
     float lse = 0.f, delta = 0.f;  // of this thread's query
     if (x.n > 0) {
       const float* s = sums_of(x) + static_cast<int64_t>(x.row0 / kSumRows) * (2 * kSumRows) + r;
-      lse = s[0], delta = s[kSumRows];
+      lse = load_past_l1(s), delta = load_past_l1(s + kSumRows);
       ok = bring();
     }
     while (x.n >= 0 && ok) {
@@ -414,7 +414,7 @@ __global__ void __launch_bounds__(CfgQ<D>::kThreads, CfgQ<D>::kCtas)
       const Block next = hear();
       if (next.n > 0) {
         const float* s = sums_of(next) + static_cast<int64_t>(next.row0 / kSumRows) * (2 * kSumRows) + r;
-        lse = s[0], delta = s[kSumRows];
+        lse = load_past_l1(s), delta = load_past_l1(s + kSumRows);
         if (!(ok = bring())) break;
       }
       // this thread's 64 dims of a row; a warp's 32 rows through shared memory, so that a store covers whole lines
@@ -471,9 +471,10 @@ __global__ void __launch_bounds__(CfgQ<D>::kThreads, CfgQ<D>::kCtas)
         const __nv_bfloat16 *k = static_cast<const __nv_bfloat16*>(a.k.p), *v = static_cast<const __nv_bfloat16*>(a.v.p);
         const int64_t h0 = static_cast<int64_t>(x.head) * d, hk = static_cast<int64_t>(x.head / G) * d;
         const float* s = sums_of(x) + static_cast<int64_t>(i / kSumRows) * (2 * kSumRows) + i % kSumRows;
-        grad_query_row<__nv_bfloat16, D>(q + (x.q0 + i) * a.q.stride + h0, d_o + (x.q0 + i) * g.d_o.stride + h0, s[0],
-                                         s[kSumRows], k + x.k0 * a.k.stride + hk, a.k.stride, v + x.k0 * a.v.stride + hk,
-                                         a.v.stride, min(i + x.off + 1, x.lk), d, a.scale, z);
+        grad_query_row<__nv_bfloat16, D>(q + (x.q0 + i) * a.q.stride + h0, d_o + (x.q0 + i) * g.d_o.stride + h0,
+                                         load_past_l1(s), load_past_l1(s + kSumRows), k + x.k0 * a.k.stride + hk,
+                                         a.k.stride, v + x.k0 * a.v.stride + hk, a.v.stride, min(i + x.off + 1, x.lk), d,
+                                         a.scale, z);
 #pragma unroll
         for (int m = 0; m < D / 32; ++m) {
           const int c = m * 32 + lane;

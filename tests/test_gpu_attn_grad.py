@@ -297,6 +297,33 @@ def test_infinities_and_nan_reach_only_what_sees_them(F, dtype, d, Hq, Hkv, valu
                 assert fine[:60].all() == (name == "dq"), name
 
 
+@pytest.mark.parametrize("dtype,d,Hq,Hkv", [("bf16", 64, 2, 1), ("bf16", 128, 2, 1), ("bf16", 32, 16, 1), ("bf16", 128, 16, 1),
+                                            ("f32", 64, 2, 1), ("f32", 128, 16, 1)])
+@pytest.mark.parametrize("value", [math.nan, math.inf, -math.inf])
+def test_infinities_and_nan_reach_all_that_sees_them(F, dtype, d, Hq, Hkv, value):
+    """Where the definition's gradient is not finite, neither is the result."""
+    lens = [150, 40]
+    cu = _cu(lens)
+    for what in ("k", "v", "dO", "q", "dlse"):
+        q, k, v, dO = _inputs(lens, lens, Hq, Hkv, d, dtype, 6)
+        dlse = _rand(q.shape[:2], "f32", 9)
+        x = dict(q=q, k=k, v=v, dO=dO)
+        if what == "dlse":
+            dlse[100, 1] = value
+        else:
+            x[what][100 if what in ("dO", "q") else 60, 0, 3] = value
+        o, lse = _forward(F, q, k, v, _dev(cu), _dev(cu), 150)
+        got = F.attn_prompt_backward(q, k, v, o, lse, dO, _dev(cu), max_q=150, dlse=dlse)
+        with np.errstate(all="ignore"):
+            want = O.prompt_grad(_np(q), _np(k), _np(v), cu, cu, d ** -0.5, _np(dO), _np(dlse))
+        for name, w in zip(("dq", "dk", "dv"), want):
+            fine = torch.isfinite(torch.from_numpy(w).cuda())
+            lost = ~fine & torch.isfinite(got[name])
+            assert not lost.any(), (what, name, lost.nonzero()[:4].tolist(), int(lost.sum()), int((~fine).sum()))
+            extra = fine & ~torch.isfinite(got[name])
+            assert not extra.any(), (what, name, extra.nonzero()[:4].tolist(), int(extra.sum()))
+
+
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
 @pytest.mark.parametrize("lq,lk,Hq,Hkv,d", [
     ([1500], [1500], 8, 1, 64), ([900], [1700], 16, 1, 128), ([700, 20, 333], [700, 20, 333], 12, 1, 32),
@@ -311,6 +338,19 @@ def test_keys_shared_by_several_ctas(F, dtype, lq, lk, Hq, Hkv, d):
     _, _, want, A = attention_grad(q, k, v, cu_q, cu_k, d ** -0.5, dO)
     _check(got, want, A, dtype, _S(q, k, d ** -0.5))
     again = F.attn_prompt_backward(q, k, v, o, lse, dO, _dev(cu_q), _dev(cu_k), max(lq))
+    assert all(torch.equal(got[n], again[n]) for n in got)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("lens,Hq,Hkv,d", [([1500] + [16] * 40, 8, 1, 64), ([7] * 30 + [1200, 1], 8, 2, 128), ([16] * 50 + [2100], 16, 2, 32)])
+def test_one_long_sequence_beside_short_ones(F, dtype, lens, Hq, Hkv, d):
+    q, k, v, dO = _inputs(lens, lens, Hq, Hkv, d, dtype, 41)
+    cu = _cu(lens)
+    o, lse = _forward(F, q, k, v, _dev(cu), _dev(cu), max(lens))
+    got = F.attn_prompt_backward(q, k, v, o, lse, dO, _dev(cu), max_q=max(lens))
+    _, _, want, A = attention_grad(q, k, v, cu, cu, d ** -0.5, dO)
+    _check(got, want, A, dtype, _S(q, k, d ** -0.5))
+    again = F.attn_prompt_backward(q, k, v, o, lse, dO, _dev(cu), max_q=max(lens))
     assert all(torch.equal(got[n], again[n]) for n in got)
 
 

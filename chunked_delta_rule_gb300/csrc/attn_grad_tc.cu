@@ -9,6 +9,7 @@
 // time).  A CTA owns 128 rows of K and V; the queries of all heads of the group come
 // past, 128 at a time (64 at d = 64, with two CTAs on an SM):
 //   load warp    TMA: Q and dO of a tile, through a ring of pairs
+//   clear warp   zeros in the rows of a tile that lie past the sequence
 //   MMA warp     X, Y and the sums' products in the order that keeps the tensor
 //                cores ahead of the softmax warps, see the loop
 //   softmax      64 columns of a row a thread (32: 290 us for 281 for 12 ragged documents of
@@ -62,10 +63,12 @@ struct Cfg {
   static constexpr uint32_t kCols = D == 64 ? 256 : 512;
 };
 struct Bars {
-  uint64_t own, full[6], empty[6], x, y, p, ds, drain, stall;
+  uint64_t own, full[6], empty[6], raw[6], x, y, p, ds, drain, stall;
   uint32_t tmem, failed;
   uint32_t bad[2][4];  // rows that are not finite, a bit each
 };
+constexpr int kRaw = 12;  // from full to raw
+static_assert(offsetof(Bars, raw) == offsetof(Bars, full) + kRaw * sizeof(uint64_t), "places");
 template <int D>
 constexpr int smem_bytes() {
   return Cfg<D>::kRing + Cfg<D>::kExtra + 1024 + static_cast<int>(sizeof(Bars));
@@ -89,6 +92,48 @@ __device__ __forceinline__ uint64_t sdesc_plain16(uint32_t saddr) {
   d |= static_cast<uint64_t>(1) << 46;
   return d;
 }
+// Tile i's places in the ring.  The first tile (Q) is read until the tile's last product, the second (dO) until its last
+// but two; they change places from use to use, so that each copy has a whole tile's products of time.
+template <int P>
+__device__ __forceinline__ int place_of(int i, int second) {
+  return 2 * (i % P) + ((i / P + second) & 1);
+}
+// A head's last tile may reach past the sequence, into the next one's rows or what lies behind the last one.  Their weights
+// are 0, but 0 times one that is not finite would have every key of the sequence computed again (8 x 2000 tokens of 12
+// heads of 64, NaN behind the last: 41.8 ms for 0.2; 4000 of 16 over 4 heads of 128: 102 ms).  So these rows become zeros
+// before the tile counts as copied: by one warp, tiles i, i + each, ... below n, of which `live` rows stay.  (Stores one
+// after another with the wait by one lane: 12 ragged documents of 16 over 4 heads of 128 269 us, so 262.)
+template <int D>
+__device__ __noinline__ void clear_rows(Bars* bar, uint8_t* ring, int i, int n, int each, int live, uint32_t* status,
+                                        uint64_t limit) {
+  using C = Cfg<D>;
+  constexpr int N = C::kN;
+  const int lane = threadIdx.x & 31;
+  uint32_t parity = 0;  // a bit each place
+  for (; i < n; i += each)
+    for (int second = 0; second < 2; ++second) {
+      const int slot = place_of<C::kPairs>(i, second);
+      if (!__all_sync(0xffffffffu, mbar_wait_sleep(&bar->raw[slot], (parity >> slot) & 1, limit))) {
+        if (lane == 0) {
+          atomicExch(status, kStatusTimeout);
+          *static_cast<volatile uint32_t*>(&bar->failed) = 1;
+        }
+        return;
+      }
+      parity ^= 1u << slot;
+      uint8_t* tile = ring + slot * C::kTileBytes + lane * 16;
+#pragma unroll 4
+      for (int x = live * 128; x < N * 128; x += 512) {
+#pragma unroll
+        for (int c = 0; c < D / 64; ++c)
+          if (x + lane * 16 < N * 128) *reinterpret_cast<uint4*>(tile + c * N * 128 + x) = make_uint4(0u, 0u, 0u, 0u);
+      }
+      fence_proxy_async();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&bar->full[slot]);
+    }
+}
+
 template <int D>
 __global__ void __launch_bounds__(Cfg<D>::kThreads, Cfg<D>::kCtas)
     attn_grad_tc_kernel(const __grid_constant__ CUtensorMap own1, const __grid_constant__ CUtensorMap own2,
@@ -117,6 +162,7 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, Cfg<D>::kCtas)
     for (int i = 0; i < 2 * P; ++i) {
       mbar_init(&bar->full[i], 1);
       mbar_init(&bar->empty[i], 1);
+      mbar_init(&bar->raw[i], 1);
     }
     mbar_init(&bar->x, 1);
     mbar_init(&bar->y, 1);
@@ -155,6 +201,7 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, Cfg<D>::kCtas)
   const int first = max(row0 - off, 0) / N * N, each = lq > first ? (lq - first + N - 1) / N : 0;
   const int64_t all = static_cast<int64_t>(each) * G;
   const int i0 = static_cast<int>(all * rank / t.split), n = static_cast<int>(all * (rank + 1) / t.split) - i0;
+  const int live = lq - first - (each - 1) * N;  // rows of a head's last tile
   __syncthreads();
   const uint32_t tmem = bar->tmem;
   wait_for_previous();  // what the sums' kernel wrote is there
@@ -169,9 +216,7 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, Cfg<D>::kCtas)
     *static_cast<volatile uint32_t*>(&bar->failed) = 1;
     return false;
   };
-  // Tile i's places in the ring.  The first tile (Q) is read until the tile's last product, the second (dO) until its last
-  // but two; they change places from use to use, so that each copy has a whole tile's products of time.
-  auto place = [&](int i, int second) { return 2 * (i % P) + ((i / P + second) & 1); };
+  auto place = [&](int i, int second) { return place_of<P>(i, second); };
 
   // registers: the softmax threads take what the last warpgroup gives up
   // (128 x 200 + 128 x 56 = 256 x 128; 256 x 208 + 128 x 88 = 384 x 168)
@@ -195,18 +240,19 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, Cfg<D>::kCtas)
       }
       for (; loads < 2 * n && ok; ++loads) {
         const int i = loads >> 1, second = loads & 1, st = i % P, use = i / P, slot = place(i, second);
-        if (use > 0 && !(ok = wait(&bar->empty[slot], (use - 1) & 1))) break;
+        // (what the copy needs comes before the wait for its place)
         const int h = head * G + (i0 + i) / each, at = first + (i0 + i) % each * N;
         const int row = static_cast<int>(q0 + at);
         const bool image = !second;  // its place was last read by the product before the one that freed this
-        mbar_arrive_expect_tx(&bar->full[slot], C::kTileBytes + (image ? C::kImage : 0));
+        uint64_t* full = bar->full + slot + (at + N > lq ? kRaw : 0);
+        const uint8_t* from = g.images + (static_cast<int64_t>(h) * g.blocks + first_block(q0, b) + at / kSumRows) * kImageBytes +
+                              at % kSumRows * 32;
+        if (use > 0 && !(ok = wait(&bar->empty[slot], (use - 1) & 1))) break;
+        mbar_arrive_expect_tx(full, C::kTileBytes + (image ? C::kImage : 0));
         for (int c = 0; c < D / 64; ++c)
-          tma_load_3d(ring + slot * C::kTileBytes + c * N * 128, second ? &past2 : &past1, &bar->full[slot], c * 64, h, row);
+          tma_load_3d(ring + slot * C::kTileBytes + c * N * 128, second ? &past2 : &past1, full, c * 64, h, row);
         if (image)
-          bulk_load(images + st * C::kImage,
-                    g.images + (static_cast<int64_t>(h) * g.blocks + first_block(q0, b) + at / kSumRows) * kImageBytes +
-                        at % kSumRows * 32,
-                    C::kImage, &bar->full[slot]);
+          bulk_load(images + st * C::kImage, from, C::kImage, full);
       }
       // every copy has landed before the CTA may end
       if (own) wait(&bar->own, 0);
@@ -279,6 +325,9 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, Cfg<D>::kCtas)
           ok = wait(m, i & 1);  // so that the next arrival counts for the next tile
         }
     }
+    __syncwarp();
+  } else if (warp == C::kMmaWarp + 2) {
+    if (n > 0 && live < N) clear_rows<D>(bar, ring, each - 1 - i0 % each, n, each, live, t.status, t.limit);
     __syncwarp();
   } else if (warp < C::kLoadWarp) {
     if (D == 64) asm volatile("setmaxnreg.inc.sync.aligned.u32 200;");

@@ -259,6 +259,38 @@ def test_rows_behind_the_last_sequence_and_past_max_q(F, dtype):
     _check(got, want, A, dtype, _S(q[:-9], k[:-9], d ** -0.5))
 
 
+@pytest.mark.parametrize("dtype,lens,Hq,Hkv,d", [("bf16", [2000] * 8, 12, 12, 64), ("bf16", [4000], 16, 4, 128), ("bf16", [70] * 90, 8, 2, 128),
+                                                 ("bf16", [2999], 8, 1, 32), ("f32", [1999], 8, 2, 128)])
+def test_rows_past_a_sequence_cost_no_time(F, dtype, lens, Hq, Hkv, d):
+    """Queries and their gradients that are not finite behind the last sequence, as memory that was never written may hold
+    them, and in front of each: the same bits in dk and dv, and not some hundred times as long, as with zeros there."""
+    n = sum(lens) + 9
+    cu = _dev([5 + x for x in _cu(lens)])
+    q, k, v, dO = _inputs([n], [n], Hq, Hkv, d, dtype, 3)
+    p = F.AttnParams(B=len(lens), Hq=Hq, Hkv=Hkv, d=d, dtype=F.FALCON_BF16 if dtype == "bf16" else F.FALCON_F32, max_q=max(lens),
+                     tokens=n, k_tokens=n)
+    ws = F.alloc_workspace(F.falcon_attn_prompt_backward_workspace_size(p))
+    o, lse = _forward(F, q, k, v, cu, cu, max(lens))
+    times, results = [], []
+    for value in (0.0, math.nan):
+        for x in (q, dO):
+            x[:5], x[-4:] = value, value
+        out = {m: torch.zeros_like(x) for m, x in (("dk", k), ("dv", v))}
+        ms = []
+        for _ in range(5):
+            a, b = (torch.cuda.Event(enable_timing=True) for _ in range(2))
+            a.record()
+            F.falcon_attn_prompt_backward(p, q, k, v, cu, cu, o, lse, dO, None, out, ws)
+            b.record()
+            b.synchronize()
+            ms.append(a.elapsed_time(b))
+        assert F.falcon_workspace_status(ws) == F.FALCON_OK
+        times.append(min(ms))
+        results.append(out)
+    assert all(torch.equal(results[0][m], results[1][m]) for m in results[0])
+    assert times[1] < 4 * times[0] + 0.05, times
+
+
 @pytest.mark.parametrize("dtype,d,Hq,Hkv", [("bf16", 64, 2, 1), ("bf16", 128, 2, 1), ("bf16", 32, 2, 1), ("f32", 64, 2, 1),
                                               ("f32", 128, 2, 1), ("f32", 16, 16, 1), ("f32", 128, 16, 1),
                                               ("bf16", 64, 16, 1), ("bf16", 128, 16, 1)])

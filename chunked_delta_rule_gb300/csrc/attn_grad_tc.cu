@@ -121,15 +121,7 @@ __device__ __noinline__ void clear_rows(Bars* bar, uint8_t* ring, int i, int n, 
         return;
       }
       parity ^= 1u << slot;
-      uint8_t* tile = ring + slot * C::kTileBytes + lane * 16;
-#pragma unroll 4
-      for (int x = live * 128; x < N * 128; x += 512) {
-#pragma unroll
-        for (int c = 0; c < D / 64; ++c)
-          if (x + lane * 16 < N * 128) *reinterpret_cast<uint4*>(tile + c * N * 128 + x) = make_uint4(0u, 0u, 0u, 0u);
-      }
-      fence_proxy_async();
-      __syncwarp();
+      zero_rows<N, D / 64>(ring + slot * C::kTileBytes, live);
       if (lane == 0) mbar_arrive(&bar->full[slot]);
     }
 }

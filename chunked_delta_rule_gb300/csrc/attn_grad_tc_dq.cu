@@ -5,6 +5,7 @@
 // A CTA takes blocks of 128 queries of one head as it gets ready for them, the longest first; per block the keys come past,
 // 128 at a time (d = 64: 64, with two CTAs on an SM).
 //   load warp    TMA: Q and dO of the next block, K and V through a ring of pairs
+//   clear warp   zeros in the rows of a tile that lie past the sequence
 //   MMA warp     ... Y(i) X(i + 1) dQ(i) Y(i + 1) ...: P(i + 1) is formed under dQ(i) and Y(i + 1), dS(i) under X(i + 1)
 //   softmax      64 columns of a row a thread: P from X, dS from P and Y; dS goes back to TMEM in bf16
 //   warps        over Y, as the A operand of dQ
@@ -51,11 +52,13 @@ struct Block {
   int64_t q0, k0;
 };
 struct BarsQ {
-  uint64_t ready, full[10], empty[10], x, x_read, y, ds, drain, stall, told[2], heard[2];
+  uint64_t ready, full[10], empty[10], raw[10], x, x_read, y, ds, drain, stall, told[2], heard[2];
   Block next[2];  // what the loading warp tells the others
   uint64_t held;  // until when rows that are computed again may hold up the CTA's next block
   uint32_t tmem;
 };
+constexpr int kRaw = 20;  // from full to raw
+static_assert(offsetof(BarsQ, raw) == offsetof(BarsQ, full) + kRaw * sizeof(uint64_t), "places");
 template <int D>
 constexpr int smem_bytes() {  // the ring, the rows of dQ on their way out
   return CfgQ<D>::kRing + CfgQ<D>::kOwnBytes + 1024 + static_cast<int>(sizeof(BarsQ));
@@ -98,6 +101,7 @@ __global__ void __launch_bounds__(CfgQ<D>::kThreads, CfgQ<D>::kCtas)
     for (int i = 0; i < 2 * P; ++i) {
       mbar_init(&bar->full[i], 1);
       mbar_init(&bar->empty[i], 1);
+      mbar_init(&bar->raw[i], 1);
     }
     mbar_init(&bar->x, 1);
     mbar_init(&bar->x_read, C::kWarps + 1);
@@ -107,7 +111,7 @@ __global__ void __launch_bounds__(CfgQ<D>::kThreads, CfgQ<D>::kCtas)
     mbar_init(&bar->stall, 1);
     for (int i = 0; i < 2; ++i) {
       mbar_init(&bar->told[i], 1);
-      mbar_init(&bar->heard[i], C::kWarps + 2);
+      mbar_init(&bar->heard[i], C::kWarps + 3);
     }
     bar->held = 0;
     fence_mbar_init();
@@ -181,8 +185,6 @@ __global__ void __launch_bounds__(CfgQ<D>::kThreads, CfgQ<D>::kCtas)
   if (warp >= C::kLoadWarp) {
     if (D == 64) asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
     else asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
-    if (last) wait_for_previous();
-    __syncwarp();
   }
   // In every role: tiles, pairs = those of the blocks before, begun = blocks with tiles before.
   int tiles = 0, pairs = 0, begun = 0;
@@ -199,15 +201,17 @@ __global__ void __launch_bounds__(CfgQ<D>::kThreads, CfgQ<D>::kCtas)
         mbar_arrive(&bar->told[told & 1]);
       }
       if (x.n < 0) break;
+      const int cut = x.n * N > x.lk ? x.n - 1 : x.n;  // the tile that reaches past the sequence
       if (lane == 0 && x.n > 0)
         for (int l = 0; l < 2 * (O + x.n) && ok; ++l, ++loads) {
           const int j = pairs + (l >> 1), second = l & 1, slot = place(j, second), i = (l >> 1) - O;
+          uint64_t* full = bar->full + slot + (i == cut ? kRaw : 0);  // of K and V
           if (j >= P && !(ok = wait(&bar->empty[slot], (j / P - 1) & 1))) break;
           uint8_t* to = ring + slot * C::kTileBytes;
           if (i >= 0) {
-            mbar_arrive_expect_tx(&bar->full[slot], C::kTileBytes);
+            mbar_arrive_expect_tx(full, C::kTileBytes);
             for (int c = 0; c < D / 64; ++c)
-              tma_load_3d(to + c * N * 128, second ? &v_map : &k_map, &bar->full[slot], c * 64, x.head / G,
+              tma_load_3d(to + c * N * 128, second ? &v_map : &k_map, full, c * 64, x.head / G,
                           static_cast<int>(x.k0 + i * N));
           } else if (D == 128 || second) {
             // d = 64: both places of the pair are free
@@ -296,6 +300,22 @@ __global__ void __launch_bounds__(CfgQ<D>::kThreads, CfgQ<D>::kCtas)
         }
       ok = __all_sync(0xffffffffu, ok);
       tiles += x.n, pairs += O + x.n;
+    }
+  } else if (warp == C::kMmaWarp + 2) {
+    // The last keys' tile may reach past the sequence: zeros there before it counts as copied, see the kernel of dK and dV.
+    // (NaN in all rows behind the last of 8 x 2000 tokens of 12 heads of 64: a call of 11.4 ms without it for 0.21.)
+    uint32_t parity = 0;  // a bit each place
+    for (Block x = hear(); x.n >= 0 && ok; x = hear()) {
+      if (x.n == 0) continue;
+      pairs += O + x.n;
+      if (x.n * N <= x.lk) continue;
+      for (int second = 0; second < 2 && ok; ++second) {
+        const int slot = place(pairs - 1, second);
+        if (!(ok = __all_sync(0xffffffffu, wait(&bar->raw[slot], (parity >> slot) & 1)))) break;
+        parity ^= 1u << slot;
+        zero_rows<N, D / 64>(ring + slot * C::kTileBytes, x.lk - (x.n - 1) * N);
+        if (lane == 0) mbar_arrive(&bar->full[slot]);
+      }
     }
   } else if (warp < C::kLoadWarp) {
     if (D == 64) asm volatile("setmaxnreg.inc.sync.aligned.u32 200;");
@@ -485,6 +505,7 @@ __global__ void __launch_bounds__(CfgQ<D>::kThreads, CfgQ<D>::kCtas)
     }
     tc_fence_before();
   }
+  if (last) wait_for_previous();
   __syncthreads();
   if (warp == C::kMmaWarp) {
     tc_fence_after();

@@ -61,6 +61,22 @@ __device__ __forceinline__ bool elect_one() {
   return r != 0;
 }
 
+// Rows [live, N) of a tile in slabs of 64 bf16 columns become zeros, by a warp; the tensor cores see them once an arrival
+// after this has been waited for.
+template <int N, int SLABS>
+__device__ __forceinline__ void zero_rows(uint8_t* tile, int live) {
+  const int lane = threadIdx.x & 31;
+#pragma unroll 4
+  for (int x = live * 128; x < N * 128; x += 512) {
+#pragma unroll
+    for (int c = 0; c < SLABS; ++c)
+      if (x + lane * 16 < N * 128)
+        *reinterpret_cast<uint4*>(tile + c * N * 128 + x + lane * 16) = make_uint4(0u, 0u, 0u, 0u);
+  }
+  fence_proxy_async();
+  __syncwarp();
+}
+
 // [tokens, H, d] bf16 rows, boxes of 64 columns x `rows` tokens: zeros past a row's end
 inline bool make_rows_map(CUtensorMap* m, const RowsIn& r, int64_t tokens, int H, int d, int rows = kTile) {
   EncodeFn enc = get_encode();

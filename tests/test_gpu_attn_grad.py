@@ -291,6 +291,39 @@ def test_rows_past_a_sequence_cost_no_time(F, dtype, lens, Hq, Hkv, d):
     assert times[1] < 4 * times[0] + 0.05, times
 
 
+@pytest.mark.parametrize("dtype,lens,Hq,Hkv,d", [("bf16", [2000] * 8, 12, 12, 64), ("bf16", [4000], 16, 4, 128), ("bf16", [70] * 90, 8, 2, 128),
+                                                 ("bf16", [2999], 8, 1, 32), ("bf16", [1, 3, 129, 65, 64, 128, 200] * 5, 4, 2, 64),
+                                                 ("bf16", [1, 3, 129, 65, 64, 128, 200] * 5, 4, 2, 128), ("f32", [1999], 8, 2, 128)])
+def test_keys_past_a_sequence_cost_no_time(F, dtype, lens, Hq, Hkv, d):
+    """The same of dq, with all operands not finite around the sequences; and of the three together."""
+    n = sum(lens) + 9
+    cu = _dev([5 + x for x in _cu(lens)])
+    x = q, k, v, dO = _inputs([n], [n], Hq, Hkv, d, dtype, 3)
+    p = F.AttnParams(B=len(lens), Hq=Hq, Hkv=Hkv, d=d, dtype=F.FALCON_BF16 if dtype == "bf16" else F.FALCON_F32, max_q=max(lens),
+                     tokens=n, k_tokens=n)
+    ws = F.alloc_workspace(F.falcon_attn_prompt_backward_workspace_size(p))
+    o, lse = _forward(F, q, k, v, cu, cu, max(lens))
+    for names in (("dq",), ("dq", "dk", "dv")):
+        times, results = [], []
+        for value in (0.0, math.nan):
+            for t in x:
+                t[:5], t[-4:] = value, value
+            out = {m: torch.zeros_like(t) for m, t in (("dq", q), ("dk", k), ("dv", v)) if m in names}
+            ms = []
+            for _ in range(5):
+                a, b = (torch.cuda.Event(enable_timing=True) for _ in range(2))
+                a.record()
+                F.falcon_attn_prompt_backward(p, q, k, v, cu, cu, o, lse, dO, None, out, ws)
+                b.record()
+                b.synchronize()
+                ms.append(a.elapsed_time(b))
+            assert F.falcon_workspace_status(ws) == F.FALCON_OK
+            times.append(min(ms))
+            results.append(out)
+        assert all(torch.equal(results[0][m], results[1][m]) for m in names)
+        assert times[1] < 4 * times[0] + 0.05, times
+
+
 @pytest.mark.parametrize("dtype,d,Hq,Hkv", [("bf16", 64, 2, 1), ("bf16", 128, 2, 1), ("bf16", 32, 2, 1), ("f32", 64, 2, 1),
                                               ("f32", 128, 2, 1), ("f32", 16, 16, 1), ("f32", 128, 16, 1),
                                               ("bf16", 64, 16, 1), ("bf16", 128, 16, 1)])

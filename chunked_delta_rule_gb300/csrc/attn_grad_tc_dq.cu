@@ -14,7 +14,7 @@
 // of the next block comes before the rows of the last one are written, so that its first products run meanwhile: of
 // 20 us that a CTA a block took at 1130 tokens, d = 128, 5 were its beginning and its end (12 documents, 16 heads: 137 us,
 // now 113; blocks dealt out beforehand: 130).
-// d = 128: 2050 cycles a tile, 1536 of them products: Y, dS, dQ and the next Y follow one another.
+// d = 128: 2020 cycles a tile (16384 tokens), 1536 of them products: Y, dS, dQ and the next Y follow one another.
 //
 // dS is rounded to bf16 as K is held in it: at most 2^-8.  Everything else is fp32.
 //
